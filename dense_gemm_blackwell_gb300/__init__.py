@@ -23,6 +23,8 @@ __all__ = [
     "gemm_version", "gemm_schedule_model", "gemm_schedule_choose", "gemm_plan_work_unit", "GemmWorkUnit", "Plan",
     "GemmMachine", "gemm_plan_schedule", "gemm_machine_gb300",
     "matmul", "header_functions",
+    "LoraPlan", "lora_matmul", "rope_table", "qk_norm_rope", "qk_norm_rope_backward", "PagedAttentionPlan",
+    "serving_header_functions",
 ]
 
 # ---------------------------------------------------------------- constants (include/gemm.h)
@@ -448,3 +450,7 @@ def matmul(a, b, *, out=None, out_dtype=None, scale_a=None, scale_b=None, flags=
         plan = _plan_cache[key] = Plan(desc)
     plan.run(a, b, out, scale_a, scale_b)
     return out
+
+
+from .serving import (LoraPlan, PagedAttentionPlan, lora_matmul, qk_norm_rope, qk_norm_rope_backward,  # noqa: E402
+                      rope_table, serving_header_functions)

@@ -64,6 +64,15 @@ __host__ __device__ constexpr uint64_t smem_desc_sw128_mn_lbo(uint32_t smem_addr
            (uint64_t(2) << 61) | uint64_t((smem_addr >> 4) & 0x3FFFu);
 }
 
+// K-major operand, one 32-byte row of K (16 16-bit elements, one MMA's K) per
+// M or N element, 32-byte swizzle: eight rows form a 256-byte atom.
+constexpr uint64_t kSmemDescSw32KMajorBase =
+    (uint64_t(1) << 16) | (uint64_t(256 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(6) << 61);
+
+__host__ __device__ constexpr uint64_t smem_desc_sw32(uint32_t smem_addr) {
+    return kSmemDescSw32KMajorBase | uint64_t((smem_addr >> 4) & 0x3FFFu);
+}
+
 // Instruction descriptor of tcgen05.mma kind::f16 / kind::f8f6f4 (public PTX ISA):
 //   [4,6) D format (0 = f16, 1 = f32)   [7,10) A format   [10,13) B format
 //   [15] A major (0 = K)       [16] B major      [17,23) N >> 3   [24,29) M >> 4
@@ -134,6 +143,23 @@ struct PersistentParams {
     // last launch that completed, [1] CTAs of the running launch that finished.
     uint32_t* sk_epoch;
 };
+
+// Low-rank adapters beside a projection (lora.cu): after the K blocks of X W^T
+// a tile runs further K = 16 steps into the same accumulator, `steps` per
+// adapter that occurs among its rows: T (rows of other adapters zero) times
+// that adapter's B.  counts and ids are written by the kernel that computes T,
+// which this launch follows.
+struct LoraTail {
+    CUtensorMap tmap_t;       // T: (columns, tile rows, [m block][slot]), box (16, 128, 1)
+    CUtensorMap tmap_b;       // B: (rank, N, adapter), box (16, tile_n / cta_group, 1)
+    const int32_t* counts;    // [m block]: adapters among the block's rows
+    const int32_t* ids;       // [m block][slot]: which
+    int32_t max_adapters;     // slots per m block
+    int32_t steps;            // K = 16 steps per adapter
+    int32_t b_steps;          // of which this many cover B's columns (steps = b_steps, or twice that for two-term T)
+};
+constexpr uint32_t kTailRowBytes = 32;           // one row of one step's operand
+constexpr uint32_t kTailStepBytesA = 128 * kTailRowBytes;
 
 // The epoch of this launch: one past the last completed one (never 0, the
 // flags' initial value).  A CTA reads the same value whenever it asks before

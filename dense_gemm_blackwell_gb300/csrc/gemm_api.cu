@@ -29,6 +29,7 @@
 #include "common.cuh"
 #include "launch.h"
 #include "mx_ptx.cuh"
+#include "serving_host.h"
 #include "units.cuh"
 
 namespace {
@@ -750,6 +751,141 @@ static void host_pipe_free(HostPipe* hp) {
     delete hp;
 }
 
+// The launch parameters of a persistent 16-bit, tf32 or fp8 plan on these operands (scales excepted).
+static gemm_status_t persistent_params(gemm_plan_s* plan, const void* A, const void* B, void* D, PersistentParams* out) {
+    const gemm_desc_t& d = plan->desc;
+    const gemm_plan_info_t& info = plan->info;
+    const int eb_a = elem_bytes(d.dtype_a), eb_b = elem_bytes(d.dtype_b), eb_d = elem_bytes(d.dtype_d);
+    std::memset(out, 0, sizeof(*out));
+    PersistentParams& p = *out;
+    const int cg = info.cta_group;
+    const int64_t batch_maps = d.batch;
+    // Tensor maps depend on the pointers only: re-encode when they change.
+    if (!plan->maps_valid || plan->map_ptrs[0] != A || plan->map_ptrs[1] != B || plan->map_ptrs[2] != D) {
+        plan->maps_valid = false;
+        const bool mn_a = d.major_a == GEMM_MN_MAJOR, mn_b = d.major_b == GEMM_MN_MAJOR;
+        // K-major: (K, rows) boxes of one 128-byte atom x rows (k_atoms per
+        // stage).  MN-major: (rows, K) boxes of 64 x tile_k.
+        const int atom_k = (int)(128 / eb_a);
+        const bool ok_a = mn_a ? encode_map(&plan->maps[0], d.dtype_a, A, d.M, d.K, d.lda, batch_maps, d.stride_a,
+                                            (int)(128 / eb_a), info.tile_k)
+                               : encode_map(&plan->maps[0], d.dtype_a, A, d.K, d.M, d.lda, batch_maps, d.stride_a,
+                                            atom_k, 128);
+        const bool ok_b = mn_b ? encode_map(&plan->maps[1], d.dtype_b, B, d.N, d.K, d.ldb, batch_maps, d.stride_b,
+                                            (int)(128 / eb_b), info.tile_k)
+                               : encode_map(&plan->maps[1], d.dtype_b, B, d.K, d.N, d.ldb, batch_maps, d.stride_b,
+                                            atom_k, std::min(info.tile_n, 256) / cg);
+        if (!ok_a || !ok_b ||
+            !encode_map(&plan->maps[2], d.dtype_d, D, d.N, d.M, d.ldd, batch_maps, d.stride_d, 128 / eb_d, 32)) {
+            g_last_cuda_error = (int)cudaErrorInvalidValue;
+            return GEMM_ERR_CUDA;
+        }
+        plan->map_ptrs[0] = A;
+        plan->map_ptrs[1] = B;
+        plan->map_ptrs[2] = D;
+        plan->maps_valid = true;
+    }
+    p.tmap_a = plan->maps[0];
+    p.tmap_b = plan->maps[1];
+    p.tmap_d = plan->maps[2];
+    p.status = plan->status;
+    p.M = (int32_t)d.M; p.N = (int32_t)d.N; p.K = (int32_t)d.K; p.batch = (int32_t)d.batch;
+    fill_schedule(d, info, p);
+    p.tile_n = info.tile_n;
+    p.stages = info.stages;
+    p.tmem_cols = info.tmem_cols;
+    p.tmem_stages = info.tmem_stages;
+    p.batched = d.batch > 1 ? 1 : 0;
+    p.tile_k = info.tile_k;
+    p.k_atoms = (int32_t)(info.tile_k * eb_a / 128);   // 128-byte K atoms per stage
+    p.mma_kind = d.dtype_a == GEMM_TF32 ? dgb::kMmaKindTF32 : dgb::kMmaKindF16;
+    // A/B formats: kind::f16 0 = f16, 1 = bf16; kind::tf32 2 = tf32
+    p.mn_major_a = d.major_a == GEMM_MN_MAJOR;
+    p.mn_box_elems = (int32_t)(128 / eb_a);
+    p.mn_major_b = d.major_b == GEMM_MN_MAJOR;
+    // one MMA covers at most 256 columns (512-wide tiles issue two)
+    const uint32_t fmt = d.dtype_a == GEMM_BF16 ? 1u : (d.dtype_a == GEMM_TF32 ? 2u : 0u);
+    p.acc_f16 = (d.flags & GEMM_FLAG_ACCUM_F16) ? 1 : 0;
+    p.idesc = dgb::make_idesc2(fmt, fmt, (uint32_t)info.tile_m, (uint32_t)std::min(info.tile_n, 256),
+                               (uint32_t)p.mn_major_a, (uint32_t)p.mn_major_b, p.acc_f16 ? 0u : 1u);
+    p.stage_bytes_a = (uint32_t)(128 * info.tile_k * eb_a);
+    p.stage_bytes_b = (uint32_t)((info.tile_n / cg) * info.tile_k * eb_b);
+    p.flags = d.flags;
+    p.timeout_ns = d.wait_timeout_ns;
+    // Single long-K problems revisit A panels across the waves of a raster
+    // group and stream D out; batched problems touch every panel once.
+    p.l2_hints = (d.batch == 1 && p.num_k_blocks >= 8 && !(d.flags & GEMM_FLAG_NO_L2_HINTS))
+                     ? (dgb::kHintKeepA | dgb::kHintStreamD) : 0u;
+    p.direct_store = info.epilogue;
+    p.d_ptr = D;
+    p.ldd = d.ldd;
+    p.stride_d = d.stride_d;
+    if (info.stream_k_tiles > 0 && plan->sk_flags != nullptr) {
+        p.sk_tiles = info.stream_k_tiles;
+        p.sk_flags = plan->sk_flags;
+        p.sk_epoch = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(plan->status) + kSkEpochOffset);
+        p.sk_partials = plan->sk_partials;
+    }
+    return GEMM_OK;
+}
+
+namespace dgb {
+
+gemm_status_t status_of(cudaError_t e) { return e == cudaSuccess ? GEMM_OK : cuda_fail(e); }
+
+gemm_status_t device_facts(DeviceFacts* out) {
+    // attributes of a device never change: looked up once (sms 0 = not yet)
+    static std::atomic<int> sms[kMaxDevices], optin[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) {
+        g_last_cuda_error = (int)e;
+        return GEMM_ERR_NO_DEVICE;
+    }
+    out->device = dev;
+    if (dev < kMaxDevices && (out->sms = sms[dev].load(std::memory_order_acquire)) > 0) {
+        out->smem_optin = optin[dev].load(std::memory_order_relaxed);
+        return GEMM_OK;
+    }
+    int major = 0, minor = 0;
+    if ((e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev)) != cudaSuccess) return cuda_fail(e);
+    if ((e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev)) != cudaSuccess) return cuda_fail(e);
+    if (major != 10 || minor != 3) return GEMM_ERR_NO_DEVICE;
+    if ((e = cudaDeviceGetAttribute(&out->sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return cuda_fail(e);
+    if ((e = cudaDeviceGetAttribute(&out->smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess)
+        return cuda_fail(e);
+    if (dev < kMaxDevices) {
+        optin[dev].store(out->smem_optin, std::memory_order_relaxed);
+        sms[dev].store(out->sms, std::memory_order_release);
+    }
+    return GEMM_OK;
+}
+
+gemm_status_t product_params(gemm_plan_t plan, const void* A, const void* B, void* D, PersistentParams* out) {
+    // the tensor maps are encoded afresh: callers run one plan on ever changing operands
+    plan->maps_valid = false;
+    return persistent_params(plan, A, B, D, out);
+}
+
+gemm_status_t encode_steps_map(CUtensorMap* m, int dtype, const void* base, int64_t cols, int64_t rows, int64_t count, int64_t ld,
+                               int64_t stride, int box_rows) {
+    EncodeTiledFn enc = get_encode_fn();
+    const int eb = elem_bytes(dtype);
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)count};
+    cuuint64_t strides[2] = {(cuuint64_t)(ld * eb), (cuuint64_t)(stride * eb)};
+    cuuint32_t box[3] = {(cuuint32_t)(32 / eb), (cuuint32_t)box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    if (!enc || enc(m, tma_dtype(dtype), 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
+        g_last_cuda_error = (int)cudaErrorInvalidValue;
+        return GEMM_ERR_CUDA;
+    }
+    return GEMM_OK;
+}
+
+}  // namespace dgb
+
 extern "C" {
 
 gemm_status_t gemm_plan_query(const gemm_desc_t* desc, const gemm_device_props_t* props, gemm_plan_info_t* info) {
@@ -910,76 +1046,10 @@ gemm_status_t gemm_run(gemm_plan_t plan, const void* A, const void* B, void* D, 
     if (scaled && (!aligned16(scale_a) || !aligned16(scale_b))) return GEMM_ERR_ALIGNMENT;
 
     // persistent pipelines
-    PersistentParams p;
-    std::memset(&p, 0, sizeof(p));
     const int cg = info.cta_group;
-    const int64_t batch_maps = d.batch;
-    // Tensor maps depend on the pointers only: re-encode when they change.
-    if (!plan->maps_valid || plan->map_ptrs[0] != A || plan->map_ptrs[1] != B || plan->map_ptrs[2] != D) {
-        plan->maps_valid = false;
-        const bool mn_a = d.major_a == GEMM_MN_MAJOR, mn_b = d.major_b == GEMM_MN_MAJOR;
-        // K-major: (K, rows) boxes of one 128-byte atom x rows (k_atoms per
-        // stage).  MN-major: (rows, K) boxes of 64 x tile_k.
-        const int atom_k = (int)(128 / eb_a);
-        const bool ok_a = mn_a ? encode_map(&plan->maps[0], d.dtype_a, A, d.M, d.K, d.lda, batch_maps, d.stride_a,
-                                            (int)(128 / eb_a), info.tile_k)
-                               : encode_map(&plan->maps[0], d.dtype_a, A, d.K, d.M, d.lda, batch_maps, d.stride_a,
-                                            atom_k, 128);
-        const bool ok_b = mn_b ? encode_map(&plan->maps[1], d.dtype_b, B, d.N, d.K, d.ldb, batch_maps, d.stride_b,
-                                            (int)(128 / eb_b), info.tile_k)
-                               : encode_map(&plan->maps[1], d.dtype_b, B, d.K, d.N, d.ldb, batch_maps, d.stride_b,
-                                            atom_k, std::min(info.tile_n, 256) / cg);
-        if (!ok_a || !ok_b ||
-            !encode_map(&plan->maps[2], d.dtype_d, D, d.N, d.M, d.ldd, batch_maps, d.stride_d, 128 / eb_d, 32)) {
-            g_last_cuda_error = (int)cudaErrorInvalidValue;
-            return GEMM_ERR_CUDA;
-        }
-        plan->map_ptrs[0] = A;
-        plan->map_ptrs[1] = B;
-        plan->map_ptrs[2] = D;
-        plan->maps_valid = true;
-    }
-    p.tmap_a = plan->maps[0];
-    p.tmap_b = plan->maps[1];
-    p.tmap_d = plan->maps[2];
-    p.status = plan->status;
-    p.M = (int32_t)d.M; p.N = (int32_t)d.N; p.K = (int32_t)d.K; p.batch = (int32_t)d.batch;
-    fill_schedule(d, info, p);
-    p.tile_n = info.tile_n;
-    p.stages = info.stages;
-    p.tmem_cols = info.tmem_cols;
-    p.tmem_stages = info.tmem_stages;
-    p.batched = d.batch > 1 ? 1 : 0;
-    p.tile_k = info.tile_k;
-    p.k_atoms = (int32_t)(info.tile_k * eb_a / 128);   // 128-byte K atoms per stage
-    p.mma_kind = d.dtype_a == GEMM_TF32 ? dgb::kMmaKindTF32 : dgb::kMmaKindF16;
-    // A/B formats: kind::f16 0 = f16, 1 = bf16; kind::tf32 2 = tf32
-    p.mn_major_a = d.major_a == GEMM_MN_MAJOR;
-    p.mn_box_elems = (int32_t)(128 / eb_a);
-    p.mn_major_b = d.major_b == GEMM_MN_MAJOR;
-    // one MMA covers at most 256 columns (512-wide tiles issue two)
-    const uint32_t fmt = d.dtype_a == GEMM_BF16 ? 1u : (d.dtype_a == GEMM_TF32 ? 2u : 0u);
-    p.acc_f16 = (d.flags & GEMM_FLAG_ACCUM_F16) ? 1 : 0;
-    p.idesc = dgb::make_idesc2(fmt, fmt, (uint32_t)info.tile_m, (uint32_t)std::min(info.tile_n, 256),
-                               (uint32_t)p.mn_major_a, (uint32_t)p.mn_major_b, p.acc_f16 ? 0u : 1u);
-    p.stage_bytes_a = (uint32_t)(128 * info.tile_k * eb_a);
-    p.stage_bytes_b = (uint32_t)((info.tile_n / cg) * info.tile_k * eb_b);
-    p.flags = d.flags;
-    p.timeout_ns = d.wait_timeout_ns;
-    // Single long-K problems revisit A panels across the waves of a raster
-    // group and stream D out; batched problems touch every panel once.
-    p.l2_hints = (d.batch == 1 && p.num_k_blocks >= 8 && !(d.flags & GEMM_FLAG_NO_L2_HINTS))
-                     ? (dgb::kHintKeepA | dgb::kHintStreamD) : 0u;
-    p.direct_store = info.epilogue;
-    p.d_ptr = D;
-    p.ldd = d.ldd;
-    p.stride_d = d.stride_d;
-    if (info.stream_k_tiles > 0 && plan->sk_flags != nullptr) {
-        p.sk_tiles = info.stream_k_tiles;
-        p.sk_flags = plan->sk_flags;
-        p.sk_epoch = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(plan->status) + kSkEpochOffset);
-        p.sk_partials = plan->sk_partials;
-    }
+    PersistentParams p;
+    const gemm_status_t filled = persistent_params(plan, A, B, D, &p);
+    if (filled != GEMM_OK) return filled;
     if (info.kernel == GEMM_KERNEL_FP8_BLOCK) {
         p.scale_a = scale_a;
         p.scale_b = scale_b;

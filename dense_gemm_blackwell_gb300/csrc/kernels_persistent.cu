@@ -84,11 +84,12 @@ __host__ __device__ constexpr int batch_loads() { return OUT == GEMM_F32 ? 3 : 2
 // 256 / CG rows further on in the stage.  The two column halves are handed
 // back separately, so a tile starts with the left halves of its first
 // kWideLeadStages stages before it waits for the right half.
-template <int CG, int ATOMS, int HALVES>
+// TAIL: the tile's adapter steps follow its K blocks (producer_loop, kTail).
+template <int CG, int ATOMS, int HALVES, bool TAIL = false>
 __device__ __forceinline__ void mma_issuer(const PersistentParams& p, uint8_t* ring, uint32_t stage_bytes,
                                            uint32_t tmem_base, uint32_t full0, uint32_t empty0, uint32_t tfull0,
                                            uint32_t tempty0, uint32_t drain_bar, volatile uint32_t* abort_flag,
-                                           int cluster_id, int num_clusters) {
+                                           int cluster_id, int num_clusters, const LoraTail* tail = nullptr) {
     const int S = p.stages;
     const int TS = p.tmem_stages;
     const uint64_t tmo = p.timeout_ns;
@@ -229,6 +230,33 @@ __device__ __forceinline__ void mma_issuer(const PersistentParams& p, uint8_t* r
             if (++stage == S) { stage = 0; phase ^= 1u; }
         }
         if (aborted) break;
+        if constexpr (TAIL) {
+            if (u.role != kUnitContributor) {
+                griddep_wait();
+                int b, mb, nb;
+                tile_coords(p, t, b, mb, nb);
+                const int total = __ldcg(tail->counts + mb) * tail->steps;
+                for (int s0 = 0; s0 < total; s0 += 4 * ATOMS) {
+                    if (!wait_phase_warp<false>(full(stage), phase, abort_flag, tmo, p.status, kRoleMma, stage, t)) {
+                        aborted = true;
+                        break;
+                    }
+                    if (issuer) {
+                        tc_fence_after();
+                        const uint32_t sa = smem_u32(ring + (size_t)stage * stage_bytes);
+                        const uint64_t da = smem_desc_sw32(sa), db = smem_desc_sw32(sa + p.stage_bytes_a);
+                        const int n16 = min(4 * ATOMS, total - s0);
+                        const uint64_t step_b = (uint64_t)(p.tile_n / CG) * kTailRowBytes / 16u;
+                        for (int j = 0; j < n16; ++j)
+                            mma_f16<CG>(d_tmem, da + (uint64_t)j * (kTailStepBytesA / 16u), db + j * step_b, p.idesc, 1u);
+                        commit_to<CG>(empty(stage));
+                    }
+                    __syncwarp();
+                    if (++stage == S) { stage = 0; phase ^= 1u; }
+                }
+                if (aborted) break;
+            }
+        }
         if (issuer) {
             commit_to<CG>(tfull(acc, 0));
             if (HALVES == 2) commit_to<CG>(tfull(acc, 1));
@@ -244,8 +272,8 @@ __device__ __forceinline__ void mma_issuer(const PersistentParams& p, uint8_t* r
     __syncwarp();
 }
 
-template <int CG, int OUT>
-__global__ void __launch_bounds__(kThreads, 1) persistent_kernel(const __grid_constant__ PersistentParams p) {
+template <int CG, int OUT, bool TAIL>
+__device__ __forceinline__ void persistent_body(const PersistentParams& p, const LoraTail* tail) {
     constexpr int kOutBytes = (OUT == GEMM_F32) ? 4 : 2;
     constexpr int kChunkCols = 128 / kOutBytes;   // output columns per 128-byte staging row
 
@@ -310,7 +338,10 @@ __global__ void __launch_bounds__(kThreads, 1) persistent_kernel(const __grid_co
     // Set-up above overlaps the previous kernel of the stream; its results are
     // visible from here on.  The next GEMM may be launched now: its CTAs take
     // SMs as this grid's CTAs leave and wait in griddep_wait.
-    griddep_wait();
+    // With a tail the kernel just before computes T: that one waits for its
+    // predecessors before it lets this one start, so X, W and everything older
+    // are complete already, and only the tail waits (producer_loop, mma_issuer).
+    if constexpr (!TAIL) griddep_wait();
     griddep_launch_dependents();
 
     const int cluster_id = blockIdx.x / CG;
@@ -321,7 +352,23 @@ __global__ void __launch_bounds__(kThreads, 1) persistent_kernel(const __grid_co
         // ------------------------------------------------------------ TMA producers
         // warp 0: A (+ B's first half of a 512-wide tile); the second producer: the rest of B
         const bool first = warp == 0;
-        if (p.tile_n > 256) {
+        if constexpr (TAIL) {      // tiles up to 256 wide, K-major operands
+            if (p.k_atoms == 2) {
+                if (first)
+                    producer_loop<CG, 2, 1, kPartA, true, true>(p, ring, stage_bytes, p.tile_k, full0, empty0, abort_flag, rank,
+                                                                cluster_id, num_clusters, tail);
+                else
+                    producer_loop<CG, 2, 1, kPartB0, true, true>(p, ring, stage_bytes, p.tile_k, full0, empty0, abort_flag, rank,
+                                                                 cluster_id, num_clusters, tail);
+            } else {
+                if (first)
+                    producer_loop<CG, 1, 1, kPartA, true, true>(p, ring, stage_bytes, p.tile_k, full0, empty0, abort_flag, rank,
+                                                                cluster_id, num_clusters, tail);
+                else
+                    producer_loop<CG, 1, 1, kPartB0, true, true>(p, ring, stage_bytes, p.tile_k, full0, empty0, abort_flag, rank,
+                                                                 cluster_id, num_clusters, tail);
+            }
+        } else if (p.tile_n > 256) {
             if (first)
                 producer_loop<CG, 1, 2, kPartA | kPartB0, true>(p, ring, stage_bytes, p.tile_k, full0, empty0, abort_flag,
                                                           rank, cluster_id, num_clusters);
@@ -349,7 +396,14 @@ __global__ void __launch_bounds__(kThreads, 1) persistent_kernel(const __grid_co
         if (leader) {
             // the stage depth is a template argument: this warp runs the
             // kernel's tightest loop, so no per-stage branching on it
-            if (p.tile_n > 256)
+            if constexpr (TAIL) {
+                if (p.k_atoms == 2)
+                    mma_issuer<CG, 2, 1, true>(p, ring, stage_bytes, tmem_base, full0, empty0, tfull0, tempty0, drain_bar,
+                                               abort_flag, cluster_id, num_clusters, tail);
+                else
+                    mma_issuer<CG, 1, 1, true>(p, ring, stage_bytes, tmem_base, full0, empty0, tfull0, tempty0, drain_bar,
+                                               abort_flag, cluster_id, num_clusters, tail);
+            } else if (p.tile_n > 256)
                 mma_issuer<CG, 1, 2>(p, ring, stage_bytes, tmem_base, full0, empty0, tfull0, tempty0, drain_bar,
                                      abort_flag, cluster_id, num_clusters);
             else if (p.k_atoms == 2)
@@ -629,9 +683,19 @@ __global__ void __launch_bounds__(kThreads, 1) persistent_kernel(const __grid_co
 }
 
 template <int CG, int OUT>
-static cudaError_t launch_typed(const PersistentParams& p, int grid, size_t smem, cudaStream_t stream) {
-    auto kern = persistent_kernel<CG, OUT>;
-    static std::atomic<int> smem_set[kMaxDevices];
+__global__ void __launch_bounds__(kThreads, 1) persistent_kernel(const __grid_constant__ PersistentParams p) {
+    persistent_body<CG, OUT, false>(p, nullptr);
+}
+
+template <int CG, int OUT>
+__global__ void __launch_bounds__(kThreads, 1) adapters_kernel(const __grid_constant__ PersistentParams p,
+                                                               const __grid_constant__ LoraTail tail) {
+    persistent_body<CG, OUT, true>(p, &tail);
+}
+
+template <int CG, typename Kernel, typename... Args>
+static cudaError_t launch_pipeline(Kernel kern, std::atomic<int> (&smem_set)[kMaxDevices], int grid, size_t smem,
+                                   cudaStream_t stream, const Args&... args) {
     cudaError_t e = ensure_smem_limit(kern, smem, smem_set);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -648,7 +712,20 @@ static cudaError_t launch_typed(const PersistentParams& p, int grid, size_t smem
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int CG, int OUT>
+static cudaError_t launch_typed(const PersistentParams& p, int grid, size_t smem, cudaStream_t stream) {
+    static std::atomic<int> smem_set[kMaxDevices];
+    return launch_pipeline<CG>(persistent_kernel<CG, OUT>, smem_set, grid, smem, stream, p);
+}
+
+template <int CG, int OUT>
+static cudaError_t launch_adapters_typed(const PersistentParams& p, const LoraTail& tail, int grid, size_t smem,
+                                         cudaStream_t stream) {
+    static std::atomic<int> smem_set[kMaxDevices];
+    return launch_pipeline<CG>(adapters_kernel<CG, OUT>, smem_set, grid, smem, stream, p, tail);
 }
 
 template <int CG, int OUT>
@@ -703,6 +780,24 @@ cudaError_t launch_persistent(const PersistentParams& p, int cta_group, int dtyp
     case GEMM_F32: return launch_typed<2, GEMM_F32>(p, grid, smem_bytes, stream);
     case GEMM_BF16: return launch_typed<2, GEMM_BF16>(p, grid, smem_bytes, stream);
     case GEMM_F16: return launch_typed<2, GEMM_F16>(p, grid, smem_bytes, stream);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_adapters(const PersistentParams& p, const LoraTail& tail, int cta_group, int dtype_d, int grid,
+                            size_t smem_bytes, cudaStream_t stream) {
+    if (cta_group == 1) {
+        switch (dtype_d) {
+        case GEMM_F32: return launch_adapters_typed<1, GEMM_F32>(p, tail, grid, smem_bytes, stream);
+        case GEMM_BF16: return launch_adapters_typed<1, GEMM_BF16>(p, tail, grid, smem_bytes, stream);
+        case GEMM_F16: return launch_adapters_typed<1, GEMM_F16>(p, tail, grid, smem_bytes, stream);
+        default: return cudaErrorInvalidValue;
+        }
+    }
+    switch (dtype_d) {
+    case GEMM_F32: return launch_adapters_typed<2, GEMM_F32>(p, tail, grid, smem_bytes, stream);
+    case GEMM_BF16: return launch_adapters_typed<2, GEMM_BF16>(p, tail, grid, smem_bytes, stream);
+    case GEMM_F16: return launch_adapters_typed<2, GEMM_F16>(p, tail, grid, smem_bytes, stream);
     default: return cudaErrorInvalidValue;
     }
 }

@@ -16,6 +16,19 @@ cudaError_t launch_single_cta(const SingleParams& p, int dtype_d, int batch, siz
 cudaError_t launch_persistent(const PersistentParams& p, int cta_group, int dtype_d, int grid,
                               size_t smem_bytes, cudaStream_t stream);
 
+// The persistent kernel with adapter steps after each tile's K blocks (LoraTail); K-major 16-bit operands, tile_n <= 256.
+// Follows the kernel that computes T on the same stream, immediately.
+cudaError_t launch_adapters(const PersistentParams& p, const LoraTail& tail, int cta_group, int dtype_d, int grid,
+                            size_t smem_bytes, cudaStream_t stream);
+
+// The launch parameters of a plan's product on these operands (gemm_api.cu).
+gemm_status_t product_params(gemm_plan_t plan, const void* A, const void* B, void* D, PersistentParams* out);
+
+// Tensor map of `count` row-major (rows x cols) matrices of 16-bit elements, `ld` elements between rows and `stride` between
+// matrices; box (16, box_rows, 1), 32-byte swizzle (gemm_api.cu).
+gemm_status_t encode_steps_map(CUtensorMap* m, int dtype, const void* base, int64_t cols, int64_t rows, int64_t count, int64_t ld,
+                               int64_t stride, int box_rows);
+
 // How many clusters of `cta_group` CTAs with `smem_bytes` of dynamic shared
 // memory can be resident at once (0 if the query fails).
 int persistent_max_active_clusters(int cta_group, int dtype_d, size_t smem_bytes);

@@ -1,0 +1,8 @@
+// paged_attn_bf16_e4m3.cu -- instantiations of the paged attention kernel (paged_attn.cuh).
+#include "paged_attn.cuh"
+
+namespace dgb {
+
+cudaError_t attn_variant_bf16_e4m3(int head_dim, AttnVariant* v) { return attn_variant<__half, __nv_bfloat16, true>(head_dim, v); }
+
+}  // namespace dgb

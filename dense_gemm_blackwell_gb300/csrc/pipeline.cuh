@@ -152,10 +152,14 @@ constexpr uint32_t kPartA = 1u, kPartB0 = 2u, kPartB1 = 4u, kPartsAll = 7u;
 // on the slices the previous one read last (8192^3 on GB300: 845 -> 694 MB
 // read from DRAM, 1.2 % faster at the power cap).  Only the summation order
 // of the tile changes; a kernel that applies per-K-block scales keeps it off.
-template <int CG, int ATOMS = 1, int HALVES = 1, uint32_t PARTS = kPartsAll, bool kSerpentine = false>
+// kTail: after the K blocks of a unit that ends its tile, the tile's adapter
+// steps (LoraTail), 4 * ATOMS of them to a stage: step j's 128 rows of T at
+// j * 4 KB of the stage's A area, its rows of B at j * b_rows * 32 bytes of the
+// B area.
+template <int CG, int ATOMS = 1, int HALVES = 1, uint32_t PARTS = kPartsAll, bool kSerpentine = false, bool kTail = false>
 __device__ void producer_loop(const PersistentParams& p, uint8_t* ring, uint32_t stage_bytes, int tile_k,
                               uint32_t full0, uint32_t empty0, volatile uint32_t* abort_flag, uint32_t rank,
-                              int cluster_id, int num_clusters) {
+                              int cluster_id, int num_clusters, const LoraTail* tail = nullptr) {
     constexpr uint32_t parts = PARTS;
     const int S = p.stages;
     const bool leader = rank == 0;
@@ -232,7 +236,47 @@ __device__ void producer_loop(const PersistentParams& p, uint8_t* ring, uint32_t
             ++issued;
             if (++stage == S) { stage = 0; phase ^= 1u; }
         }
+        if constexpr (kTail) {
+            if (aborted || u.role == kUnitContributor) continue;
+            griddep_wait();     // the kernel that computes T, counts and ids is done
+            const int total = __ldcg(tail->counts + mb) * tail->steps;
+            for (int s0 = 0; s0 < total; s0 += 4 * ATOMS) {
+                if (!wait_phase_warp<false, true>(empty0 + 8u * stage, phase ^ 1u, abort_flag, tmo, p.status,
+                                                  kRoleProducer, stage, t)) {
+                    aborted = true;
+                    break;
+                }
+                if (elect_one()) {
+                    const uint32_t fb = fb0 + 8u * stage;
+                    const int n16 = min(4 * ATOMS, total - s0);
+                    const uint32_t step_b = (uint32_t)b_rows * kTailRowBytes;
+                    if (leader && (parts & kPartA) != 0)
+                        mbar_arrive_expect_tx(full0 + 8u * stage, (uint32_t)(CG * n16) * (kTailStepBytesA + step_b));
+                    const uint32_t sa = smem_u32(ring + (size_t)stage * stage_bytes);
+                    const uint32_t sb = sa + p.stage_bytes_a;
+                    for (int j = 0; j < n16; ++j) {
+                        const int slot = (s0 + j) / tail->steps, c = s0 + j - slot * tail->steps;
+                        if constexpr ((parts & kPartA) != 0) {
+                            const int z = mb * tail->max_adapters + slot;
+                            if constexpr (CG == 1) tma_load_3d(sa + j * kTailStepBytesA, &tail->tmap_t, fb, c * 16, 0, z);
+                            else tma_load_3d_pair(sa + j * kTailStepBytesA, &tail->tmap_t, fb, c * 16, (int)rank * 128, z);
+                        }
+                        if constexpr ((parts & kPartB0) != 0) {
+                            const int id = __ldcg(tail->ids + (size_t)mb * tail->max_adapters + slot);
+                            const int x = (c % tail->b_steps) * 16;
+                            if constexpr (CG == 1) tma_load_3d(sb + j * step_b, &tail->tmap_b, fb, x, b_row, id);
+                            else tma_load_3d_pair(sb + j * step_b, &tail->tmap_b, fb, x, b_row, id);
+                        }
+                    }
+                }
+                __syncwarp();
+                ++issued;
+                if (++stage == S) { stage = 0; phase ^= 1u; }
+            }
+        }
     }
+    // a launch with a tail may end only after the kernel it follows, whatever tiles it had
+    if constexpr (kTail) griddep_wait();
     if (!aborted) {
         // Tail: wait until the MMA released every slot, so that no commit
         // arrives on this CTA's barriers after it exits.

@@ -1,0 +1,544 @@
+"""Operators that stand between the products of an attention block (include/serving.h).
+
+* :class:`LoraPlan`, :func:`lora_matmul`: a shared projection with the low-rank adapter of each token's request.
+* :func:`qk_norm_rope`, :func:`qk_norm_rope_backward`: RMS norm of query and key heads with their rotary positions in one
+  pass, optionally into a paged key-value cache; :func:`rope_table` makes the cosines and sines.
+* :class:`PagedAttentionPlan`: attention of one new token per sequence over that cache.
+
+As in the rest of the package this is argument marshalling: shapes, types, strides and devices are checked here, the
+work is enqueued by the CUDA library on torch's current stream (or the one given), and errors raise GemmError (from the
+library) or ValueError / TypeError (from these checks).
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+import os
+import re
+
+from . import (GEMM_BF16, GEMM_E4M3, GEMM_F16, GEMM_F32, GEMM_OK, GemmDeviceError, GemmError, GemmPlanInfo, _dtype_code,
+               current_stream_handle, lib)
+
+SERVING_HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "serving.h")
+_I32, _I64, _F32, _PTR = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
+
+
+class LoraDesc(ctypes.Structure):
+    _fields_ = [("tokens", _I64), ("n", _I64), ("k", _I64), ("rank", _I32), ("adapters", _I32), ("dtype", _I32),
+                ("dtype_y", _I32), ("ldx", _I64), ("ldw", _I64), ("ldy", _I64), ("flags", ctypes.c_uint32), ("tile_n", _I32), ("stages", _I32),
+                ("max_ctas", _I32), ("wait_timeout_ns", ctypes.c_uint64)]
+
+
+class LoraArgs(ctypes.Structure):
+    _fields_ = [("x", _PTR), ("w", _PTR), ("a", _PTR), ("lda", _I64), ("stride_a", _I64), ("b", _PTR), ("ldb", _I64),
+                ("stride_b", _I64), ("adapter", _PTR), ("scale", _PTR), ("y", _PTR)]
+
+
+class LoraPlanInfo(ctypes.Structure):
+    _fields_ = [("product", GemmPlanInfo), ("steps_per_adapter", _I32), ("max_adapters_per_tile", _I32),
+                ("shrink_k_split", _I32), ("shrink_grid", _I32), ("workspace_bytes", _I64)]
+
+
+class QkNormRopeArgs(ctypes.Structure):
+    _fields_ = [("tokens", _I32), ("heads", _I32), ("kv_heads", _I32), ("head_dim", _I32), ("rot_dim", _I32),
+                ("interleaved", _I32), ("norm", _I32), ("dtype", _I32), ("eps", _F32), ("table_rows", _I32),
+                ("table", _PTR), ("positions", _PTR), ("q_weight", _PTR), ("k_weight", _PTR), ("q", _PTR), ("k", _PTR),
+                ("q_token", _I64), ("q_head", _I64), ("k_token", _I64), ("k_head", _I64),
+                ("q_out", _PTR), ("k_out", _PTR),
+                ("q_out_token", _I64), ("q_out_head", _I64), ("k_out_token", _I64), ("k_out_head", _I64),
+                ("v", _PTR), ("v_token", _I64), ("v_head", _I64), ("k_cache", _PTR), ("v_cache", _PTR),
+                ("k_page", _I64), ("k_place", _I64), ("k_chead", _I64), ("v_page", _I64), ("v_place", _I64), ("v_chead", _I64),
+                ("slots", _PTR), ("num_pages", _I64), ("page_size", _I32), ("dtype_cache", _I32),
+                ("k_scale", _F32), ("v_scale", _F32)]
+
+
+class QkNormRopeGrads(ctypes.Structure):
+    _fields_ = [("dq_out", _PTR), ("dk_out", _PTR),
+                ("dq_out_token", _I64), ("dq_out_head", _I64), ("dk_out_token", _I64), ("dk_out_head", _I64),
+                ("dq", _PTR), ("dk", _PTR), ("dq_token", _I64), ("dq_head", _I64), ("dk_token", _I64), ("dk_head", _I64),
+                ("dq_weight", _PTR), ("dk_weight", _PTR), ("workspace", _PTR), ("workspace_bytes", _I64)]
+
+
+class PagedAttnDesc(ctypes.Structure):
+    _fields_ = [("max_batch", _I32), ("heads", _I32), ("kv_heads", _I32), ("head_dim", _I32), ("page_size", _I32),
+                ("dtype", _I32), ("dtype_cache", _I32), ("window", _I32), ("max_ctas", _I32)]
+
+
+class PagedAttnPlanInfo(ctypes.Structure):
+    _fields_ = [("grid", _I32), ("tile_tokens", _I32), ("head_groups", _I32), ("smem_bytes", _I32),
+                ("workspace_bytes", _I64)]
+
+
+class PagedAttnArgs(ctypes.Structure):
+    _fields_ = [("batch", _I32), ("table_width", _I32), ("q", _PTR), ("q_batch", _I64), ("q_head", _I64),
+                ("k_cache", _PTR), ("v_cache", _PTR), ("k_page", _I64), ("k_place", _I64), ("k_head", _I64),
+                ("v_page", _I64), ("v_place", _I64), ("v_head", _I64), ("num_pages", _I64),
+                ("block_table", _PTR), ("table_stride", _I64), ("lengths", _PTR),
+                ("out", _PTR), ("out_batch", _I64), ("out_head", _I64), ("lse", _PTR),
+                ("scale", _F32), ("k_scale", _F32), ("v_scale", _F32)]
+
+
+def serving_header_functions():
+    """Names of the functions include/serving.h declares."""
+    text = open(SERVING_HEADER).read()
+    return sorted(set(re.findall(r"^(?:gemm_status_t|int64_t)\s+(\w+)\s*\(", text, re.M)))
+
+
+_declared = None
+
+
+def _lib():
+    """The library with the serving functions' signatures declared."""
+    global _declared
+    if _declared is None:
+        L = lib()
+        ref = ctypes.POINTER
+        for name, args in (("lora_plan_create", [ref(_PTR), ref(LoraDesc)]), ("lora_plan_info", [_PTR, ref(LoraPlanInfo)]),
+                           ("lora_run", [_PTR, ref(LoraArgs), _PTR]), ("lora_sync_status", [_PTR, _PTR, ref(GemmDeviceError)]),
+                           ("lora_plan_destroy", [_PTR]), ("qk_norm_rope_run", [ref(QkNormRopeArgs), _PTR]),
+                           ("qk_norm_rope_backward", [ref(QkNormRopeArgs), ref(QkNormRopeGrads), _PTR]),
+                           ("paged_attn_plan_create", [ref(_PTR), ref(PagedAttnDesc)]),
+                           ("paged_attn_plan_info", [_PTR, ref(PagedAttnPlanInfo)]),
+                           ("paged_attn_run", [_PTR, ref(PagedAttnArgs), _PTR]), ("paged_attn_plan_destroy", [_PTR])):
+            f = getattr(L, name)
+            f.argtypes, f.restype = args, ctypes.c_int
+        L.qk_norm_rope_backward_workspace.argtypes, L.qk_norm_rope_backward_workspace.restype = [], _I64
+        _declared = L
+    return _declared
+
+
+def _check(status, where):
+    if status != GEMM_OK:
+        raise GemmError(status, where)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _facts(t):
+    """What a call's checks depend on: everything about a tensor but its address and contents."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+def _need(cond, text):
+    if not cond:
+        raise ValueError(text)
+
+
+def _rows_ok(t, name):
+    _need(t.shape[-1] <= 1 or t.stride(-1) == 1, "%s: the last dimension must be contiguous" % name)
+
+
+class _Plan:
+    """A created plan (owns the C handle); use as a context manager or call close()."""
+
+    _destroy = None
+    handle = None
+
+    def close(self):
+        if self.handle is not None:
+            getattr(_lib(), self._destroy)(self.handle)
+            self.handle = None
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ---------------------------------------------------------------- low-rank adapters beside a projection
+
+def _torch_types():
+    import torch
+    return {GEMM_BF16: torch.bfloat16, GEMM_F16: torch.float16, GEMM_F32: torch.float32, GEMM_E4M3: torch.float8_e4m3fn}
+
+
+class LoraPlan(_Plan):
+    """Y = X W^T + scale_i (X A_i^T) B_i^T with i = adapter[token]; a negative i: the projection alone.
+
+    X [tokens, k], W [n, k], A [adapters, rank, k], B [adapters, n, rank], Y [tokens, n]; X, W, A and B of one 16-bit
+    type.  Rows may be padded (ldx, ldw, ldy in elements, 0 = packed; A's and B's strides are taken from the tensors).
+    """
+
+    _destroy = "lora_plan_destroy"
+
+    def __init__(self, tokens, n, k, *, rank, adapters, dtype=GEMM_BF16, dtype_y=None, ldx=0, ldw=0, ldy=0, flags=0,
+                 tile_n=0, stages=0, max_ctas=0, wait_timeout_ns=0):
+        d = LoraDesc()
+        d.tokens, d.n, d.k, d.rank, d.adapters = tokens, n, k, rank, adapters
+        d.dtype, d.dtype_y = dtype, dtype if dtype_y is None else dtype_y
+        d.ldx, d.ldw, d.ldy = ldx, ldw, ldy
+        d.flags, d.tile_n, d.stages, d.max_ctas, d.wait_timeout_ns = flags, tile_n, stages, max_ctas, wait_timeout_ns
+        h = _PTR()
+        _check(_lib().lora_plan_create(ctypes.byref(h), ctypes.byref(d)), "lora_plan_create")
+        self.handle, self.desc = h, d
+        self.info = LoraPlanInfo()
+        _check(_lib().lora_plan_info(h, ctypes.byref(self.info)), "lora_plan_info")
+        self._args = {}
+
+    def _checked(self, x, w, a, b, adapter, y, scale):
+        import torch
+        d = self.desc
+        types = _torch_types()
+        for name, t, shape, kind in (("x", x, (d.tokens, d.k), types[d.dtype]), ("w", w, (d.n, d.k), types[d.dtype]),
+                                     ("a", a, (d.adapters, d.rank, d.k), types[d.dtype]),
+                                     ("b", b, (d.adapters, d.n, d.rank), types[d.dtype]),
+                                     ("adapter", adapter, (d.tokens,), torch.int32), ("y", y, (d.tokens, d.n), types[d.dtype_y]),
+                                     ("scale", scale, (d.adapters,), torch.float32)):
+            if t is None:
+                continue
+            if t.dtype != kind:
+                raise TypeError("%s: %s expected, got %s" % (name, kind, t.dtype))
+            _need(tuple(t.shape) == shape, "%s: shape %s expected, got %s" % (name, shape, tuple(t.shape)))
+            _need(t.is_cuda and t.get_device() == x.get_device(), "%s: must be on x's CUDA device" % name)
+            _rows_ok(t, name)
+        for name, t, ld, cols in (("x", x, d.ldx, d.k), ("w", w, d.ldw, d.k), ("y", y, d.ldy, d.n)):
+            _need(t.shape[0] <= 1 or t.stride(0) == (ld or cols), "%s: rows %d apart, the plan has %d" % (name, t.stride(0), ld or cols))
+        g = LoraArgs()
+        g.lda, g.stride_a, g.ldb, g.stride_b = a.stride(1), a.stride(0), b.stride(1), b.stride(0)
+        return g
+
+    def run(self, x, w, a, b, adapter, y, scale=None, stream=None):
+        """Enqueue on `stream` (default: torch's current stream)."""
+        key = (_facts(x), _facts(w), _facts(a), _facts(b), _facts(adapter), _facts(y), _facts(scale))
+        checked = self._args.get(key)
+        if checked is None:
+            checked = self._args[key] = self._checked(x, w, a, b, adapter, y, scale)
+        g = LoraArgs.from_buffer_copy(checked)
+        g.x, g.w, g.a, g.b, g.adapter, g.y = (x.data_ptr(), w.data_ptr(), a.data_ptr(), b.data_ptr(), adapter.data_ptr(),
+                                              y.data_ptr())
+        if scale is not None:
+            g.scale = scale.data_ptr()
+        _check(_lib().lora_run(self.handle, ctypes.byref(g), current_stream_handle() if stream is None else stream), "lora_run")
+        return y
+
+    def sync_status(self, stream=None):
+        """(status, GemmDeviceError): synchronises the stream and reads the device error record."""
+        rec = GemmDeviceError()
+        s = _lib().lora_sync_status(self.handle, current_stream_handle() if stream is None else stream, ctypes.byref(rec))
+        return s, rec
+
+
+_lora_plans = {}
+
+
+def lora_matmul(x, w, a, b, adapter, *, scale=None, out=None, out_dtype=None):
+    """Y = X W^T + scale_i (X A_i^T) B_i^T (see LoraPlan); plans are kept per shape, layout, device and stream."""
+    import torch
+    _need(x.dim() == 2 and w.dim() == 2 and a.dim() == 3 and b.dim() == 3, "x [M, K], w [N, K], a [L, R, K], b [L, N, R] expected")
+    _rows_ok(x, "x")
+    _rows_ok(w, "w")
+    if out is None:
+        out = torch.empty(x.shape[0], w.shape[0], dtype=out_dtype or x.dtype, device=x.device)
+    stream = current_stream_handle()
+    ld = lambda t: max(t.stride(0), t.shape[1])  # noqa: E731  (a single row's stride says nothing)
+    key = (x.get_device(), stream, x.shape, w.shape, a.shape, x.dtype, out.dtype, ld(x), ld(w), ld(out))
+    plan = _lora_plans.get(key)
+    if plan is None:
+        plan = _lora_plans[key] = LoraPlan(x.shape[0], w.shape[0], x.shape[1], rank=a.shape[1], adapters=a.shape[0],
+                                           dtype=_dtype_code(x.dtype), dtype_y=_dtype_code(out.dtype), ldx=ld(x),
+                                           ldw=ld(w), ldy=ld(out))
+    return plan.run(x, w, a, b, adapter, out, scale=scale, stream=stream)
+
+
+# ---------------------------------------------------------------- head norms and rotary positions
+
+def rope_table(positions, rot_dim, *, base=10000.0, factor=1.0, scaling="linear", original_positions=None, beta_fast=32.0,
+               beta_slow=1.0, attention_factor=None, device="cuda"):
+    """cos and sin of every position below `positions`: [positions, 2, rot_dim / 2] fp32, computed in fp64.
+
+    Pair i turns by position * f_i, f_i = base^(-2i / rot_dim).  `factor` > 1 stretches the table to longer contexts:
+      "linear"  positions are divided by the factor;
+      "base"    the base becomes base * factor^(rot_dim / (rot_dim - 2)): the fastest pair keeps its frequency, the
+                slowest is divided by the factor;
+      "blend"   pairs that turn at least beta_fast times within original_positions keep f_i, those that turn at most
+                beta_slow times get f_i / factor, and those between are blended linearly over the pair index; cos and
+                sin are multiplied by attention_factor (default 0.1 ln(factor) + 1), which scales q . k by its square.
+    """
+    import torch
+    _need(rot_dim > 0 and rot_dim % 2 == 0 and positions > 0, "rot_dim must be even and positive, positions positive")
+    _need(scaling in ("linear", "base", "blend"), "scaling: 'linear', 'base' or 'blend'")
+    _need(factor >= 1.0, "factor must be at least 1")
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64)
+    if scaling == "base" and factor != 1.0:
+        _need(rot_dim > 2, "scaling 'base' needs rot_dim above 2")
+        base = base * factor ** (rot_dim / (rot_dim - 2.0))
+    freq = base ** (-i / rot_dim)
+    gain = 1.0
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "blend" and factor != 1.0:
+        _need(original_positions is not None and original_positions > 0, "scaling 'blend' needs original_positions")
+        # the pair index at which a pair turns `turns` times within original_positions
+        at = lambda turns: rot_dim * math.log(original_positions / (2 * math.pi * turns)) / (2 * math.log(base))  # noqa: E731
+        low, high = max(math.floor(at(beta_fast)), 0), min(math.ceil(at(beta_slow)), rot_dim - 1)
+        keep = 1.0 - ((i / 2 - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
+        freq = freq * keep + freq / factor * (1.0 - keep)
+        gain = 0.1 * math.log(factor) + 1.0 if attention_factor is None else attention_factor
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * freq.to(device)
+    return torch.stack((angle.cos() * gain, angle.sin() * gain), 1).float().contiguous()
+
+
+def _check_rows(name, t, tokens, dim, kind, device):
+    if t is None:
+        return
+    if t.dtype != kind:
+        raise TypeError("%s: %s expected, got %s" % (name, kind, t.dtype))
+    _need(t.dim() == 3 and t.shape[0] == tokens and t.shape[2] == dim, "%s: [tokens, heads, head_dim] expected, got %s" % (name, tuple(t.shape)))
+    _need(t.get_device() == device, "%s: must be on q's CUDA device" % name)
+    _rows_ok(t, name)
+
+
+def _rope_args(q, k, positions, table, q_weight, k_weight, eps, interleaved, norm):
+    """The fields forward and backward share, checked; everything but addresses."""
+    import torch
+    _need(q.dim() == 3 and q.is_cuda, "q: [tokens, heads, head_dim] on a CUDA device expected")
+    tokens, heads, dim = q.shape
+    dev = q.get_device()
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("q: bfloat16 or float16 expected, got %s" % q.dtype)
+    _check_rows("q", q, tokens, dim, q.dtype, dev)
+    _check_rows("k", k, tokens, dim, q.dtype, dev)
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if t is not None:
+            _need(norm, "%s: given without norm" % name)
+            if t.dtype != q.dtype:
+                raise TypeError("%s: %s expected, got %s" % (name, q.dtype, t.dtype))
+            _need(tuple(t.shape) == (dim,) and t.is_contiguous() and t.get_device() == dev, "%s: [head_dim], contiguous, on q's device" % name)
+    if positions.dtype != torch.int32:
+        raise TypeError("positions: int32 expected, got %s" % positions.dtype)
+    _need(tuple(positions.shape) == (tokens,) and positions.is_contiguous() and positions.get_device() == dev, "positions: [tokens], contiguous, on q's device")
+    if table.dtype != torch.float32:
+        raise TypeError("table: float32 expected, got %s" % table.dtype)
+    _need(table.dim() == 3 and table.shape[1] == 2 and table.is_contiguous() and table.get_device() == dev, "table: [positions, 2, rot_dim / 2], contiguous, on q's device")
+    g = QkNormRopeArgs()
+    g.tokens, g.heads, g.kv_heads, g.head_dim, g.rot_dim = tokens, heads, 0 if k is None else k.shape[1], dim, 2 * table.shape[2]
+    g.interleaved, g.norm, g.dtype, g.eps, g.table_rows = int(interleaved), int(norm), _dtype_code(q.dtype), eps, table.shape[0]
+    g.q_token, g.q_head = q.stride(0), q.stride(1)
+    if k is not None:
+        g.k_token, g.k_head = k.stride(0), k.stride(1)
+    return g
+
+
+def _check_cache(name, cache, kv_heads, dim, like, device):
+    import torch
+    if cache.dtype not in (like, torch.float8_e4m3fn):
+        raise TypeError("%s: %s or float8_e4m3fn expected, got %s" % (name, like, cache.dtype))
+    _need(cache.dim() == 4 and cache.shape[2] == kv_heads and cache.shape[3] == dim,
+          "%s: [pages, page_size, kv_heads, head_dim] expected, got %s" % (name, tuple(cache.shape)))
+    _need(cache.get_device() == device, "%s: must be on q's CUDA device" % name)
+    _rows_ok(cache, name)
+
+
+def _checked_rope(q, k, positions, table, q_weight, k_weight, eps, interleaved, norm, q_out, k_out, v, k_cache, v_cache, slots):
+    import torch
+    g = _rope_args(q, k, positions, table, q_weight, k_weight, eps, interleaved, norm)
+    dev = q.get_device()
+    _check_rows("q_out", q_out, g.tokens, g.head_dim, q.dtype, dev)
+    _need(q_out.shape == q.shape, "q_out: q's shape expected")
+    g.q_out_token, g.q_out_head = q_out.stride(0), q_out.stride(1)
+    if k_out is not None:
+        _need(k is not None and k_out.shape == k.shape, "k_out: k's shape expected")
+        _check_rows("k_out", k_out, g.tokens, g.head_dim, q.dtype, dev)
+        g.k_out_token, g.k_out_head = k_out.stride(0), k_out.stride(1)
+    if k_cache is not None:
+        _need(k is not None and v is not None and v_cache is not None and slots is not None, "a cache append needs k, v, k_cache, v_cache and slots")
+        _check_rows("v", v, g.tokens, g.head_dim, q.dtype, dev)
+        _need(v.shape == k.shape, "v: k's shape expected")
+        _check_cache("k_cache", k_cache, g.kv_heads, g.head_dim, q.dtype, dev)
+        _check_cache("v_cache", v_cache, g.kv_heads, g.head_dim, q.dtype, dev)
+        _need(v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype, "v_cache: k_cache's shape and type expected")
+        if slots.dtype != torch.int32:
+            raise TypeError("slots: int32 expected, got %s" % slots.dtype)
+        _need(tuple(slots.shape) == (g.tokens,) and slots.is_contiguous() and slots.get_device() == dev, "slots: [tokens], contiguous, on q's device")
+        g.v_token, g.v_head = v.stride(0), v.stride(1)
+        g.k_page, g.k_place, g.k_chead = k_cache.stride()[:3]
+        g.v_page, g.v_place, g.v_chead = v_cache.stride()[:3]
+        g.num_pages, g.page_size, g.dtype_cache = k_cache.shape[0], k_cache.shape[1], _dtype_code(k_cache.dtype)
+    else:
+        _need(v is None and v_cache is None and slots is None, "v, v_cache and slots go with k_cache")
+        _need(k is None or k_out is not None, "k needs k_out or a cache")
+    return g
+
+
+_rope_checked = {}
+_rope_backward_checked = {}
+
+
+def qk_norm_rope(q, k, positions, table, *, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, norm=True, q_out=None,
+                 k_out=None, v=None, k_cache=None, v_cache=None, slots=None, k_scale=1.0, v_scale=1.0, stream=None):
+    """RMS norm of every head row of q [tokens, heads, head_dim] and k [tokens, kv_heads, head_dim] (or None), then its
+    rotary position, in one pass; returns (q_out, k_out).
+
+    table: from rope_table, its width sets how much of the head is rotated; positions: int32 [tokens].  interleaved:
+    pairs of neighbours instead of halves.  norm=False leaves the rows as they are before the rotation; a weight of None
+    counts as ones.  q_out and k_out default to new tensors (k_out only without a cache) and may be q and k themselves.
+    With k_cache, v_cache [pages, page_size, kv_heads, head_dim] the keys and v's values also go to slots [tokens] (int32:
+    page * page_size + place, negative: nowhere); a float8_e4m3fn cache holds them divided by k_scale / v_scale.
+    """
+    import torch
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None and k_cache is None and k is not None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    key = (_facts(q), _facts(k), _facts(positions), _facts(table), _facts(q_weight), _facts(k_weight), eps, interleaved, norm,
+           _facts(q_out), _facts(k_out), _facts(v), _facts(k_cache), _facts(v_cache), _facts(slots))
+    checked = _rope_checked.get(key)
+    if checked is None:
+        checked = _rope_checked[key] = _checked_rope(q, k, positions, table, q_weight, k_weight, eps, interleaved, norm, q_out,
+                                                     k_out, v, k_cache, v_cache, slots)
+    g = QkNormRopeArgs.from_buffer_copy(checked)
+    g.table, g.positions, g.q, g.q_out = table.data_ptr(), positions.data_ptr(), q.data_ptr(), q_out.data_ptr()
+    if k is not None:
+        g.k, g.k_out = k.data_ptr(), _ptr(k_out)
+    if norm:
+        g.q_weight, g.k_weight = _ptr(q_weight), _ptr(k_weight)
+    if k_cache is not None:
+        g.v, g.k_cache, g.v_cache, g.slots = v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr()
+        g.k_scale, g.v_scale = k_scale, v_scale
+    _check(_lib().qk_norm_rope_run(ctypes.byref(g), current_stream_handle() if stream is None else stream), "qk_norm_rope")
+    return q_out, k_out
+
+
+def _checked_rope_backward(dq_out, dk_out, q, k, positions, table, q_weight, k_weight, eps, interleaved, norm, dq, dk):
+    g = _rope_args(q, k, positions, table, q_weight, k_weight, eps, interleaved, norm)
+    d = QkNormRopeGrads()
+    _need((dk_out is None) == (k is None), "dk goes with k")
+    for name, t, like in (("dq", dq_out, q), ("dk", dk_out, k), ("dq_out", dq, q), ("dk_out", dk, k)):
+        if like is not None:
+            _check_rows(name, t, g.tokens, g.head_dim, q.dtype, q.get_device())
+            _need(t.shape == like.shape, "%s: the forward input's shape expected" % name)
+    d.dq_out_token, d.dq_out_head, d.dq_token, d.dq_head = dq_out.stride(0), dq_out.stride(1), dq.stride(0), dq.stride(1)
+    if k is not None:
+        d.dk_out_token, d.dk_out_head, d.dk_token, d.dk_head = dk_out.stride(0), dk_out.stride(1), dk.stride(0), dk.stride(1)
+    return g, d
+
+
+def qk_norm_rope_backward(dq, dk, q, k, positions, table, *, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, norm=True,
+                          dq_out=None, dk_out=None, stream=None):
+    """Gradients of qk_norm_rope: (of q, of k, of q_weight, of k_weight), the last two fp32 or None without a weight.
+
+    dq, dk: the gradients of the forward's outputs; q, k: the forward's inputs.  dq_out, dk_out: where the gradients of q
+    and k go (default: new tensors; may be dq and dk themselves).
+    """
+    import torch
+    if dq_out is None:
+        dq_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if dk_out is None and k is not None:
+        dk_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    key = (_facts(dq), _facts(dk), _facts(q), _facts(k), _facts(positions), _facts(table), _facts(q_weight), _facts(k_weight), eps,
+           interleaved, norm, _facts(dq_out), _facts(dk_out))
+    checked = _rope_backward_checked.get(key)
+    if checked is None:
+        checked = _rope_backward_checked[key] = _checked_rope_backward(dq, dk, q, k, positions, table, q_weight, k_weight, eps,
+                                                                       interleaved, norm, dq_out, dk_out)
+    g, d = QkNormRopeArgs.from_buffer_copy(checked[0]), QkNormRopeGrads.from_buffer_copy(checked[1])
+    g.table, g.positions, g.q = table.data_ptr(), positions.data_ptr(), q.data_ptr()
+    d.dq_out, d.dq = dq.data_ptr(), dq_out.data_ptr()
+    if k is not None:
+        g.k, d.dk_out, d.dk = k.data_ptr(), dk.data_ptr(), dk_out.data_ptr()
+    dqw = dkw = None
+    if norm and (q_weight is not None or k_weight is not None):
+        # one buffer: the two weight gradients, then the library's workspace
+        L = _lib()
+        need = L.qk_norm_rope_backward_workspace()
+        n = q.shape[2]
+        buf = torch.empty(2 * n + need // 4, dtype=torch.float32, device=q.device)
+        if q_weight is not None:
+            g.q_weight = q_weight.data_ptr()
+            dqw = buf[:n]
+            d.dq_weight = dqw.data_ptr()
+        if k_weight is not None and k is not None:
+            g.k_weight = k_weight.data_ptr()
+            dkw = buf[n:2 * n]
+            d.dk_weight = dkw.data_ptr()
+        d.workspace, d.workspace_bytes = buf.data_ptr() + 8 * n, need
+    _check(_lib().qk_norm_rope_backward(ctypes.byref(g), ctypes.byref(d), current_stream_handle() if stream is None else stream),
+           "qk_norm_rope_backward")
+    return dq_out, dk_out, dqw, dkw
+
+
+# ---------------------------------------------------------------- attention of one token over a paged cache
+
+class PagedAttentionPlan(_Plan):
+    """softmax(scale q K^T) V of one new token per sequence over a paged cache.
+
+    Holds the workspace of up to `max_batch` sequences; query head h reads kv head h // (heads // kv_heads).  window > 0:
+    each token sees the last `window` positions only.  dtype_cache: dtype, or GEMM_E4M3 (values times k_scale / v_scale).
+    """
+
+    _destroy = "paged_attn_plan_destroy"
+
+    def __init__(self, max_batch, *, heads, kv_heads, head_dim, page_size, dtype=GEMM_BF16, dtype_cache=None, window=0, max_ctas=0):
+        d = PagedAttnDesc()
+        d.max_batch, d.heads, d.kv_heads, d.head_dim, d.page_size = max_batch, heads, kv_heads, head_dim, page_size
+        d.dtype, d.dtype_cache, d.window, d.max_ctas = dtype, dtype if dtype_cache is None else dtype_cache, window, max_ctas
+        h = _PTR()
+        _check(_lib().paged_attn_plan_create(ctypes.byref(h), ctypes.byref(d)), "paged_attn_plan_create")
+        self.handle, self.desc = h, d
+        self.info = PagedAttnPlanInfo()
+        _check(_lib().paged_attn_plan_info(h, ctypes.byref(self.info)), "paged_attn_plan_info")
+        self._args = {}
+
+    def _checked(self, q, k_cache, v_cache, block_table, lengths, out, lse):
+        import torch
+        d = self.desc
+        types = _torch_types()
+        _need(q.dim() == 3 and q.is_cuda, "q: [batch, heads, head_dim] on a CUDA device expected")
+        batch, dev = q.shape[0], q.get_device()
+        _need(batch <= d.max_batch, "q: %d sequences, the plan holds %d" % (batch, d.max_batch))
+        for name, t in (("q", q), ("out", out)):
+            if t.dtype != types[d.dtype]:
+                raise TypeError("%s: %s expected, got %s" % (name, types[d.dtype], t.dtype))
+            _need(tuple(t.shape) == (batch, d.heads, d.head_dim) and t.get_device() == dev, "%s: [batch, heads, head_dim] of the plan, on q's device" % name)
+            _rows_ok(t, name)
+        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+            if t.dtype != types[d.dtype_cache]:
+                raise TypeError("%s: %s expected, got %s" % (name, types[d.dtype_cache], t.dtype))
+            _check_cache(name, t, d.kv_heads, d.head_dim, types[d.dtype], dev)
+            _need(t.shape[1] == d.page_size and t.shape[0] == k_cache.shape[0], "%s: the plan's page size, as many pages as k_cache" % name)
+        for name, t, dims in (("block_table", block_table, 2), ("lengths", lengths, 1)):
+            if t.dtype != torch.int32:
+                raise TypeError("%s: int32 expected, got %s" % (name, t.dtype))
+            _need(t.dim() == dims and t.shape[0] == batch and t.get_device() == dev, "%s: one row per sequence, on q's device" % name)
+            _rows_ok(t, name)
+        if lse is not None:
+            if lse.dtype != torch.float32:
+                raise TypeError("lse: float32 expected, got %s" % lse.dtype)
+            _need(tuple(lse.shape) == (batch, d.heads) and lse.is_contiguous() and lse.get_device() == dev, "lse: [batch, heads], contiguous, on q's device")
+        g = PagedAttnArgs()
+        g.batch, g.table_width, g.table_stride = batch, block_table.shape[1], block_table.stride(0)
+        g.q_batch, g.q_head, g.out_batch, g.out_head = q.stride(0), q.stride(1), out.stride(0), out.stride(1)
+        g.k_page, g.k_place, g.k_head = k_cache.stride()[:3]
+        g.v_page, g.v_place, g.v_head = v_cache.stride()[:3]
+        g.num_pages = k_cache.shape[0]
+        return g
+
+    def run(self, q, k_cache, v_cache, block_table, lengths, out, *, lse=None, scale=None, k_scale=1.0, v_scale=1.0, stream=None):
+        """Enqueue on `stream` (default: torch's current stream); returns out.
+
+        q, out [batch, heads, head_dim]; k_cache, v_cache [pages, page_size, kv_heads, head_dim], any strides with a
+        contiguous last dimension; block_table int32 [batch, width]: the pages of each sequence in order; lengths int32
+        [batch]; lse: fp32 [batch, heads] for the logarithm of the softmax sums; scale: default head_dim^-0.5.
+        """
+        key = (_facts(q), _facts(k_cache), _facts(v_cache), _facts(block_table), _facts(lengths), _facts(out), _facts(lse))
+        checked = self._args.get(key)
+        if checked is None:
+            checked = self._args[key] = self._checked(q, k_cache, v_cache, block_table, lengths, out, lse)
+        g = PagedAttnArgs.from_buffer_copy(checked)
+        g.q, g.k_cache, g.v_cache, g.block_table = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr()
+        g.lengths, g.out = lengths.data_ptr(), out.data_ptr()
+        if lse is not None:
+            g.lse = lse.data_ptr()
+        g.scale = self.desc.head_dim ** -0.5 if scale is None else scale
+        g.k_scale, g.v_scale = k_scale, v_scale
+        _check(_lib().paged_attn_run(self.handle, ctypes.byref(g), current_stream_handle() if stream is None else stream), "paged_attn_run")
+        return out
