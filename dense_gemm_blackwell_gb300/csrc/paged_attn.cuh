@@ -10,21 +10,23 @@
 // as the 16 rows of the tile.
 //
 // Work.  A segment is one (sequence, kv head, group of up to 16 query heads);
-// its positions are cut into tiles of 64.  All segments' tiles, laid end to
-// end, are cut into equal contiguous ranges, one per CTA of a grid that fills
-// the device once, so ragged lengths balance without any host knowledge of
-// them and a long cache is split as often as the device needs.  A CTA that
-// holds a whole segment writes its output; otherwise it leaves (m, l, O) in
-// the workspace, and the last of the segment's CTAs to arrive (a counter, no
-// waiting) joins them in the order of the positions, so results do not depend
-// on timing.
+// its positions are cut into tiles of four warps' steps.  All segments' tiles,
+// laid end to end with kAttnSegmentCost empty units before each segment (what
+// starting and ending one costs), are cut into equal contiguous ranges, one
+// per CTA of a grid that fills the device once, so ragged lengths balance
+// without any host knowledge of them and a long cache is split as often as the
+// device needs.  A CTA that holds a whole segment writes its output; otherwise
+// it leaves (m, l, O) in the workspace, and the last of the segment's CTAs to
+// arrive (a counter, no waiting) joins them in the order of the positions, so
+// results do not depend on timing.
 //
-// Inside a CTA each of four warps takes 16 positions of every tile on its own:
-// its own copy pipeline (kStages deep, no block barrier), its own running
-// maximum and sum, joined with the other warps' at the segment's end.  The
-// copies run ahead across segment ends.  Rows of K and V lie in shared memory
-// at an odd number of 16-byte chunks apart, so the eight rows of a matrix load
-// fall into different banks.
+// Inside a CTA each of four warps takes its own positions of every tile (16,
+// or 32 where rows are short): its own copy pipeline (kAttnStages deep, no
+// block barrier), its own running maximum and sum, joined with the other
+// warps' at the segment's end in the pipeline slots just consumed.  The copies
+// run ahead across segment ends.  Rows of K and V lie in shared memory at an
+// odd number of 16-byte chunks apart, so the eight rows of a matrix load fall
+// into different banks.
 #pragma once
 
 #include <cfloat>
@@ -40,24 +42,34 @@
 
 namespace dgb {
 
+__host__ __device__ constexpr int next_pow2(int v) { return v <= 1 ? 1 : 2 * next_pow2((v + 1) / 2); }
+
 template <int KD, bool FP8>
 struct AttnShape {
     static constexpr int kDim = KD * 16;                 // head elements held (head_dim rounded up)
-    static constexpr int kChunks = FP8 ? KD : 2 * KD;    // 16-byte chunks of a row
+    static constexpr int kBytes = FP8 ? 1 : 2;
+    static constexpr int kChunks = KD * kBytes;          // 16-byte chunks of a row
+    static constexpr int kTokens = kChunks <= 8 || FP8 ? 32 : 16;   // positions of one warp's step
+    static constexpr int kTile = kAttnWarps * kTokens;
     static constexpr int kPitch = (kChunks | 1) * 16;    // bytes between rows
-    static constexpr int kRowsBytes = kAttnWarpTokens * kPitch;
-    static constexpr int kStageBytes = 2 * kRowsBytes;   // one warp's keys and values of one step
-    static constexpr int kMergePitch = kDim + 4;         // floats
-    static constexpr int kRingBytes = kAttnWarps * kAttnStages * kStageBytes;
-    static constexpr int kAddrBytes = kAttnWarps * kAttnWarpTokens * 16;
+    static constexpr int kRowsBytes = kTokens * kPitch;
+    static constexpr int kMergePitch = kDim + 4;         // floats; a slot also takes one warp's O at a segment's end
     static constexpr int kMergeBytes = 16 * kMergePitch * 4;
-    static constexpr int kSmemBytes = kRingBytes + kAddrBytes + kMergeBytes;
+    static constexpr int kStageBytes = 2 * kRowsBytes > kMergeBytes ? 2 * kRowsBytes : kMergeBytes;
+    static constexpr int kRingBytes = kAttnWarps * kAttnStages * kStageBytes;
+    static constexpr int kAddrBytes = kAttnWarps * kTokens * 16;
+    static constexpr int kSmemBytes = kRingBytes + kAddrBytes;
     static constexpr int kSlotFloats = 16 * kDim + 32;   // one partial: O, m, l
+    // copies: a power of two of lanes per row
+    static constexpr int kLanesPerRow = next_pow2(kChunks);
+    static constexpr int kRowsPerCopy = 32 / kLanesPerRow;
+    static constexpr int kCopies = kTokens / kRowsPerCopy;
 };
 
-// Position in the list of all tiles: tile `tile` of `tiles` of segment (b, hv).
+// Position in the list of all tiles: tile `tile` of `tiles` of segment (b, hv), `left` units before the range's end.
 struct TileWalk {
     int b, hv, tile, tiles, first, length;   // positions [first, length)
+    int64_t left;                            // > 0: this tile belongs to the range
 };
 
 __device__ __forceinline__ void sequence_span(const AttnParams& p, int b, int& first, int& length) {
@@ -66,8 +78,9 @@ __device__ __forceinline__ void sequence_span(const AttnParams& p, int b, int& f
     if (length > most) length = (int)most;
     first = p.window > 0 ? max(0, length - p.window) : 0;
 }
+template <int TILE>
 __device__ __forceinline__ int tiles_of(int first, int length) {
-    return (int)(((int64_t)length - first + kAttnTile - 1) / kAttnTile);
+    return (int)(((uint32_t)(length - first) + (TILE - 1)) / TILE);
 }
 
 template <typename T, typename TQ, bool FP8, int KD>
@@ -80,39 +93,50 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
     __shared__ float warp_m[kAttnWarps][16], warp_l[kAttnWarps][16];
     __shared__ uint32_t stage_mask[kAttnWarps][kAttnStages];
     __shared__ int join_now;
-
-    griddep_wait();
-    griddep_launch_dependents();
+    constexpr int kTokens = S::kTokens;
+    constexpr uint32_t kFull = kTokens == 32 ? 0xFFFFFFFFu : 0xFFFFu;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quad = lane >> 2, j4 = lane & 3;
     const int HV = p.segments_per_sequence;
     const int B = p.a.batch;
     uint8_t* ring = smem + (size_t)warp * kAttnStages * S::kStageBytes;
-    longlong2* addr = reinterpret_cast<longlong2*>(smem + S::kRingBytes) + warp * kAttnWarpTokens;
-    float* merge = reinterpret_cast<float*>(smem + S::kRingBytes + S::kAddrBytes);
+    longlong2* addr = reinterpret_cast<longlong2*>(smem + S::kRingBytes) + warp * kTokens;
+    const int row_chunks = p.head_dim * S::kBytes / 16;
+    if (row_chunks < S::kChunks) {
+        // chunks past head_dim are never copied: zeros, for the products that run over them
+        for (int i = threadIdx.x; i < S::kRingBytes / 16; i += kAttnThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+    }
+    griddep_wait();
+    griddep_launch_dependents();
 
     auto out_row = [&](int b, int head) { return static_cast<TQ*>(p.a.out) + b * p.a.out_batch + head * p.a.out_head; };
+    auto write_empty = [&]() {      // outputs of sequences without a visible position
+        for (int b = blockIdx.x; b < B; b += gridDim.x) {
+            int first, length;
+            sequence_span(p, b, first, length);
+            if (length > first) continue;
+            for (int i = threadIdx.x; i < p.heads * (p.head_dim / 2); i += kAttnThreads) {
+                const int h = i / (p.head_dim / 2);
+                reinterpret_cast<uint32_t*>(out_row(b, h))[i - h * (p.head_dim / 2)] = 0u;
+            }
+            if (p.a.lse)
+                for (int h = threadIdx.x; h < p.heads; h += kAttnThreads) p.a.lse[(int64_t)b * p.heads + h] = -INFINITY;
+        }
+    };
 
     // ---------------------------------------------------------------- this CTA's range of tiles
-    // Sum of all sequences' tiles, and empty sequences' outputs on the way.
-    int64_t mine = 0;
-    for (int b = threadIdx.x; b < B; b += kAttnThreads) {
+    auto units_of = [&](int b) -> int64_t {      // of one sequence
         int first, length;
+        if (b >= B) return 0;
         sequence_span(p, b, first, length);
-        mine += (int64_t)tiles_of(first, length) * HV;
-    }
-    for (int b = blockIdx.x; b < B; b += gridDim.x) {
-        int first, length;
-        sequence_span(p, b, first, length);
-        if (length > first) continue;
-        for (int i = threadIdx.x; i < p.heads * (p.head_dim / 2); i += kAttnThreads) {
-            const int h = i / (p.head_dim / 2);
-            reinterpret_cast<uint32_t*>(out_row(b, h))[i - h * (p.head_dim / 2)] = 0u;
-        }
-        if (p.a.lse)
-            for (int h = threadIdx.x; h < p.heads; h += kAttnThreads) p.a.lse[(int64_t)b * p.heads + h] = -INFINITY;
-    }
+        const int t = tiles_of<S::kTile>(first, length);
+        return t > 0 ? (int64_t)(t + kAttnSegmentCost) * HV : 0;
+    };
+    const int64_t first_units = units_of(threadIdx.x);
+    int64_t mine = first_units;
+    for (int b = threadIdx.x + kAttnThreads; b < B; b += kAttnThreads) mine += units_of(b);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     if (lane == 0) scan_part[warp] = mine;
@@ -120,21 +144,19 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
     int64_t total = 0;
 #pragma unroll
     for (int w = 0; w < kAttnWarps; ++w) total += scan_part[w];
-    if (total == 0) return;
-    // Small problems leave CTAs idle rather than cut segments below kAttnMinTiles tiles a CTA.
-    const int ctas = (int)min((int64_t)gridDim.x, (total + kAttnMinTiles - 1) / kAttnMinTiles);
-    if ((int)blockIdx.x >= ctas) return;
-    const int64_t range0 = total * blockIdx.x / ctas, range1 = total * (blockIdx.x + 1) / ctas;
-    // The sequence that holds tile range0: scan 128 sequences at a time.
+    // Small problems leave CTAs idle rather than cut segments finely.
+    const int ctas = (int)min((int64_t)gridDim.x, (total + kAttnMinUnits - 1) / kAttnMinUnits);
+    if ((int)blockIdx.x >= ctas) {
+        write_empty();
+        return;
+    }
+    auto range_start = [&](int c) { return total * c / ctas; };
+    const int64_t range0 = range_start(blockIdx.x), range1 = range_start(blockIdx.x + 1);
+    // The sequence that holds unit range0: scan 128 sequences at a time.
     int64_t before = 0;
     for (int base = 0; base < B; base += kAttnThreads) {
         const int b = base + threadIdx.x;
-        int64_t v = 0;
-        if (b < B) {
-            int first, length;
-            sequence_span(p, b, first, length);
-            v = (int64_t)tiles_of(first, length) * HV;
-        }
+        const int64_t v = base == 0 ? first_units : units_of(b);
         int64_t incl = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -159,69 +181,103 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
         if (before > range0) break;
     }
     __syncthreads();
-    const int steps = (int)(range1 - range0);
 
     TileWalk at;      // the step being computed
     at.b = found_b;
     sequence_span(p, at.b, at.first, at.length);
-    at.tiles = tiles_of(at.first, at.length);
-    at.hv = (int)(found_rest / at.tiles);
-    at.tile = (int)(found_rest - (int64_t)at.hv * at.tiles);
-    TileWalk ahead = at;   // the step whose addresses are fetched next
+    at.tiles = tiles_of<S::kTile>(at.first, at.length);
+    const int per_segment = at.tiles + kAttnSegmentCost;
+    at.hv = found_rest <= INT_MAX ? (int)found_rest / per_segment : (int)(found_rest / per_segment);
+    at.tile = (int)(found_rest - (int64_t)at.hv * per_segment) - kAttnSegmentCost;
+    at.left = range1 - range0;
+    int64_t unit = range0;           // of the step being computed
+    if (at.tile < 0) {               // the range starts with (part of) a segment's empty units
+        at.left += at.tile;
+        unit -= at.tile;
+        at.tile = 0;
+    }
+    TileWalk ahead = at;             // the step whose addresses are fetched next
     auto advance = [&](TileWalk& w) {
+        --w.left;
         if (++w.tile < w.tiles) return;
+        w.left -= kAttnSegmentCost;
         w.tile = 0;
         if (++w.hv < HV) return;
         w.hv = 0;
         do {
-            if (++w.b >= B) return;      // past the last tile: not used
+            if (++w.b >= B) {        // past the last tile
+                w.left = 0;
+                return;
+            }
             sequence_span(p, w.b, w.first, w.length);
-            w.tiles = tiles_of(w.first, w.length);
+            w.tiles = tiles_of<S::kTile>(w.first, w.length);
         } while (w.tiles == 0);
     };
 
     // ---------------------------------------------------------------- copies
-    // Lane r < 16 fetches the page of its row r of the next step; the number is used one step later.
+    // Lane r fetches the page of its row r of the next step; the number is used one step later.
+    const int copy_row = lane / S::kLanesPerRow, copy_chunk = lane % S::kLanesPerRow;
+    const bool copies = copy_chunk < row_chunks;
+    const uint32_t copy_dst = smem_u32(ring) + copy_row * S::kPitch + copy_chunk * 16;
+    const uint8_t* kbase = static_cast<const uint8_t*>(p.a.k_cache) + copy_chunk * 16;
+    const uint8_t* vbase = static_cast<const uint8_t*>(p.a.v_cache) + copy_chunk * 16;
+    const int64_t k_place = p.a.k_place * S::kBytes, v_place = p.a.v_place * S::kBytes;
     int next_page = -1, next_place = 0, next_head = 0;
+    bool next_live = false;
     auto fetch = [&]() {
-        const int64_t pos = (int64_t)ahead.first + (int64_t)ahead.tile * kAttnTile + warp * kAttnWarpTokens + (lane & 15);
+        next_live = ahead.left > 0;
+        if (!next_live) return;
+        const uint32_t pos = (uint32_t)ahead.first + (uint32_t)ahead.tile * S::kTile + warp * kTokens + (lane & (kTokens - 1));
         next_page = -1;
         next_head = ahead.hv / p.head_groups;
-        if (pos < ahead.length) {
-            const int col = p.page_shift >= 0 ? (int)pos >> p.page_shift : (int)pos / p.page_size;
+        if (pos < (uint32_t)ahead.length) {
+            const int col = p.page_shift >= 0 ? (int)(pos >> p.page_shift) : (int)(pos / (uint32_t)p.page_size);
             next_place = (int)pos - col * p.page_size;
             next_page = p.a.block_table[ahead.b * p.a.table_stride + col];
         }
         advance(ahead);
     };
-    const uint8_t* kbase = static_cast<const uint8_t*>(p.a.k_cache);
-    const uint8_t* vbase = static_cast<const uint8_t*>(p.a.v_cache);
-    const int row_chunks = p.head_dim * (FP8 ? 1 : 2) / 16;
     auto issue = [&](int stage) {
-        const bool have = lane < 16 && next_page >= 0 && next_page < p.a.num_pages;
-        const uint32_t mask = __ballot_sync(0xffffffffu, have);
-        if (lane < 16) {
-            const int64_t pg = have ? next_page : 0, pl = have ? next_place : 0;
-            longlong2 o;
-            o.x = (pg * p.a.k_page + pl * p.a.k_place + next_head * p.a.k_head) * (FP8 ? 1 : 2);
-            o.y = (pg * p.a.v_page + pl * p.a.v_place + next_head * p.a.v_head) * (FP8 ? 1 : 2);
-            addr[lane] = o;
-        }
-        if (lane == 0) stage_mask[warp][stage] = mask;
-        __syncwarp();
-        if (mask) {
-            const uint32_t dst = smem_u32(ring + (size_t)stage * S::kStageBytes);
-            constexpr int kAll = kAttnWarpTokens * S::kChunks;
+        if (next_live) {
+            const bool have = next_page >= 0 && next_page < p.a.num_pages;
+            const int page0 = __shfl_sync(0xffffffffu, next_page, 0);
+            const uint32_t mask = __ballot_sync(0xffffffffu, have) & kFull;
+            if (lane == 0) stage_mask[warp][stage] = mask;
+            const uint32_t dst = copy_dst + stage * S::kStageBytes;
+            if (mask == kFull && __all_sync(0xffffffffu, next_page == page0)) {
+                // one page holds all rows (the common case): they lie one place stride apart
+                const int64_t place0 = __shfl_sync(0xffffffffu, next_place, 0) + copy_row;
+                const uint8_t* kp = kbase + (page0 * p.a.k_page + next_head * p.a.k_head) * S::kBytes + place0 * k_place;
+                const uint8_t* vp = vbase + (page0 * p.a.v_page + next_head * p.a.v_head) * S::kBytes + place0 * v_place;
+                if (copies) {
 #pragma unroll
-            for (int i = 0; i < (kAll + 31) / 32; ++i) {
-                const int idx = lane + 32 * i;
-                if (kAll % 32 != 0 && idx >= kAll) break;
-                const int row = idx / S::kChunks, ch = idx - row * S::kChunks;
-                const longlong2 o = addr[row];
-                const bool in = ((mask >> row) & 1u) && ch < row_chunks;
-                const uint32_t d = dst + row * S::kPitch + ch * 16;
-                cp_async_16_zfill(d, in ? kbase + o.x + ch * 16 : kbase, in ? 16u : 0u);
-                cp_async_16_zfill(d + S::kRowsBytes, in ? vbase + o.y + ch * 16 : vbase, in ? 16u : 0u);
+                    for (int i = 0; i < S::kCopies; ++i) {
+                        cp_async_16(dst + i * S::kRowsPerCopy * S::kPitch, kp);
+                        cp_async_16(dst + i * S::kRowsPerCopy * S::kPitch + S::kRowsBytes, vp);
+                        kp += S::kRowsPerCopy * k_place;
+                        vp += S::kRowsPerCopy * v_place;
+                    }
+                }
+            } else if (mask) {
+                // rows on several pages, or past the end (those become zeros)
+                if (lane < kTokens) {
+                    const int64_t pg = have ? next_page : 0, pl = have ? next_place : 0;
+                    longlong2 o;
+                    o.x = (pg * p.a.k_page + next_head * p.a.k_head) * S::kBytes + pl * k_place;
+                    o.y = (pg * p.a.v_page + next_head * p.a.v_head) * S::kBytes + pl * v_place;
+                    addr[lane] = o;
+                }
+                __syncwarp();
+                if (copies) {
+#pragma unroll
+                    for (int i = 0; i < S::kCopies; ++i) {
+                        const int row = copy_row + i * S::kRowsPerCopy;
+                        const longlong2 o = addr[row];
+                        const uint32_t bytes = (mask >> row) & 1u ? 16u : 0u;
+                        cp_async_16_zfill(dst + i * S::kRowsPerCopy * S::kPitch, kbase + o.x, bytes);
+                        cp_async_16_zfill(dst + i * S::kRowsPerCopy * S::kPitch + S::kRowsBytes, vbase + o.y, bytes);
+                    }
+                }
             }
         }
         cp_async_commit();
@@ -254,6 +310,12 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
             q[kk][3] = in1 && db < p.head_dim ? *reinterpret_cast<const uint32_t*>(q1 + db) : 0u;
         }
         sc0 = sc1 = p.score_log2;
+        if (p.negate) {
+#pragma unroll
+            for (int kk = 0; kk < KD; ++kk)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[kk][i] ^= 0x80008000u;
+        }
         if constexpr (FP8 && !std::is_same<T, TQ>::value) {
             // bf16 queries against f16 keys: each row is scaled by a power of two to a largest element in [1, 2)
             // (exact; elements 2^-24 of the largest and smaller lose bits) and its scores are scaled back
@@ -275,8 +337,8 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
             const int e0 = min(max((int)(__float_as_uint(top0) >> 23), 1), 252);
             const int e1 = min(max((int)(__float_as_uint(top1) >> 23), 1), 252);
             const float d0 = __uint_as_float((uint32_t)(254 - e0) << 23), d1 = __uint_as_float((uint32_t)(254 - e1) << 23);
-            sc0 *= __uint_as_float((uint32_t)e0 << 23);
-            sc1 *= __uint_as_float((uint32_t)e1 << 23);
+            sc0 = fmaxf(sc0 * __uint_as_float((uint32_t)e0 << 23), FLT_MIN);
+            sc1 = fmaxf(sc1 * __uint_as_float((uint32_t)e1 << 23), FLT_MIN);
 #pragma unroll
             for (int kk = 0; kk < KD; ++kk)
 #pragma unroll
@@ -298,112 +360,122 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
         const uint32_t mask = stage_mask[warp][stage];
         if (!mask) return;
         const uint32_t ks = smem_u32(ring + (size_t)stage * S::kStageBytes), vs = ks + S::kRowsBytes;
-        float s[2][4] = {};
-        if constexpr (FP8) {
-            // one 32-bit word of a lane is four neighbouring elements of its row: two f16 pairs, the b0 and b1 of one step
-            const uint32_t row = (lane & 7) + ((lane >> 3) & 1) * 8;
-            const uint32_t base = ks + row * S::kPitch + (lane >> 4) * 16;
+        const bool two = rows > 8;              // rows 8..15 hold queries
+        constexpr int kN = kTokens / 8;         // 8-position column tiles of S
+        float s[kN][4];
 #pragma unroll
-            for (int kk = 0; kk < KD; kk += 2) {
-                if (kk + 1 < KD) {
+        for (int t = 0; t < kTokens / 16; ++t) {
+            // two accumulators per column tile: the chains of dependent products are half as long
+            float x[2][4] = {}, y[2][4] = {};
+            if constexpr (FP8) {
+                // one 32-bit word of a lane is four neighbouring elements of its row: two f16 pairs, the b0 and b1 of one step
+                const uint32_t row = t * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+                const uint32_t base = ks + row * S::kPitch + (lane >> 4) * 16;
+#pragma unroll
+                for (int kk = 0; kk < KD; kk += 2) {
+                    if (kk + 1 < KD) {
+                        uint32_t r[4];
+                        ldmatrix_x4(base + kk * 16, r);
+                        mma_16816<T>(x[0], q[kk], e4m3x2_to_half2(r[0]), e4m3x2_to_half2(r[0] >> 16));
+                        mma_16816<T>(x[1], q[kk], e4m3x2_to_half2(r[1]), e4m3x2_to_half2(r[1] >> 16));
+                        mma_16816<T>(y[0], q[kk + 1], e4m3x2_to_half2(r[2]), e4m3x2_to_half2(r[2] >> 16));
+                        mma_16816<T>(y[1], q[kk + 1], e4m3x2_to_half2(r[3]), e4m3x2_to_half2(r[3] >> 16));
+                    } else {
+                        uint32_t r[2];
+                        ldmatrix_x2(ks + (t * 16 + (lane & 15)) * S::kPitch + kk * 16, r);
+                        mma_16816<T>(x[0], q[kk], e4m3x2_to_half2(r[0]), e4m3x2_to_half2(r[0] >> 16));
+                        mma_16816<T>(x[1], q[kk], e4m3x2_to_half2(r[1]), e4m3x2_to_half2(r[1] >> 16));
+                    }
+                }
+            } else {
+                const uint32_t row = t * 16 + (lane & 7) + (lane >> 4) * 8;
+                const uint32_t base = ks + row * S::kPitch + ((lane >> 3) & 1) * 16;
+#pragma unroll
+                for (int kk = 0; kk < KD; ++kk) {
                     uint32_t r[4];
-                    ldmatrix_x4(base + kk * 16, r);
-                    mma_16816<T>(s[0], q[kk], e4m3x2_to_half2(r[0]), e4m3x2_to_half2(r[0] >> 16));
-                    mma_16816<T>(s[1], q[kk], e4m3x2_to_half2(r[1]), e4m3x2_to_half2(r[1] >> 16));
-                    mma_16816<T>(s[0], q[kk + 1], e4m3x2_to_half2(r[2]), e4m3x2_to_half2(r[2] >> 16));
-                    mma_16816<T>(s[1], q[kk + 1], e4m3x2_to_half2(r[3]), e4m3x2_to_half2(r[3] >> 16));
-                } else {
-                    uint32_t r[2];
-                    ldmatrix_x2(ks + (lane & 15) * S::kPitch + kk * 16, r);
-                    mma_16816<T>(s[0], q[kk], e4m3x2_to_half2(r[0]), e4m3x2_to_half2(r[0] >> 16));
-                    mma_16816<T>(s[1], q[kk], e4m3x2_to_half2(r[1]), e4m3x2_to_half2(r[1] >> 16));
+                    ldmatrix_x4(base + kk * 32, r);
+                    mma_16816<T>(kk & 1 ? y[0] : x[0], q[kk], r[0], r[1]);
+                    mma_16816<T>(kk & 1 ? y[1] : x[1], q[kk], r[2], r[3]);
                 }
             }
-        } else {
-            const uint32_t row = (lane & 7) + (lane >> 4) * 8;
-            const uint32_t base = ks + row * S::kPitch + ((lane >> 3) & 1) * 16;
-#pragma unroll
-            for (int kk = 0; kk < KD; ++kk) {
-                uint32_t r[4];
-                ldmatrix_x4(base + kk * 32, r);
-                mma_16816<T>(s[0], q[kk], r[0], r[1]);
-                mma_16816<T>(s[1], q[kk], r[2], r[3]);
-            }
-        }
-        // scores in log2 units; masked positions to -inf
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            s[n][0] *= sc0;
-            s[n][1] *= sc0;
-            s[n][2] *= sc1;
-            s[n][3] *= sc1;
-        }
-        if (mask != 0xFFFFu) {
 #pragma unroll
             for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[2 * t + n][i] = x[n][i] + y[n][i];
+        }
+        if (mask != kFull) {
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     if (!((mask >> (n * 8 + 2 * j4 + i)) & 1u)) s[n][i] = s[n][i + 2] = -INFINITY;
         }
-        float top0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-        float top1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+        // Running maximum in log2 units (the scale sc is positive, see load_query), then the probabilities.
+        auto softmax_rows = [&](int h, float sc, float& m, float& l) {
+            float top = fmaxf(s[0][2 * h], s[0][2 * h + 1]);
 #pragma unroll
-        for (int d = 1; d < 4; d <<= 1) {
-            top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, d));
-            top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, d));
-        }
-        if (__any_sync(0xffffffffu, top0 > m0 || top1 > m1)) {
-            const float n0 = fmaxf(m0, top0), n1 = fmaxf(m1, top1);
-            const float f0 = exp2_fast(m0 - n0), f1 = exp2_fast(m1 - n1);
-            m0 = n0;
-            m1 = n1;
-            l0 *= f0;
-            l1 *= f1;
+            for (int n = 1; n < kN; ++n) top = fmaxf(top, fmaxf(s[n][2 * h], s[n][2 * h + 1]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            top *= sc;
+            if (__any_sync(0xffffffffu, top > m)) {
+                const float fresh = fmaxf(m, top);
+                const float f = exp2_fast(m - fresh);
+                m = fresh;
+                l *= f;
 #pragma unroll
-            for (int n = 0; n < 2 * KD; ++n) {
-                o[n][0] *= f0;
-                o[n][1] *= f0;
-                o[n][2] *= f1;
-                o[n][3] *= f1;
+                for (int n = 0; n < 2 * KD; ++n) {
+                    o[n][2 * h] *= f;
+                    o[n][2 * h + 1] *= f;
+                }
             }
-        }
+            float sum = 0.f;
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            s[n][0] = exp2_fast(s[n][0] - m0);
-            s[n][1] = exp2_fast(s[n][1] - m0);
-            s[n][2] = exp2_fast(s[n][2] - m1);
-            s[n][3] = exp2_fast(s[n][3] - m1);
-            l0 += s[n][0] + s[n][1];
-            l1 += s[n][2] + s[n][3];
-        }
-        // Probabilities as the 16-bit left operand of the product with V (the matrix instruction takes 16-bit operands);
-        // their sum l is taken in fp32 before that rounding, O stays fp32.
-        const uint32_t a[4] = {round2<T>(s[0][0], s[0][1]), round2<T>(s[0][2], s[0][3]),
-                               round2<T>(s[1][0], s[1][1]), round2<T>(s[1][2], s[1][3])};
-        const uint32_t vrow = vs + ((lane & 7) + ((lane >> 3) & 1) * 8) * S::kPitch;
-        if constexpr (FP8) {
-            // a transposed load moves pairs of elements: bytes (t0 d0, t0 d1, t1 d0, t1 d1); reordered to pairs of
-            // tokens, the even elements of a 16-element block form one 8-column tile and the odd ones another
-            auto tile = [&](int blk, uint32_t lo, uint32_t hi) {
-                const uint32_t x = __byte_perm(lo, 0u, 0x3120), y = __byte_perm(hi, 0u, 0x3120);
-                mma_16816<T>(o[2 * blk], a, e4m3x2_to_half2(x), e4m3x2_to_half2(y));
-                mma_16816<T>(o[2 * blk + 1], a, e4m3x2_to_half2(x >> 16), e4m3x2_to_half2(y >> 16));
-            };
-#pragma unroll
-            for (int blk = 0; blk < KD; blk += 2) {
-                uint32_t r[4];
-                // the last odd block loads its own chunk twice
-                ldmatrix_x4_trans(vrow + (blk + (blk + 1 < KD ? (lane >> 4) : 0)) * 16, r);
-                tile(blk, r[0], r[1]);
-                if (blk + 1 < KD) tile(blk + 1, r[2], r[3]);
+            for (int n = 0; n < kN; ++n) {
+                s[n][2 * h] = exp2_fast(fmaf(s[n][2 * h], sc, -m));
+                s[n][2 * h + 1] = exp2_fast(fmaf(s[n][2 * h + 1], sc, -m));
+                sum += s[n][2 * h] + s[n][2 * h + 1];
             }
+            l += sum;
+        };
+        softmax_rows(0, sc0, m0, l0);
+        if (two) {
+            softmax_rows(1, sc1, m1, l1);
         } else {
 #pragma unroll
-            for (int blk = 0; blk < KD; ++blk) {
-                uint32_t r[4];
-                ldmatrix_x4_trans(vrow + blk * 32 + (lane >> 4) * 16, r);
-                mma_16816<T>(o[2 * blk], a, r[0], r[1]);
-                mma_16816<T>(o[2 * blk + 1], a, r[2], r[3]);
+            for (int n = 0; n < kN; ++n) s[n][2] = s[n][3] = 0.f;
+        }
+#pragma unroll
+        for (int t = 0; t < kTokens / 16; ++t) {
+            // Probabilities as the 16-bit left operand of the product with V (the matrix instruction takes 16-bit
+            // operands); their sum l is taken in fp32 before that rounding, O stays fp32.
+            const uint32_t a[4] = {round2<T>(s[2 * t][0], s[2 * t][1]), round2<T>(s[2 * t][2], s[2 * t][3]),
+                                   round2<T>(s[2 * t + 1][0], s[2 * t + 1][1]), round2<T>(s[2 * t + 1][2], s[2 * t + 1][3])};
+            const uint32_t vrow = vs + (t * 16 + (lane & 7) + ((lane >> 3) & 1) * 8) * S::kPitch;
+            if constexpr (FP8) {
+                // a transposed load moves pairs of elements: bytes (t0 d0, t0 d1, t1 d0, t1 d1); reordered to pairs of
+                // tokens, the even elements of a 16-element block form one 8-column tile and the odd ones another
+                auto tile = [&](int blk, uint32_t lo, uint32_t hi) {
+                    const uint32_t x = __byte_perm(lo, 0u, 0x3120), y = __byte_perm(hi, 0u, 0x3120);
+                    mma_16816<T>(o[2 * blk], a, e4m3x2_to_half2(x), e4m3x2_to_half2(y));
+                    mma_16816<T>(o[2 * blk + 1], a, e4m3x2_to_half2(x >> 16), e4m3x2_to_half2(y >> 16));
+                };
+#pragma unroll
+                for (int blk = 0; blk < KD; blk += 2) {
+                    uint32_t r[4];
+                    // the last odd block loads its own chunk twice
+                    ldmatrix_x4_trans(vrow + (blk + (blk + 1 < KD ? (lane >> 4) : 0)) * 16, r);
+                    tile(blk, r[0], r[1]);
+                    if (blk + 1 < KD) tile(blk + 1, r[2], r[3]);
+                }
+            } else {
+#pragma unroll
+                for (int blk = 0; blk < KD; ++blk) {
+                    uint32_t r[4];
+                    ldmatrix_x4_trans(vrow + blk * 32 + (lane >> 4) * 16, r);
+                    mma_16816<T>(o[2 * blk], a, r[0], r[1]);
+                    mma_16816<T>(o[2 * blk + 1], a, r[2], r[3]);
+                }
             }
         }
     };
@@ -431,8 +503,9 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
         if (p.a.lse) p.a.lse[(int64_t)b * p.heads + head0 + row] = l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -INFINITY;
     };
 
-    // The segment's positions of this CTA are done: join the warps, then write or leave a partial.
-    auto flush = [&](int64_t tile_index) {
+    // The segment's positions of this CTA are done: join the warps, then write or leave a partial.  Each warp lays its O
+    // into the pipeline slot it just consumed (free until the next copies are issued).
+    auto flush = [&](int stage) {
 #pragma unroll
         for (int d = 1; d < 4; d <<= 1) {
             l0 += __shfl_xor_sync(0xffffffffu, l0, d);
@@ -444,46 +517,39 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
             warp_l[warp][quad] = l0;
             warp_l[warp][quad + 8] = l1;
         }
+        float* own = reinterpret_cast<float*>(ring + (size_t)stage * S::kStageBytes);
+        each_o([&](int r, int d, float x, float y) {
+            if (r < rows) *reinterpret_cast<float2*>(own + r * S::kMergePitch + d) = make_float2(x, y);
+        });
         __syncthreads();
-        float M0 = -FLT_MAX, M1 = -FLT_MAX;
-#pragma unroll
-        for (int w = 0; w < kAttnWarps; ++w) {
-            M0 = fmaxf(M0, warp_m[w][quad]);
-            M1 = fmaxf(M1, warp_m[w][quad + 8]);
-        }
-        const float f0 = exp2_fast(m0 - M0), f1 = exp2_fast(m1 - M1);
-        // one warp after the other adds its share (a fixed order)
-        for (int w = 0; w < kAttnWarps; ++w) {
-            if (warp == w)
-                each_o([&](int r, int d, float x, float y) {
-                    if (r >= rows) return;
-                    const float f = r < 8 ? f0 : f1;
-                    float2* at2 = reinterpret_cast<float2*>(merge + r * S::kMergePitch + d);
-                    float2 v = make_float2(x * f, y * f);
-                    if (w > 0) {
-                        v.x += at2->x;
-                        v.y += at2->y;
-                    }
-                    *at2 = v;
-                });
-            __syncthreads();
-        }
-        auto row_ml = [&](int r, float& m, float& l) {
+        auto joined = [&](int r, int d, float& m, float& l) {     // four columns of a row, over the warps in order
             m = -FLT_MAX;
             l = 0.f;
 #pragma unroll
             for (int w = 0; w < kAttnWarps; ++w) m = fmaxf(m, warp_m[w][r]);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) l = fmaf(warp_l[w][r], exp2_fast(warp_m[w][r] - m), l);
+            for (int w = 0; w < kAttnWarps; ++w) {
+                const float f = exp2_fast(warp_m[w][r] - m);
+                const float4 x = *reinterpret_cast<const float4*>(smem + ((size_t)w * kAttnStages + stage) * S::kStageBytes +
+                                                                  (r * S::kMergePitch + d) * 4);
+                l = fmaf(warp_l[w][r], f, l);
+                v.x = fmaf(x.x, f, v.x);
+                v.y = fmaf(x.y, f, v.y);
+                v.z = fmaf(x.z, f, v.z);
+                v.w = fmaf(x.w, f, v.w);
+            }
+            return v;
         };
-        const int64_t seg0 = tile_index - at.tile, seg1 = seg0 + at.tiles;   // the segment's tiles
+        const int64_t seg0 = unit - at.tile, seg1 = seg0 + at.tiles;   // the segment's tiles, as units
         const int quarter = p.head_dim / 4;
-        if (seg0 >= range0 && seg1 <= range1) {
+        // the CTAs that share the segment: those of its first and last tile and all between
+        const bool whole = seg0 >= range0 && seg1 <= range1;
+        if (whole) {
             for (int i = threadIdx.x; i < rows * quarter; i += kAttnThreads) {
                 const int r = i / quarter, d = (i - r * quarter) * 4;
                 float m, l;
-                row_ml(r, m, l);
-                const float4 v = *reinterpret_cast<const float4*>(merge + r * S::kMergePitch + d);
+                const float4 v = joined(r, d, m, l);
                 const float f = l > 0.f || l != l ? p.a.v_scale / l : 0.f;
                 *reinterpret_cast<uint2*>(out_row(at.b, head0 + r) + d) =
                     make_uint2(round2<TQ>(v.x * f, v.y * f), round2<TQ>(v.z * f, v.w * f));
@@ -495,15 +561,13 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
         float* slot = p.partials + ((int64_t)blockIdx.x * 2 + (first_segment ? 0 : 1)) * S::kSlotFloats;
         for (int i = threadIdx.x; i < rows * quarter; i += kAttnThreads) {
             const int r = i / quarter, d = (i - r * quarter) * 4;
-            __stcg(reinterpret_cast<float4*>(slot + r * S::kDim + d), *reinterpret_cast<const float4*>(merge + r * S::kMergePitch + d));
-        }
-        if (threadIdx.x < rows) {
             float m, l;
-            row_ml(threadIdx.x, m, l);
-            __stcg(slot + 16 * S::kDim + threadIdx.x, m);
-            __stcg(slot + 16 * S::kDim + 16 + threadIdx.x, l);
+            __stcg(reinterpret_cast<float4*>(slot + r * S::kDim + d), joined(r, d, m, l));
+            if (d == 0) {
+                __stcg(slot + 16 * S::kDim + r, m);
+                __stcg(slot + 16 * S::kDim + 16 + r, l);
+            }
         }
-        // the CTAs that share the segment: those of its first and last tile and all between
         const int c0 = (int)(((seg0 + 1) * ctas - 1) / total), c1 = (int)((seg1 * ctas - 1) / total);
         uint32_t* counter = p.counters + (int64_t)at.b * HV + at.hv;
         __threadfence();
@@ -512,7 +576,8 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
         __syncthreads();
         if (join_now) {
             __threadfence();
-            const bool c0_first = total * c0 / ctas == seg0;
+            // the first CTA's other slot, if it ended another segment before this one
+            const bool c0_first = range_start(c0) >= seg0 - kAttnSegmentCost;
             auto slot_of = [&](int c) {
                 return p.partials + ((int64_t)c * 2 + (c == c0 && !c0_first ? 1 : 0)) * S::kSlotFloats;
             };
@@ -547,40 +612,41 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
     fetch();
 #pragma unroll
     for (int i = 0; i < kAttnStages - 1; ++i) {
-        if (i < steps) {
-            issue(i);
-            if (i + 1 < steps) fetch();
-        } else {
-            cp_async_commit();
-        }
+        issue(i);
+        fetch();
     }
-    load_query();
+    if (at.left > 0) load_query();
     int stage = 0, fill = kAttnStages - 1;
-    for (int i = 0; i < steps; ++i) {
+    while (at.left > 0) {
         cp_async_wait<kAttnStages - 2>();
         __syncwarp();
-        // the slot computed on in the previous step is free
-        if (i + kAttnStages - 1 < steps) {
-            issue(fill);
-            if (i + kAttnStages < steps) fetch();
-        } else {
-            cp_async_commit();
-        }
+        issue(fill);              // the slot computed on in the previous step
+        fetch();
         compute(stage);
-        if (at.tile + 1 == at.tiles || i + 1 == steps) {
-            flush(range0 + i);
-            first_segment = false;
-            if (i + 1 < steps) {
-                advance(at);
-                load_query();
+        if (at.tile + 1 == at.tiles || at.left == 1) {
+            flush(stage);
+            if (row_chunks < S::kChunks) {      // O went over the zeros behind head_dim
+                const int pad = S::kChunks - row_chunks;
+                for (int i = lane; i < kTokens * pad; i += 32)
+                    *reinterpret_cast<uint4*>(ring + (size_t)stage * S::kStageBytes + (i / pad) * S::kPitch + (row_chunks + i % pad) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                __syncwarp();
             }
+            first_segment = false;
+            const int64_t left = at.left;
+            advance(at);
+            unit += left - at.left;
+            if (at.left > 0) load_query();
         } else {
             ++at.tile;
+            --at.left;
+            ++unit;
         }
         if (++stage == kAttnStages) stage = 0;
         if (++fill == kAttnStages) fill = 0;
     }
     cp_async_wait<0>();
+    write_empty();
 }
 
 template <typename T, typename TQ, bool FP8, int KD>
@@ -598,6 +664,7 @@ cudaError_t attn_prepare(AttnVariant* v) {
     if (e != cudaSuccess) return e;
     v->smem_bytes = S::kSmemBytes;
     v->slot_floats = S::kSlotFloats;
+    v->tile_tokens = S::kTile;
     v->launch = &attn_launch<T, TQ, FP8, KD>;
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v->ctas_per_sm, kern, kAttnThreads, S::kSmemBytes);
 }

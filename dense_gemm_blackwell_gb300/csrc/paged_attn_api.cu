@@ -1,4 +1,6 @@
 // paged_attn_api.cu -- host side of the paged attention operator (include/serving.h): plans, checks and launches.
+#include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 #include <new>
@@ -65,7 +67,7 @@ gemm_status_t paged_attn_plan_create(paged_attn_plan_t* out, const paged_attn_de
     p->counter_bytes = ((int64_t)desc->max_batch * desc->kv_heads * p->head_groups * 4 + 255) / 256 * 256;
     const int64_t partial_bytes = (int64_t)grid * 2 * v.slot_floats * 4;
     p->info.grid = grid;
-    p->info.tile_tokens = kAttnTile;
+    p->info.tile_tokens = v.tile_tokens;
     p->info.head_groups = p->head_groups;
     p->info.smem_bytes = v.smem_bytes;
     p->info.workspace_bytes = p->counter_bytes + partial_bytes;
@@ -113,7 +115,10 @@ gemm_status_t paged_attn_run(paged_attn_plan_t plan, const paged_attn_args_t* ar
     p.window = d.window;
     p.head_groups = plan->head_groups;
     p.segments_per_sequence = d.kv_heads * plan->head_groups;
-    p.score_log2 = (float)((double)a.scale * (double)a.k_scale * 1.4426950408889634);
+    const double scale = (double)a.scale * (double)a.k_scale;
+    p.negate = scale < 0;
+    // a scale of zero becomes the smallest normal number, so that masked scores (-inf) times it stay -inf
+    p.score_log2 = std::max((float)(std::fabs(scale) * 1.4426950408889634), FLT_MIN);
     p.counters = static_cast<uint32_t*>(plan->memory);
     p.partials = reinterpret_cast<float*>(static_cast<char*>(plan->memory) + plan->counter_bytes);
     return status_of(plan->variant.launch(p, plan->info.grid, reinterpret_cast<cudaStream_t>(stream)));

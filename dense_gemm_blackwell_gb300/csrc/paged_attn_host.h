@@ -11,10 +11,9 @@ namespace dgb {
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
-constexpr int kAttnWarpTokens = 16;                          // positions of one warp's step
-constexpr int kAttnTile = kAttnWarps * kAttnWarpTokens;      // positions of one tile
 constexpr int kAttnStages = 3;                               // steps in flight per warp
-constexpr int kAttnMinTiles = 2;                             // fewest tiles a CTA is given while others idle
+constexpr int kAttnSegmentCost = 2;                          // units of work a segment costs beyond its tiles
+constexpr int kAttnMinUnits = 4;                             // fewest units a CTA is given while others idle
 
 struct AttnParams {
     paged_attn_args_t a;
@@ -22,14 +21,15 @@ struct AttnParams {
     int32_t page_shift;               // log2(page_size), or -1
     int32_t head_groups;              // ceil(group / 16)
     int32_t segments_per_sequence;    // kv_heads * head_groups
-    float score_log2;                 // scale * k_scale * log2(e)
+    float score_log2;                 // |scale * k_scale| * log2(e), at least the smallest normal number
+    int32_t negate;                   // scale * k_scale < 0: the queries' signs are flipped
     float* partials;                  // [CTA][2] slots: O[16][dim], m[16], l[16]
     uint32_t* counters;               // [sequence][segment]: CTAs that left their partial; zero between launches
 };
 
 struct AttnVariant {
     cudaError_t (*launch)(const AttnParams&, int grid, cudaStream_t) = nullptr;
-    int smem_bytes = 0, slot_floats = 0, ctas_per_sm = 0;
+    int smem_bytes = 0, slot_floats = 0, ctas_per_sm = 0, tile_tokens = 0;
 };
 
 cudaError_t attn_variant_bf16(int head_dim, AttnVariant* v);          // bf16 queries and cache
