@@ -4,16 +4,17 @@
 //
 // A head row of head_dim 16-bit elements is held by 8, 16 or 32 neighbouring
 // lanes, eight elements (one 16-byte load) each: a row is read once, its sum
-// of squares is reduced by shuffles, and it is written once.  A lane group
-// takes several rows of one token in turn, so the token's cosines and sines
-// (the same for every head) stay in registers.  The kernels are bound by
-// memory: four rows' loads (two rows' x and dy in the backward pass) are
-// issued before the first is used.
+// of squares is reduced by shuffles, and it is written once.  The kernels are
+// bound by memory; what competes with it is the instruction count, so a lane
+// group takes several rows of one kind (queries, keys or values) of one token
+// and prepares their common factors once.
 //
-// Rotated pairs are y_a' = y_a c - y_b s and y_b' = y_a s + y_b c, written here
-// for every element e with partner e' as  y_e' = y_e c + y_e' s_e  with
-// s_e = -s for the first element of a pair and +s for the second; the backward
-// pass turns the other way (s_e negated).
+// With the pairs' rotation y_a' = y_a c - y_b s, y_b' = y_a s + y_b c and
+// y = x r w, every element e with partner e' is
+//   y_e = r (x_e (w_e c_e) + x_e' (w_e' s_e)),
+// s_e = -s for the first element of a pair and +s for the second: the two
+// bracketed factors depend on the token and the kind only, and the partners
+// are exchanged as loaded, two 16-bit elements to a register.
 #include <algorithm>
 #include <cstdint>
 
@@ -37,296 +38,335 @@ enum RopePairs {
     kPairsAny = 2          // either layout, any even rot: through shared memory
 };
 
+enum RowKind { kQueries = 0, kKeys = 1, kValues = 2 };
+
 struct RopeParams {
     qk_norm_rope_args_t a;
     qk_norm_rope_grads_t g;
-    int32_t rows_per_group;   // head rows of one token a lane group takes
-    int32_t rows;             // head rows per token (queries, keys and, with a cache, values)
-    uint32_t groups;          // lane groups per token
-    uint32_t items;           // tokens x groups, below 2^31
-    float* partials;          // backward: [block][2][kMaxHeadDim]
+    int32_t rows_per_group;     // head rows of one token a lane group takes
+    uint32_t q_groups, k_groups;    // lane groups per token for queries; for keys (and for values, with a cache)
+    uint32_t groups;            // lane groups per token
+    uint32_t items;             // forward: tokens x groups, below 2^31
+    uint32_t q_blocks;          // backward: blocks [0, q_blocks) take queries, the rest keys
+    float* partials;            // backward: [block][kMaxHeadDim]
 };
 
 __device__ __forceinline__ uint4 load_row16(const void* p) {
     return __ldcs(static_cast<const uint4*>(p));
 }
 
-template <int LANES>
-__device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
-// This lane's eight cosines and signed sines of a token.  `live`: the lane holds rotated elements.
-template <int PAIRS>
-__device__ __forceinline__ void load_turn(const qk_norm_rope_args_t& a, int token, int e0, bool live, float sign,
-                                          float (&c)[8], float (&s)[8]) {
+// A token's factors for this lane's eight elements: own[i] = w_e c_e, other[i] = w_e' s_e (sign +1: forward; -1: the turn
+// back).  `weight` NULL: ones.  Elements that are not rotated: own = w_e, other = 0 (and their partners are taken as 0).
+template <typename T, int PAIRS>
+__device__ __forceinline__ void load_factors(const qk_norm_rope_args_t& a, const T* weight, int token, int e0, bool act, bool live,
+                                             float sign, float (&own)[8], float (&other)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        c[i] = 1.f;
-        s[i] = 0.f;
+        own[i] = 1.f;
+        other[i] = 0.f;
     }
-    if (!live) return;
-    const int half = a.rot_dim / 2;
-    const int pos = min(max(a.positions[token], 0), a.table_rows - 1);
-    const float* row = a.table + (size_t)pos * a.rot_dim;
-    if constexpr (PAIRS == kPairsHalves) {
-        const bool second = e0 >= half;
-        const int i0 = second ? e0 - half : e0;
-        const float sg = second ? sign : -sign;
-        const float4 c0 = *reinterpret_cast<const float4*>(row + i0), c1 = *reinterpret_cast<const float4*>(row + i0 + 4);
-        const float4 s0 = *reinterpret_cast<const float4*>(row + half + i0),
-                     s1 = *reinterpret_cast<const float4*>(row + half + i0 + 4);
-        c[0] = c0.x; c[1] = c0.y; c[2] = c0.z; c[3] = c0.w;
-        c[4] = c1.x; c[5] = c1.y; c[6] = c1.z; c[7] = c1.w;
-        s[0] = sg * s0.x; s[1] = sg * s0.y; s[2] = sg * s0.z; s[3] = sg * s0.w;
-        s[4] = sg * s1.x; s[5] = sg * s1.y; s[6] = sg * s1.z; s[7] = sg * s1.w;
-    } else if constexpr (PAIRS == kPairsNeighbours) {
-        const float4 cc = *reinterpret_cast<const float4*>(row + e0 / 2);
-        const float4 ss = *reinterpret_cast<const float4*>(row + half + e0 / 2);
-        c[0] = c[1] = cc.x; c[2] = c[3] = cc.y; c[4] = c[5] = cc.z; c[6] = c[7] = cc.w;
-        s[0] = -sign * ss.x; s[1] = sign * ss.x; s[2] = -sign * ss.y; s[3] = sign * ss.y;
-        s[4] = -sign * ss.z; s[5] = sign * ss.z; s[6] = -sign * ss.w; s[7] = sign * ss.w;
-    } else {
+    if (live) {
+        const int half = a.rot_dim / 2;
+        const int pos = min(max(a.positions[token], 0), a.table_rows - 1);
+        const float* row = a.table + (size_t)pos * a.rot_dim;
+        if constexpr (PAIRS == kPairsHalves) {
+            const bool second = e0 >= half;
+            const int i0 = second ? e0 - half : e0;
+            const float sg = second ? sign : -sign;
+            const float4 c0 = *reinterpret_cast<const float4*>(row + i0), c1 = *reinterpret_cast<const float4*>(row + i0 + 4);
+            const float4 s0 = *reinterpret_cast<const float4*>(row + half + i0),
+                         s1 = *reinterpret_cast<const float4*>(row + half + i0 + 4);
+            own[0] = c0.x; own[1] = c0.y; own[2] = c0.z; own[3] = c0.w;
+            own[4] = c1.x; own[5] = c1.y; own[6] = c1.z; own[7] = c1.w;
+            other[0] = sg * s0.x; other[1] = sg * s0.y; other[2] = sg * s0.z; other[3] = sg * s0.w;
+            other[4] = sg * s1.x; other[5] = sg * s1.y; other[6] = sg * s1.z; other[7] = sg * s1.w;
+        } else if constexpr (PAIRS == kPairsNeighbours) {
+            const float4 cc = *reinterpret_cast<const float4*>(row + e0 / 2);
+            const float4 ss = *reinterpret_cast<const float4*>(row + half + e0 / 2);
+            own[0] = own[1] = cc.x; own[2] = own[3] = cc.y; own[4] = own[5] = cc.z; own[6] = own[7] = cc.w;
+            other[0] = -sign * ss.x; other[1] = sign * ss.x; other[2] = -sign * ss.y; other[3] = sign * ss.y;
+            other[4] = -sign * ss.z; other[5] = sign * ss.z; other[6] = -sign * ss.w; other[7] = sign * ss.w;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int e = e0 + i;
-            if (e >= a.rot_dim) continue;
-            const int at = a.interleaved ? e / 2 : (e < half ? e : e - half);
-            const bool second = a.interleaved ? (e & 1) : e >= half;
-            c[i] = row[at];
-            s[i] = second ? sign * row[half + at] : -sign * row[half + at];
-        }
-    }
-}
-
-// y turned in place.  `mate`: kPairsHalves, the lane that holds the partners; `row`: kPairsAny, this lane group's shared
-// row.  Elements past rot_dim keep their bits (a product with s = 0 would turn an infinity into NaN).
-template <int PAIRS>
-__device__ __forceinline__ void turn(const qk_norm_rope_args_t& a, int e0, bool live, int mate, float* row,
-                                     const float (&c)[8], const float (&s)[8], float (&y)[8]) {
-    if constexpr (PAIRS == kPairsHalves) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float other = __shfl_sync(0xffffffffu, y[i], mate);
-            if (live) y[i] = fmaf(other, s[i], y[i] * c[i]);
-        }
-    } else if constexpr (PAIRS == kPairsNeighbours) {
-        if (live) {
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                const float u = y[i], v = y[i + 1];
-                y[i] = fmaf(v, s[i], u * c[i]);
-                y[i + 1] = fmaf(u, s[i + 1], v * c[i + 1]);
+            for (int i = 0; i < 8; ++i) {
+                const int e = e0 + i;
+                if (e >= a.rot_dim) continue;
+                const int at = a.interleaved ? e / 2 : (e < half ? e : e - half);
+                const bool second = a.interleaved ? (e & 1) : e >= half;
+                own[i] = row[at];
+                other[i] = second ? sign * row[half + at] : -sign * row[half + at];
             }
         }
+    }
+    if (weight == nullptr || !act) return;
+    float w[8];
+    unpack8<T>(*reinterpret_cast<const uint4*>(weight + e0), w);
+    if (live) {
+        if constexpr (PAIRS == kPairsHalves) {
+            float v[8];
+            unpack8<T>(*reinterpret_cast<const uint4*>(weight + (e0 < a.rot_dim / 2 ? e0 + a.rot_dim / 2 : e0 - a.rot_dim / 2)), v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) other[i] *= v[i];
+        } else if constexpr (PAIRS == kPairsNeighbours) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) other[i] *= w[i ^ 1];
+        } else {
+            const int half = a.rot_dim / 2;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int e = e0 + i;
+                if (e >= a.rot_dim) continue;
+                other[i] *= (float)weight[a.interleaved ? (e ^ 1) : (e < half ? e + half : e - half)];
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) own[i] *= w[i];
+}
+
+// The partners of x[0..7] (packed in `raw`).  `mate`: kPairsHalves, the lane that holds them; `row`: kPairsAny, this lane
+// group's shared row.  Called by every lane of the warp.
+template <typename T, int PAIRS>
+__device__ __forceinline__ void partners(const qk_norm_rope_args_t& a, int e0, bool live, int mate, float* row, const uint4& raw,
+                                         const float (&x)[8], float (&z)[8]) {
+    if constexpr (PAIRS == kPairsHalves) {
+        uint4 r;
+        r.x = __shfl_sync(0xffffffffu, raw.x, mate);
+        r.y = __shfl_sync(0xffffffffu, raw.y, mate);
+        r.z = __shfl_sync(0xffffffffu, raw.z, mate);
+        r.w = __shfl_sync(0xffffffffu, raw.w, mate);
+        if (!live) r = make_uint4(0, 0, 0, 0);
+        unpack8<T>(r, z);
+    } else if constexpr (PAIRS == kPairsNeighbours) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = live ? x[i ^ 1] : 0.f;
     } else {
         const int half = a.rot_dim / 2;
         __syncwarp();
         if (live) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) row[e0 + i] = y[i];
+            for (int i = 0; i < 8; ++i) row[e0 + i] = x[i];
         }
         __syncwarp();
-        if (live) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int e = e0 + i;
-                if (e >= a.rot_dim) continue;
-                const int at = a.interleaved ? (e ^ 1) : (e < half ? e + half : e - half);
-                y[i] = fmaf(row[at], s[i], y[i] * c[i]);
-            }
+        for (int i = 0; i < 8; ++i) {
+            const int e = e0 + i;
+            const int at = a.interleaved ? (e ^ 1) : (e < half ? e + half : e - half);
+            z[i] = e < a.rot_dim ? row[at] : 0.f;
         }
-        __syncwarp();
     }
 }
 
+template <int LANES, int PAIRS>
+struct RowLane {
+    int e0;        // this lane's first element
+    bool act;      // it holds elements of the row
+    bool live;     // ... rotated ones
+    int mate;      // kPairsHalves: the lane of the warp with the partners
+    __device__ __forceinline__ explicit RowLane(const qk_norm_rope_args_t& a) {
+        e0 = (threadIdx.x % LANES) * 8;
+        act = e0 < a.head_dim;
+        live = act && e0 < a.rot_dim;
+        const int step = a.rot_dim / 16;
+        mate = (threadIdx.x & 31) + (PAIRS == kPairsHalves && live ? (e0 < a.rot_dim / 2 ? step : -step) : 0);
+    }
+};
+
 template <typename T, int LANES, int PAIRS>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const __grid_constant__ RopeParams p) {
     constexpr int kAhead = 4;   // rows whose loads are in flight
     __shared__ float scratch[PAIRS == kPairsAny ? (kRopeThreads / LANES) * LANES * 8 : 1];
     griddep_wait();
     griddep_launch_dependents();
     const qk_norm_rope_args_t& a = p.a;
-    const int l = threadIdx.x % LANES;
-    const int e0 = l * 8;
-    const bool act = e0 < a.head_dim;
-    const bool live = act && e0 < a.rot_dim;
+    const RowLane<LANES, PAIRS> me(a);
+    const int e0 = me.e0;
     float* srow = scratch + (PAIRS == kPairsAny ? (threadIdx.x / LANES) * LANES * 8 : 0);
-    // the lane (of the warp) with the partners of this lane's elements
-    const int step = a.rot_dim / 16;
-    const int mate = (threadIdx.x & 31) + (PAIRS == kPairsHalves && live ? (e0 < a.rot_dim / 2 ? step : -step) : 0);
     const uint32_t item = blockIdx.x * (uint32_t)(kRopeThreads / LANES) + threadIdx.x / LANES;
     const bool valid = item < p.items;
     const int token = valid ? (int)(item / p.groups) : 0;
-    const int r0 = valid ? (int)(item % p.groups) * p.rows_per_group : 0;
-    const int r1 = valid ? min(r0 + p.rows_per_group, p.rows) : 0;
+    const uint32_t part = valid ? item % p.groups : 0;
+    const RowKind kind = part < p.q_groups ? kQueries : (part < p.q_groups + p.k_groups ? kKeys : kValues);
+    const int h0 = (int)(part - (kind == kQueries ? 0 : p.q_groups + (kind == kKeys ? 0 : p.k_groups))) * p.rows_per_group;
+    const int rows = valid && me.act ? min(p.rows_per_group, (kind == kQueries ? a.heads : a.kv_heads) - h0) : 0;
 
-    float c[8], s[8];
-    load_turn<PAIRS>(a, token, e0, live, 1.f, c, s);
-    uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-    const bool has_wq = a.norm && a.q_weight, has_wk = a.norm && a.k_weight;
-    if (has_wq && act) wq = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q_weight) + e0);
-    if (has_wk && act) wk = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.k_weight) + e0);
-    const float inv_d = 1.f / (float)a.head_dim;
-    bool stored = false;        // this token has a cache slot
-    int64_t k_at = 0, v_at = 0;
-    if (a.k_cache) {
-        const int slot = a.slots[token];
-        stored = slot >= 0 && slot < a.num_pages * a.page_size;
-        const int page = slot / a.page_size, place = slot % a.page_size;
-        k_at = page * a.k_page + place * a.k_place;
-        v_at = page * a.v_page + place * a.v_place;
+    const T* src;
+    int64_t src_step;
+    T* dst = nullptr;
+    int64_t dst_step = 0;
+    if (kind == kQueries) {
+        src = static_cast<const T*>(a.q) + token * a.q_token + h0 * a.q_head + e0;
+        src_step = a.q_head;
+        dst = static_cast<T*>(a.q_out) + token * a.q_out_token + h0 * a.q_out_head + e0;
+        dst_step = a.q_out_head;
+    } else if (kind == kKeys) {
+        src = static_cast<const T*>(a.k) + token * a.k_token + h0 * a.k_head + e0;
+        src_step = a.k_head;
+        if (a.k_out) {
+            dst = static_cast<T*>(a.k_out) + token * a.k_out_token + h0 * a.k_out_head + e0;
+            dst_step = a.k_out_head;
+        }
+    } else {
+        src = static_cast<const T*>(a.v) + token * a.v_token + h0 * a.v_head + e0;
+        src_step = a.v_head;
     }
-    const int H = a.heads, G = a.kv_heads;
+    // the cache rows of this token
     const bool fp8 = a.dtype_cache == GEMM_E4M3;
-
-    auto source = [&](int r) -> const T* {
-        if (r < H) return static_cast<const T*>(a.q) + token * a.q_token + r * a.q_head + e0;
-        if (r < H + G) return static_cast<const T*>(a.k) + token * a.k_token + (r - H) * a.k_head + e0;
-        return static_cast<const T*>(a.v) + token * a.v_token + (r - H - G) * a.v_head + e0;
-    };
-    auto append = [&](void* cache, int64_t at, float scale, const float (&y)[8]) {
+    uint8_t* slot_row = nullptr;
+    int64_t slot_step = 0;
+    float slot_scale = 1.f;
+    if (a.k_cache && kind != kQueries) {
+        const int slot = a.slots[token];
+        if (slot >= 0 && slot < a.num_pages * a.page_size) {
+            const int page = slot / a.page_size, place = slot % a.page_size;
+            const int es = fp8 ? 1 : 2;
+            const int64_t at = kind == kKeys ? page * a.k_page + place * a.k_place + h0 * a.k_chead
+                                             : page * a.v_page + place * a.v_place + h0 * a.v_chead;
+            slot_row = static_cast<uint8_t*>(kind == kKeys ? a.k_cache : a.v_cache) + (at + e0) * es;
+            slot_step = (kind == kKeys ? a.k_chead : a.v_chead) * es;
+            slot_scale = kind == kKeys ? a.k_scale : a.v_scale;
+        }
+    }
+    auto append = [&](const float (&y)[8]) {
         if (fp8) {
             uint2 w;
-            w.x = e4m3x4(__fdiv_rn(y[0], scale), __fdiv_rn(y[1], scale), __fdiv_rn(y[2], scale), __fdiv_rn(y[3], scale));
-            w.y = e4m3x4(__fdiv_rn(y[4], scale), __fdiv_rn(y[5], scale), __fdiv_rn(y[6], scale), __fdiv_rn(y[7], scale));
-            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + at + e0) = w;
+            w.x = e4m3x4(__fdiv_rn(y[0], slot_scale), __fdiv_rn(y[1], slot_scale), __fdiv_rn(y[2], slot_scale), __fdiv_rn(y[3], slot_scale));
+            w.y = e4m3x4(__fdiv_rn(y[4], slot_scale), __fdiv_rn(y[5], slot_scale), __fdiv_rn(y[6], slot_scale), __fdiv_rn(y[7], slot_scale));
+            *reinterpret_cast<uint2*>(slot_row) = w;
         } else {
-            *reinterpret_cast<uint4*>(static_cast<T*>(cache) + at + e0) = round8<T>(y);
+            *reinterpret_cast<uint4*>(slot_row) = round8<T>(y);
         }
     };
+    float own[8], other[8];
+    const T* weight = a.norm ? static_cast<const T*>(kind == kQueries ? a.q_weight : a.k_weight) : nullptr;
+    if (kind != kValues)
+        load_factors<T, PAIRS>(a, weight, token, e0, me.act, me.live, 1.f, own, other);
+    const float inv_d = 1.f / (float)a.head_dim;
     // every lane of a warp runs the same number of batches (the shuffles need them all)
     for (int b = 0; b < p.rows_per_group; b += kAhead) {
         uint4 raw[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int r = r0 + b + u;
             raw[u] = make_uint4(0, 0, 0, 0);
-            if (b + u < p.rows_per_group && r < r1 && act) raw[u] = load_row16(source(r));
+            if (b + u < rows) raw[u] = load_row16(src);
+            src += src_step;
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             if (b + u >= p.rows_per_group) break;
-            const int r = r0 + b + u;
-            const bool on = r < r1 && act;
-            float y[8];
-            unpack8<T>(raw[u], y);
-            if (r >= H + G) {
-                // values: copied (every lane of the group agrees on r; other groups of the warp may not)
-                if (on && stored) append(a.v_cache, v_at + (r - H - G) * a.v_chead, a.v_scale, y);
+            const bool on = b + u < rows;
+            float x[8];
+            unpack8<T>(raw[u], x);
+            if (__all_sync(0xffffffffu, kind == kValues)) {      // a warp of values: copied
+                if (on && slot_row) append(x);
+                if (slot_row) slot_row += slot_step;
+                continue;
             }
-            const bool is_q = r < H;
+            float inv = 1.f;
             if (a.norm) {
                 float sum = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum = fmaf(y[i], y[i], sum);
-                sum = group_sum<LANES>(sum);
-                const float inv = rsqrtf(fmaf(sum, inv_d, a.eps));
+                for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] *= inv;
-                if (is_q ? has_wq : has_wk) {
-                    float w[8];
-                    unpack8<T>(is_q ? wq : wk, w);
+                for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                inv = rsqrtf(fmaf(sum, inv_d, a.eps));
+            }
+            float z[8];
+            partners<T, PAIRS>(a, e0, me.live, me.mate, srow, raw[u], x, z);
+            if (kind != kValues) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] *= w[i];
-                }
+                for (int i = 0; i < 8; ++i) x[i] = inv * fmaf(z[i], other[i], x[i] * own[i]);
             }
-            turn<PAIRS>(a, e0, live, mate, srow, c, s, y);
-            if (!on || r >= H + G) continue;
-            if (is_q) {
-                *reinterpret_cast<uint4*>(static_cast<T*>(a.q_out) + token * a.q_out_token + r * a.q_out_head + e0) = round8<T>(y);
-            } else {
-                const int h = r - H;
-                if (a.k_out)
-                    *reinterpret_cast<uint4*>(static_cast<T*>(a.k_out) + token * a.k_out_token + h * a.k_out_head + e0) = round8<T>(y);
-                if (stored) append(a.k_cache, k_at + h * a.k_chead, a.k_scale, y);
+            if (on) {
+                if (dst) *reinterpret_cast<uint4*>(dst) = round8<T>(x);
+                if (slot_row) append(x);
             }
+            if (dst) dst += dst_step;
+            if (slot_row) slot_row += slot_step;
         }
     }
 }
 
 // Backward: with g the incoming gradient turned back, n = x r, r = rsqrt(mean x^2 + eps):
-//   dweight = sum g n,   dx = r (g w - n mean(g w n)).
-// The two row sums (x^2 and g w x; mean(g w n) = r mean(g w x)) are reduced side by side.  A lane group walks items of
-// the whole grid and keeps its share of both weight gradients in registers; the block adds its groups' in a fixed order
-// and leaves one partial per block for weight_grad_kernel.
+//   dweight = sum g n,   dx = r (g w - n mean(g w n)) = r (g w - x k),  k = r^2 mean(g w x).
+// The two row sums (x^2 and g w x) are reduced side by side.  A block takes queries or keys only, so that one weight and
+// one weight gradient stay in registers while its lane groups walk the tokens; it adds its groups' gradients in a fixed
+// order and leaves one partial for weight_grad_kernel.
 template <typename T, int LANES, int PAIRS>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_backward_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 3) norm_rope_backward_kernel(const __grid_constant__ RopeParams p) {
     constexpr int kAhead = 2;
     __shared__ float scratch[PAIRS == kPairsAny ? (kRopeThreads / LANES) * LANES * 8 : 1];
-    __shared__ float sums[kRopeThreads / 32][2][LANES * 8];
+    __shared__ float sums[kRopeThreads / 32][LANES * 8];
     griddep_wait();
     griddep_launch_dependents();
     const qk_norm_rope_args_t& a = p.a;
     const qk_norm_rope_grads_t& gr = p.g;
-    const int l = threadIdx.x % LANES;
-    const int e0 = l * 8;
-    const bool act = e0 < a.head_dim;
-    const bool live = act && e0 < a.rot_dim;
+    const RowLane<LANES, PAIRS> me(a);
+    const int e0 = me.e0;
     float* srow = scratch + (PAIRS == kPairsAny ? (threadIdx.x / LANES) * LANES * 8 : 0);
-    const int step = a.rot_dim / 16;
-    const int mate = (threadIdx.x & 31) + (PAIRS == kPairsHalves && live ? (e0 < a.rot_dim / 2 ? step : -step) : 0);
-    uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-    const bool has_wq = a.norm && a.q_weight, has_wk = a.norm && a.k_weight;
-    if (has_wq && act) wq = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q_weight) + e0);
-    if (has_wk && act) wk = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.k_weight) + e0);
+    const bool is_q = blockIdx.x < p.q_blocks;
+    const uint32_t block = is_q ? blockIdx.x : blockIdx.x - p.q_blocks, blocks = is_q ? p.q_blocks : gridDim.x - p.q_blocks;
+    const uint32_t groups = is_q ? p.q_groups : p.k_groups;
+    const uint32_t items = (uint32_t)a.tokens * groups;
+    const int heads = is_q ? a.heads : a.kv_heads;
+    const T* x_base = static_cast<const T*>(is_q ? a.q : a.k) + e0;
+    const T* g_base = static_cast<const T*>(is_q ? gr.dq_out : gr.dk_out) + e0;
+    T* d_base = static_cast<T*>(is_q ? gr.dq : gr.dk) + e0;
+    const int64_t x_token = is_q ? a.q_token : a.k_token, x_head = is_q ? a.q_head : a.k_head;
+    const int64_t g_token = is_q ? gr.dq_out_token : gr.dk_out_token, g_head = is_q ? gr.dq_out_head : gr.dk_out_head;
+    const int64_t d_token = is_q ? gr.dq_token : gr.dk_token, d_head = is_q ? gr.dq_head : gr.dk_head;
+    const T* weight = a.norm ? static_cast<const T*>(is_q ? a.q_weight : a.k_weight) : nullptr;
+    float w[8], dw[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        w[i] = 1.f;
+        dw[i] = 0.f;
+    }
+    if (weight && me.act) unpack8<T>(*reinterpret_cast<const uint4*>(weight + e0), w);
     const float inv_d = 1.f / (float)a.head_dim;
-    const int H = a.heads;
-    float dwq[8] = {}, dwk[8] = {};
 
-    const uint32_t groups_grid = gridDim.x * (uint32_t)(kRopeThreads / LANES);
-    const uint32_t first = blockIdx.x * (uint32_t)(kRopeThreads / LANES) + threadIdx.x / LANES;
-    const uint32_t warp_first = blockIdx.x * (uint32_t)(kRopeThreads / LANES) + (threadIdx.x & ~31) / LANES;
+    const uint32_t step = blocks * (uint32_t)(kRopeThreads / LANES);
+    const uint32_t warp_first = block * (uint32_t)(kRopeThreads / LANES) + (threadIdx.x & ~31) / LANES;
     // warp-uniform trip count: the warp's first group has the most items
-    for (uint32_t base = warp_first, item = first; base < p.items; base += groups_grid, item += groups_grid) {
-        const bool valid = item < p.items;
-        const int token = valid ? (int)(item / p.groups) : 0;
-        const int r0 = valid ? (int)(item % p.groups) * p.rows_per_group : 0;
-        const int r1 = valid ? min(r0 + p.rows_per_group, p.rows) : 0;
-        float c[8], s[8];
-        load_turn<PAIRS>(a, token, e0, live, -1.f, c, s);
+    for (uint32_t base = warp_first; base < items; base += step) {
+        const uint32_t item = base + (threadIdx.x & 31) / LANES;
+        const bool valid = item < items;
+        const int token = valid ? (int)(item / groups) : 0;
+        const int h0 = valid ? (int)(item % groups) * p.rows_per_group : 0;
+        const int rows = valid && me.act ? min(p.rows_per_group, heads - h0) : 0;
+        const T* xs = x_base + token * x_token + h0 * x_head;
+        const T* gs = g_base + token * g_token + h0 * g_head;
+        T* ds = d_base + token * d_token + h0 * d_head;
+        float own[8], other[8];
+        load_factors<T, PAIRS>(a, nullptr, token, e0, me.act, me.live, -1.f, own, other);
         for (int b = 0; b < p.rows_per_group; b += kAhead) {
             uint4 rx[kAhead], rg[kAhead];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                const int r = r0 + b + u;
                 rx[u] = rg[u] = make_uint4(0, 0, 0, 0);
-                if (b + u < p.rows_per_group && r < r1 && act) {
-                    const bool is_q = r < H;
-                    const int h = is_q ? r : r - H;
-                    rx[u] = load_row16(is_q ? static_cast<const T*>(a.q) + token * a.q_token + h * a.q_head + e0
-                                            : static_cast<const T*>(a.k) + token * a.k_token + h * a.k_head + e0);
-                    rg[u] = load_row16(is_q ? static_cast<const T*>(gr.dq_out) + token * gr.dq_out_token + h * gr.dq_out_head + e0
-                                            : static_cast<const T*>(gr.dk_out) + token * gr.dk_out_token + h * gr.dk_out_head + e0);
+                if (b + u < rows) {
+                    rx[u] = load_row16(xs);
+                    rg[u] = load_row16(gs);
                 }
+                xs += x_head;
+                gs += g_head;
             }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 if (b + u >= p.rows_per_group) break;
-                const int r = r0 + b + u;
-                const bool on = r < r1 && act, is_q = r < H;
-                const int h = is_q ? r : r - H;
-                float x[8], g[8];
-                unpack8<T>(rx[u], x);
+                float g[8], z[8];
                 unpack8<T>(rg[u], g);
-                turn<PAIRS>(a, e0, live, mate, srow, c, s, g);
+                partners<T, PAIRS>(a, e0, me.live, me.mate, srow, rg[u], g, z);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) g[i] = fmaf(z[i], other[i], g[i] * own[i]);
                 if (a.norm) {
-                    float gw[8];
-                    if (is_q ? has_wq : has_wk) {
-                        unpack8<T>(is_q ? wq : wk, gw);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) gw[i] *= g[i];
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) gw[i] = g[i];
-                    }
+                    float x[8];
+                    unpack8<T>(rx[u], x);
                     float sq = 0.f, dot = 0.f;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         sq = fmaf(x[i], x[i], sq);
-                        dot = fmaf(gw[i], x[i], dot);
+                        dot = fmaf(g[i] * w[i], x[i], dot);
                     }
 #pragma unroll
                     for (int o = LANES / 2; o > 0; o >>= 1) {
@@ -334,60 +374,49 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_backward_kernel(const 
                         dot += __shfl_xor_sync(0xffffffffu, dot, o);
                     }
                     const float inv = rsqrtf(fmaf(sq, inv_d, a.eps));
-                    const float k = inv * inv * dot * inv_d;     // r^2 mean(g w x): dx = r (g w - x k)
+                    const float k = inv * inv * dot * inv_d;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float gn = g[i] * (x[i] * inv);
-                        if (on) {
-                            if (is_q) dwq[i] += gn;
-                            else dwk[i] += gn;
-                        }
-                        g[i] = inv * fmaf(-x[i], k, gw[i]);
+                        dw[i] = fmaf(g[i] * inv, x[i], dw[i]);      // rows past the end hold zeros
+                        g[i] = inv * fmaf(-x[i], k, g[i] * w[i]);
                     }
                 }
-                if (!on) continue;
-                if (is_q) *reinterpret_cast<uint4*>(static_cast<T*>(gr.dq) + token * gr.dq_token + h * gr.dq_head + e0) = round8<T>(g);
-                else *reinterpret_cast<uint4*>(static_cast<T*>(gr.dk) + token * gr.dk_token + h * gr.dk_head + e0) = round8<T>(g);
+                if (b + u < rows) *reinterpret_cast<uint4*>(ds) = round8<T>(g);
+                ds += d_head;
             }
         }
     }
-    if (!p.partials) return;
+    if (!(is_q ? gr.dq_weight : gr.dk_weight)) return;
     // groups of a warp, then warps of the block, in a fixed order
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
 #pragma unroll
-        for (int o = LANES; o < 32; o <<= 1) {
-            dwq[i] += __shfl_xor_sync(0xffffffffu, dwq[i], o);
-            dwk[i] += __shfl_xor_sync(0xffffffffu, dwk[i], o);
-        }
-        if ((threadIdx.x & 31) < LANES) {
-            sums[threadIdx.x / 32][0][e0 + i] = dwq[i];
-            sums[threadIdx.x / 32][1][e0 + i] = dwk[i];
-        }
+        for (int o = LANES; o < 32; o <<= 1) dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], o);
+        if ((threadIdx.x & 31) < LANES) sums[threadIdx.x / 32][e0 + i] = dw[i];
     }
     __syncthreads();
-    for (int t = threadIdx.x; t < 2 * LANES * 8; t += kRopeThreads) {
-        const int which = t / (LANES * 8), e = t % (LANES * 8);
+    for (int e = threadIdx.x; e < LANES * 8; e += kRopeThreads) {
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < kRopeThreads / 32; ++w) v += sums[w][which][e];
-        p.partials[((size_t)blockIdx.x * 2 + which) * kMaxHeadDim + e] = v;
+        for (int i = 0; i < kRopeThreads / 32; ++i) v += sums[i][e];
+        p.partials[(size_t)blockIdx.x * kMaxHeadDim + e] = v;
     }
 }
 
-// dq_weight / dk_weight = the blocks' partials, added in a fixed order: 32 columns per block, 32 strips of partials.
-__global__ void __launch_bounds__(1024) weight_grad_kernel(const float* partials, int blocks, int head_dim,
+// dq_weight / dk_weight = the partials of the blocks of queries / keys, added in a fixed order: 32 columns per block of
+// this kernel, 32 strips of partials.
+__global__ void __launch_bounds__(1024) weight_grad_kernel(const float* partials, int q_blocks, int blocks, int head_dim,
                                                            float* dq_weight, float* dk_weight) {
     __shared__ float strip[32][33];
     griddep_wait();
     griddep_launch_dependents();
     const int col = threadIdx.x & 31, s = threadIdx.x >> 5;
-    const int which = blockIdx.y;
-    float* out = which ? dk_weight : dq_weight;
+    const bool keys = blockIdx.y == 1;
+    float* out = keys ? dk_weight : dq_weight;
     const int e = blockIdx.x * 32 + col;
     float v = 0.f;
     if (out && e < head_dim)
-        for (int b = s; b < blocks; b += 32) v += partials[((size_t)b * 2 + which) * kMaxHeadDim + e];
+        for (int b = (keys ? q_blocks : 0) + s; b < (keys ? blocks : q_blocks); b += 32) v += partials[(size_t)b * kMaxHeadDim + e];
     strip[s][col] = v;
     __syncthreads();
     if (s == 0 && out && e < head_dim) {
@@ -400,7 +429,7 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const float* partials
 
 namespace {
 
-constexpr int64_t kWorkspaceBytes = (int64_t)kBackwardMaxBlocks * 2 * kMaxHeadDim * sizeof(float);
+constexpr int64_t kWorkspaceBytes = (int64_t)kBackwardMaxBlocks * kMaxHeadDim * sizeof(float);
 
 gemm_status_t check_rope(const qk_norm_rope_args_t& a, bool forward) {
     if (a.tokens < 0 || a.heads < 0 || a.kv_heads < 0 || a.head_dim < 1 || a.rot_dim < 0 || a.rot_dim > a.head_dim || (a.rot_dim & 1))
@@ -458,12 +487,18 @@ cudaError_t with_kernel(const qk_norm_rope_args_t& a, F&& f) {
     return with_pairs<__half, 32>(pairs, f);
 }
 
-// Cut the rows of every token into lane groups of at most `per_group` rows.
-void cut_rows(RopeParams& p, int64_t per_group) {
-    per_group = std::min<int64_t>(std::max<int64_t>(per_group, 1), p.rows);
-    while ((int64_t)p.a.tokens * ((p.rows + per_group - 1) / per_group) > INT32_MAX - kRopeThreads) per_group *= 2;
-    p.rows_per_group = (int32_t)per_group;
-    p.groups = (uint32_t)((p.rows + per_group - 1) / per_group);
+// Cut the rows of every token into lane groups of at most `per_group` rows of one kind.
+void cut_rows(RopeParams& p, int64_t per_group, bool values) {
+    const int64_t most = std::max(p.a.heads, p.a.kv_heads);
+    per_group = std::min<int64_t>(std::max<int64_t>(per_group, 1), most);
+    for (;;) {
+        p.rows_per_group = (int32_t)per_group;
+        p.q_groups = (uint32_t)((p.a.heads + per_group - 1) / per_group);
+        p.k_groups = (uint32_t)((p.a.kv_heads + per_group - 1) / per_group);
+        p.groups = p.q_groups + p.k_groups * (values ? 2 : 1);
+        if ((int64_t)p.a.tokens * p.groups <= INT32_MAX - kRopeThreads || per_group >= most) break;
+        per_group *= 2;
+    }
     p.items = (uint32_t)p.a.tokens * p.groups;
 }
 
@@ -473,11 +508,11 @@ struct LaunchForward {
     int sms;
     template <typename T, int LANES, int PAIRS>
     cudaError_t operator()() {
-        // Few rows: one row per lane group, so that every SM gets some.  Many: up to twelve rows a group.
-        const int64_t total = (int64_t)p.a.tokens * p.rows;
-        const int64_t fill = (int64_t)sms * 2048 / LANES;
-        const int64_t want = total / std::max<int64_t>(fill, 1);
-        cut_rows(p, want < 2 ? 1 : (want < 4 ? 2 : std::min<int64_t>(12, want & ~int64_t(3))));
+        // Few rows: one row per lane group, so that every SM gets some.  Many: up to eight rows a group.
+        const bool values = p.a.k_cache != nullptr;
+        const int64_t total = (int64_t)p.a.tokens * (p.a.heads + p.a.kv_heads * (values ? 2 : 1));
+        const int64_t want = total / std::max<int64_t>((int64_t)sms * 2048 / LANES, 1);
+        cut_rows(p, want < 2 ? 1 : (want < 4 ? 2 : (want < 8 ? 4 : 8)), values);
         const int64_t blocks = ((int64_t)p.items * LANES + kRopeThreads - 1) / kRopeThreads;
         return launch_dependent(norm_rope_kernel<T, LANES, PAIRS>, dim3((unsigned)blocks), dim3(kRopeThreads), 0, stream, p);
     }
@@ -489,19 +524,27 @@ struct LaunchBackward {
     int sms;
     template <typename T, int LANES, int PAIRS>
     cudaError_t operator()() {
-        const int64_t total = (int64_t)p.a.tokens * p.rows;
-        const int64_t fill = (int64_t)sms * 2048 / LANES;
-        const int64_t want = total / std::max<int64_t>(fill, 1);
-        cut_rows(p, want < 2 ? 1 : (want < 4 ? 2 : 4));
-        const int64_t need = ((int64_t)p.items * LANES + kRopeThreads - 1) / kRopeThreads;
-        const int blocks = (int)std::min<int64_t>(need, std::min(sms * 4, kBackwardMaxBlocks));
+        const int64_t total = (int64_t)p.a.tokens * (p.a.heads + p.a.kv_heads);
+        const int64_t want = total / std::max<int64_t>((int64_t)sms * 1024 / LANES, 1);
+        cut_rows(p, want < 2 ? 1 : (want < 4 ? 2 : (want < 16 ? 4 : 8)), false);
+        // blocks in proportion to the rows, three to an SM at most
+        constexpr int64_t kPerBlock = kRopeThreads / LANES;
+        const int64_t most = std::min<int64_t>(3 * (int64_t)sms, kBackwardMaxBlocks);
+        const int64_t q_items = (int64_t)p.a.tokens * p.q_groups, k_items = (int64_t)p.a.tokens * p.k_groups;
+        int64_t q = (q_items + kPerBlock - 1) / kPerBlock, k = (k_items + kPerBlock - 1) / kPerBlock;
+        if (q + k > most) {
+            const int64_t share = most * p.a.heads / (p.a.heads + p.a.kv_heads);
+            q = std::min(q, q == 0 ? 0 : std::min(std::max<int64_t>(share, 1), most - (k ? 1 : 0)));
+            k = std::min(k, most - q);
+        }
+        p.q_blocks = (uint32_t)q;
         const bool weights = p.g.dq_weight || p.g.dk_weight;
-        p.partials = weights ? static_cast<float*>(p.g.workspace) : nullptr;
-        cudaError_t e = launch_dependent(norm_rope_backward_kernel<T, LANES, PAIRS>, dim3((unsigned)blocks), dim3(kRopeThreads), 0,
+        p.partials = static_cast<float*>(p.g.workspace);
+        cudaError_t e = launch_dependent(norm_rope_backward_kernel<T, LANES, PAIRS>, dim3((unsigned)(q + k)), dim3(kRopeThreads), 0,
                                          stream, p);
         if (e != cudaSuccess || !weights) return e;
         return launch_dependent(weight_grad_kernel, dim3((unsigned)((p.a.head_dim + 31) / 32), 2), dim3(1024), 0, stream,
-                                (const float*)p.partials, blocks, (int)p.a.head_dim, p.g.dq_weight, p.g.dk_weight);
+                                (const float*)p.partials, (int)q, (int)(q + k), (int)p.a.head_dim, p.g.dq_weight, p.g.dk_weight);
     }
 };
 
@@ -522,7 +565,6 @@ gemm_status_t qk_norm_rope_run(const qk_norm_rope_args_t* args, gemm_stream_t st
     RopeParams p{};
     p.a = *args;
     if (p.a.kv_heads == 0) p.a.k_cache = p.a.v_cache = nullptr;
-    p.rows = p.a.heads + p.a.kv_heads * (p.a.k_cache ? 2 : 1);
     return status_of(with_kernel(p.a, LaunchForward{p, reinterpret_cast<cudaStream_t>(stream), dev.sms}));
 }
 
@@ -552,7 +594,6 @@ gemm_status_t qk_norm_rope_backward(const qk_norm_rope_args_t* args, const qk_no
     RopeParams p{};
     p.a = *args;
     p.g = g;
-    p.rows = p.a.heads + p.a.kv_heads;
     return status_of(with_kernel(p.a, LaunchBackward{p, st, dev.sms}));
 }
 
