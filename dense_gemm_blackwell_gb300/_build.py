@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libdgb_gemm.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["kernels_single.cu", "kernels_persistent.cu", "kernels_fp8.cu", "kernels_mx.cu", "gemm_api.cu",
-           "schedule_model.cu", "lora.cu", "qk_norm_rope.cu", "paged_attn_api.cu", "paged_attn_bf16.cu", "paged_attn_f16.cu",
+           "schedule_model.cu", "lora.cu", "lora_skinny.cu", "qk_norm_rope.cu", "paged_attn_api.cu", "paged_attn_bf16.cu", "paged_attn_f16.cu",
            "paged_attn_bf16_e4m3.cu", "paged_attn_f16_e4m3.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

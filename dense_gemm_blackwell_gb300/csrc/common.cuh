@@ -150,16 +150,16 @@ struct PersistentParams {
 // that adapter's B.  counts and ids are written by the kernel that computes T,
 // which this launch follows.
 struct LoraTail {
-    CUtensorMap tmap_t;       // T: (columns, tile rows, [m block][slot]), box (16, 128, 1)
-    CUtensorMap tmap_b;       // B: (rank, N, adapter), box (16, tile_n / cta_group, 1)
+    CUtensorMap tmap_t;       // T: (slots x columns, tile rows, m block), box (64, 128, 1), 128-byte swizzle
+    CUtensorMap tmap_b;       // B: (rank, N, adapter), box (16, tile_n / cta_group, 1), 32-byte swizzle
     const int32_t* counts;    // [m block]: adapters among the block's rows
     const int32_t* ids;       // [m block][slot]: which
     int32_t max_adapters;     // slots per m block
     int32_t steps;            // K = 16 steps per adapter
     int32_t b_steps;          // of which this many cover B's columns (steps = b_steps, or twice that for two-term T)
 };
-constexpr uint32_t kTailRowBytes = 32;           // one row of one step's operand
-constexpr uint32_t kTailStepBytesA = 128 * kTailRowBytes;
+constexpr uint32_t kTailRowBytes = 32;           // one row of one step's B
+constexpr uint32_t kTailAtomBytes = 128 * 128;   // four steps of T: 128 rows of one 128-byte atom
 
 // The epoch of this launch: one past the last completed one (never 0, the
 // flags' initial value).  A CTA reads the same value whenever it asks before

@@ -867,16 +867,24 @@ gemm_status_t product_params(gemm_plan_t plan, const void* A, const void* B, voi
     return persistent_params(plan, A, B, D, out);
 }
 
-gemm_status_t encode_steps_map(CUtensorMap* m, int dtype, const void* base, int64_t cols, int64_t rows, int64_t count, int64_t ld,
-                               int64_t stride, int box_rows) {
+gemm_status_t encode_rows_map(CUtensorMap* m, int dtype, const void* base, int64_t k, int64_t rows, int64_t ld, int box_rows) {
+    if (encode_map(m, dtype, base, k, rows, ld, 1, 0, 64, box_rows)) return GEMM_OK;
+    g_last_cuda_error = (int)cudaErrorInvalidValue;
+    return GEMM_ERR_CUDA;
+}
+
+gemm_device_error_t* device_record(gemm_plan_t plan) { return plan->status; }
+
+gemm_status_t encode_matrices_map(CUtensorMap* m, int dtype, const void* base, int64_t cols, int64_t rows, int64_t count, int64_t ld,
+                                  int64_t stride, int row_bytes, int box_rows) {
     EncodeTiledFn enc = get_encode_fn();
     const int eb = elem_bytes(dtype);
     cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)count};
     cuuint64_t strides[2] = {(cuuint64_t)(ld * eb), (cuuint64_t)(stride * eb)};
-    cuuint32_t box[3] = {(cuuint32_t)(32 / eb), (cuuint32_t)box_rows, 1};
+    cuuint32_t box[3] = {(cuuint32_t)(row_bytes / eb), (cuuint32_t)box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     if (!enc || enc(m, tma_dtype(dtype), 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                    row_bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
         g_last_cuda_error = (int)cudaErrorInvalidValue;
         return GEMM_ERR_CUDA;

@@ -244,11 +244,12 @@ __device__ __forceinline__ void mma_issuer(const PersistentParams& p, uint8_t* r
                     if (issuer) {
                         tc_fence_after();
                         const uint32_t sa = smem_u32(ring + (size_t)stage * stage_bytes);
-                        const uint64_t da = smem_desc_sw32(sa), db = smem_desc_sw32(sa + p.stage_bytes_a);
+                        const uint64_t da = smem_desc_sw128(sa), db = smem_desc_sw32(sa + p.stage_bytes_a);
                         const int n16 = min(4 * ATOMS, total - s0);
                         const uint64_t step_b = (uint64_t)(p.tile_n / CG) * kTailRowBytes / 16u;
                         for (int j = 0; j < n16; ++j)
-                            mma_f16<CG>(d_tmem, da + (uint64_t)j * (kTailStepBytesA / 16u), db + j * step_b, p.idesc, 1u);
+                            mma_f16<CG>(d_tmem, da + (uint64_t)(j / 4) * (kTailAtomBytes / 16u) + 2u * (j % 4), db + j * step_b,
+                                        p.idesc, 1u);
                         commit_to<CG>(empty(stage));
                     }
                     __syncwarp();

@@ -25,9 +25,16 @@ cudaError_t launch_adapters(const PersistentParams& p, const LoraTail& tail, int
 gemm_status_t product_params(gemm_plan_t plan, const void* A, const void* B, void* D, PersistentParams* out);
 
 // Tensor map of `count` row-major (rows x cols) matrices of 16-bit elements, `ld` elements between rows and `stride` between
-// matrices; box (16, box_rows, 1), 32-byte swizzle (gemm_api.cu).
-gemm_status_t encode_steps_map(CUtensorMap* m, int dtype, const void* base, int64_t cols, int64_t rows, int64_t count, int64_t ld,
-                               int64_t stride, int box_rows);
+// matrices; box (row_bytes / 2, box_rows, 1) with a swizzle of row_bytes, 32 or 128 (gemm_api.cu).
+gemm_status_t encode_matrices_map(CUtensorMap* m, int dtype, const void* base, int64_t cols, int64_t rows, int64_t count, int64_t ld,
+                                  int64_t stride, int row_bytes, int box_rows);
+
+// Tensor map of a K-major 16-bit matrix (rows x K, `ld` elements between rows): box (64, box_rows), 128-byte swizzle
+// (gemm_api.cu).
+gemm_status_t encode_rows_map(CUtensorMap* m, int dtype, const void* base, int64_t k, int64_t rows, int64_t ld, int box_rows);
+
+// A plan's device error record (gemm_api.cu).
+gemm_device_error_t* device_record(gemm_plan_t plan);
 
 // How many clusters of `cta_group` CTAs with `smem_bytes` of dynamic shared
 // memory can be resident at once (0 if the query fails).

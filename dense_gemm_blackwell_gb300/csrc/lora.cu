@@ -1,24 +1,29 @@
 // lora.cu -- low-rank adapters of many requests beside a shared projection
 // (include/serving.h): Y[m] = X[m] W^T + s_i (X[m] A_i^T) B_i^T, i = adapter[m].
 //
-// Two launches.  shrink_kernel computes T = s_i X A_i^T for every token's own
-// adapter and lays it out per (m block of the product, adapter that occurs in
-// it): a [tile rows x rank] matrix whose rows of other adapters are zero.  The
-// product's persistent kernel then appends, after a tile's K blocks, one run
-// of K = 16 matrix instructions per such adapter, T times B_i, into the same
-// fp32 accumulator in tensor memory: Y is written once and rounded once, and
-// the adapters cost rank / k of the projection's matrix work per adapter in a
-// tile instead of a pass over Y.  The product's launch overlaps shrink_kernel;
-// only the appended steps wait for it (programmatic dependent launch).
+// Two launches.  A first kernel computes T = s_i X A_i^T for every token's own
+// adapter and lays it out per m block of the product: [tile rows][slot][rank],
+// one slot for each adapter that occurs among the block's rows, rows of other
+// adapters zero.  The product's persistent kernel then appends, after a tile's
+// K blocks, one run of K = 16 matrix instructions per slot, T times that
+// adapter's B, into the same fp32 accumulator in tensor memory: Y is written
+// once and rounded once, and the adapters cost rank / k of the projection's
+// matrix work per adapter in a tile instead of a pass over Y.  The product's
+// launch overlaps the first kernel; only the appended steps wait for it
+// (programmatic dependent launch).
 //
-// shrink_kernel: one CTA per (64 rows, range of adapters, range of K).  A row
-// is loaded only for its own adapter (rows of others become zeros in shared
-// memory, which also makes their T zero), so a decode batch with an adapter
-// per token reads every X row and every A_i once, and a prompt of one request
-// streams X once.  The CTAs of a cluster split K; their fp32 sums are added
-// through distributed shared memory in rank order, scaled, rounded to the
-// input type (the tensor core multiplies 16-bit operands; fp32 outputs carry T
-// as two such terms) and stored.
+// T is rounded to the input type before its product (the tensor core
+// multiplies 16-bit operands); fp32 outputs carry it as two such terms.  Its
+// sums are fp32, added in a fixed order.
+//
+// Two forms of the first kernel:
+//   gather_kernel, up to kGatherTokens tokens (decode batches, each adapter
+//   with few rows): one CTA per 16 rows of one adapter; they are gathered, and
+//   four warps split K, each with its own copy pipeline;
+//   stream_kernel, above that (prompts, long runs of one adapter): one CTA per
+//   (64 rows, range of slots, range of K); a row is loaded only for its own
+//   adapter (others are zeros in shared memory), the CTAs of a cluster split K
+//   and add their sums through distributed shared memory.
 #include <algorithm>
 #include <cstring>
 #include <new>
@@ -28,6 +33,8 @@
 #include "common.cuh"
 #include "elem.cuh"
 #include "launch.h"
+#include "lora_list.cuh"
+#include "lora_skinny.h"
 #include "serving.h"
 #include "serving_host.h"
 
@@ -35,8 +42,7 @@ namespace dgb {
 
 constexpr int kShrinkThreads = 128;
 constexpr int kShrinkRows = 64;              // tokens of one CTA, 16 per warp
-constexpr int kMaxAdapters = 4096;           // one bit each in shared memory
-constexpr int kMaxTileRows = 256;
+constexpr int kGatherTokens = 256;
 
 struct ShrinkParams {
     lora_args_t a;
@@ -45,7 +51,8 @@ struct ShrinkParams {
     int32_t tile_rows;        // rows of one m block of the product: 128 or 256
     int32_t max_adapters;     // slots per m block
     int32_t rank16;           // rank rounded up to 16
-    int32_t cols;             // columns of T: rank16, or 2 rank16 (two terms)
+    int32_t cols;             // columns of T per slot: rank16, or 2 rank16 (two terms)
+    int32_t pitch;            // elements between rows of T: max_adapters * cols
     int32_t chunks_per_cta;   // 64-element chunks of K per CTA of the cluster
     void* t;
     int32_t* counts;
@@ -53,7 +60,7 @@ struct ShrinkParams {
 };
 
 template <int NT>
-struct ShrinkShape {
+struct StreamShape {
     static constexpr int kStages = NT > 16 ? 3 : 4;
     static constexpr int kStageBytes = (kShrinkRows + NT * 8) * 128;
     static constexpr int kSumPitch = NT * 8 + 4;      // floats
@@ -66,15 +73,199 @@ __device__ __forceinline__ float4 load_cluster_f4(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ void publish_adapters(const ShrinkParams& p, int tile, const AdapterList& l, int count) {
+    if (threadIdx.x == 0) p.counts[tile] = count;
+    for (int i = threadIdx.x; i < count; i += kShrinkThreads) p.ids[(size_t)tile * p.max_adapters + i] = l.list[i];
+}
+
+// Eight scaled sums as T's row piece: one term, or for fp32 outputs the rounded value and what the rounding left.
+template <typename T>
+__device__ __forceinline__ void store_t(const ShrinkParams& p, T* at, float (&v)[8], float scale) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= scale;
+    const uint4 first = round8<T>(v);
+    *reinterpret_cast<uint4*>(at) = first;
+    if (p.cols > p.rank16) {
+        float back[8];
+        unpack8<T>(first, back);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] -= back[j];
+        *reinterpret_cast<uint4*>(at + p.rank16) = round8<T>(v);
+    }
+}
+
 // NT: 8-column tiles of the rank held (rank <= 8 NT)
+template <int NT>
+struct GatherShape {
+    // up to rank 32 a CTA leaves room on its SM for one of the product that follows (lora_skinny.cu)
+    static constexpr int kStages = NT <= 2 ? 4 : (NT <= 4 ? 3 : (NT <= 8 ? 4 : 2));
+    static constexpr int kStageBytes = (16 + NT * 8) * 128;      // one warp: 16 rows of X, the adapter's rows
+    static constexpr int kSumPitch = NT * 8 + 4;
+    static constexpr int kSmemBytes = 4 * kStages * kStageBytes + 4 * 16 * kSumPitch * 4;
+};
+
 template <typename T, int NT>
-__global__ void __launch_bounds__(kShrinkThreads) shrink_kernel(const __grid_constant__ ShrinkParams p) {
-    using S = ShrinkShape<NT>;
+__global__ void __launch_bounds__(kShrinkThreads) gather_kernel(const __grid_constant__ ShrinkParams p) {
+    using S = GatherShape<NT>;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint32_t bits[kMaxAdapters / 32];
-    __shared__ int32_t list[kMaxTileRows];
+    __shared__ AdapterList adapters;
+    __shared__ int32_t row_ids[kMaxTileRows];
+    __shared__ int32_t taken[kMaxTileRows];      // rows of each slot
+    __shared__ int32_t rows[16];
+    __shared__ int32_t my_slot, my_group;
+    float* sums = reinterpret_cast<float*>(smem + 4 * S::kStages * S::kStageBytes);
+
+    griddep_wait();
+    griddep_launch_dependents();
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tile = blockIdx.y;
+    for (int i = threadIdx.x; i < kMaxTileRows; i += kShrinkThreads) taken[i] = 0;
+    const int count = find_adapters(p.a.adapter, p.adapters, p.M, tile * p.tile_rows, p.tile_rows, adapters, row_ids, 0, p.tile_rows,
+                                    threadIdx.x, kShrinkThreads, [] { __syncthreads(); });
+    if (blockIdx.x == 0) publish_adapters(p, tile, adapters, count);
+    // The work items are the groups of 16 rows of one slot, slot after slot; this CTA takes the blockIdx.x-th.
+    for (int i = threadIdx.x; i < p.tile_rows; i += kShrinkThreads) {
+        const int id = row_ids[i];
+        if (id < 0) continue;
+        int lo = 0, hi = count - 1;              // its slot: the list ascends
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (adapters.list[mid] < id) lo = mid + 1; else hi = mid;
+        }
+        atomicAdd(&taken[lo], 1);
+    }
+    if (threadIdx.x == 0) my_slot = -1;
+    __syncthreads();
+    if (warp == 0) {
+        int before = 0;
+        for (int base = 0; base < count; base += 32) {
+            const int groups = base + lane < count ? (taken[base + lane] + 15) / 16 : 0;
+            int at = groups;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int t = __shfl_up_sync(0xffffffffu, at, o);
+                if (lane >= o) at += t;
+            }
+            const int all = __shfl_sync(0xffffffffu, at, 31);
+            const int mine = (int)blockIdx.x - before - (at - groups);
+            if (mine >= 0 && mine < groups) {
+                my_slot = base + lane;
+                my_group = mine;
+            }
+            before += all;
+        }
+    }
+    __syncthreads();
+    const int slot = my_slot;
+    if (slot < 0) return;
+    const int id = adapters.list[slot], r0 = my_group * 16;
+    T* dst = static_cast<T*>(p.t) + (size_t)tile * p.tile_rows * p.pitch + slot * p.cols;
+    if (warp == 0) {
+        // the group's rows: the r0-th to (r0 + 15)-th of the slot's
+        int n = 0;
+        for (int base = 0; base < p.tile_rows; base += 32) {
+            const bool mine = row_ids[base + lane] == id;
+            const uint32_t b = __ballot_sync(0xffffffffu, mine);
+            const int at = n + __popc(b & ((1u << lane) - 1u)) - r0;
+            if (mine && at >= 0 && at < 16) rows[at] = base + lane;
+            n += __popc(b);
+        }
+    }
+    if (my_group == 0) {
+        // zeros in the other rows (those of tokens that exist)
+        const int live = min(p.tile_rows, p.M - tile * p.tile_rows), pieces = p.cols / 8;
+        for (int i = threadIdx.x; i < live * pieces; i += kShrinkThreads) {
+            const int r = i / pieces;
+            if (row_ids[r] != id) *reinterpret_cast<uint4*>(dst + (size_t)r * p.pitch + (i - r * pieces) * 8) = make_uint4(0, 0, 0, 0);
+        }
+    }
+    __syncthreads();
+    const int n = min(16, taken[slot] - r0);
+    const float scale = p.a.scale ? p.a.scale[id] : 1.f;
+
+    // this warp's chunks of 64 elements of K
+    const int chunks = (p.K + 63) / 64;
+    const int c_begin = chunks * warp / 4, c_end = chunks * (warp + 1) / 4;
+    const uint32_t ring = smem_u32(smem) + warp * S::kStages * S::kStageBytes;
+    const T* X = static_cast<const T*>(p.a.x) + (int64_t)tile * p.tile_rows * p.ldx;
+    const T* A = static_cast<const T*>(p.a.a) + id * p.a.stride_a;
+    const int cc = lane & 7;
+    auto load = [&](int chunk, int stage) {
+        const uint32_t sx = ring + stage * S::kStageBytes, sa = sx + 16 * 128;
+        const int k = chunk * 64 + cc * 8;
+        const uint32_t bytes = (uint32_t)min(max(p.K - k, 0), 8) * 2u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = (lane >> 3) + 4 * i;
+            const bool in = bytes && r < n;
+            cp_async_16_zfill(sx + r * 128 + ((cc ^ (r & 7)) << 4), in ? X + (int64_t)rows[r] * p.ldx + k : X, in ? bytes : 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < NT * 2; ++i) {
+            const int r = (lane >> 3) + 4 * i;
+            const bool in = bytes && r < p.rank;
+            cp_async_16_zfill(sa + r * 128 + ((cc ^ (r & 7)) << 4), in ? A + (int64_t)r * p.a.lda + k : A, in ? bytes : 0u);
+        }
+    };
+    float acc[NT][4] = {};
+    __syncwarp();
+#pragma unroll
+    for (int s = 0; s < S::kStages - 1; ++s) {
+        if (c_begin + s < c_end) load(c_begin + s, s);
+        cp_async_commit();
+    }
+    int stage = 0;
+    for (int ch = c_begin; ch < c_end; ++ch) {
+        cp_async_wait<S::kStages - 2>();
+        __syncwarp();
+        if (ch + S::kStages - 1 < c_end) load(ch + S::kStages - 1, stage == 0 ? S::kStages - 1 : stage - 1);
+        cp_async_commit();
+        const uint32_t sx = ring + stage * S::kStageBytes, sa = sx + 16 * 128;
+        const int xr = lane & 15, ar = (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            uint32_t x[4];
+            ldmatrix_x4(sx + xr * 128 + (((kk * 2 + (lane >> 4)) ^ (xr & 7)) << 4), x);
+#pragma unroll
+            for (int t = 0; t < NT; t += 2) {
+                uint32_t b[4];
+                ldmatrix_x4(sa + (t * 8 + ar) * 128 + (((kk * 2 + ((lane >> 3) & 1)) ^ (ar & 7)) << 4), b);
+                mma_16816<T>(acc[t], x, b[0], b[1]);
+                mma_16816<T>(acc[t + 1], x, b[2], b[3]);
+            }
+        }
+        if (++stage == S::kStages) stage = 0;
+    }
+    cp_async_wait<0>();
+    float* own = sums + warp * 16 * S::kSumPitch;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int r = lane >> 2, c = t * 8 + (lane & 3) * 2;
+        *reinterpret_cast<float2*>(own + r * S::kSumPitch + c) = make_float2(acc[t][0], acc[t][1]);
+        *reinterpret_cast<float2*>(own + (r + 8) * S::kSumPitch + c) = make_float2(acc[t][2], acc[t][3]);
+    }
+    __syncthreads();
+    const int groups = p.rank16 / 8;
+    for (int i = threadIdx.x; i < n * groups; i += kShrinkThreads) {
+        const int r = i / groups, c = (i - r * groups) * 8;
+        float v[8] = {};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float* from = sums + (w * 16 + r) * S::kSumPitch + c;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += from[j];
+        }
+        store_t<T>(p, dst + (size_t)rows[r] * p.pitch + c, v, scale);
+    }
+}
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(kShrinkThreads) stream_kernel(const __grid_constant__ ShrinkParams p) {
+    using S = StreamShape<NT>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ AdapterList adapters;
     __shared__ int32_t row_id[kShrinkRows];
-    __shared__ int32_t found;
     float* sums = reinterpret_cast<float*>(smem + S::kStages * S::kStageBytes);
 
     griddep_wait();
@@ -83,42 +274,10 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_kernel(const __grid_con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ks = blockIdx.x, num_ks = gridDim.x;            // cluster rank and size: ranges of K
     const int row0 = blockIdx.z * kShrinkRows;
-    const int tile = row0 / p.tile_rows;
-
-    // The adapters of this m block, in ascending order.
-    for (int i = threadIdx.x; i < kMaxAdapters / 32; i += kShrinkThreads) bits[i] = 0u;
-    __syncthreads();
-    for (int i = threadIdx.x; i < p.tile_rows; i += kShrinkThreads) {
-        const int m = tile * p.tile_rows + i;
-        const int id = m < p.M ? p.a.adapter[m] : -1;
-        const bool valid = id >= 0 && id < p.adapters;
-        if (valid) atomicOr(&bits[id >> 5], 1u << (id & 31));
-        if (m >= row0 && m < row0 + kShrinkRows) row_id[m - row0] = valid ? id : -1;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        constexpr int kWords = kMaxAdapters / 32 / 32;        // words per lane
-        int n = 0;
-#pragma unroll
-        for (int w = 0; w < kWords; ++w) n += __popc(bits[lane * kWords + w]);
-        int at = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int t = __shfl_up_sync(0xffffffffu, at, o);
-            if (lane >= o) at += t;
-        }
-        if (lane == 31) found = at;
-        at -= n;
-#pragma unroll
-        for (int w = 0; w < kWords; ++w)
-            for (uint32_t word = bits[lane * kWords + w]; word; word &= word - 1) list[at++] = (lane * kWords + w) * 32 + __ffs(word) - 1;
-    }
-    __syncthreads();
-    const int count = found;
-    if (ks == 0 && blockIdx.y == 0 && row0 % p.tile_rows == 0) {
-        if (threadIdx.x == 0) p.counts[tile] = count;
-        for (int i = threadIdx.x; i < count; i += kShrinkThreads) p.ids[(size_t)tile * p.max_adapters + i] = list[i];
-    }
+    const int tile = row0 / p.tile_rows, in_tile = row0 % p.tile_rows;
+    const int count = find_adapters(p.a.adapter, p.adapters, p.M, tile * p.tile_rows, p.tile_rows, adapters, row_id, in_tile, kShrinkRows,
+                                    threadIdx.x, kShrinkThreads, [] { __syncthreads(); });
+    if (ks == 0 && blockIdx.y == 0 && in_tile == 0) publish_adapters(p, tile, adapters, count);
 
     const int chunks = (p.K + 63) / 64;
     const int c_begin = min(ks * p.chunks_per_cta, chunks), c_end = min(c_begin + p.chunks_per_cta, chunks);
@@ -127,14 +286,16 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_kernel(const __grid_con
     const T* A = static_cast<const T*>(p.a.a);
 
     for (int slot = blockIdx.y; slot < count; slot += gridDim.y) {
-        const int id = list[slot];
-        T* dst = static_cast<T*>(p.t) + (((size_t)tile * p.max_adapters + slot) * p.tile_rows + row0 % p.tile_rows) * p.cols;
+        const int id = adapters.list[slot];
+        T* dst = static_cast<T*>(p.t) + ((size_t)tile * p.tile_rows + in_tile) * p.pitch + slot * p.cols;
         const bool here = __syncthreads_or(threadIdx.x < kShrinkRows && row_id[threadIdx.x] == id);
         if (!here) {
             // none of these rows: zeros, shared by the cluster's CTAs
-            uint4* z = reinterpret_cast<uint4*>(dst);
-            const int n = kShrinkRows * p.cols / 8;
-            for (int i = ks * kShrinkThreads + threadIdx.x; i < n; i += num_ks * kShrinkThreads) z[i] = make_uint4(0, 0, 0, 0);
+            const int pieces = p.cols / 8;
+            for (int i = ks * kShrinkThreads + threadIdx.x; i < kShrinkRows * pieces; i += num_ks * kShrinkThreads) {
+                const int r = i / pieces;
+                *reinterpret_cast<uint4*>(dst + (size_t)r * p.pitch + (i - r * pieces) * 8) = make_uint4(0, 0, 0, 0);
+            }
             continue;
         }
         const bool warp_here = __any_sync(0xffffffffu, lane < 16 && row_id[warp * 16 + (lane & 15)] == id);
@@ -213,32 +374,22 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_kernel(const __grid_con
                 v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
                 v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= scale;
-            const uint4 first = round8<T>(v);
-            *reinterpret_cast<uint4*>(dst + (size_t)r * p.cols + c) = first;
-            if (p.cols > p.rank16) {
-                float back[8];
-                unpack8<T>(first, back);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] -= back[j];
-                *reinterpret_cast<uint4*>(dst + (size_t)r * p.cols + p.rank16 + c) = round8<T>(v);
-            }
+            store_t<T>(p, dst + (size_t)r * p.pitch + c, v, scale);
         }
         cluster_sync();     // the sums are read; the next slot may overwrite them and the ring
     }
 }
 
 template <typename T, int NT>
-static cudaError_t launch_shrink_typed(const ShrinkParams& p, dim3 grid, cudaStream_t stream) {
-    auto kern = shrink_kernel<T, NT>;
+static cudaError_t launch_stream_typed(const ShrinkParams& p, dim3 grid, cudaStream_t stream) {
+    auto kern = stream_kernel<T, NT>;
     static std::atomic<int> smem_set[kMaxDevices];
-    cudaError_t e = ensure_smem_limit(kern, ShrinkShape<NT>::kSmemBytes, smem_set);
+    cudaError_t e = ensure_smem_limit(kern, StreamShape<NT>::kSmemBytes, smem_set);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(kShrinkThreads);
-    cfg.dynamicSmemBytes = ShrinkShape<NT>::kSmemBytes;
+    cfg.dynamicSmemBytes = StreamShape<NT>::kSmemBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -252,13 +403,32 @@ static cudaError_t launch_shrink_typed(const ShrinkParams& p, dim3 grid, cudaStr
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+template <typename T, int NT>
+static cudaError_t launch_gather_typed(const ShrinkParams& p, dim3 grid, cudaStream_t stream) {
+    auto kern = gather_kernel<T, NT>;
+    static std::atomic<int> smem_set[kMaxDevices];
+    cudaError_t e = ensure_smem_limit(kern, GatherShape<NT>::kSmemBytes, smem_set);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kern, grid, dim3(kShrinkThreads), GatherShape<NT>::kSmemBytes, stream, p);
+}
+
+// Whether the plan's first kernel gathers rows (see the top of this file).  A rank above 128 leaves the four warps no room
+// for their own pipelines.
+static bool gathers(const lora_desc_t& d) { return d.tokens <= kGatherTokens && d.rank <= 128; }
+
 template <typename T>
-static cudaError_t launch_shrink(const ShrinkParams& p, dim3 grid, cudaStream_t stream) {
-    if (p.rank16 <= 16) return launch_shrink_typed<T, 2>(p, grid, stream);
-    if (p.rank16 <= 32) return launch_shrink_typed<T, 4>(p, grid, stream);
-    if (p.rank16 <= 64) return launch_shrink_typed<T, 8>(p, grid, stream);
-    if (p.rank16 <= 128) return launch_shrink_typed<T, 16>(p, grid, stream);
-    return launch_shrink_typed<T, 32>(p, grid, stream);
+static cudaError_t launch_shrink(const ShrinkParams& p, bool gather, dim3 grid, cudaStream_t stream) {
+    if (gather) {
+        if (p.rank16 <= 16) return launch_gather_typed<T, 2>(p, grid, stream);
+        if (p.rank16 <= 32) return launch_gather_typed<T, 4>(p, grid, stream);
+        if (p.rank16 <= 64) return launch_gather_typed<T, 8>(p, grid, stream);
+        return launch_gather_typed<T, 16>(p, grid, stream);
+    }
+    if (p.rank16 <= 16) return launch_stream_typed<T, 2>(p, grid, stream);
+    if (p.rank16 <= 32) return launch_stream_typed<T, 4>(p, grid, stream);
+    if (p.rank16 <= 64) return launch_stream_typed<T, 8>(p, grid, stream);
+    if (p.rank16 <= 128) return launch_stream_typed<T, 16>(p, grid, stream);
+    return launch_stream_typed<T, 32>(p, grid, stream);
 }
 
 }  // namespace dgb
@@ -272,7 +442,14 @@ struct lora_plan_s {
     void* memory = nullptr;       // T, counts, ids
     int64_t t_bytes = 0, count_bytes = 0;
     int32_t m_blocks = 0, rank16 = 0, cols = 0;
-    int32_t chunks_per_cta = 0, slot_groups = 0;
+    int32_t chunks_per_cta = 0;
+    dim3 shrink_grid;
+    bool gather = false;
+    bool skinny = false;          // few output tiles: lora_skinny.cu instead of the persistent kernel
+    int32_t tile_rows = 0;        // rows of an m block
+    SkinnyParams sk = {};         // everything but pointers and maps
+    dim3 skinny_grid;
+    size_t skinny_smem = 0;
 };
 
 namespace {
@@ -289,6 +466,56 @@ gemm_status_t check_desc(const lora_desc_t& d) {
     if (d.flags & ~known) return GEMM_ERR_UNSUPPORTED;
     if (d.tile_n > 256) return GEMM_ERR_UNSUPPORTED;
     return GEMM_OK;
+}
+
+// Tiles and K split of the few-tile kernel; false: the persistent kernel.  On GB300 up to 256 tokens ran 1.3 to 1.9 times
+// faster in one wave of this kernel than in the persistent one (4 x 4096 x 4096: 12.8 against 21.9 us; 200 x 4096 x 4096:
+// 20.6 against 30.0), 512 tokens 1.1 times, 777 x 1543 x 1001 slower (17.7 against 12.7).  Clusters of eight leave SMs
+// without a place in one (128 CTAs of 96 x 4096 x 4096: 38.5 us, in fours 24.9), and a second wave costs as much as the
+// first.  Within that: the least time a CTA takes to bring in its operands (about 50 bytes a cycle into an SM and 100
+// cycles a stage) and, in a cluster, to join (2,000 cycles and a tenth of one per element).
+bool plan_skinny(const lora_desc_t& d, const DeviceFacts& dev, lora_plan_s* p) {
+    // a forced choice of the persistent kernel's parameters keeps it
+    if (d.flags || d.tile_n || d.stages || d.max_ctas || d.tokens > 256) return false;
+    const int64_t m_blocks = (d.tokens + 127) / 128, k_blocks = (d.k + 63) / 64;
+    const int64_t box_m = up(std::min<int64_t>(d.tokens, 128), 8);
+    double best = 0;
+    for (int64_t tile_n = 32; tile_n <= 256; tile_n *= 2)
+        for (int64_t ks = 1; ks <= 4 && ks <= k_blocks; ks *= 2) {
+            const char* ev = getenv("SK"); if (ev && (atoi(ev) / 10 != tile_n || atoi(ev) % 10 != ks)) continue;
+            if (m_blocks * ((d.n + tile_n - 1) / tile_n) * ks > dev.sms) continue;
+            const double cost = (double)((k_blocks + ks - 1) / ks) * ((box_m + tile_n) * 128 / 50 + 100) +
+                                (ks > 1 ? 2000 + 0.1 * (double)(box_m * tile_n) : 0);
+            if (best > 0 && cost >= best) continue;
+            best = cost;
+            p->sk.tile_n = (int32_t)tile_n;
+            p->sk.k_split = (int32_t)ks;
+        }
+    if (best == 0) return false;
+    SkinnyParams& q = p->sk;
+    q.M = (int32_t)d.tokens;
+    q.N = (int32_t)d.n;
+    q.k_blocks = (int32_t)k_blocks;
+    q.box_m = (int32_t)box_m;
+    q.tmem_cols = std::max(32, q.tile_n);
+    q.sum_pitch = q.tile_n + 4;
+    q.ldy = d.ldy ? d.ldy : d.n;
+    q.timeout_ns = d.wait_timeout_ns ? d.wait_timeout_ns : 2000000000ull;
+    q.idesc = make_idesc(d.dtype == GEMM_BF16 ? 1u : 0u, 128u, (uint32_t)q.tile_n);
+    q.adapters = d.adapters;
+    // the last stage's matrix instruction reads 128 rows from its X box on: 16 KB behind the ring
+    const int64_t stage = (box_m + q.tile_n) * 128, slack = 128 * 128 + 1024;
+    // The ring leaves room for a CTA of gather_kernel (70 KB at rank 16), so that the two kernels overlap on an SM; at least
+    // four stages; and the tile's fp32 sums have to fit it.
+    const int64_t most = dev.smem_optin - 4096 - slack;       // 4096: the kernel's static shared memory, rounded up
+    const int64_t room = std::min(most, std::max<int64_t>(134 << 10, 4 * stage));
+    q.stages = (int32_t)std::min<int64_t>(kSkinnyMaxStages, room / stage);
+    const int64_t ring = std::max<int64_t>(q.stages * stage, std::min<int64_t>(d.tokens, 128) * q.sum_pitch * 4);
+    if (q.stages < 2 || ring > most) return false;
+    p->skinny_smem = (size_t)(ring + slack);
+    p->skinny_grid = dim3((unsigned)((d.n + q.tile_n - 1) / q.tile_n * q.k_split), (unsigned)m_blocks);
+    p->tile_rows = 128;
+    return true;
 }
 
 }  // namespace
@@ -322,10 +549,13 @@ gemm_status_t lora_plan_create(lora_plan_t* out, const lora_desc_t* desc) {
     if (!p) return GEMM_ERR_RESOURCES;
     p->desc = d;
     if (p->desc.ldx == 0) p->desc.ldx = d.k;
+    p->skinny = d.tokens > 0 && plan_skinny(d, dev, p);
+    // the product's plan also holds the device error record, which both kernels use
+    if (p->skinny) g.flags |= GEMM_FLAG_NO_STREAM_K;          // ... and then needs no workspace
     s = gemm_plan_create(&p->product, &g);
     gemm_plan_info_t info{};
     if (s == GEMM_OK) s = gemm_plan_info(p->product, &info);
-    if (s == GEMM_OK && info.tile_n > 256) {
+    if (s == GEMM_OK && !p->skinny && info.tile_n > 256) {
         // 512-wide tiles hand their accumulator back in halves, the second with the next tile's work under way;
         // the appended steps keep to one accumulator per tile
         gemm_plan_destroy(p->product);
@@ -338,24 +568,53 @@ gemm_status_t lora_plan_create(lora_plan_t* out, const lora_desc_t* desc) {
         lora_plan_destroy(p);
         return s;
     }
+    if (p->skinny) {
+        // what runs instead
+        info.cta_group = 1;
+        info.tile_m = 128;
+        info.tile_n = p->sk.tile_n;
+        info.tile_k = 64;
+        info.stages = p->sk.stages;
+        info.tmem_stages = 1;
+        info.tmem_cols = p->sk.tmem_cols;
+        info.grid = (int32_t)(p->skinny_grid.x * p->skinny_grid.y);
+        info.block_threads = 192;
+        info.num_tiles = (int64_t)(p->skinny_grid.x / p->sk.k_split) * p->skinny_grid.y;
+        info.stage_bytes = (p->sk.box_m + p->sk.tile_n) * 128;
+        info.pipeline_bytes = info.stages * info.stage_bytes + 8 * (2 * info.stages + 2) + 4;
+        info.smem_bytes = (int64_t)p->skinny_smem;
+        info.epilogue = 1;
+    } else {
+        p->tile_rows = info.tile_m;
+    }
     p->info.product = info;
+    p->info.product_k_split = p->skinny ? p->sk.k_split : 1;
     p->rank16 = (int32_t)up(d.rank, 16);
     p->cols = d.dtype_y == GEMM_F32 ? 2 * p->rank16 : p->rank16;
     p->info.steps_per_adapter = p->cols / 16;
     if (d.tokens > 0) {
-        p->m_blocks = (int32_t)((d.tokens + info.tile_m - 1) / info.tile_m);
-        const int64_t slots = std::min<int64_t>(d.adapters, std::min<int64_t>(info.tile_m, d.tokens));
+        p->m_blocks = (int32_t)((d.tokens + p->tile_rows - 1) / p->tile_rows);
+        const int64_t slots = std::min<int64_t>(d.adapters, std::min<int64_t>(p->tile_rows, d.tokens));
         p->info.max_adapters_per_tile = (int32_t)slots;
-        // Grid of shrink_kernel: clusters split K while that fills the device twice over and leaves every CTA four
-        // chunks of K; then CTAs share out the slots.
-        const int64_t row_blocks = (d.tokens + kShrinkRows - 1) / kShrinkRows, chunks = (d.k + 63) / 64;
-        int64_t ks = 1;
-        while (ks < 8 && row_blocks * ks * 2 <= 2 * dev.sms && chunks >= 4 * ks * 2) ks *= 2;
-        p->chunks_per_cta = (int32_t)((chunks + ks - 1) / ks);
-        p->slot_groups = (int32_t)std::min<int64_t>(slots, std::max<int64_t>(1, 4 * dev.sms / (row_blocks * ks)));
-        p->info.shrink_k_split = (int32_t)ks;
-        p->info.shrink_grid = (int32_t)(row_blocks * ks * p->slot_groups);
-        p->t_bytes = up((int64_t)p->m_blocks * slots * info.tile_m * p->cols * 2, 256);
+        p->gather = gathers(d);
+        if (p->gather) {
+            p->info.shrink_k_split = 1;
+            // as many as there can be groups of 16 rows of one adapter in an m block
+            const int64_t rows = std::min<int64_t>(d.tokens, p->tile_rows);
+            p->shrink_grid = dim3((unsigned)std::min<int64_t>(rows, slots + rows / 16), (unsigned)p->m_blocks, 1);
+        } else {
+            // clusters split K while that fills the device twice over and leaves every CTA four chunks of K; then CTAs
+            // share out the slots
+            const int64_t row_blocks = (d.tokens + kShrinkRows - 1) / kShrinkRows, chunks = (d.k + 63) / 64;
+            int64_t ks = 1;
+            while (ks < 8 && row_blocks * ks * 2 <= 2 * dev.sms && chunks >= 4 * ks * 2) ks *= 2;
+            p->chunks_per_cta = (int32_t)((chunks + ks - 1) / ks);
+            p->info.shrink_k_split = (int32_t)ks;
+            p->shrink_grid = dim3((unsigned)ks, (unsigned)std::min<int64_t>(slots, std::max<int64_t>(1, 4 * dev.sms / (row_blocks * ks))),
+                                  (unsigned)row_blocks);
+        }
+        p->info.shrink_grid = (int32_t)(p->shrink_grid.x * p->shrink_grid.y * p->shrink_grid.z);
+        p->t_bytes = up((int64_t)p->m_blocks * slots * p->tile_rows * p->cols * 2, 256);
         p->count_bytes = up((int64_t)p->m_blocks * 4, 256);
         const int64_t bytes = p->t_bytes + p->count_bytes + (int64_t)p->m_blocks * slots * 4;
         p->info.workspace_bytes = bytes + info.workspace_bytes;
@@ -394,39 +653,52 @@ gemm_status_t lora_run(lora_plan_t plan, const lora_args_t* args, gemm_stream_t 
     if (!all_aligned(16, {a.x, a.w, a.a, a.b, a.y})) return GEMM_ERR_ALIGNMENT;
     if (!all_multiples(8, {d.ldx, ldw, a.lda, a.stride_a, a.ldb, a.stride_b}) || ldy * y_bytes % 16 != 0) return GEMM_ERR_ALIGNMENT;
     const gemm_plan_info_t& info = plan->info.product;
-    PersistentParams p;
-    gemm_status_t s = product_params(plan->product, a.x, a.w, a.y, &p);
-    if (s != GEMM_OK) return s;
+    gemm_status_t s;
     char* mem = static_cast<char*>(plan->memory);
     q.ldx = d.ldx;
     q.M = (int32_t)d.tokens;
     q.K = (int32_t)d.k;
     q.rank = d.rank;
     q.adapters = d.adapters;
-    q.tile_rows = info.tile_m;
+    q.tile_rows = plan->tile_rows;
     q.max_adapters = plan->info.max_adapters_per_tile;
     q.rank16 = plan->rank16;
     q.cols = plan->cols;
+    q.pitch = q.max_adapters * q.cols;
     q.chunks_per_cta = plan->chunks_per_cta;
     q.t = mem;
     q.counts = reinterpret_cast<int32_t*>(mem + plan->t_bytes);
     q.ids = reinterpret_cast<int32_t*>(mem + plan->t_bytes + plan->count_bytes);
     LoraTail tail;
-    s = encode_steps_map(&tail.tmap_t, d.dtype, q.t, q.cols, q.tile_rows, (int64_t)plan->m_blocks * q.max_adapters, q.cols,
-                         (int64_t)q.tile_rows * q.cols, 128);
+    const int32_t box_m = plan->skinny ? plan->sk.box_m : 128;
+    s = encode_matrices_map(&tail.tmap_t, d.dtype, q.t, q.pitch, q.tile_rows, plan->m_blocks, q.pitch, (int64_t)q.tile_rows * q.pitch,
+                            128, box_m);
     if (s != GEMM_OK) return s;
     // one adapter: the stride is never used but has to be a valid one
     const int64_t stride_b = d.adapters > 1 ? a.stride_b : d.n * a.ldb;
-    if ((s = encode_steps_map(&tail.tmap_b, d.dtype, a.b, d.rank, d.n, d.adapters, a.ldb, stride_b, info.tile_n / info.cta_group)) != GEMM_OK)
+    if ((s = encode_matrices_map(&tail.tmap_b, d.dtype, a.b, d.rank, d.n, d.adapters, a.ldb, stride_b, 32, info.tile_n / info.cta_group)) != GEMM_OK)
         return s;
     tail.counts = q.counts;
     tail.ids = q.ids;
     tail.max_adapters = q.max_adapters;
     tail.steps = q.cols / 16;
     tail.b_steps = q.rank16 / 16;
-    const dim3 grid((unsigned)plan->info.shrink_k_split, (unsigned)plan->slot_groups, (unsigned)((d.tokens + kShrinkRows - 1) / kShrinkRows));
-    cudaError_t e = d.dtype == GEMM_BF16 ? launch_shrink<__nv_bfloat16>(q, grid, stream) : launch_shrink<__half>(q, grid, stream);
+    SkinnyParams sk;
+    PersistentParams p;
+    if (plan->skinny) {
+        sk = plan->sk;
+        sk.y = a.y;
+        sk.status = device_record(plan->product);
+        sk.adapter = a.adapter;
+        if ((s = encode_rows_map(&sk.tmap_x, d.dtype, a.x, d.k, d.tokens, d.ldx, box_m)) != GEMM_OK) return s;
+        if ((s = encode_rows_map(&sk.tmap_w, d.dtype, a.w, d.k, d.n, ldw, sk.tile_n)) != GEMM_OK) return s;
+    } else if ((s = product_params(plan->product, a.x, a.w, a.y, &p)) != GEMM_OK) {
+        return s;
+    }
+    cudaError_t e = d.dtype == GEMM_BF16 ? launch_shrink<__nv_bfloat16>(q, plan->gather, plan->shrink_grid, stream)
+                                         : launch_shrink<__half>(q, plan->gather, plan->shrink_grid, stream);
     if (e != cudaSuccess) return status_of(e);
+    if (plan->skinny) return status_of(launch_skinny(sk, tail, d.dtype_y, plan->skinny_grid, plan->skinny_smem, stream));
     return status_of(launch_adapters(p, tail, info.cta_group, d.dtype_y, info.grid, (size_t)info.smem_bytes, stream));
 }
 

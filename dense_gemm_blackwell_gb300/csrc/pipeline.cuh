@@ -153,9 +153,8 @@ constexpr uint32_t kPartA = 1u, kPartB0 = 2u, kPartB1 = 4u, kPartsAll = 7u;
 // read from DRAM, 1.2 % faster at the power cap).  Only the summation order
 // of the tile changes; a kernel that applies per-K-block scales keeps it off.
 // kTail: after the K blocks of a unit that ends its tile, the tile's adapter
-// steps (LoraTail), 4 * ATOMS of them to a stage: step j's 128 rows of T at
-// j * 4 KB of the stage's A area, its rows of B at j * b_rows * 32 bytes of the
-// B area.
+// steps (LoraTail), 4 * ATOMS of them to a stage: T as one 128-byte K atom per
+// four steps, like A; step j's rows of B at j * b_rows * 32 bytes of the B area.
 template <int CG, int ATOMS = 1, int HALVES = 1, uint32_t PARTS = kPartsAll, bool kSerpentine = false, bool kTail = false>
 __device__ void producer_loop(const PersistentParams& p, uint8_t* ring, uint32_t stage_bytes, int tile_k,
                               uint32_t full0, uint32_t empty0, volatile uint32_t* abort_flag, uint32_t rank,
@@ -240,32 +239,43 @@ __device__ void producer_loop(const PersistentParams& p, uint8_t* ring, uint32_t
             if (aborted || u.role == kUnitContributor) continue;
             griddep_wait();     // the kernel that computes T, counts and ids is done
             const int total = __ldcg(tail->counts + mb) * tail->steps;
+            const uint32_t step_b = (uint32_t)b_rows * kTailRowBytes;
+            // lane j holds the adapter of step j of the next stage, read a stage ahead
+            const int lane = (int)lane_id();
+            auto adapter_of = [&](int s) {
+                return (parts & kPartB0) != 0 && s < total ? __ldcg(tail->ids + (size_t)mb * tail->max_adapters + s / tail->steps) : 0;
+            };
+            int id_next = lane < 4 * ATOMS ? adapter_of(lane) : 0;
             for (int s0 = 0; s0 < total; s0 += 4 * ATOMS) {
+                const int id = id_next;
+                if (lane < 4 * ATOMS) id_next = adapter_of(s0 + 4 * ATOMS + lane);
                 if (!wait_phase_warp<false, true>(empty0 + 8u * stage, phase ^ 1u, abort_flag, tmo, p.status,
                                                   kRoleProducer, stage, t)) {
                     aborted = true;
                     break;
                 }
-                if (elect_one()) {
-                    const uint32_t fb = fb0 + 8u * stage;
-                    const int n16 = min(4 * ATOMS, total - s0);
-                    const uint32_t step_b = (uint32_t)b_rows * kTailRowBytes;
-                    if (leader && (parts & kPartA) != 0)
-                        mbar_arrive_expect_tx(full0 + 8u * stage, (uint32_t)(CG * n16) * (kTailStepBytesA + step_b));
-                    const uint32_t sa = smem_u32(ring + (size_t)stage * stage_bytes);
-                    const uint32_t sb = sa + p.stage_bytes_a;
-                    for (int j = 0; j < n16; ++j) {
-                        const int slot = (s0 + j) / tail->steps, c = s0 + j - slot * tail->steps;
-                        if constexpr ((parts & kPartA) != 0) {
-                            const int z = mb * tail->max_adapters + slot;
-                            if constexpr (CG == 1) tma_load_3d(sa + j * kTailStepBytesA, &tail->tmap_t, fb, c * 16, 0, z);
-                            else tma_load_3d_pair(sa + j * kTailStepBytesA, &tail->tmap_t, fb, c * 16, (int)rank * 128, z);
+                const bool issuer = elect_one();
+                const uint32_t fb = fb0 + 8u * stage;
+                const int n16 = min(4 * ATOMS, total - s0), atoms = (n16 + 3) / 4;
+                const uint32_t sa = smem_u32(ring + (size_t)stage * stage_bytes);
+                const uint32_t sb = sa + p.stage_bytes_a;
+                if constexpr ((parts & kPartA) != 0) {
+                    if (issuer) {
+                        if (leader)
+                            mbar_arrive_expect_tx(full0 + 8u * stage, (uint32_t)CG * (atoms * kTailAtomBytes + n16 * step_b));
+                        for (int at = 0; at < atoms; ++at) {
+                            if constexpr (CG == 1) tma_load_3d(sa + at * kTailAtomBytes, &tail->tmap_t, fb, (s0 + 4 * at) * 16, 0, mb);
+                            else tma_load_3d_pair(sa + at * kTailAtomBytes, &tail->tmap_t, fb, (s0 + 4 * at) * 16, (int)rank * 128, mb);
                         }
-                        if constexpr ((parts & kPartB0) != 0) {
-                            const int id = __ldcg(tail->ids + (size_t)mb * tail->max_adapters + slot);
-                            const int x = (c % tail->b_steps) * 16;
-                            if constexpr (CG == 1) tma_load_3d(sb + j * step_b, &tail->tmap_b, fb, x, b_row, id);
-                            else tma_load_3d_pair(sb + j * step_b, &tail->tmap_b, fb, x, b_row, id);
+                    }
+                }
+                if constexpr ((parts & kPartB0) != 0) {
+                    for (int j = 0; j < n16; ++j) {
+                        const int z = __shfl_sync(0xffffffffu, id, j);
+                        const int x = (((s0 + j) % tail->steps) % tail->b_steps) * 16;
+                        if (issuer) {
+                            if constexpr (CG == 1) tma_load_3d(sb + j * step_b, &tail->tmap_b, fb, x, b_row, z);
+                            else tma_load_3d_pair(sb + j * step_b, &tail->tmap_b, fb, x, b_row, z);
                         }
                     }
                 }

@@ -36,7 +36,8 @@ class LoraArgs(ctypes.Structure):
 
 class LoraPlanInfo(ctypes.Structure):
     _fields_ = [("product", GemmPlanInfo), ("steps_per_adapter", _I32), ("max_adapters_per_tile", _I32),
-                ("shrink_k_split", _I32), ("shrink_grid", _I32), ("workspace_bytes", _I64)]
+                ("shrink_k_split", _I32), ("shrink_grid", _I32), ("product_k_split", _I32), ("reserved0", _I32),
+                ("workspace_bytes", _I64)]
 
 
 class QkNormRopeArgs(ctypes.Structure):

@@ -47,16 +47,19 @@ typedef struct {
     int32_t dtype_y;            /* GEMM_F32, GEMM_BF16 or GEMM_F16 */
     int64_t ldx, ldw, ldy;      /* 0 = packed (k, k, n); multiples of 16 bytes */
     uint32_t flags;             /* GEMM_FLAG_CTA_GROUP_1/2, _NO_STREAM_K, _STAGE_K1/K2 as in gemm.h */
-    int32_t tile_n, stages, max_ctas;   /* as in gemm.h (tile_n up to 256); 0 = planner */
+    int32_t tile_n, stages, max_ctas;   /* as in gemm.h (tile_n up to 256); 0 = planner.  Any of these or of the flags
+                                   keeps to the persistent kernel where few tiles would take the few-tile one */
     uint64_t wait_timeout_ns;   /* bound on every device-side wait; 0 = 2 s */
 } lora_desc_t;
 
 typedef struct {
-    gemm_plan_info_t product;   /* the projection's plan */
+    gemm_plan_info_t product;   /* how the projection runs (the few-tile kernel: tiles of 128 rows, one accumulator) */
     int32_t steps_per_adapter;  /* K = 16 matrix instructions an adapter adds to a tile */
     int32_t max_adapters_per_tile;
     int32_t shrink_k_split;     /* CTAs (one cluster) that share the K range of X A_i^T */
     int32_t shrink_grid;        /* CTAs of the kernel that computes T */
+    int32_t product_k_split;    /* few-tile kernel: CTAs (one cluster) that share a tile's K; otherwise 1 */
+    int32_t reserved0;
     int64_t workspace_bytes;    /* device memory of the plan, the product's included */
 } lora_plan_info_t;
 
