@@ -18,8 +18,10 @@
 //
 // Two forms of the first kernel:
 //   gather_kernel, up to kGatherTokens tokens (decode batches, each adapter
-//   with few rows): one CTA per 16 rows of one adapter; they are gathered, and
-//   four warps split K, each with its own copy pipeline;
+//   with few rows): a CTA per token, of which every eighth of an adapter goes
+//   on, with its row and the adapter's next seven.  Its time is latency,
+//   so nothing is staged: eight warps split K and load 16-byte pieces of A_i
+//   and of the rows straight into matrix fragments, many at once;
 //   stream_kernel, above that (prompts, long runs of one adapter): one CTA per
 //   (64 rows, range of slots, range of K); a row is loaded only for its own
 //   adapter (others are zeros in shared memory), the CTAs of a cluster split K
@@ -94,169 +96,166 @@ __device__ __forceinline__ void store_t(const ShrinkParams& p, T* at, float (&v)
     }
 }
 
-// NT: 8-column tiles of the rank held (rank <= 8 NT)
-template <int NT>
-struct GatherShape {
-    // up to rank 32 a CTA leaves room on its SM for one of the product that follows (lora_skinny.cu)
-    static constexpr int kStages = NT <= 2 ? 4 : (NT <= 4 ? 3 : (NT <= 8 ? 4 : 2));
-    static constexpr int kStageBytes = (16 + NT * 8) * 128;      // one warp: 16 rows of X, the adapter's rows
-    static constexpr int kSumPitch = NT * 8 + 4;
-    static constexpr int kSmemBytes = 4 * kStages * kStageBytes + 4 * 16 * kSumPitch * 4;
-};
+constexpr int kGatherWarps = 8, kGatherThreads = 32 * kGatherWarps;
+constexpr int kGatherRows = 8;               // tokens of one CTA: the columns of the matrix instruction
 
-template <typename T, int NT>
-__global__ void __launch_bounds__(kShrinkThreads) gather_kernel(const __grid_constant__ ShrinkParams p) {
-    using S = GatherShape<NT>;
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ AdapterList adapters;
-    __shared__ int32_t row_ids[kMaxTileRows];
-    __shared__ int32_t taken[kMaxTileRows];      // rows of each slot
-    __shared__ int32_t rows[16];
-    __shared__ int32_t my_slot, my_group;
-    float* sums = reinterpret_cast<float*>(smem + 4 * S::kStages * S::kStageBytes);
+// The 16 bytes at elements k .. k + 7 of a row of K elements; elements past the row's end are zeros and not read.
+template <typename T>
+__device__ __forceinline__ uint4 load_piece(const T* row, int k, int K, bool in) {
+    if (in && k + 8 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (in && k < K) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (k + e < K) w[e / 2] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(row + k + e)) << (16 * (e & 1));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
-    griddep_wait();
-    griddep_launch_dependents();
+// MT: 16-row tiles of the rank held (rank <= 16 MT).  The matrix instruction has A_i's rows as its 16 rows and the tokens
+// as its 8 columns.  Lane (g, j) = (lane / 4, lane % 4) loads elements 8 j .. 8 j + 7 of every 32 of K of its rows: two
+// instructions' worth of fragments, in an order of k that is the same for both operands, so that no data moves between
+// lanes.
+template <typename T, int MT>
+__global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_constant__ ShrinkParams p) {
+    constexpr int kBatch = MT == 1 ? 8 : (MT == 2 ? 4 : (MT == 4 ? 2 : 1));     // 32-element chunks whose loads are in flight
+    constexpr int kSumPitch = MT * 16 + 4;
+    __shared__ uint32_t bits[kMaxAdapters / 32];         // adapters that occur in the m block
+    __shared__ uint32_t same[kMaxTileRows / 32];         // its rows of this CTA's adapter
+    __shared__ __align__(16) float sums[kGatherWarps][kGatherRows][kSumPitch];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tile = blockIdx.y;
-    for (int i = threadIdx.x; i < kMaxTileRows; i += kShrinkThreads) taken[i] = 0;
-    const int count = find_adapters(p.a.adapter, p.adapters, p.M, tile * p.tile_rows, p.tile_rows, adapters, row_ids, 0, p.tile_rows,
-                                    threadIdx.x, kShrinkThreads, [] { __syncthreads(); });
-    if (blockIdx.x == 0) publish_adapters(p, tile, adapters, count);
-    // The work items are the groups of 16 rows of one slot, slot after slot; this CTA takes the blockIdx.x-th.
-    for (int i = threadIdx.x; i < p.tile_rows; i += kShrinkThreads) {
-        const int id = row_ids[i];
-        if (id < 0) continue;
-        int lo = 0, hi = count - 1;              // its slot: the list ascends
-        while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (adapters.list[mid] < id) lo = mid + 1; else hi = mid;
-        }
-        atomicAdd(&taken[lo], 1);
-    }
-    if (threadIdx.x == 0) my_slot = -1;
+    const int tile = blockIdx.y, lead = blockIdx.x, m0 = tile * p.tile_rows;
+    const int words = (p.adapters + 31) / 32;
+    for (int i = threadIdx.x; i < words; i += kGatherThreads) bits[i] = 0u;
     __syncthreads();
-    if (warp == 0) {
-        int before = 0;
-        for (int base = 0; base < count; base += 32) {
-            const int groups = base + lane < count ? (taken[base + lane] + 15) / 16 : 0;
-            int at = groups;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int t = __shfl_up_sync(0xffffffffu, at, o);
-                if (lane >= o) at += t;
-            }
-            const int all = __shfl_sync(0xffffffffu, at, 31);
-            const int mine = (int)blockIdx.x - before - (at - groups);
-            if (mine >= 0 && mine < groups) {
-                my_slot = base + lane;
-                my_group = mine;
-            }
-            before += all;
-        }
-    }
-    __syncthreads();
-    const int slot = my_slot;
-    if (slot < 0) return;
-    const int id = adapters.list[slot], r0 = my_group * 16;
-    T* dst = static_cast<T*>(p.t) + (size_t)tile * p.tile_rows * p.pitch + slot * p.cols;
-    if (warp == 0) {
-        // the group's rows: the r0-th to (r0 + 15)-th of the slot's
-        int n = 0;
-        for (int base = 0; base < p.tile_rows; base += 32) {
-            const bool mine = row_ids[base + lane] == id;
-            const uint32_t b = __ballot_sync(0xffffffffu, mine);
-            const int at = n + __popc(b & ((1u << lane) - 1u)) - r0;
-            if (mine && at >= 0 && at < 16) rows[at] = base + lane;
-            n += __popc(b);
-        }
-    }
-    if (my_group == 0) {
-        // zeros in the other rows (those of tokens that exist)
-        const int live = min(p.tile_rows, p.M - tile * p.tile_rows), pieces = p.cols / 8;
-        for (int i = threadIdx.x; i < live * pieces; i += kShrinkThreads) {
-            const int r = i / pieces;
-            if (row_ids[r] != id) *reinterpret_cast<uint4*>(dst + (size_t)r * p.pitch + (i - r * pieces) * 8) = make_uint4(0, 0, 0, 0);
-        }
-    }
-    __syncthreads();
-    const int n = min(16, taken[slot] - r0);
-    const float scale = p.a.scale ? p.a.scale[id] : 1.f;
-
-    // this warp's chunks of 64 elements of K
-    const int chunks = (p.K + 63) / 64;
-    const int c_begin = chunks * warp / 4, c_end = chunks * (warp + 1) / 4;
-    const uint32_t ring = smem_u32(smem) + warp * S::kStages * S::kStageBytes;
-    const T* X = static_cast<const T*>(p.a.x) + (int64_t)tile * p.tile_rows * p.ldx;
-    const T* A = static_cast<const T*>(p.a.a) + id * p.a.stride_a;
-    const int cc = lane & 7;
-    auto load = [&](int chunk, int stage) {
-        const uint32_t sx = ring + stage * S::kStageBytes, sa = sx + 16 * 128;
-        const int k = chunk * 64 + cc * 8;
-        const uint32_t bytes = (uint32_t)min(max(p.K - k, 0), 8) * 2u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = (lane >> 3) + 4 * i;
-            const bool in = bytes && r < n;
-            cp_async_16_zfill(sx + r * 128 + ((cc ^ (r & 7)) << 4), in ? X + (int64_t)rows[r] * p.ldx + k : X, in ? bytes : 0u);
-        }
-#pragma unroll
-        for (int i = 0; i < NT * 2; ++i) {
-            const int r = (lane >> 3) + 4 * i;
-            const bool in = bytes && r < p.rank;
-            cp_async_16_zfill(sa + r * 128 + ((cc ^ (r & 7)) << 4), in ? A + (int64_t)r * p.a.lda + k : A, in ? bytes : 0u);
-        }
+    griddep_wait();
+    griddep_launch_dependents();
+    auto adapter_of = [&](int i) {       // of row i of the m block; -1: none
+        if (i >= p.tile_rows || m0 + i >= p.M) return -1;
+        const int a = p.a.adapter[m0 + i];
+        return a >= 0 && a < p.adapters ? a : -1;
     };
-    float acc[NT][4] = {};
-    __syncwarp();
+    static_assert(kGatherThreads == kMaxTileRows, "a thread per row");
+    const int id = adapter_of(lead), mine = adapter_of(threadIdx.x);
+    if (mine >= 0) atomicOr(&bits[mine >> 5], 1u << (mine & 31));
+    const uint32_t ballot = __ballot_sync(0xffffffffu, mine == id);
+    if (lane == 0) same[warp] = ballot;
+    __syncthreads();
+    if (lead == 0) {
+        // the m block's list of adapters, for the product
+        if (warp == 0) {
+            int done = 0;
+            for (int base = 0; base < words; base += 32) {
+                uint32_t word = base + lane < words ? bits[base + lane] : 0u;
+                int at = __popc(word);
 #pragma unroll
-    for (int s = 0; s < S::kStages - 1; ++s) {
-        if (c_begin + s < c_end) load(c_begin + s, s);
-        cp_async_commit();
-    }
-    int stage = 0;
-    for (int ch = c_begin; ch < c_end; ++ch) {
-        cp_async_wait<S::kStages - 2>();
-        __syncwarp();
-        if (ch + S::kStages - 1 < c_end) load(ch + S::kStages - 1, stage == 0 ? S::kStages - 1 : stage - 1);
-        cp_async_commit();
-        const uint32_t sx = ring + stage * S::kStageBytes, sa = sx + 16 * 128;
-        const int xr = lane & 15, ar = (lane & 7) + (lane >> 4) * 8;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            uint32_t x[4];
-            ldmatrix_x4(sx + xr * 128 + (((kk * 2 + (lane >> 4)) ^ (xr & 7)) << 4), x);
-#pragma unroll
-            for (int t = 0; t < NT; t += 2) {
-                uint32_t b[4];
-                ldmatrix_x4(sa + (t * 8 + ar) * 128 + (((kk * 2 + ((lane >> 3) & 1)) ^ (ar & 7)) << 4), b);
-                mma_16816<T>(acc[t], x, b[0], b[1]);
-                mma_16816<T>(acc[t + 1], x, b[2], b[3]);
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int t = __shfl_up_sync(0xffffffffu, at, o);
+                    if (lane >= o) at += t;
+                }
+                const int all = __shfl_sync(0xffffffffu, at, 31);
+                at += done - __popc(word);
+                for (; word; word &= word - 1) p.ids[(size_t)tile * p.max_adapters + at++] = (base + lane) * 32 + __ffs(word) - 1;
+                done += all;
             }
+            if (lane == 0) p.counts[tile] = done;
         }
-        if (++stage == S::kStages) stage = 0;
     }
-    cp_async_wait<0>();
-    float* own = sums + warp * 16 * S::kSumPitch;
+    if (id < 0) return;
+    // This row leads a group if the number of its adapter's rows before it is a multiple of eight.
+    int before = 0;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int r = lane >> 2, c = t * 8 + (lane & 3) * 2;
-        *reinterpret_cast<float2*>(own + r * S::kSumPitch + c) = make_float2(acc[t][0], acc[t][1]);
-        *reinterpret_cast<float2*>(own + (r + 8) * S::kSumPitch + c) = make_float2(acc[t][2], acc[t][3]);
+    for (int w = 0; w < kMaxTileRows / 32; ++w)
+        before += __popc(same[w] & (w < (lead >> 5) ? 0xffffffffu : (w == (lead >> 5) ? (1u << (lead & 31)) - 1u : 0u)));
+    if (before % kGatherRows != 0) return;
+    // its slot: adapters of the block with smaller numbers
+    int slot = 0;
+    for (int w = lane; w < words; w += 32)
+        slot += __popc(bits[w] & (w < (id >> 5) ? 0xffffffffu : (w == (id >> 5) ? (1u << (id & 31)) - 1u : 0u)));
+    slot = __reduce_add_sync(0xffffffffu, slot);
+    // the i-th row of the group, counted from the leader; -1 past the last
+    auto row_of = [&](int i) {
+        int skip = before + i;
+        for (int w = 0; w < kMaxTileRows / 32; ++w) {
+            const int here = __popc(same[w]);
+            if (skip < here) {
+                uint32_t left = same[w];
+                for (; skip > 0; --skip) left &= left - 1;
+                return w * 32 + __ffs(left) - 1;
+            }
+            skip -= here;
+        }
+        return -1;
+    };
+
+    const int g = lane >> 2, j = lane & 3;
+    const int chunks = (p.K + 31) / 32;
+    const int c_end = chunks * (warp + 1) / kGatherWarps;
+    const int my_row = row_of(g);
+    const bool in_x = my_row >= 0;
+    const T* X = static_cast<const T*>(p.a.x) + (int64_t)(m0 + (in_x ? my_row : 0)) * p.ldx;
+    const T* A = static_cast<const T*>(p.a.a) + id * p.a.stride_a + (int64_t)g * p.a.lda;
+    const int64_t a_step = 8 * p.a.lda;
+    float acc[MT][4] = {};
+    const int c_begin = chunks * warp / kGatherWarps;
+    // A_i comes from DRAM: what the first batch does not load is brought to L2 meanwhile
+    for (int c = c_begin + kBatch; c < c_end; c += 2) {
+        // 128 bytes of a row: two chunks, one lane in four
+        const int k = c * 32 + j * 8;
+#pragma unroll
+        for (int t = 0; t < 2 * MT; ++t)
+            if (j == 0 && t * 8 + g < p.rank && k < p.K) asm volatile("prefetch.global.L2 [%0];" ::"l"(A + t * a_step + k));
+    }
+    for (int c = c_begin; c < c_end; c += kBatch) {
+        uint4 x[kBatch], w[kBatch][2 * MT];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int k = (c + u) * 32 + j * 8;
+            const bool in = c + u < c_end;
+            x[u] = load_piece(X, k, p.K, in && in_x);
+#pragma unroll
+            for (int t = 0; t < 2 * MT; ++t) w[u][t] = load_piece(A + t * a_step, k, p.K, in && t * 8 + g < p.rank);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                const uint4 &lo = w[u][2 * t], &hi = w[u][2 * t + 1];
+                const uint32_t f0[4] = {lo.x, hi.x, lo.y, hi.y}, f1[4] = {lo.z, hi.z, lo.w, hi.w};
+                mma_16816<T>(acc[t], f0, x[u].x, x[u].y);
+                mma_16816<T>(acc[t], f1, x[u].z, x[u].w);
+            }
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        sums[warp][2 * j][t * 16 + g] = acc[t][0];
+        sums[warp][2 * j + 1][t * 16 + g] = acc[t][1];
+        sums[warp][2 * j][t * 16 + g + 8] = acc[t][2];
+        sums[warp][2 * j + 1][t * 16 + g + 8] = acc[t][3];
+    }
+    T* dst = static_cast<T*>(p.t) + (size_t)tile * p.tile_rows * p.pitch + slot * p.cols;
+    if (before == 0) {
+        // zeros in the other rows (those of tokens that exist)
+        const int live = min(p.tile_rows, p.M - m0), pieces = p.cols / 8;
+        for (int i = threadIdx.x; i < live * pieces; i += kGatherThreads) {
+            const int r = i / pieces;
+            if (!((same[r >> 5] >> (r & 31)) & 1u)) *reinterpret_cast<uint4*>(dst + (size_t)r * p.pitch + (i - r * pieces) * 8) = make_uint4(0, 0, 0, 0);
+        }
     }
     __syncthreads();
+    const float scale = p.a.scale ? p.a.scale[id] : 1.f;
     const int groups = p.rank16 / 8;
-    for (int i = threadIdx.x; i < n * groups; i += kShrinkThreads) {
+    for (int i = threadIdx.x; i < kGatherRows * groups; i += kGatherThreads) {
         const int r = i / groups, c = (i - r * groups) * 8;
+        const int row = row_of(r);
+        if (row < 0) break;
         float v[8] = {};
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const float* from = sums + (w * 16 + r) * S::kSumPitch + c;
+        for (int q = 0; q < kGatherWarps; ++q)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += from[j];
-        }
-        store_t<T>(p, dst + (size_t)rows[r] * p.pitch + c, v, scale);
+            for (int e = 0; e < 8; ++e) v[e] += sums[q][r][c + e];
+        store_t<T>(p, dst + (size_t)row * p.pitch + c, v, scale);
     }
 }
 
@@ -403,26 +402,17 @@ static cudaError_t launch_stream_typed(const ShrinkParams& p, dim3 grid, cudaStr
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <typename T, int NT>
-static cudaError_t launch_gather_typed(const ShrinkParams& p, dim3 grid, cudaStream_t stream) {
-    auto kern = gather_kernel<T, NT>;
-    static std::atomic<int> smem_set[kMaxDevices];
-    cudaError_t e = ensure_smem_limit(kern, GatherShape<NT>::kSmemBytes, smem_set);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(kern, grid, dim3(kShrinkThreads), GatherShape<NT>::kSmemBytes, stream, p);
-}
-
-// Whether the plan's first kernel gathers rows (see the top of this file).  A rank above 128 leaves the four warps no room
-// for their own pipelines.
+// Whether the plan's first kernel gathers rows (see the top of this file).  A rank above 128 does not fit its registers.
 static bool gathers(const lora_desc_t& d) { return d.tokens <= kGatherTokens && d.rank <= 128; }
 
 template <typename T>
 static cudaError_t launch_shrink(const ShrinkParams& p, bool gather, dim3 grid, cudaStream_t stream) {
     if (gather) {
-        if (p.rank16 <= 16) return launch_gather_typed<T, 2>(p, grid, stream);
-        if (p.rank16 <= 32) return launch_gather_typed<T, 4>(p, grid, stream);
-        if (p.rank16 <= 64) return launch_gather_typed<T, 8>(p, grid, stream);
-        return launch_gather_typed<T, 16>(p, grid, stream);
+        const dim3 block(kGatherThreads);
+        if (p.rank16 <= 16) return launch_dependent(gather_kernel<T, 1>, grid, block, 0, stream, p);
+        if (p.rank16 <= 32) return launch_dependent(gather_kernel<T, 2>, grid, block, 0, stream, p);
+        if (p.rank16 <= 64) return launch_dependent(gather_kernel<T, 4>, grid, block, 0, stream, p);
+        return launch_dependent(gather_kernel<T, 8>, grid, block, 0, stream, p);
     }
     if (p.rank16 <= 16) return launch_stream_typed<T, 2>(p, grid, stream);
     if (p.rank16 <= 32) return launch_stream_typed<T, 4>(p, grid, stream);
@@ -481,8 +471,7 @@ bool plan_skinny(const lora_desc_t& d, const DeviceFacts& dev, lora_plan_s* p) {
     const int64_t box_m = up(std::min<int64_t>(d.tokens, 128), 8);
     double best = 0;
     for (int64_t tile_n = 32; tile_n <= 256; tile_n *= 2)
-        for (int64_t ks = 1; ks <= 4 && ks <= k_blocks; ks *= 2) {
-            const char* ev = getenv("SK"); if (ev && (atoi(ev) / 10 != tile_n || atoi(ev) % 10 != ks)) continue;
+        for (int64_t ks = 1; ks <= kSkinnyMaxSplit && ks <= k_blocks; ks *= 2) {
             if (m_blocks * ((d.n + tile_n - 1) / tile_n) * ks > dev.sms) continue;
             const double cost = (double)((k_blocks + ks - 1) / ks) * ((box_m + tile_n) * 128 / 50 + 100) +
                                 (ks > 1 ? 2000 + 0.1 * (double)(box_m * tile_n) : 0);
@@ -505,10 +494,9 @@ bool plan_skinny(const lora_desc_t& d, const DeviceFacts& dev, lora_plan_s* p) {
     q.adapters = d.adapters;
     // the last stage's matrix instruction reads 128 rows from its X box on: 16 KB behind the ring
     const int64_t stage = (box_m + q.tile_n) * 128, slack = 128 * 128 + 1024;
-    // The ring leaves room for a CTA of gather_kernel (70 KB at rank 16), so that the two kernels overlap on an SM; at least
-    // four stages; and the tile's fp32 sums have to fit it.
     const int64_t most = dev.smem_optin - 4096 - slack;       // 4096: the kernel's static shared memory, rounded up
-    const int64_t room = std::min(most, std::max<int64_t>(134 << 10, 4 * stage));
+    // room beside it for a CTA of gather_kernel (8 KB), so that the two kernels overlap on an SM
+    const int64_t room = most - (12 << 10);
     q.stages = (int32_t)std::min<int64_t>(kSkinnyMaxStages, room / stage);
     const int64_t ring = std::max<int64_t>(q.stages * stage, std::min<int64_t>(d.tokens, 128) * q.sum_pitch * 4);
     if (q.stages < 2 || ring > most) return false;
@@ -599,9 +587,7 @@ gemm_status_t lora_plan_create(lora_plan_t* out, const lora_desc_t* desc) {
         p->gather = gathers(d);
         if (p->gather) {
             p->info.shrink_k_split = 1;
-            // as many as there can be groups of 16 rows of one adapter in an m block
-            const int64_t rows = std::min<int64_t>(d.tokens, p->tile_rows);
-            p->shrink_grid = dim3((unsigned)std::min<int64_t>(rows, slots + rows / 16), (unsigned)p->m_blocks, 1);
+            p->shrink_grid = dim3((unsigned)std::min<int64_t>(d.tokens, p->tile_rows), (unsigned)p->m_blocks, 1);
         } else {
             // clusters split K while that fills the device twice over and leaves every CTA four chunks of K; then CTAs
             // share out the slots

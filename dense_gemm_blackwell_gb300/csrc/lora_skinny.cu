@@ -2,7 +2,7 @@
 // output tiles: decode batches and other short products, where the time is
 // the stream of W and every SM has to take part in it.
 //
-// One cluster of 1, 2, 4 or 8 CTAs computes one (128 tokens x tile_n) tile of
+// One cluster of 1, 2 or 4 CTAs computes one (128 tokens x tile_n) tile of
 // Y, its CTAs splitting K and the tile's adapter steps evenly: each streams its
 // share of X and W through a TMA ring and accumulates with tcgen05.mma into its
 // own tensor memory, then the fp32 sums are added through distributed shared
@@ -38,7 +38,7 @@ constexpr int kSkinnyThreads = 192;
 
 __device__ __forceinline__ float4 peer_f4(uint32_t addr) {
     float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
     return v;
 }
 
@@ -255,45 +255,57 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1) skinny_kernel(const __grid_
         const int pieces = p.tile_n / 4, all = rows * pieces;
         const int i1 = all * (r + 1) / KS;
         const uint32_t mine = smem_u32(ring);
-        for (int i = all * r / KS + (int)threadIdx.x; i < i1; i += kSkinnyThreads) {
-            const int row = i / pieces, c = (i - row * pieces) * 4;
-            const uint32_t at = (uint32_t)(row * p.sum_pitch + c) * 4u;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (KS > 1) {
-                for (int q = 0; q < KS; ++q) {
-                    const float4 x = peer_f4(map_to_cta(mine, (uint32_t)q) + at);
-                    v.x += x.x;
-                    v.y += x.y;
-                    v.z += x.z;
-                    v.w += x.w;
-                }
-            } else {
-                v = *reinterpret_cast<const float4*>(ring + at);
+        constexpr int kAhead = 4;      // pieces of a thread whose loads are in flight
+        for (int i0 = all * r / KS + (int)threadIdx.x; i0 < i1; i0 += kAhead * kSkinnyThreads) {
+            float4 x[kAhead][kSkinnyMaxSplit];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int i = i0 + u * kSkinnyThreads;
+                if (i >= i1) break;
+                const uint32_t at = mine + (uint32_t)(i / pieces * p.sum_pitch + i % pieces * 4) * 4u;
+#pragma unroll
+                for (int q = 0; q < kSkinnyMaxSplit; ++q)
+                    if (q < KS) x[u][q] = peer_f4(KS > 1 ? map_to_cta(at, (uint32_t)q) : at);
             }
-            const int n = n0 + c;
-            if (n >= p.N) continue;
-            const int64_t o = (int64_t)(m0 + row) * p.ldy + n;
-            const float f[4] = {v.x, v.y, v.z, v.w};
-            if constexpr (OUT == GEMM_F32) {
-                float* y = static_cast<float*>(p.y) + o;
-                if (n + 4 <= p.N) {
-                    *reinterpret_cast<float4*>(y) = v;
-                } else {
-                    for (int j = 0; n + j < p.N; ++j) y[j] = f[j];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int i = i0 + u * kSkinnyThreads;
+                if (i >= i1) break;
+                const int row = i / pieces, c = (i - row * pieces) * 4;
+                float4 v = x[u][0];
+#pragma unroll
+                for (int q = 1; q < kSkinnyMaxSplit; ++q) {
+                    if (q >= KS) break;
+                    v.x += x[u][q].x;
+                    v.y += x[u][q].y;
+                    v.z += x[u][q].z;
+                    v.w += x[u][q].w;
                 }
-            } else {
-                uint16_t* y = static_cast<uint16_t*>(p.y) + o;
-                const uint2 w = make_uint2(pack2<OUT>(f[0], f[1]), pack2<OUT>(f[2], f[3]));
-                if (n + 4 <= p.N) {
-                    *reinterpret_cast<uint2*>(y) = w;
+                const int n = n0 + c;
+                if (n >= p.N) continue;
+                const int64_t o = (int64_t)(m0 + row) * p.ldy + n;
+                const float f[4] = {v.x, v.y, v.z, v.w};
+                if constexpr (OUT == GEMM_F32) {
+                    float* y = static_cast<float*>(p.y) + o;
+                    if (n + 4 <= p.N) {
+                        *reinterpret_cast<float4*>(y) = v;
+                    } else {
+                        for (int j = 0; n + j < p.N; ++j) y[j] = f[j];
+                    }
                 } else {
-                    const uint16_t h[4] = {(uint16_t)w.x, (uint16_t)(w.x >> 16), (uint16_t)w.y, (uint16_t)(w.y >> 16)};
-                    for (int j = 0; n + j < p.N; ++j) y[j] = h[j];
+                    uint16_t* y = static_cast<uint16_t*>(p.y) + o;
+                    const uint2 w = make_uint2(pack2<OUT>(f[0], f[1]), pack2<OUT>(f[2], f[3]));
+                    if (n + 4 <= p.N) {
+                        *reinterpret_cast<uint2*>(y) = w;
+                    } else {
+                        const uint16_t h[4] = {(uint16_t)w.x, (uint16_t)(w.x >> 16), (uint16_t)w.y, (uint16_t)(w.y >> 16)};
+                        for (int j = 0; n + j < p.N; ++j) y[j] = h[j];
+                    }
                 }
             }
         }
     }
-    if (KS > 1) cluster_sync(); else __syncthreads();     // peers have read this CTA's sums
+    if (KS > 1) cluster_sync_relaxed(); else __syncthreads();     // peers have read this CTA's sums
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc<1>(tmem, (uint32_t)p.tmem_cols);

@@ -11,6 +11,7 @@
 namespace dgb {
 
 constexpr int kSkinnyMaxStages = 16;
+constexpr int kSkinnyMaxSplit = 4;    // CTAs of a cluster
 
 struct SkinnyParams {
     CUtensorMap tmap_x;       // X: (K, tokens), box (64, box_m), 128-byte swizzle
