@@ -95,6 +95,9 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
     __shared__ int join_now;
     constexpr int kTokens = S::kTokens;
     constexpr uint32_t kFull = kTokens == 32 ? 0xFFFFFFFFu : 0xFFFFu;
+    // Probabilities are held times 2^kShift, which O and l share.  As f16 operands they keep their 11 bits down to 2^-29 that
+    // way (2^-14 without); 2^15 is the largest power whose probability of one is a finite f16.
+    constexpr float kShift = std::is_same<T, __half>::value ? 15.f : 0.f;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quad = lane >> 2, j4 = lane & 3;
@@ -410,7 +413,7 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
                 for (int i = 0; i < 2; ++i)
                     if (!((mask >> (n * 8 + 2 * j4 + i)) & 1u)) s[n][i] = s[n][i + 2] = -INFINITY;
         }
-        // Running maximum in log2 units (the scale sc is positive, see load_query), then the probabilities.
+        // Running maximum in log2 units (the scale sc is positive, see load_query), then the probabilities times 2^kShift.
         auto softmax_rows = [&](int h, float sc, float& m, float& l) {
             float top = fmaxf(s[0][2 * h], s[0][2 * h + 1]);
 #pragma unroll
@@ -432,8 +435,8 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
             float sum = 0.f;
 #pragma unroll
             for (int n = 0; n < kN; ++n) {
-                s[n][2 * h] = exp2_fast(fmaf(s[n][2 * h], sc, -m));
-                s[n][2 * h + 1] = exp2_fast(fmaf(s[n][2 * h + 1], sc, -m));
+                s[n][2 * h] = exp2_fast(fmaf(s[n][2 * h], sc, kShift - m));
+                s[n][2 * h + 1] = exp2_fast(fmaf(s[n][2 * h + 1], sc, kShift - m));
                 sum += s[n][2 * h] + s[n][2 * h + 1];
             }
             l += sum;
@@ -500,7 +503,7 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
     };
     constexpr float kLn2 = 0.693147180559945309f;
     auto write_lse = [&](int b, int row, float m, float l) {
-        if (p.a.lse) p.a.lse[(int64_t)b * p.heads + head0 + row] = l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (p.a.lse) p.a.lse[(int64_t)b * p.heads + head0 + row] = l > 0.f || l != l ? (m + (log2f(l) - kShift)) * kLn2 : -INFINITY;
     };
 
     // The segment's positions of this CTA are done: join the warps, then write or leave a partial.  Each warp lays its O

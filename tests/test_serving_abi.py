@@ -1,0 +1,230 @@
+"""Host-side tests of include/serving.h (no GPU): the library exports every declared function, the binding's structures
+have the header's layout, requests that cannot be served are refused before any device is touched, and rope_table is
+its formulas."""
+import ctypes
+import math
+import os
+import shutil
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+import dense_gemm_blackwell_gb300 as dg
+from dense_gemm_blackwell_gb300 import serving
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    dg.build()
+
+
+def test_library_exports_every_declared_function():
+    names = dg.serving_header_functions()
+    assert {"lora_plan_create", "lora_run", "lora_sync_status", "lora_plan_destroy", "qk_norm_rope_run", "qk_norm_rope_backward",
+            "qk_norm_rope_backward_workspace", "paged_attn_plan_create", "paged_attn_run", "paged_attn_plan_destroy"} <= set(names)
+    raw = ctypes.CDLL(dg._LIB_PATH)
+    for n in names:
+        assert hasattr(raw, n), n
+
+
+@pytest.mark.skipif(shutil.which("gcc") is None, reason="no C compiler")
+def test_structures_match_the_header(tmp_path):
+    pairs = {"lora_desc_t": serving.LoraDesc, "lora_args_t": serving.LoraArgs, "lora_plan_info_t": serving.LoraPlanInfo,
+             "qk_norm_rope_args_t": serving.QkNormRopeArgs, "qk_norm_rope_grads_t": serving.QkNormRopeGrads,
+             "paged_attn_desc_t": serving.PagedAttnDesc, "paged_attn_plan_info_t": serving.PagedAttnPlanInfo,
+             "paged_attn_args_t": serving.PagedAttnArgs}
+    lines = []
+    for name, cls in pairs.items():
+        lines.append('printf("%s - %%zu\\n", sizeof(%s));' % (name, name))
+        for field, _ in cls._fields_:
+            lines.append('printf("%s %s %%zu\\n", offsetof(%s, %s));' % (name, field, name, field))
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "serving.h"\nint main(void) {\n%s\nreturn 0;\n}\n' % "\n".join(lines))
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-std=c99", "-I" + os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    for line in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.splitlines():
+        name, field, value = line.split()
+        cls = pairs[name]
+        assert int(value) == (ctypes.sizeof(cls) if field == "-" else getattr(cls, field).offset), line
+
+
+def no_device_or_ok(status):
+    return status == (dg.GEMM_OK if torch.cuda.is_available() else dg.GEMM_ERR_NO_DEVICE)
+
+
+def lora_status(**kw):
+    d = serving.LoraDesc()
+    base = dict(tokens=16, n=64, k=64, rank=16, adapters=4, dtype=dg.GEMM_BF16, dtype_y=dg.GEMM_BF16)
+    for name, value in {**base, **kw}.items():
+        setattr(d, name, value)
+    h = ctypes.c_void_p()
+    s = serving._lib().lora_plan_create(ctypes.byref(h), ctypes.byref(d))
+    if s == dg.GEMM_OK:
+        serving._lib().lora_plan_destroy(h)
+    return s
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(tokens=-1), dg.GEMM_ERR_INVALID_ARG), (dict(n=0), dg.GEMM_ERR_INVALID_ARG), (dict(k=0), dg.GEMM_ERR_INVALID_ARG),
+    (dict(rank=0), dg.GEMM_ERR_INVALID_ARG), (dict(adapters=0), dg.GEMM_ERR_INVALID_ARG),
+    (dict(rank=12), dg.GEMM_ERR_UNSUPPORTED), (dict(rank=264), dg.GEMM_ERR_UNSUPPORTED),
+    (dict(adapters=4097), dg.GEMM_ERR_UNSUPPORTED), (dict(dtype=dg.GEMM_F32), dg.GEMM_ERR_UNSUPPORTED),
+    (dict(dtype=dg.GEMM_E4M3), dg.GEMM_ERR_UNSUPPORTED), (dict(dtype_y=dg.GEMM_E4M3), dg.GEMM_ERR_UNSUPPORTED),
+    (dict(tile_n=512), dg.GEMM_ERR_UNSUPPORTED), (dict(tokens=65535 * 64 + 1), dg.GEMM_ERR_UNSUPPORTED),
+    (dict(flags=dg.GEMM_FLAG_SINGLE_CTA), dg.GEMM_ERR_UNSUPPORTED), (dict(flags=dg.GEMM_FLAG_ACCUM_F16), dg.GEMM_ERR_UNSUPPORTED),
+])
+def test_lora_plan_refuses(kw, status):
+    assert lora_status(**kw) == status
+
+
+def test_lora_plan_accepts_what_it_documents():
+    for kw in (dict(), dict(rank=8), dict(rank=256, adapters=4096), dict(tokens=0), dict(dtype=dg.GEMM_F16, dtype_y=dg.GEMM_F32)):
+        assert no_device_or_ok(lora_status(**kw)), kw
+    assert serving._lib().lora_plan_create(None, None) == dg.GEMM_ERR_INVALID_ARG
+    assert serving._lib().lora_run(None, None, None) == dg.GEMM_ERR_INVALID_ARG
+    assert serving._lib().lora_plan_info(None, None) == dg.GEMM_ERR_INVALID_ARG
+    assert serving._lib().lora_sync_status(None, None, None) == dg.GEMM_ERR_INVALID_ARG
+    assert serving._lib().lora_plan_destroy(None) == dg.GEMM_OK
+
+
+def rope_args(**kw):
+    """A complete forward request on made-up, aligned addresses (never dereferenced: refusals come first)."""
+    a = serving.QkNormRopeArgs()
+    base = dict(tokens=4, heads=2, kv_heads=1, head_dim=64, rot_dim=64, norm=1, dtype=dg.GEMM_BF16, eps=1e-6, table_rows=8,
+                table=1 << 20, positions=1 << 21, q_weight=1 << 22, k_weight=1 << 22, q=1 << 23, k=1 << 24, q_token=192, q_head=64,
+                k_token=192, k_head=64, q_out=1 << 25, k_out=1 << 26, q_out_token=128, q_out_head=64, k_out_token=64, k_out_head=64,
+                dtype_cache=dg.GEMM_BF16, page_size=16, num_pages=4, k_scale=1.0, v_scale=1.0)
+    for name, value in {**base, **kw}.items():
+        setattr(a, name, value)
+    return a
+
+
+CACHE = dict(v=1 << 27, v_token=192, v_head=64, k_cache=1 << 28, v_cache=1 << 29, k_page=1024, k_place=64, k_chead=64, v_page=1024,
+             v_place=64, v_chead=64, slots=1 << 30)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(tokens=-1), dg.GEMM_ERR_INVALID_ARG), (dict(rot_dim=66), dg.GEMM_ERR_INVALID_ARG), (dict(rot_dim=31), dg.GEMM_ERR_INVALID_ARG),
+    (dict(head_dim=60, rot_dim=32), dg.GEMM_ERR_UNSUPPORTED), (dict(head_dim=264, rot_dim=64), dg.GEMM_ERR_UNSUPPORTED),
+    (dict(dtype=dg.GEMM_F32), dg.GEMM_ERR_UNSUPPORTED), (dict(table=None), dg.GEMM_ERR_INVALID_ARG),
+    (dict(positions=None), dg.GEMM_ERR_INVALID_ARG), (dict(table_rows=0), dg.GEMM_ERR_INVALID_ARG), (dict(q=None), dg.GEMM_ERR_INVALID_ARG),
+    (dict(q_out=None), dg.GEMM_ERR_INVALID_ARG), (dict(k_out=None), dg.GEMM_ERR_INVALID_ARG), (dict(q=(1 << 23) + 2), dg.GEMM_ERR_ALIGNMENT),
+    (dict(q_token=196), dg.GEMM_ERR_ALIGNMENT), (dict(k_out_head=60), dg.GEMM_ERR_ALIGNMENT), (dict(q_weight=(1 << 22) + 8), dg.GEMM_ERR_ALIGNMENT),
+    (dict(CACHE, v=None), dg.GEMM_ERR_INVALID_ARG), (dict(CACHE, slots=None), dg.GEMM_ERR_INVALID_ARG),
+    (dict(CACHE, v_cache=None), dg.GEMM_ERR_INVALID_ARG), (dict(CACHE, page_size=0), dg.GEMM_ERR_INVALID_ARG),
+    (dict(CACHE, dtype_cache=dg.GEMM_F16), dg.GEMM_ERR_UNSUPPORTED), (dict(CACHE, dtype_cache=dg.GEMM_E4M3, k_scale=0.0), dg.GEMM_ERR_INVALID_ARG),
+    (dict(CACHE, k_place=68), dg.GEMM_ERR_ALIGNMENT), (dict(CACHE, k_cache=(1 << 28) + 8), dg.GEMM_ERR_ALIGNMENT),
+])
+def test_rope_refuses(kw, status):
+    assert serving._lib().qk_norm_rope_run(ctypes.byref(rope_args(**kw)), None) == status
+
+
+def test_rope_without_work_is_a_no_op():
+    assert serving._lib().qk_norm_rope_run(ctypes.byref(rope_args(tokens=0, q=None, k=None)), None) == dg.GEMM_OK
+    assert serving._lib().qk_norm_rope_run(ctypes.byref(rope_args(heads=0, kv_heads=0, q=None, k=None)), None) == dg.GEMM_OK
+    assert serving._lib().qk_norm_rope_run(None, None) == dg.GEMM_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("args,grads,status", [
+    (dict(q_weight=None), dict(dq_weight=1 << 20), dg.GEMM_ERR_INVALID_ARG),      # a gradient of no weight
+    (dict(norm=0), dict(dq_weight=1 << 20), dg.GEMM_ERR_INVALID_ARG),
+    (dict(), dict(dq_weight=1 << 20, workspace=None), dg.GEMM_ERR_INVALID_ARG),
+    (dict(), dict(dq_weight=1 << 20, workspace_bytes=64), dg.GEMM_ERR_INVALID_ARG),
+    (dict(), dict(dq=None), dg.GEMM_ERR_INVALID_ARG), (dict(), dict(dk_out=None), dg.GEMM_ERR_INVALID_ARG),
+    (dict(), dict(dq_token=12), dg.GEMM_ERR_ALIGNMENT),
+])
+def test_rope_backward_refuses(args, grads, status):
+    g = serving.QkNormRopeGrads()
+    base = dict(dq_out=1 << 23, dk_out=1 << 24, dq=1 << 25, dk=1 << 26, dq_out_token=128, dq_out_head=64, dk_out_token=64, dk_out_head=64,
+                dq_token=128, dq_head=64, dk_token=64, dk_head=64, workspace=1 << 27,
+                workspace_bytes=serving._lib().qk_norm_rope_backward_workspace())
+    for name, value in {**base, **grads}.items():
+        setattr(g, name, value)
+    assert serving._lib().qk_norm_rope_backward(ctypes.byref(rope_args(**args)), ctypes.byref(g), None) == status
+
+
+def attn_status(**kw):
+    d = serving.PagedAttnDesc()
+    base = dict(max_batch=4, heads=8, kv_heads=2, head_dim=64, page_size=16, dtype=dg.GEMM_BF16, dtype_cache=dg.GEMM_BF16)
+    for name, value in {**base, **kw}.items():
+        setattr(d, name, value)
+    h = ctypes.c_void_p()
+    s = serving._lib().paged_attn_plan_create(ctypes.byref(h), ctypes.byref(d))
+    if s == dg.GEMM_OK:
+        serving._lib().paged_attn_plan_destroy(h)
+    return s
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(max_batch=-1), dg.GEMM_ERR_INVALID_ARG), (dict(heads=7), dg.GEMM_ERR_INVALID_ARG), (dict(kv_heads=0), dg.GEMM_ERR_INVALID_ARG),
+    (dict(page_size=0), dg.GEMM_ERR_INVALID_ARG), (dict(window=-1), dg.GEMM_ERR_INVALID_ARG), (dict(head_dim=60), dg.GEMM_ERR_UNSUPPORTED),
+    (dict(head_dim=264), dg.GEMM_ERR_UNSUPPORTED), (dict(head_dim=72, dtype_cache=dg.GEMM_E4M3), dg.GEMM_ERR_UNSUPPORTED),
+    (dict(dtype=dg.GEMM_F32), dg.GEMM_ERR_UNSUPPORTED), (dict(dtype_cache=dg.GEMM_F16), dg.GEMM_ERR_UNSUPPORTED),
+    (dict(dtype_cache=dg.GEMM_E5M2), dg.GEMM_ERR_UNSUPPORTED),
+])
+def test_paged_attn_plan_refuses(kw, status):
+    assert attn_status(**kw) == status
+
+
+def test_paged_attn_plan_accepts_what_it_documents():
+    for kw in (dict(), dict(head_dim=8), dict(head_dim=256, dtype=dg.GEMM_F16, dtype_cache=dg.GEMM_E4M3), dict(page_size=1), dict(max_batch=0)):
+        assert no_device_or_ok(attn_status(**kw)), kw
+    assert serving._lib().paged_attn_run(None, None, None) == dg.GEMM_ERR_INVALID_ARG
+    assert serving._lib().paged_attn_plan_destroy(None) == dg.GEMM_OK
+
+
+def test_python_layer_refuses_host_tensors():
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        dg.qk_norm_rope(x, None, torch.zeros(4, dtype=torch.int32), torch.zeros(8, 2, 32))
+
+
+# ---------------------------------------------------------------- rope_table
+
+def plain_table(positions, freq, gain=1.0):
+    a = np.outer(np.arange(positions, dtype=np.float64), freq)
+    return np.stack((np.cos(a) * gain, np.sin(a) * gain), 1)
+
+
+def test_rope_table_is_its_formulas():
+    """fp32 values of fp64 cosines: half an fp32 unit of values up to the gain, 2^-24 each; torch and numpy round cos and sin
+    differently by at most a few fp64 units of angles below 1e5 (1e5 * 2^-53 = 1.1e-11)."""
+    rot, n = 48, 999
+    i = np.arange(0, rot, 2)
+    plain = 500000.0 ** (-i / rot)
+    tol = 2.0 ** -24 + 1e-10
+
+    def check(table, want):
+        assert table.dtype == torch.float32 and tuple(table.shape) == (n, 2, rot // 2) and table.is_contiguous()
+        assert np.max(np.abs(table.double().numpy() - want)) <= tol * max(1.0, np.max(np.abs(want)))
+
+    check(dg.rope_table(n, rot, base=500000.0, device="cpu"), plain_table(n, plain))
+    check(dg.rope_table(n, rot, base=500000.0, factor=4.0, device="cpu"), plain_table(n, plain / 4))
+    stretched = (500000.0 * 4 ** (rot / (rot - 2))) ** (-i / rot)
+    assert stretched[0] == 1.0 and abs(stretched[-1] / plain[-1] - 0.25) < 1e-12      # fastest kept, slowest divided
+    check(dg.rope_table(n, rot, base=500000.0, factor=4.0, scaling="base", device="cpu"), plain_table(n, stretched))
+    # blend: pairs by the number of turns within the original context
+    orig, factor = 8192, 8.0
+    blended = dg.rope_table(n, rot, base=500000.0, factor=factor, scaling="blend", original_positions=orig, device="cpu")
+    index = lambda turns: rot * math.log(orig / (2 * math.pi * turns)) / (2 * math.log(500000.0))  # noqa: E731
+    low, high = max(math.floor(index(32)), 0), min(math.ceil(index(1)), rot - 1)
+    keep = 1 - np.clip((i / 2 - low) / (high - low), 0, 1)
+    turns = orig * plain / (2 * math.pi)
+    assert np.all(keep[turns > 80] == 1) and np.all(keep[turns < 0.5] == 0)
+    gain = 0.1 * math.log(factor) + 1
+    check(blended, plain_table(n, plain * keep + plain / factor * (1 - keep), gain))
+    check(dg.rope_table(n, rot, base=500000.0, factor=factor, scaling="blend", original_positions=orig, attention_factor=1.0, device="cpu"),
+          plain_table(n, plain * keep + plain / factor * (1 - keep)))
+
+
+@pytest.mark.parametrize("kw", [dict(rot_dim=3), dict(rot_dim=0), dict(positions=0), dict(scaling="other"), dict(factor=0.5),
+                                dict(factor=2.0, scaling="blend"), dict(rot_dim=2, factor=2.0, scaling="base")])
+def test_rope_table_refuses(kw):
+    args = dict(positions=8, rot_dim=8, device="cpu")
+    args.update(kw)
+    with pytest.raises(ValueError):
+        dg.rope_table(args.pop("positions"), args.pop("rot_dim"), **args)
