@@ -89,6 +89,13 @@ __device__ __forceinline__ void ldmatrix_x2(uint32_t addr, uint32_t (&r)[2]) {
                  : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
 }
 
+// An 8 x 8 matrix of 16-bit elements held like a fragment (lane l: row l / 4, columns 2 (l mod 4) and + 1), transposed.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
 // c (16 x 8, fp32) += a (16 x 16) * b (16 x 8), 16-bit operands.
 template <typename T>
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);

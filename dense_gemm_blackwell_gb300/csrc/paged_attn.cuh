@@ -4,12 +4,15 @@
 // paged_attn_bf16_e4m3.cu, paged_attn_f16_e4m3.cu).
 //
 // out = softmax(scale q K^T) V for the query heads that share a kv head.  The
-// cache's keys and values are read once, so the kernel is bound by memory; the
-// arithmetic (4 flops per cache element and query head) is kept off the
-// critical path by warp-level matrix instructions with the shared query heads
-// as the 16 rows of the tile.
+// cache's keys and values are read once, so the kernel should be bound by
+// memory; the arithmetic (4 flops per cache element and query head) runs on
+// warp-level matrix instructions.  Their 16-row side holds what there is much
+// of -- positions in S^T = K Q^T, head elements in O^T = V^T P^T -- and their
+// 8-column side the query heads, so up to eight shared heads waste nothing: with
+// the heads as the 16 rows a step took twice the instructions, and on GB300 its
+// latency, not the loads, was the bound (64 ragged sequences: 50.6 us).
 //
-// Work.  A segment is one (sequence, kv head, group of up to 16 query heads);
+// Work.  A segment is one (sequence, kv head, group of 8 or 16 query heads);
 // its positions are cut into tiles of four warps' steps.  All segments' tiles,
 // laid end to end with kAttnSegmentCost empty units before each segment (what
 // starting and ending one costs), are cut into equal contiguous ranges, one
@@ -21,8 +24,7 @@
 // results do not depend on timing.
 //
 // Inside a CTA each of four warps takes its own positions of every tile (16,
-// or 32 where rows are short): its own copy pipeline (kAttnStages deep, no
-// block barrier), its own running maximum and sum, joined with the other
+// or 32 where rows are short): its own copy pipeline (no block barrier), its own running maximum and sum, joined with the other
 // warps' at the segment's end in the pipeline slots just consumed.  The copies
 // run ahead across segment ends.  Rows of K and V lie in shared memory at an
 // odd number of 16-byte chunks apart, so the eight rows of a matrix load fall
@@ -44,8 +46,11 @@ namespace dgb {
 
 __host__ __device__ constexpr int next_pow2(int v) { return v <= 1 ? 1 : 2 * next_pow2((v + 1) / 2); }
 
-template <int KD, bool FP8>
+// KD: 16-element blocks of a head; NH: 8-head tiles of a segment.
+template <int KD, bool FP8, int NH>
 struct AttnShape {
+    static constexpr int kHeads = 8 * NH;
+    static constexpr int kStages = 3;                    // steps in flight per warp
     static constexpr int kDim = KD * 16;                 // head elements held (head_dim rounded up)
     static constexpr int kBytes = FP8 ? 1 : 2;
     static constexpr int kChunks = KD * kBytes;          // 16-byte chunks of a row
@@ -54,12 +59,12 @@ struct AttnShape {
     static constexpr int kPitch = (kChunks | 1) * 16;    // bytes between rows
     static constexpr int kRowsBytes = kTokens * kPitch;
     static constexpr int kMergePitch = kDim + 4;         // floats; a slot also takes one warp's O at a segment's end
-    static constexpr int kMergeBytes = 16 * kMergePitch * 4;
+    static constexpr int kMergeBytes = kHeads * kMergePitch * 4;
     static constexpr int kStageBytes = 2 * kRowsBytes > kMergeBytes ? 2 * kRowsBytes : kMergeBytes;
-    static constexpr int kRingBytes = kAttnWarps * kAttnStages * kStageBytes;
+    static constexpr int kRingBytes = kAttnWarps * kStages * kStageBytes;
     static constexpr int kAddrBytes = kAttnWarps * kTokens * 16;
     static constexpr int kSmemBytes = kRingBytes + kAddrBytes;
-    static constexpr int kSlotFloats = 16 * kDim + 32;   // one partial: O, m, l
+    static constexpr int kSlotFloats = kHeads * (kDim + 2);   // one partial: O, m, l
     // copies: a power of two of lanes per row
     static constexpr int kLanesPerRow = next_pow2(kChunks);
     static constexpr int kRowsPerCopy = 32 / kLanesPerRow;
@@ -83,15 +88,15 @@ __device__ __forceinline__ int tiles_of(int first, int length) {
     return (int)(((uint32_t)(length - first) + (TILE - 1)) / TILE);
 }
 
-template <typename T, typename TQ, bool FP8, int KD>
+template <typename T, typename TQ, bool FP8, int KD, int NH>
 __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kernel(const __grid_constant__ AttnParams p) {
-    using S = AttnShape<KD, FP8>;
+    using S = AttnShape<KD, FP8, NH>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t scan_part[kAttnWarps];
     __shared__ int found_b;
     __shared__ int64_t found_rest;
-    __shared__ float warp_m[kAttnWarps][16], warp_l[kAttnWarps][16];
-    __shared__ uint32_t stage_mask[kAttnWarps][kAttnStages];
+    __shared__ float warp_m[kAttnWarps][S::kHeads], warp_l[kAttnWarps][S::kHeads];
+    __shared__ uint32_t stage_mask[kAttnWarps][S::kStages];
     __shared__ int join_now;
     constexpr int kTokens = S::kTokens;
     constexpr uint32_t kFull = kTokens == 32 ? 0xFFFFFFFFu : 0xFFFFu;
@@ -103,7 +108,7 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
     const int quad = lane >> 2, j4 = lane & 3;
     const int HV = p.segments_per_sequence;
     const int B = p.a.batch;
-    uint8_t* ring = smem + (size_t)warp * kAttnStages * S::kStageBytes;
+    uint8_t* ring = smem + (size_t)warp * S::kStages * S::kStageBytes;
     longlong2* addr = reinterpret_cast<longlong2*>(smem + S::kRingBytes) + warp * kTokens;
     const int row_chunks = p.head_dim * S::kBytes / 16;
     if (row_chunks < S::kChunks) {
@@ -225,23 +230,29 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
     const uint8_t* kbase = static_cast<const uint8_t*>(p.a.k_cache) + copy_chunk * 16;
     const uint8_t* vbase = static_cast<const uint8_t*>(p.a.v_cache) + copy_chunk * 16;
     const int64_t k_place = p.a.k_place * S::kBytes, v_place = p.a.v_place * S::kBytes;
-    int next_page = -1, next_place = 0, next_head = 0;
-    bool next_live = false;
+    struct Next {
+        int page, place, head;
+        bool live;
+    };
     auto fetch = [&]() {
-        next_live = ahead.left > 0;
-        if (!next_live) return;
+        Next next;
+        next.live = ahead.left > 0;
+        next.page = -1;
+        next.place = next.head = 0;
+        if (!next.live) return next;
         const uint32_t pos = (uint32_t)ahead.first + (uint32_t)ahead.tile * S::kTile + warp * kTokens + (lane & (kTokens - 1));
-        next_page = -1;
-        next_head = ahead.hv / p.head_groups;
+        next.head = ahead.hv / p.head_groups;
         if (pos < (uint32_t)ahead.length) {
             const int col = p.page_shift >= 0 ? (int)(pos >> p.page_shift) : (int)(pos / (uint32_t)p.page_size);
-            next_place = (int)pos - col * p.page_size;
-            next_page = p.a.block_table[ahead.b * p.a.table_stride + col];
+            next.place = (int)pos - col * p.page_size;
+            next.page = p.a.block_table[ahead.b * p.a.table_stride + col];
         }
         advance(ahead);
+        return next;
     };
-    auto issue = [&](int stage) {
-        if (next_live) {
+    auto issue = [&](const Next& next, int stage) {
+        const int next_page = next.page, next_place = next.place, next_head = next.head;
+        if (next.live) {
             const bool have = next_page >= 0 && next_page < p.a.num_pages;
             const int page0 = __shfl_sync(0xffffffffu, next_page, 0);
             const uint32_t mask = __ballot_sync(0xffffffffu, have) & kFull;
@@ -288,219 +299,212 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
     };
 
     // ---------------------------------------------------------------- state of the running softmax
-    uint32_t q[KD][4];
-    float o[2 * KD][4];
-    float m0 = -FLT_MAX, m1 = -FLT_MAX, l0 = 0.f, l1 = 0.f;   // rows quad and quad + 8
-    float sc0 = 0.f, sc1 = 0.f;                               // score -> log2 units
-    int rows = 0, head0 = 0;
+    // O^T: o[n][blk], heads n * 8 + 2 j4 and + 1 (elements 0, 2 and 1, 3), dims of block blk: quad and quad + 8 (elements 0, 1
+    // and 2, 3), or 2 quad and 2 quad + 1 for E4M3 caches.  m, l: of the same two heads of each tile.
+    uint32_t q[NH][KD][2];
+    float o[NH][KD][4];
+    float m[NH][2], l[NH][2];
+    float sc[NH][2];                                          // score -> log2 units
+    int rows = 0, head0 = 0;                                  // the segment's query heads
     bool first_segment = true;
 
     auto load_query = [&]() {
         const int kvh = at.hv / p.head_groups, hg = at.hv - kvh * p.head_groups;
-        head0 = kvh * p.group + hg * 16;
-        rows = min(16, p.group - hg * 16);
-        const TQ* q0 = static_cast<const TQ*>(p.a.q) + at.b * p.a.q_batch + (int64_t)(head0 + quad) * p.a.q_head;
-        const TQ* q1 = q0 + 8 * p.a.q_head;
-        const bool in0 = quad < rows, in1 = quad + 8 < rows;
+        head0 = kvh * p.group + hg * S::kHeads;
+        rows = min(S::kHeads, p.group - hg * S::kHeads);
 #pragma unroll
-        for (int kk = 0; kk < KD; ++kk) {
-            // the two element pairs of this lane: (2j, 2j+1) and (2j+8, 2j+9), or, for E4M3 caches, four neighbours
-            // (the product's order over the head dimension is free; see the key fragments)
-            const int da = kk * 16 + (FP8 ? 4 * j4 : 2 * j4), db = FP8 ? da + 2 : da + 8;
-            q[kk][0] = in0 && da < p.head_dim ? *reinterpret_cast<const uint32_t*>(q0 + da) : 0u;
-            q[kk][1] = in1 && da < p.head_dim ? *reinterpret_cast<const uint32_t*>(q1 + da) : 0u;
-            q[kk][2] = in0 && db < p.head_dim ? *reinterpret_cast<const uint32_t*>(q0 + db) : 0u;
-            q[kk][3] = in1 && db < p.head_dim ? *reinterpret_cast<const uint32_t*>(q1 + db) : 0u;
-        }
-        sc0 = sc1 = p.score_log2;
-        if (p.negate) {
+        for (int n = 0; n < NH; ++n) {
+            const TQ* row = static_cast<const TQ*>(p.a.q) + at.b * p.a.q_batch + (int64_t)(head0 + n * 8 + quad) * p.a.q_head;
+            const bool in = n * 8 + quad < rows;
 #pragma unroll
-            for (int kk = 0; kk < KD; ++kk)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) q[kk][i] ^= 0x80008000u;
-        }
-        if constexpr (FP8 && !std::is_same<T, TQ>::value) {
-            // bf16 queries against f16 keys: each row is scaled by a power of two to a largest element in [1, 2)
-            // (exact; elements 2^-24 of the largest and smaller lose bits) and its scores are scaled back
-            float top0 = 0.f, top1 = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < KD; ++kk)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 v = unpack2<TQ>(q[kk][i]);
-                    float& top = (i & 1) ? top1 : top0;
-                    top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
-                }
-#pragma unroll
-            for (int s = 1; s < 4; s <<= 1) {
-                top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, s));
-                top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, s));
+            for (int kk = 0; kk < KD; ++kk) {
+                // the two element pairs of this lane: (2j, 2j+1) and (2j+8, 2j+9), or, for E4M3 caches, four neighbours
+                // (the product's order over the head dimension is free; see the key fragments)
+                const int da = kk * 16 + (FP8 ? 4 * j4 : 2 * j4), db = FP8 ? da + 2 : da + 8;
+                q[n][kk][0] = in && da < p.head_dim ? *reinterpret_cast<const uint32_t*>(row + da) : 0u;
+                q[n][kk][1] = in && db < p.head_dim ? *reinterpret_cast<const uint32_t*>(row + db) : 0u;
             }
-            // biased exponents, kept where 2^e and 2^-e are normal numbers
-            const int e0 = min(max((int)(__float_as_uint(top0) >> 23), 1), 252);
-            const int e1 = min(max((int)(__float_as_uint(top1) >> 23), 1), 252);
-            const float d0 = __uint_as_float((uint32_t)(254 - e0) << 23), d1 = __uint_as_float((uint32_t)(254 - e1) << 23);
-            sc0 = fmaxf(sc0 * __uint_as_float((uint32_t)e0 << 23), FLT_MIN);
-            sc1 = fmaxf(sc1 * __uint_as_float((uint32_t)e1 << 23), FLT_MIN);
-#pragma unroll
-            for (int kk = 0; kk < KD; ++kk)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 v = unpack2<TQ>(q[kk][i]);
-                    const float d = (i & 1) ? d1 : d0;
-                    q[kk][i] = round2<T>(v.x * d, v.y * d);
-                }
         }
 #pragma unroll
-        for (int n = 0; n < 2 * KD; ++n)
+        for (int n = 0; n < NH; ++n) {
+            sc[n][0] = sc[n][1] = p.score_log2;
+            if (p.negate) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
-        m0 = m1 = -FLT_MAX;
-        l0 = l1 = 0.f;
+                for (int kk = 0; kk < KD; ++kk) {
+                    q[n][kk][0] ^= 0x80008000u;
+                    q[n][kk][1] ^= 0x80008000u;
+                }
+            }
+            if constexpr (FP8 && !std::is_same<T, TQ>::value) {
+                // bf16 queries against f16 keys: each head is scaled by a power of two to a largest element in [1, 2)
+                // (exact; elements 2^-14 of the largest and smaller lose bits) and its scores are scaled back
+                float top = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < KD; ++kk)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 v = unpack2<TQ>(q[n][kk][i]);
+                        top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+                    }
+#pragma unroll
+                for (int s = 1; s < 4; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+                // biased exponent, kept where 2^e and 2^-e are normal numbers
+                const int e = min(max((int)(__float_as_uint(top) >> 23), 1), 252);
+                const float down = __uint_as_float((uint32_t)(254 - e) << 23);
+                const float up = __uint_as_float((uint32_t)e << 23);
+#pragma unroll
+                for (int kk = 0; kk < KD; ++kk)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 v = unpack2<TQ>(q[n][kk][i]);
+                        q[n][kk][i] = round2<T>(v.x * down, v.y * down);
+                    }
+                // this lane loaded head quad and scales scores of heads 2 j4 and 2 j4 + 1
+                sc[n][0] = fmaxf(sc[n][0] * __shfl_sync(0xffffffffu, up, 8 * j4), FLT_MIN);
+                sc[n][1] = fmaxf(sc[n][1] * __shfl_sync(0xffffffffu, up, 8 * j4 + 4), FLT_MIN);
+            }
+#pragma unroll
+            for (int blk = 0; blk < KD; ++blk)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[n][blk][i] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                m[n][i] = -FLT_MAX;
+                l[n][i] = 0.f;
+            }
+        }
     };
 
     auto compute = [&](int stage) {
         const uint32_t mask = stage_mask[warp][stage];
         if (!mask) return;
         const uint32_t ks = smem_u32(ring + (size_t)stage * S::kStageBytes), vs = ks + S::kRowsBytes;
-        const bool two = rows > 8;              // rows 8..15 hold queries
-        constexpr int kN = kTokens / 8;         // 8-position column tiles of S
-        float s[kN][4];
+        constexpr int kT = kTokens / 16;        // 16-position row tiles of S^T
+        float s[NH][kT][4];
 #pragma unroll
-        for (int t = 0; t < kTokens / 16; ++t) {
-            // two accumulators per column tile: the chains of dependent products are half as long
-            float x[2][4] = {}, y[2][4] = {};
+        for (int t = 0; t < kT; ++t) {
+            // two accumulators: the chains of dependent products are half as long
+            float x[NH][4] = {}, y[NH][4] = {};
             if constexpr (FP8) {
-                // one 32-bit word of a lane is four neighbouring elements of its row: two f16 pairs, the b0 and b1 of one step
-                const uint32_t row = t * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
-                const uint32_t base = ks + row * S::kPitch + (lane >> 4) * 16;
+                // One 32-bit word of a lane is four neighbouring elements of its row: two f16 pairs, the two k halves of one
+                // step.  A load covers two 16-element blocks.
+                const uint32_t base = ks + (t * 16 + (lane & 15)) * S::kPitch;
 #pragma unroll
                 for (int kk = 0; kk < KD; kk += 2) {
+                    uint32_t r[4];
+                    ldmatrix_x4(base + (kk + (kk + 1 < KD ? (lane >> 4) : 0)) * 16, r);
+                    const uint32_t a0[4] = {e4m3x2_to_half2(r[0]), e4m3x2_to_half2(r[1]), e4m3x2_to_half2(r[0] >> 16),
+                                            e4m3x2_to_half2(r[1] >> 16)};
+#pragma unroll
+                    for (int n = 0; n < NH; ++n) mma_16816<T>(x[n], a0, q[n][kk][0], q[n][kk][1]);
                     if (kk + 1 < KD) {
-                        uint32_t r[4];
-                        ldmatrix_x4(base + kk * 16, r);
-                        mma_16816<T>(x[0], q[kk], e4m3x2_to_half2(r[0]), e4m3x2_to_half2(r[0] >> 16));
-                        mma_16816<T>(x[1], q[kk], e4m3x2_to_half2(r[1]), e4m3x2_to_half2(r[1] >> 16));
-                        mma_16816<T>(y[0], q[kk + 1], e4m3x2_to_half2(r[2]), e4m3x2_to_half2(r[2] >> 16));
-                        mma_16816<T>(y[1], q[kk + 1], e4m3x2_to_half2(r[3]), e4m3x2_to_half2(r[3] >> 16));
-                    } else {
-                        uint32_t r[2];
-                        ldmatrix_x2(ks + (t * 16 + (lane & 15)) * S::kPitch + kk * 16, r);
-                        mma_16816<T>(x[0], q[kk], e4m3x2_to_half2(r[0]), e4m3x2_to_half2(r[0] >> 16));
-                        mma_16816<T>(x[1], q[kk], e4m3x2_to_half2(r[1]), e4m3x2_to_half2(r[1] >> 16));
+                        const uint32_t a1[4] = {e4m3x2_to_half2(r[2]), e4m3x2_to_half2(r[3]), e4m3x2_to_half2(r[2] >> 16),
+                                                e4m3x2_to_half2(r[3] >> 16)};
+#pragma unroll
+                        for (int n = 0; n < NH; ++n) mma_16816<T>(y[n], a1, q[n][kk + 1][0], q[n][kk + 1][1]);
                     }
                 }
             } else {
-                const uint32_t row = t * 16 + (lane & 7) + (lane >> 4) * 8;
-                const uint32_t base = ks + row * S::kPitch + ((lane >> 3) & 1) * 16;
+                const uint32_t base = ks + (t * 16 + (lane & 15)) * S::kPitch + (lane >> 4) * 16;
 #pragma unroll
                 for (int kk = 0; kk < KD; ++kk) {
-                    uint32_t r[4];
-                    ldmatrix_x4(base + kk * 32, r);
-                    mma_16816<T>(kk & 1 ? y[0] : x[0], q[kk], r[0], r[1]);
-                    mma_16816<T>(kk & 1 ? y[1] : x[1], q[kk], r[2], r[3]);
+                    uint32_t a[4];
+                    ldmatrix_x4(base + kk * 32, a);
+#pragma unroll
+                    for (int n = 0; n < NH; ++n) mma_16816<T>(kk & 1 ? y[n] : x[n], a, q[n][kk][0], q[n][kk][1]);
                 }
             }
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < NH; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[2 * t + n][i] = x[n][i] + y[n][i];
+                for (int i = 0; i < 4; ++i) s[n][t][i] = x[n][i] + y[n][i];
         }
         if (mask != kFull) {
 #pragma unroll
-            for (int n = 0; n < kN; ++n)
+            for (int t = 0; t < kT; ++t)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (!((mask >> (n * 8 + 2 * j4 + i)) & 1u)) s[n][i] = s[n][i + 2] = -INFINITY;
+                for (int h = 0; h < 2; ++h)
+                    if (!((mask >> (t * 16 + quad + 8 * h)) & 1u)) {
+#pragma unroll
+                        for (int n = 0; n < NH; ++n) s[n][t][2 * h] = s[n][t][2 * h + 1] = -INFINITY;
+                    }
         }
-        // Running maximum in log2 units (the scale sc is positive, see load_query), then the probabilities times 2^kShift.
-        auto softmax_rows = [&](int h, float sc, float& m, float& l) {
-            float top = fmaxf(s[0][2 * h], s[0][2 * h + 1]);
+        // Running maxima in log2 units (the scales sc are positive, see load_query).
+        float top[NH][2];
+        bool grows = false;
 #pragma unroll
-            for (int n = 1; n < kN; ++n) top = fmaxf(top, fmaxf(s[n][2 * h], s[n][2 * h + 1]));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            top *= sc;
-            if (__any_sync(0xffffffffu, top > m)) {
-                const float fresh = fmaxf(m, top);
-                const float f = exp2_fast(m - fresh);
-                m = fresh;
-                l *= f;
+        for (int n = 0; n < NH; ++n)
 #pragma unroll
-                for (int n = 0; n < 2 * KD; ++n) {
-                    o[n][2 * h] *= f;
-                    o[n][2 * h + 1] *= f;
+            for (int i = 0; i < 2; ++i) {
+                float v = fmaxf(s[n][0][i], s[n][0][2 + i]);
+#pragma unroll
+                for (int t = 1; t < kT; ++t) v = fmaxf(v, fmaxf(s[n][t][i], s[n][t][2 + i]));
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+                top[n][i] = v * sc[n][i];
+                grows |= top[n][i] > m[n][i];
+            }
+        if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+            for (int n = 0; n < NH; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float fresh = fmaxf(m[n][i], top[n][i]);
+                    const float f = exp2_fast(m[n][i] - fresh);
+                    m[n][i] = fresh;
+                    l[n][i] *= f;
+#pragma unroll
+                    for (int blk = 0; blk < KD; ++blk) {
+                        o[n][blk][i] *= f;
+                        o[n][blk][2 + i] *= f;
+                    }
                 }
-            }
-            float sum = 0.f;
-#pragma unroll
-            for (int n = 0; n < kN; ++n) {
-                s[n][2 * h] = exp2_fast(fmaf(s[n][2 * h], sc, kShift - m));
-                s[n][2 * h + 1] = exp2_fast(fmaf(s[n][2 * h + 1], sc, kShift - m));
-                sum += s[n][2 * h] + s[n][2 * h + 1];
-            }
-            l += sum;
-        };
-        softmax_rows(0, sc0, m0, l0);
-        if (two) {
-            softmax_rows(1, sc1, m1, l1);
-        } else {
-#pragma unroll
-            for (int n = 0; n < kN; ++n) s[n][2] = s[n][3] = 0.f;
         }
+        // Probabilities times 2^kShift, as the 16-bit right operand P^T of the product with V (the matrix instruction takes
+        // 16-bit operands); their sum l is taken in fp32 before that rounding, O stays fp32.
 #pragma unroll
-        for (int t = 0; t < kTokens / 16; ++t) {
-            // Probabilities as the 16-bit left operand of the product with V (the matrix instruction takes 16-bit
-            // operands); their sum l is taken in fp32 before that rounding, O stays fp32.
-            const uint32_t a[4] = {round2<T>(s[2 * t][0], s[2 * t][1]), round2<T>(s[2 * t][2], s[2 * t][3]),
-                                   round2<T>(s[2 * t + 1][0], s[2 * t + 1][1]), round2<T>(s[2 * t + 1][2], s[2 * t + 1][3])};
-            const uint32_t vrow = vs + (t * 16 + (lane & 7) + ((lane >> 3) & 1) * 8) * S::kPitch;
+        for (int t = 0; t < kT; ++t) {
+            uint32_t b[NH][2];
+#pragma unroll
+            for (int n = 0; n < NH; ++n) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[n][t][i] = exp2_fast(fmaf(s[n][t][i], sc[n][i & 1], kShift - m[n][i & 1]));
+                l[n][0] += s[n][t][0] + s[n][t][2];
+                l[n][1] += s[n][t][1] + s[n][t][3];
+                b[n][0] = transpose_8x8(round2<T>(s[n][t][0], s[n][t][1]));
+                b[n][1] = transpose_8x8(round2<T>(s[n][t][2], s[n][t][3]));
+            }
             if constexpr (FP8) {
                 // a transposed load moves pairs of elements: bytes (t0 d0, t0 d1, t1 d0, t1 d1); reordered to pairs of
-                // tokens, the even elements of a 16-element block form one 8-column tile and the odd ones another
+                // positions, a 16-element block's even elements are rows 0..7 of its tile and its odd ones rows 8..15
+                const uint32_t base = vs + (t * 16 + (lane & 15)) * S::kPitch;
                 auto tile = [&](int blk, uint32_t lo, uint32_t hi) {
-                    const uint32_t x = __byte_perm(lo, 0u, 0x3120), y = __byte_perm(hi, 0u, 0x3120);
-                    mma_16816<T>(o[2 * blk], a, e4m3x2_to_half2(x), e4m3x2_to_half2(y));
-                    mma_16816<T>(o[2 * blk + 1], a, e4m3x2_to_half2(x >> 16), e4m3x2_to_half2(y >> 16));
+                    const uint32_t u = __byte_perm(lo, 0u, 0x3120), v = __byte_perm(hi, 0u, 0x3120);
+                    const uint32_t a[4] = {e4m3x2_to_half2(u), e4m3x2_to_half2(u >> 16), e4m3x2_to_half2(v), e4m3x2_to_half2(v >> 16)};
+#pragma unroll
+                    for (int n = 0; n < NH; ++n) mma_16816<T>(o[n][blk], a, b[n][0], b[n][1]);
                 };
 #pragma unroll
                 for (int blk = 0; blk < KD; blk += 2) {
                     uint32_t r[4];
                     // the last odd block loads its own chunk twice
-                    ldmatrix_x4_trans(vrow + (blk + (blk + 1 < KD ? (lane >> 4) : 0)) * 16, r);
+                    ldmatrix_x4_trans(base + (blk + (blk + 1 < KD ? (lane >> 4) : 0)) * 16, r);
                     tile(blk, r[0], r[1]);
                     if (blk + 1 < KD) tile(blk + 1, r[2], r[3]);
                 }
             } else {
+                const uint32_t base = vs + (t * 16 + (lane & 7) + (lane >> 4) * 8) * S::kPitch + ((lane >> 3) & 1) * 16;
 #pragma unroll
                 for (int blk = 0; blk < KD; ++blk) {
-                    uint32_t r[4];
-                    ldmatrix_x4_trans(vrow + blk * 32 + (lane >> 4) * 16, r);
-                    mma_16816<T>(o[2 * blk], a, r[0], r[1]);
-                    mma_16816<T>(o[2 * blk + 1], a, r[2], r[3]);
+                    uint32_t a[4];
+                    ldmatrix_x4_trans(base + blk * 32, a);
+#pragma unroll
+                    for (int n = 0; n < NH; ++n) mma_16816<T>(o[n][blk], a, b[n][0], b[n][1]);
                 }
             }
         }
     };
 
-    // This thread's elements of O as (row, column) pairs: fn(row, dim, value).
-    auto each_o = [&](auto&& fn) {
-#pragma unroll
-        for (int blk = 0; blk < KD; ++blk)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {        // rows quad, quad + 8
-                const int r = quad + 8 * h;
-                if constexpr (FP8) {
-                    const int d = blk * 16 + 4 * j4;
-                    fn(r, d, o[2 * blk][2 * h], o[2 * blk + 1][2 * h]);
-                    fn(r, d + 2, o[2 * blk][2 * h + 1], o[2 * blk + 1][2 * h + 1]);
-                } else {
-                    const int d = blk * 16 + 2 * j4;
-                    fn(r, d, o[2 * blk][2 * h], o[2 * blk][2 * h + 1]);
-                    fn(r, d + 8, o[2 * blk + 1][2 * h], o[2 * blk + 1][2 * h + 1]);
-                }
-            }
-    };
     constexpr float kLn2 = 0.693147180559945309f;
     auto write_lse = [&](int b, int row, float m, float l) {
         if (p.a.lse) p.a.lse[(int64_t)b * p.heads + head0 + row] = l > 0.f || l != l ? (m + (log2f(l) - kShift)) * kLn2 : -INFINITY;
@@ -509,21 +513,27 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
     // The segment's positions of this CTA are done: join the warps, then write or leave a partial.  Each warp lays its O
     // into the pipeline slot it just consumed (free until the next copies are issued).
     auto flush = [&](int stage) {
-#pragma unroll
-        for (int d = 1; d < 4; d <<= 1) {
-            l0 += __shfl_xor_sync(0xffffffffu, l0, d);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, d);
-        }
-        if (j4 == 0) {
-            warp_m[warp][quad] = m0;
-            warp_m[warp][quad + 8] = m1;
-            warp_l[warp][quad] = l0;
-            warp_l[warp][quad + 8] = l1;
-        }
         float* own = reinterpret_cast<float*>(ring + (size_t)stage * S::kStageBytes);
-        each_o([&](int r, int d, float x, float y) {
-            if (r < rows) *reinterpret_cast<float2*>(own + r * S::kMergePitch + d) = make_float2(x, y);
-        });
+#pragma unroll
+        for (int n = 0; n < NH; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = n * 8 + 2 * j4 + i;
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], d);
+                if (quad == 0) {
+                    warp_m[warp][r] = m[n][i];
+                    warp_l[warp][r] = l[n][i];
+                }
+                if (r < rows) {
+#pragma unroll
+                    for (int blk = 0; blk < KD; ++blk) {
+                        const int d = blk * 16 + (FP8 ? 2 * quad : quad);
+                        own[r * S::kMergePitch + d] = o[n][blk][i];
+                        own[r * S::kMergePitch + d + (FP8 ? 1 : 8)] = o[n][blk][2 + i];
+                    }
+                }
+            }
         __syncthreads();
         auto joined = [&](int r, int d, float& m, float& l) {     // four columns of a row, over the warps in order
             m = -FLT_MAX;
@@ -534,7 +544,7 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
 #pragma unroll
             for (int w = 0; w < kAttnWarps; ++w) {
                 const float f = exp2_fast(warp_m[w][r] - m);
-                const float4 x = *reinterpret_cast<const float4*>(smem + ((size_t)w * kAttnStages + stage) * S::kStageBytes +
+                const float4 x = *reinterpret_cast<const float4*>(smem + ((size_t)w * S::kStages + stage) * S::kStageBytes +
                                                                   (r * S::kMergePitch + d) * 4);
                 l = fmaf(warp_l[w][r], f, l);
                 v.x = fmaf(x.x, f, v.x);
@@ -567,8 +577,8 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
             float m, l;
             __stcg(reinterpret_cast<float4*>(slot + r * S::kDim + d), joined(r, d, m, l));
             if (d == 0) {
-                __stcg(slot + 16 * S::kDim + r, m);
-                __stcg(slot + 16 * S::kDim + 16 + r, l);
+                __stcg(slot + S::kHeads * S::kDim + r, m);
+                __stcg(slot + S::kHeads * (S::kDim + 1) + r, l);
             }
         }
         const int c0 = (int)(((seg0 + 1) * ctas - 1) / total), c1 = (int)((seg1 * ctas - 1) / total);
@@ -586,20 +596,37 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
             };
             for (int i = threadIdx.x; i < rows * quarter; i += kAttnThreads) {
                 const int r = i / quarter, d = (i - r * quarter) * 4;
+                // eight partials' loads at a time
+                constexpr int kMany = 8;
                 float M = -FLT_MAX, L = 0.f;
-#pragma unroll 8
-                for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(slot_of(c) + 16 * S::kDim + r));
+                for (int c = c0; c <= c1; c += kMany) {
+                    float x[kMany];
+#pragma unroll
+                    for (int u = 0; u < kMany; ++u) x[u] = __ldcg(slot_of(min(c + u, c1)) + S::kHeads * S::kDim + r);
+#pragma unroll
+                    for (int u = 0; u < kMany; ++u) M = fmaxf(M, x[u]);
+                }
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                for (int c = c0; c <= c1; ++c) {
-                    const float* sl = slot_of(c);
-                    const float f = exp2_fast(__ldcg(sl + 16 * S::kDim + r) - M);
-                    const float4 x = __ldcg(reinterpret_cast<const float4*>(sl + r * S::kDim + d));
-                    L = fmaf(__ldcg(sl + 16 * S::kDim + 16 + r), f, L);
-                    v.x = fmaf(x.x, f, v.x);
-                    v.y = fmaf(x.y, f, v.y);
-                    v.z = fmaf(x.z, f, v.z);
-                    v.w = fmaf(x.w, f, v.w);
+                for (int c = c0; c <= c1; c += kMany) {
+                    float pm[kMany], pl[kMany];
+                    float4 x[kMany];
+#pragma unroll
+                    for (int u = 0; u < kMany; ++u) {
+                        const float* sl = slot_of(min(c + u, c1));
+                        pm[u] = __ldcg(sl + S::kHeads * S::kDim + r);
+                        pl[u] = __ldcg(sl + S::kHeads * (S::kDim + 1) + r);
+                        x[u] = __ldcg(reinterpret_cast<const float4*>(sl + r * S::kDim + d));
+                    }
+#pragma unroll
+                    for (int u = 0; u < kMany; ++u) {
+                        if (c + u > c1) break;
+                        const float f = exp2_fast(pm[u] - M);
+                        L = fmaf(pl[u], f, L);
+                        v.x = fmaf(x[u].x, f, v.x);
+                        v.y = fmaf(x[u].y, f, v.y);
+                        v.z = fmaf(x[u].z, f, v.z);
+                        v.w = fmaf(x[u].w, f, v.w);
+                    }
                 }
                 const float f = L > 0.f || L != L ? p.a.v_scale / L : 0.f;
                 *reinterpret_cast<uint2*>(out_row(at.b, head0 + r) + d) =
@@ -612,19 +639,23 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
     };
 
     // ---------------------------------------------------------------- the loop
-    fetch();
+    Next next;
+    {
+        // the first steps' page numbers and the first query are fetched together
+        Next begin[S::kStages];
 #pragma unroll
-    for (int i = 0; i < kAttnStages - 1; ++i) {
-        issue(i);
-        fetch();
+        for (int i = 0; i < S::kStages; ++i) begin[i] = fetch();
+        if (at.left > 0) load_query();
+#pragma unroll
+        for (int i = 0; i < S::kStages - 1; ++i) issue(begin[i], i);
+        next = begin[S::kStages - 1];
     }
-    if (at.left > 0) load_query();
-    int stage = 0, fill = kAttnStages - 1;
+    int stage = 0, fill = S::kStages - 1;
     while (at.left > 0) {
-        cp_async_wait<kAttnStages - 2>();
+        cp_async_wait<S::kStages - 2>();
         __syncwarp();
-        issue(fill);              // the slot computed on in the previous step
-        fetch();
+        issue(next, fill);        // the slot computed on in the previous step
+        next = fetch();
         compute(stage);
         if (at.tile + 1 == at.tiles || at.left == 1) {
             flush(stage);
@@ -645,41 +676,46 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
             --at.left;
             ++unit;
         }
-        if (++stage == kAttnStages) stage = 0;
-        if (++fill == kAttnStages) fill = 0;
+        if (++stage == S::kStages) stage = 0;
+        if (++fill == S::kStages) fill = 0;
     }
     cp_async_wait<0>();
     write_empty();
 }
 
-template <typename T, typename TQ, bool FP8, int KD>
+template <typename T, typename TQ, bool FP8, int KD, int NH>
 cudaError_t attn_launch(const AttnParams& p, int grid, cudaStream_t stream) {
-    return launch_dependent(paged_attn_kernel<T, TQ, FP8, KD>, dim3((unsigned)grid), dim3(kAttnThreads), AttnShape<KD, FP8>::kSmemBytes,
-                            stream, p);
+    return launch_dependent(paged_attn_kernel<T, TQ, FP8, KD, NH>, dim3((unsigned)grid), dim3(kAttnThreads),
+                            AttnShape<KD, FP8, NH>::kSmemBytes, stream, p);
 }
 
 // Raises the kernel's shared-memory limit and says how many CTAs an SM holds.
-template <typename T, typename TQ, bool FP8, int KD>
+template <typename T, typename TQ, bool FP8, int KD, int NH>
 cudaError_t attn_prepare(AttnVariant* v) {
-    using S = AttnShape<KD, FP8>;
-    auto kern = paged_attn_kernel<T, TQ, FP8, KD>;
+    using S = AttnShape<KD, FP8, NH>;
+    auto kern = paged_attn_kernel<T, TQ, FP8, KD, NH>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes);
     if (e != cudaSuccess) return e;
     v->smem_bytes = S::kSmemBytes;
     v->slot_floats = S::kSlotFloats;
     v->tile_tokens = S::kTile;
-    v->launch = &attn_launch<T, TQ, FP8, KD>;
+    v->heads = S::kHeads;
+    v->launch = &attn_launch<T, TQ, FP8, KD, NH>;
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v->ctas_per_sm, kern, kAttnThreads, S::kSmemBytes);
 }
 
-// The head sizes held: head_dim is rounded up to one of them.
+// The head sizes held: head_dim is rounded up to one of them.  Up to eight query heads a kv head take one 8-head tile.
+template <typename T, typename TQ, bool FP8, int NH>
+cudaError_t attn_variant_heads(int head_dim, AttnVariant* v) {
+    if (head_dim <= 64) return attn_prepare<T, TQ, FP8, 4, NH>(v);
+    if (head_dim <= 80) return attn_prepare<T, TQ, FP8, 5, NH>(v);
+    if (head_dim <= 96) return attn_prepare<T, TQ, FP8, 6, NH>(v);
+    if (head_dim <= 128) return attn_prepare<T, TQ, FP8, 8, NH>(v);
+    return attn_prepare<T, TQ, FP8, 16, NH>(v);
+}
 template <typename T, typename TQ, bool FP8>
-cudaError_t attn_variant(int head_dim, AttnVariant* v) {
-    if (head_dim <= 64) return attn_prepare<T, TQ, FP8, 4>(v);
-    if (head_dim <= 80) return attn_prepare<T, TQ, FP8, 5>(v);
-    if (head_dim <= 96) return attn_prepare<T, TQ, FP8, 6>(v);
-    if (head_dim <= 128) return attn_prepare<T, TQ, FP8, 8>(v);
-    return attn_prepare<T, TQ, FP8, 16>(v);
+cudaError_t attn_variant(int head_dim, int group, AttnVariant* v) {
+    return group <= 8 ? attn_variant_heads<T, TQ, FP8, 1>(head_dim, v) : attn_variant_heads<T, TQ, FP8, 2>(head_dim, v);
 }
 
 }  // namespace dgb

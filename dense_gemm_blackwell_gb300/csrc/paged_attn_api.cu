@@ -46,10 +46,11 @@ gemm_status_t paged_attn_plan_create(paged_attn_plan_t* out, const paged_attn_de
     DeviceFacts dev;
     if ((s = device_facts(&dev)) != GEMM_OK) return s;
     AttnVariant v;
+    const int group = desc->heads / desc->kv_heads;
     const bool fp8 = desc->dtype_cache == GEMM_E4M3;
     cudaError_t e = desc->dtype == GEMM_BF16
-                        ? (fp8 ? attn_variant_bf16_e4m3(desc->head_dim, &v) : attn_variant_bf16(desc->head_dim, &v))
-                        : (fp8 ? attn_variant_f16_e4m3(desc->head_dim, &v) : attn_variant_f16(desc->head_dim, &v));
+                        ? (fp8 ? attn_variant_bf16_e4m3(desc->head_dim, group, &v) : attn_variant_bf16(desc->head_dim, group, &v))
+                        : (fp8 ? attn_variant_f16_e4m3(desc->head_dim, group, &v) : attn_variant_f16(desc->head_dim, group, &v));
     if (e != cudaSuccess) return status_of(e);
     if (v.ctas_per_sm < 1) return GEMM_ERR_RESOURCES;
     paged_attn_plan_s* p = new (std::nothrow) paged_attn_plan_s();
@@ -57,8 +58,8 @@ gemm_status_t paged_attn_plan_create(paged_attn_plan_t* out, const paged_attn_de
     p->desc = *desc;
     p->variant = v;
     p->device = dev.device;
-    p->group = desc->heads / desc->kv_heads;
-    p->head_groups = (p->group + 15) / 16;
+    p->group = group;
+    p->head_groups = (group + v.heads - 1) / v.heads;
     p->page_shift = -1;
     for (int i = 0; i < 31; ++i)
         if (desc->page_size == (1 << i)) p->page_shift = i;

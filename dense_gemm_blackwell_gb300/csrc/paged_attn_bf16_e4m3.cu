@@ -3,6 +3,6 @@
 
 namespace dgb {
 
-cudaError_t attn_variant_bf16_e4m3(int head_dim, AttnVariant* v) { return attn_variant<__half, __nv_bfloat16, true>(head_dim, v); }
+cudaError_t attn_variant_bf16_e4m3(int head_dim, int group, AttnVariant* v) { return attn_variant<__half, __nv_bfloat16, true>(head_dim, group, v); }
 
 }  // namespace dgb

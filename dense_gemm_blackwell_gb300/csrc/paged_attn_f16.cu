@@ -3,6 +3,6 @@
 
 namespace dgb {
 
-cudaError_t attn_variant_f16(int head_dim, AttnVariant* v) { return attn_variant<__half, __half, false>(head_dim, v); }
+cudaError_t attn_variant_f16(int head_dim, int group, AttnVariant* v) { return attn_variant<__half, __half, false>(head_dim, group, v); }
 
 }  // namespace dgb
