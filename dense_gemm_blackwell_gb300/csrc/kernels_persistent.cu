@@ -151,6 +151,32 @@ __device__ __forceinline__ void mma_issuer(const PersistentParams& p, uint8_t* r
             }
             issued_any = true;
         };
+        // TAIL: the tile's adapter steps, on every half; false on an abort
+        auto run_tail = [&]() {
+            griddep_wait();
+            int b, mb, nb;
+            tile_coords(p, t, b, mb, nb);
+            const int total = __ldcg(tail->counts + mb) * tail->steps;
+            const uint64_t step_b = (uint64_t)(p.tile_n / (CG * HALVES)) * kTailRowBytes / 16u;
+            for (int s0 = 0; s0 < total; s0 += 4 * ATOMS) {
+                if (!wait_phase_warp<false>(full(stage), phase, abort_flag, tmo, p.status, kRoleMma, stage, t)) return false;
+                if (issuer) {
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(ring + (size_t)stage * stage_bytes);
+                    const uint64_t da = smem_desc_sw128(sa), db = smem_desc_sw32(sa + p.stage_bytes_a);
+                    const int n16 = min(4 * ATOMS, total - s0);
+                    for (int j = 0; j < n16; ++j)
+#pragma unroll
+                        for (int h = 0; h < HALVES; ++h)
+                            mma_f16<CG>(d_tmem + (uint32_t)(h * 256), da + (uint64_t)(j / 4) * (kTailAtomBytes / 16u) + 2u * (j % 4),
+                                        db + (uint64_t)(h * 4 * ATOMS + j) * step_b, p.idesc, 1u);
+                    commit_to<CG>(empty(stage));
+                }
+                __syncwarp();
+                if (++stage == S) { stage = 0; phase ^= 1u; }
+            }
+            return true;
+        };
         int kb = u.kb0;
         if constexpr (HALVES == 2) {
             const int n = u.kb1 - u.kb0;
@@ -174,10 +200,20 @@ __device__ __forceinline__ void mma_issuer(const PersistentParams& p, uint8_t* r
                     if (issuer) {
                         issue_stage(stage, (halves & kHalfLeft) ? 0 : 1, (halves & kHalfRight) ? 2 : 1, i == 0, i == L);
                         commit_to<CG>(empty(stage));
-                        if (i == n - 1) commit_to<CG>(tfull(acc, 0));
+                        if (!TAIL && i == n - 1) commit_to<CG>(tfull(acc, 0));
                     }
                     __syncwarp();
                     if (++stage == S) { stage = 0; phase ^= 1u; }
+                    if constexpr (TAIL) {
+                        if (i == n - 1) {
+                            if (!run_tail()) {
+                                aborted = true;
+                                break;
+                            }
+                            if (issuer) commit_to<CG>(tfull(acc, 0));
+                            __syncwarp();
+                        }
+                    }
                 }
                 if (aborted) break;
                 if (issuer) commit_to<CG>(tfull(acc, 1));
@@ -231,31 +267,9 @@ __device__ __forceinline__ void mma_issuer(const PersistentParams& p, uint8_t* r
         }
         if (aborted) break;
         if constexpr (TAIL) {
-            if (u.role != kUnitContributor) {
-                griddep_wait();
-                int b, mb, nb;
-                tile_coords(p, t, b, mb, nb);
-                const int total = __ldcg(tail->counts + mb) * tail->steps;
-                for (int s0 = 0; s0 < total; s0 += 4 * ATOMS) {
-                    if (!wait_phase_warp<false>(full(stage), phase, abort_flag, tmo, p.status, kRoleMma, stage, t)) {
-                        aborted = true;
-                        break;
-                    }
-                    if (issuer) {
-                        tc_fence_after();
-                        const uint32_t sa = smem_u32(ring + (size_t)stage * stage_bytes);
-                        const uint64_t da = smem_desc_sw128(sa), db = smem_desc_sw32(sa + p.stage_bytes_a);
-                        const int n16 = min(4 * ATOMS, total - s0);
-                        const uint64_t step_b = (uint64_t)(p.tile_n / CG) * kTailRowBytes / 16u;
-                        for (int j = 0; j < n16; ++j)
-                            mma_f16<CG>(d_tmem, da + (uint64_t)(j / 4) * (kTailAtomBytes / 16u) + 2u * (j % 4), db + j * step_b,
-                                        p.idesc, 1u);
-                        commit_to<CG>(empty(stage));
-                    }
-                    __syncwarp();
-                    if (++stage == S) { stage = 0; phase ^= 1u; }
-                }
-                if (aborted) break;
+            if (u.role != kUnitContributor && !run_tail()) {
+                aborted = true;
+                break;
             }
         }
         if (issuer) {
@@ -353,8 +367,15 @@ __device__ __forceinline__ void persistent_body(const PersistentParams& p, const
         // ------------------------------------------------------------ TMA producers
         // warp 0: A (+ B's first half of a 512-wide tile); the second producer: the rest of B
         const bool first = warp == 0;
-        if constexpr (TAIL) {      // tiles up to 256 wide, K-major operands
-            if (p.k_atoms == 2) {
+        if constexpr (TAIL) {      // K-major operands
+            if (p.tile_n > 256) {
+                if (first)
+                    producer_loop<CG, 1, 2, kPartA | kPartB0, true, true>(p, ring, stage_bytes, p.tile_k, full0, empty0, abort_flag,
+                                                                          rank, cluster_id, num_clusters, tail);
+                else
+                    producer_loop<CG, 1, 2, kPartB1, true, true>(p, ring, stage_bytes, p.tile_k, full0, empty0, abort_flag, rank,
+                                                                 cluster_id, num_clusters, tail);
+            } else if (p.k_atoms == 2) {
                 if (first)
                     producer_loop<CG, 2, 1, kPartA, true, true>(p, ring, stage_bytes, p.tile_k, full0, empty0, abort_flag, rank,
                                                                 cluster_id, num_clusters, tail);
@@ -398,7 +419,10 @@ __device__ __forceinline__ void persistent_body(const PersistentParams& p, const
             // the stage depth is a template argument: this warp runs the
             // kernel's tightest loop, so no per-stage branching on it
             if constexpr (TAIL) {
-                if (p.k_atoms == 2)
+                if (p.tile_n > 256)
+                    mma_issuer<CG, 1, 2, true>(p, ring, stage_bytes, tmem_base, full0, empty0, tfull0, tempty0, drain_bar,
+                                               abort_flag, cluster_id, num_clusters, tail);
+                else if (p.k_atoms == 2)
                     mma_issuer<CG, 2, 1, true>(p, ring, stage_bytes, tmem_base, full0, empty0, tfull0, tempty0, drain_bar,
                                                abort_flag, cluster_id, num_clusters, tail);
                 else
@@ -716,10 +740,17 @@ static cudaError_t launch_pipeline(Kernel kern, std::atomic<int> (&smem_set)[kMa
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// The shared-memory limit set for a kernel on each device: one record per kernel, for a second one would lower the limit
+// that the first believes in.
+template <int CG, int OUT>
+static std::atomic<int> (&persistent_smem())[kMaxDevices] {
+    static std::atomic<int> smem_set[kMaxDevices];
+    return smem_set;
+}
+
 template <int CG, int OUT>
 static cudaError_t launch_typed(const PersistentParams& p, int grid, size_t smem, cudaStream_t stream) {
-    static std::atomic<int> smem_set[kMaxDevices];
-    return launch_pipeline<CG>(persistent_kernel<CG, OUT>, smem_set, grid, smem, stream, p);
+    return launch_pipeline<CG>(persistent_kernel<CG, OUT>, persistent_smem<CG, OUT>(), grid, smem, stream, p);
 }
 
 template <int CG, int OUT>
@@ -732,8 +763,7 @@ static cudaError_t launch_adapters_typed(const PersistentParams& p, const LoraTa
 template <int CG, int OUT>
 static int max_clusters_typed(size_t smem) {
     auto kern = persistent_kernel<CG, OUT>;
-    static std::atomic<int> smem_set[kMaxDevices];
-    if (ensure_smem_limit(kern, smem, smem_set) != cudaSuccess) return 0;
+    if (ensure_smem_limit(kern, smem, persistent_smem<CG, OUT>()) != cudaSuccess) return 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(CG, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);

@@ -16,7 +16,7 @@ cudaError_t launch_single_cta(const SingleParams& p, int dtype_d, int batch, siz
 cudaError_t launch_persistent(const PersistentParams& p, int cta_group, int dtype_d, int grid,
                               size_t smem_bytes, cudaStream_t stream);
 
-// The persistent kernel with adapter steps after each tile's K blocks (LoraTail); K-major 16-bit operands, tile_n <= 256.
+// The persistent kernel with adapter steps after each tile's K blocks (LoraTail); K-major 16-bit operands.
 // Follows the kernel that computes T on the same stream, immediately.
 cudaError_t launch_adapters(const PersistentParams& p, const LoraTail& tail, int cta_group, int dtype_d, int grid,
                             size_t smem_bytes, cudaStream_t stream);

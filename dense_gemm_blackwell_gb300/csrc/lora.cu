@@ -454,7 +454,6 @@ gemm_status_t check_desc(const lora_desc_t& d) {
     if (d.tokens > 65535ll * kShrinkRows) return GEMM_ERR_UNSUPPORTED;      // the shrink grid's z extent
     const uint32_t known = GEMM_FLAG_CTA_GROUP_1 | GEMM_FLAG_CTA_GROUP_2 | GEMM_FLAG_NO_STREAM_K | GEMM_FLAG_STAGE_K1 | GEMM_FLAG_STAGE_K2;
     if (d.flags & ~known) return GEMM_ERR_UNSUPPORTED;
-    if (d.tile_n > 256) return GEMM_ERR_UNSUPPORTED;
     return GEMM_OK;
 }
 
@@ -543,15 +542,6 @@ gemm_status_t lora_plan_create(lora_plan_t* out, const lora_desc_t* desc) {
     s = gemm_plan_create(&p->product, &g);
     gemm_plan_info_t info{};
     if (s == GEMM_OK) s = gemm_plan_info(p->product, &info);
-    if (s == GEMM_OK && !p->skinny && info.tile_n > 256) {
-        // 512-wide tiles hand their accumulator back in halves, the second with the next tile's work under way;
-        // the appended steps keep to one accumulator per tile
-        gemm_plan_destroy(p->product);
-        p->product = nullptr;
-        g.tile_n = 256;
-        s = gemm_plan_create(&p->product, &g);
-        if (s == GEMM_OK) s = gemm_plan_info(p->product, &info);
-    }
     if (s != GEMM_OK) {
         lora_plan_destroy(p);
         return s;
@@ -662,7 +652,7 @@ gemm_status_t lora_run(lora_plan_t plan, const lora_args_t* args, gemm_stream_t 
     if (s != GEMM_OK) return s;
     // one adapter: the stride is never used but has to be a valid one
     const int64_t stride_b = d.adapters > 1 ? a.stride_b : d.n * a.ldb;
-    if ((s = encode_matrices_map(&tail.tmap_b, d.dtype, a.b, d.rank, d.n, d.adapters, a.ldb, stride_b, 32, info.tile_n / info.cta_group)) != GEMM_OK)
+    if ((s = encode_matrices_map(&tail.tmap_b, d.dtype, a.b, d.rank, d.n, d.adapters, a.ldb, stride_b, 32, std::min(info.tile_n, 256) / info.cta_group)) != GEMM_OK)
         return s;
     tail.counts = q.counts;
     tail.ids = q.ids;

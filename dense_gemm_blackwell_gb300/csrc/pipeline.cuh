@@ -152,9 +152,10 @@ constexpr uint32_t kPartA = 1u, kPartB0 = 2u, kPartB1 = 4u, kPartsAll = 7u;
 // on the slices the previous one read last (8192^3 on GB300: 845 -> 694 MB
 // read from DRAM, 1.2 % faster at the power cap).  Only the summation order
 // of the tile changes; a kernel that applies per-K-block scales keeps it off.
-// kTail: after the K blocks of a unit that ends its tile, the tile's adapter
-// steps (LoraTail), 4 * ATOMS of them to a stage: T as one 128-byte K atom per
-// four steps, like A; step j's rows of B at j * b_rows * 32 bytes of the B area.
+// kTail: after the K blocks of a unit that ends its tile (before a split unit's
+// right-half repeats), the tile's adapter steps (LoraTail), 4 * ATOMS of them to
+// a stage: T as one 128-byte K atom per four steps, like A; step j's rows of B
+// at j times their size of the B area (of each half's share of it).
 template <int CG, int ATOMS = 1, int HALVES = 1, uint32_t PARTS = kPartsAll, bool kSerpentine = false, bool kTail = false>
 __device__ void producer_loop(const PersistentParams& p, uint8_t* ring, uint32_t stage_bytes, int tile_k,
                               uint32_t full0, uint32_t empty0, volatile uint32_t* abort_flag, uint32_t rank,
@@ -188,6 +189,60 @@ __device__ void producer_loop(const PersistentParams& p, uint8_t* ring, uint32_t
         // 512-wide tiles: the unit's stages, split ones included (units.cuh)
         const int n = u.kb1 - u.kb0;
         const int L = split_stages(u, HALVES == 2);
+        // kTail: the tile's adapter steps; false on an abort
+        auto run_tail = [&]() {
+            griddep_wait();     // the kernel that computes T, counts and ids is done
+            const int total = __ldcg(tail->counts + mb) * tail->steps;
+            constexpr bool any_b = (parts & (kPartB0 | kPartB1)) != 0;
+            const uint32_t step_b = (uint32_t)(b_rows / HALVES) * kTailRowBytes;    // of one half
+            // lane j holds the adapter of step j of the next stage, read a stage ahead
+            const int lane = (int)lane_id();
+            auto adapter_of = [&](int s) {
+                return any_b && s < total ? __ldcg(tail->ids + (size_t)mb * tail->max_adapters + s / tail->steps) : 0;
+            };
+            int id_next = lane < 4 * ATOMS ? adapter_of(lane) : 0;
+            for (int s0 = 0; s0 < total; s0 += 4 * ATOMS) {
+                const int id = id_next;
+                if (lane < 4 * ATOMS) id_next = adapter_of(s0 + 4 * ATOMS + lane);
+                if (!wait_phase_warp<false, true>(empty0 + 8u * stage, phase ^ 1u, abort_flag, tmo, p.status,
+                                                  kRoleProducer, stage, t))
+                    return false;
+                const bool issuer = elect_one();
+                const uint32_t fb = fb0 + 8u * stage;
+                const int n16 = min(4 * ATOMS, total - s0), atoms = (n16 + 3) / 4;
+                const uint32_t sa = smem_u32(ring + (size_t)stage * stage_bytes);
+                const uint32_t sb = sa + p.stage_bytes_a;
+                if constexpr ((parts & kPartA) != 0) {
+                    if (issuer) {
+                        if (leader)
+                            mbar_arrive_expect_tx(full0 + 8u * stage, (uint32_t)CG * (atoms * kTailAtomBytes + n16 * HALVES * step_b));
+                        for (int at = 0; at < atoms; ++at) {
+                            if constexpr (CG == 1) tma_load_3d(sa + at * kTailAtomBytes, &tail->tmap_t, fb, (s0 + 4 * at) * 16, 0, mb);
+                            else tma_load_3d_pair(sa + at * kTailAtomBytes, &tail->tmap_t, fb, (s0 + 4 * at) * 16, (int)rank * 128, mb);
+                        }
+                    }
+                }
+                if constexpr (any_b) {
+                    for (int j = 0; j < n16; ++j) {
+                        const int z = __shfl_sync(0xffffffffu, id, j);
+                        const int x = (((s0 + j) % tail->steps) % tail->b_steps) * 16;
+#pragma unroll
+                        for (int h = 0; h < HALVES; ++h) {
+                            if ((parts & (kPartB0 << h)) == 0 || !issuer) continue;
+                            // a 512-wide tile's halves lie 256 rows apart in B and one area of four steps apart in the stage
+                            const int row = HALVES == 1 ? b_row : nb * p.tile_n + h * 256 + (int)rank * (b_rows / HALVES);
+                            const uint32_t dst = sb + (uint32_t)(h * 4 * ATOMS + j) * step_b;
+                            if constexpr (CG == 1) tma_load_3d(dst, &tail->tmap_b, fb, x, row, z);
+                            else tma_load_3d_pair(dst, &tail->tmap_b, fb, x, row, z);
+                        }
+                    }
+                }
+                __syncwarp();
+                ++issued;
+                if (++stage == S) { stage = 0; phase ^= 1u; }
+            }
+            return true;
+        };
         for (int i = 0; i < n + L; ++i) {
             int walk, halves;
             stage_of(i, n, L, walk, halves);
@@ -234,54 +289,12 @@ __device__ void producer_loop(const PersistentParams& p, uint8_t* ring, uint32_t
             __syncwarp();
             ++issued;
             if (++stage == S) { stage = 0; phase ^= 1u; }
-        }
-        if constexpr (kTail) {
-            if (aborted || u.role == kUnitContributor) continue;
-            griddep_wait();     // the kernel that computes T, counts and ids is done
-            const int total = __ldcg(tail->counts + mb) * tail->steps;
-            const uint32_t step_b = (uint32_t)b_rows * kTailRowBytes;
-            // lane j holds the adapter of step j of the next stage, read a stage ahead
-            const int lane = (int)lane_id();
-            auto adapter_of = [&](int s) {
-                return (parts & kPartB0) != 0 && s < total ? __ldcg(tail->ids + (size_t)mb * tail->max_adapters + s / tail->steps) : 0;
-            };
-            int id_next = lane < 4 * ATOMS ? adapter_of(lane) : 0;
-            for (int s0 = 0; s0 < total; s0 += 4 * ATOMS) {
-                const int id = id_next;
-                if (lane < 4 * ATOMS) id_next = adapter_of(s0 + 4 * ATOMS + lane);
-                if (!wait_phase_warp<false, true>(empty0 + 8u * stage, phase ^ 1u, abort_flag, tmo, p.status,
-                                                  kRoleProducer, stage, t)) {
+            // the last stage of every half but the right one's repeats (split units): both halves take the tail here
+            if constexpr (kTail) {
+                if (i == n - 1 && u.role != kUnitContributor && !run_tail()) {
                     aborted = true;
                     break;
                 }
-                const bool issuer = elect_one();
-                const uint32_t fb = fb0 + 8u * stage;
-                const int n16 = min(4 * ATOMS, total - s0), atoms = (n16 + 3) / 4;
-                const uint32_t sa = smem_u32(ring + (size_t)stage * stage_bytes);
-                const uint32_t sb = sa + p.stage_bytes_a;
-                if constexpr ((parts & kPartA) != 0) {
-                    if (issuer) {
-                        if (leader)
-                            mbar_arrive_expect_tx(full0 + 8u * stage, (uint32_t)CG * (atoms * kTailAtomBytes + n16 * step_b));
-                        for (int at = 0; at < atoms; ++at) {
-                            if constexpr (CG == 1) tma_load_3d(sa + at * kTailAtomBytes, &tail->tmap_t, fb, (s0 + 4 * at) * 16, 0, mb);
-                            else tma_load_3d_pair(sa + at * kTailAtomBytes, &tail->tmap_t, fb, (s0 + 4 * at) * 16, (int)rank * 128, mb);
-                        }
-                    }
-                }
-                if constexpr ((parts & kPartB0) != 0) {
-                    for (int j = 0; j < n16; ++j) {
-                        const int z = __shfl_sync(0xffffffffu, id, j);
-                        const int x = (((s0 + j) % tail->steps) % tail->b_steps) * 16;
-                        if (issuer) {
-                            if constexpr (CG == 1) tma_load_3d(sb + j * step_b, &tail->tmap_b, fb, x, b_row, z);
-                            else tma_load_3d_pair(sb + j * step_b, &tail->tmap_b, fb, x, b_row, z);
-                        }
-                    }
-                }
-                __syncwarp();
-                ++issued;
-                if (++stage == S) { stage = 0; phase ^= 1u; }
             }
         }
     }

@@ -237,6 +237,15 @@ __global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const __grid
             *reinterpret_cast<uint4*>(slot_row) = round8<T>(y);
         }
     };
+    uint4 raw[kAhead];
+    auto load_batch = [&](int b) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            raw[u] = make_uint4(0, 0, 0, 0);
+            if (b + u < rows) raw[u] = load_row16(src);
+            src += src_step;
+        }
+    };
     float own[8], other[8];
     const T* weight = a.norm ? static_cast<const T*>(kind == kQueries ? a.q_weight : a.k_weight) : nullptr;
     if (kind != kValues)
@@ -244,13 +253,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const __grid
     const float inv_d = 1.f / (float)a.head_dim;
     // every lane of a warp runs the same number of batches (the shuffles need them all)
     for (int b = 0; b < p.rows_per_group; b += kAhead) {
-        uint4 raw[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            raw[u] = make_uint4(0, 0, 0, 0);
-            if (b + u < rows) raw[u] = load_row16(src);
-            src += src_step;
-        }
+        load_batch(b);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             if (b + u >= p.rows_per_group) break;
@@ -293,8 +296,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const __grid
 // one weight gradient stay in registers while its lane groups walk the tokens; it adds its groups' gradients in a fixed
 // order and leaves one partial for weight_grad_kernel.
 template <typename T, int LANES, int PAIRS>
-__global__ void __launch_bounds__(kRopeThreads, 3) norm_rope_backward_kernel(const __grid_constant__ RopeParams p) {
-    constexpr int kAhead = 2;
+__global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_backward_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int kAhead = 4;
     __shared__ float scratch[PAIRS == kPairsAny ? (kRopeThreads / LANES) * LANES * 8 : 1];
     __shared__ float sums[kRopeThreads / 32][LANES * 8];
     griddep_wait();
@@ -337,10 +340,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) norm_rope_backward_kernel(con
         const T* xs = x_base + token * x_token + h0 * x_head;
         const T* gs = g_base + token * g_token + h0 * g_head;
         T* ds = d_base + token * d_token + h0 * d_head;
-        float own[8], other[8];
-        load_factors<T, PAIRS>(a, nullptr, token, e0, me.act, me.live, -1.f, own, other);
-        for (int b = 0; b < p.rows_per_group; b += kAhead) {
-            uint4 rx[kAhead], rg[kAhead];
+        uint4 rx[kAhead], rg[kAhead];
+        auto load_batch = [&](int b) {
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 rx[u] = rg[u] = make_uint4(0, 0, 0, 0);
@@ -351,6 +352,12 @@ __global__ void __launch_bounds__(kRopeThreads, 3) norm_rope_backward_kernel(con
                 xs += x_head;
                 gs += g_head;
             }
+        };
+        load_batch(0);       // on the way while the factors' chain of loads (position, table) runs
+        float own[8], other[8];
+        load_factors<T, PAIRS>(a, nullptr, token, e0, me.act, me.live, -1.f, own, other);
+        for (int b = 0; b < p.rows_per_group; b += kAhead) {
+            if (b > 0) load_batch(b);
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 if (b + u >= p.rows_per_group) break;
@@ -508,11 +515,12 @@ struct LaunchForward {
     int sms;
     template <typename T, int LANES, int PAIRS>
     cudaError_t operator()() {
-        // Few rows: one row per lane group, so that every SM gets some.  Many: up to eight rows a group.
+        // As few rows per lane group as fit the device at once (four blocks to an SM), eight at most: a group's time is
+        // mostly latency up to there.
         const bool values = p.a.k_cache != nullptr;
         const int64_t total = (int64_t)p.a.tokens * (p.a.heads + p.a.kv_heads * (values ? 2 : 1));
-        const int64_t want = total / std::max<int64_t>((int64_t)sms * 2048 / LANES, 1);
-        cut_rows(p, want < 2 ? 1 : (want < 4 ? 2 : (want < 8 ? 4 : 8)), values);
+        const int64_t resident = (int64_t)sms * 4 * kRopeThreads / LANES, want = (total + resident - 1) / resident;
+        cut_rows(p, want <= 1 ? 1 : (want <= 2 ? 2 : (want <= 4 ? 4 : 8)), values);
         const int64_t blocks = ((int64_t)p.items * LANES + kRopeThreads - 1) / kRopeThreads;
         return launch_dependent(norm_rope_kernel<T, LANES, PAIRS>, dim3((unsigned)blocks), dim3(kRopeThreads), 0, stream, p);
     }
@@ -525,11 +533,11 @@ struct LaunchBackward {
     template <typename T, int LANES, int PAIRS>
     cudaError_t operator()() {
         const int64_t total = (int64_t)p.a.tokens * (p.a.heads + p.a.kv_heads);
-        const int64_t want = total / std::max<int64_t>((int64_t)sms * 1024 / LANES, 1);
-        cut_rows(p, want < 2 ? 1 : (want < 4 ? 2 : (want < 16 ? 4 : 8)), false);
-        // blocks in proportion to the rows, three to an SM at most
+        const int64_t resident = (int64_t)sms * 2 * kRopeThreads / LANES, want = (total + resident - 1) / resident;
+        cut_rows(p, want <= 1 ? 1 : (want <= 2 ? 2 : (want <= 16 ? 4 : 8)), false);
+        // blocks in proportion to the rows, two to an SM (what their registers allow) at most
         constexpr int64_t kPerBlock = kRopeThreads / LANES;
-        const int64_t most = std::min<int64_t>(3 * (int64_t)sms, kBackwardMaxBlocks);
+        const int64_t most = std::min<int64_t>(2 * (int64_t)sms, kBackwardMaxBlocks);
         const int64_t q_items = (int64_t)p.a.tokens * p.q_groups, k_items = (int64_t)p.a.tokens * p.k_groups;
         int64_t q = (q_items + kPerBlock - 1) / kPerBlock, k = (k_items + kPerBlock - 1) / kPerBlock;
         if (q + k > most) {

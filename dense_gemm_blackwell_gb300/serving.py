@@ -7,7 +7,9 @@
 
 As in the rest of the package this is argument marshalling: shapes, types, strides and devices are checked here, the
 work is enqueued by the CUDA library on torch's current stream (or the one given), and errors raise GemmError (from the
-library) or ValueError / TypeError (from these checks).
+library) or ValueError / TypeError (from these checks).  Outputs that are not given are allocated by torch on its current
+stream: pass them when `stream` is another one.  A plan's launches share its workspace, so launches of one plan (and graphs
+that captured it) must follow one another.
 """
 from __future__ import annotations
 
@@ -117,9 +119,9 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _facts(t):
-    """What a call's checks depend on: everything about a tensor but its address and contents."""
-    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+def _facts(*tensors):
+    """What a call's checks depend on: everything about its tensors but their addresses and contents."""
+    return tuple([None if t is None else (t.shape, t.stride(), t.dtype, t.get_device()) for t in tensors])
 
 
 def _need(cond, text):
@@ -209,7 +211,7 @@ class LoraPlan(_Plan):
 
     def run(self, x, w, a, b, adapter, y, scale=None, stream=None):
         """Enqueue on `stream` (default: torch's current stream)."""
-        key = (_facts(x), _facts(w), _facts(a), _facts(b), _facts(adapter), _facts(y), _facts(scale))
+        key = _facts(x, w, a, b, adapter, y, scale)
         checked = self._args.get(key)
         if checked is None:
             checked = self._args[key] = self._checked(x, w, a, b, adapter, y, scale)
@@ -232,7 +234,11 @@ _lora_plans = {}
 
 
 def lora_matmul(x, w, a, b, adapter, *, scale=None, out=None, out_dtype=None):
-    """Y = X W^T + scale_i (X A_i^T) B_i^T (see LoraPlan); plans are kept per shape, layout, device and stream."""
+    """Y = X W^T + scale_i (X A_i^T) B_i^T (see LoraPlan).
+
+    Plans are kept per shape, layout, device and stream: graphs captured on one stream share them, so replay those one
+    after the other (or give each a LoraPlan of its own).
+    """
     import torch
     _need(x.dim() == 2 and w.dim() == 2 and a.dim() == 3 and b.dim() == 3, "x [M, K], w [N, K], a [L, R, K], b [L, N, R] expected")
     _rows_ok(x, "x")
@@ -372,6 +378,7 @@ def _checked_rope(q, k, positions, table, q_weight, k_weight, eps, interleaved, 
 
 _rope_checked = {}
 _rope_backward_checked = {}
+_rope_workspaces = {}
 
 
 def qk_norm_rope(q, k, positions, table, *, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, norm=True, q_out=None,
@@ -390,8 +397,7 @@ def qk_norm_rope(q, k, positions, table, *, q_weight=None, k_weight=None, eps=1e
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if k_out is None and k_cache is None and k is not None:
         k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    key = (_facts(q), _facts(k), _facts(positions), _facts(table), _facts(q_weight), _facts(k_weight), eps, interleaved, norm,
-           _facts(q_out), _facts(k_out), _facts(v), _facts(k_cache), _facts(v_cache), _facts(slots))
+    key = (eps, interleaved, norm, _facts(q, k, positions, table, q_weight, k_weight, q_out, k_out, v, k_cache, v_cache, slots))
     checked = _rope_checked.get(key)
     if checked is None:
         checked = _rope_checked[key] = _checked_rope(q, k, positions, table, q_weight, k_weight, eps, interleaved, norm, q_out,
@@ -435,8 +441,7 @@ def qk_norm_rope_backward(dq, dk, q, k, positions, table, *, q_weight=None, k_we
         dq_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if dk_out is None and k is not None:
         dk_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    key = (_facts(dq), _facts(dk), _facts(q), _facts(k), _facts(positions), _facts(table), _facts(q_weight), _facts(k_weight), eps,
-           interleaved, norm, _facts(dq_out), _facts(dk_out))
+    key = (eps, interleaved, norm, _facts(dq, dk, q, k, positions, table, q_weight, k_weight, dq_out, dk_out))
     checked = _rope_backward_checked.get(key)
     if checked is None:
         checked = _rope_backward_checked[key] = _checked_rope_backward(dq, dk, q, k, positions, table, q_weight, k_weight, eps,
@@ -448,20 +453,26 @@ def qk_norm_rope_backward(dq, dk, q, k, positions, table, *, q_weight=None, k_we
         g.k, d.dk_out, d.dk = k.data_ptr(), dk.data_ptr(), dk_out.data_ptr()
     dqw = dkw = None
     if norm and (q_weight is not None or k_weight is not None):
-        # one buffer: the two weight gradients, then the library's workspace
-        L = _lib()
-        need = L.qk_norm_rope_backward_workspace()
-        n = q.shape[2]
-        buf = torch.empty(2 * n + need // 4, dtype=torch.float32, device=q.device)
+        if stream is None:
+            stream = current_stream_handle()
+        n, device = q.shape[2], q.device
         if q_weight is not None:
             g.q_weight = q_weight.data_ptr()
-            dqw = buf[:n]
+            dqw = torch.empty(n, dtype=torch.float32, device=device)
             d.dq_weight = dqw.data_ptr()
         if k_weight is not None and k is not None:
             g.k_weight = k_weight.data_ptr()
-            dkw = buf[n:2 * n]
+            dkw = torch.empty(n, dtype=torch.float32, device=device)
             d.dk_weight = dkw.data_ptr()
-        d.workspace, d.workspace_bytes = buf.data_ptr() + 8 * n, need
+        # the library's workspace: one per device and stream (a stream's calls follow one another), or the graph's own
+        place = (q.get_device(), stream)
+        capturing = torch.cuda.is_current_stream_capturing()
+        work = None if capturing else _rope_workspaces.get(place)
+        if work is None:
+            work = torch.empty(_lib().qk_norm_rope_backward_workspace(), dtype=torch.uint8, device=device)
+            if not capturing:
+                _rope_workspaces[place] = work
+        d.workspace, d.workspace_bytes = work.data_ptr(), work.numel()
     _check(_lib().qk_norm_rope_backward(ctypes.byref(g), ctypes.byref(d), current_stream_handle() if stream is None else stream),
            "qk_norm_rope_backward")
     return dq_out, dk_out, dqw, dkw
@@ -530,7 +541,7 @@ class PagedAttentionPlan(_Plan):
         contiguous last dimension; block_table int32 [batch, width]: the pages of each sequence in order; lengths int32
         [batch]; lse: fp32 [batch, heads] for the logarithm of the softmax sums; scale: default head_dim^-0.5.
         """
-        key = (_facts(q), _facts(k_cache), _facts(v_cache), _facts(block_table), _facts(lengths), _facts(out), _facts(lse))
+        key = _facts(q, k_cache, v_cache, block_table, lengths, out, lse)
         checked = self._args.get(key)
         if checked is None:
             checked = self._args[key] = self._checked(q, k_cache, v_cache, block_table, lengths, out, lse)

@@ -47,7 +47,7 @@ typedef struct {
     int32_t dtype_y;            /* GEMM_F32, GEMM_BF16 or GEMM_F16 */
     int64_t ldx, ldw, ldy;      /* 0 = packed (k, k, n); multiples of 16 bytes */
     uint32_t flags;             /* GEMM_FLAG_CTA_GROUP_1/2, _NO_STREAM_K, _STAGE_K1/K2 as in gemm.h */
-    int32_t tile_n, stages, max_ctas;   /* as in gemm.h (tile_n up to 256); 0 = planner.  Any of these or of the flags
+    int32_t tile_n, stages, max_ctas;   /* as in gemm.h; 0 = planner.  Any of these or of the flags
                                    keeps to the persistent kernel where few tiles would take the few-tile one */
     uint64_t wait_timeout_ns;   /* bound on every device-side wait; 0 = 2 s */
 } lora_desc_t;

@@ -132,12 +132,21 @@ def test_many_adapters(tokens, adapters):
 @pytest.mark.parametrize("kw", [dict(flags=dg.GEMM_FLAG_CTA_GROUP_1), dict(flags=dg.GEMM_FLAG_CTA_GROUP_2),
                                 dict(flags=dg.GEMM_FLAG_NO_STREAM_K), dict(flags=dg.GEMM_FLAG_STAGE_K1),
                                 dict(flags=dg.GEMM_FLAG_CTA_GROUP_2 | dg.GEMM_FLAG_STAGE_K2), dict(tile_n=64), dict(tile_n=256),
-                                dict(max_ctas=3), dict(stages=2)])
+                                dict(tile_n=512), dict(tile_n=512, flags=dg.GEMM_FLAG_CTA_GROUP_2), dict(max_ctas=3), dict(stages=2)])
 @pytest.mark.parametrize("tokens,n,k", [(40, 300, 8200), (600, 1100, 1030)])
 def test_persistent_kernel_choices(tokens, n, k, kw):
     """Forced tiles, CTA groups, stage depths and splits (40 x 300 x 8200 splits its few tiles along K) give the same Y."""
     info = check_exact(tokens, n, k, 24, 6, "mixed", **kw)
     assert info.product_k_split == 1
+
+
+@pytest.mark.parametrize("rank,kind", [(16, "runs"), (64, "runs"), (24, "mixed")])
+def test_wide_tiles(rank, kind):
+    """512-wide tiles, whose halves are handed back apart: the steps join both before the left one goes (65 K blocks: the split
+    schedule; 5: the plain one)."""
+    info = check_exact(2100, 4104, 4104, rank, 5, kind, out=torch.bfloat16, tile_n=512, flags=dg.GEMM_FLAG_CTA_GROUP_2)
+    assert info.product.tile_n == 512
+    check_exact(700, 1030, 300, rank, 5, kind, out=torch.bfloat16, tile_n=512, flags=dg.GEMM_FLAG_CTA_GROUP_2)
 
 
 def test_clusters_split_k_and_steps():

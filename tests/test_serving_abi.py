@@ -74,7 +74,7 @@ def lora_status(**kw):
     (dict(rank=12), dg.GEMM_ERR_UNSUPPORTED), (dict(rank=264), dg.GEMM_ERR_UNSUPPORTED),
     (dict(adapters=4097), dg.GEMM_ERR_UNSUPPORTED), (dict(dtype=dg.GEMM_F32), dg.GEMM_ERR_UNSUPPORTED),
     (dict(dtype=dg.GEMM_E4M3), dg.GEMM_ERR_UNSUPPORTED), (dict(dtype_y=dg.GEMM_E4M3), dg.GEMM_ERR_UNSUPPORTED),
-    (dict(tile_n=512), dg.GEMM_ERR_UNSUPPORTED), (dict(tokens=65535 * 64 + 1), dg.GEMM_ERR_UNSUPPORTED),
+    (dict(tokens=65535 * 64 + 1), dg.GEMM_ERR_UNSUPPORTED),
     (dict(flags=dg.GEMM_FLAG_SINGLE_CTA), dg.GEMM_ERR_UNSUPPORTED), (dict(flags=dg.GEMM_FLAG_ACCUM_F16), dg.GEMM_ERR_UNSUPPORTED),
 ])
 def test_lora_plan_refuses(kw, status):
