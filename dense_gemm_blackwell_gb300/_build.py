@@ -2,7 +2,9 @@
 
 Produces ``dense_gemm_blackwell_gb300/libdgb_gemm.so`` (git-ignored).  The
 library links the CUDA runtime statically and resolves the driver's tensor-map
-encoder at run time, so it loads on machines without a GPU.
+encoder at run time, so it loads on machines without a GPU.  Next to it,
+``_tensor_facts.so``: a small Python extension for the serving operators'
+binding (the CUDA library itself knows neither Python nor torch).
 """
 from __future__ import annotations
 
@@ -11,12 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdgb_gemm.so")
+FACTS = os.path.join(PKG, "_tensor_facts.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["kernels_single.cu", "kernels_persistent.cu", "kernels_fp8.cu", "kernels_mx.cu", "gemm_api.cu",
@@ -34,17 +38,45 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found; the CUDA toolkit is required to build the library")
 
 
+def torch_headers():
+    """Folder of the installed torch if it and Python come with C++ headers, else None."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    needed = (os.path.join(root, "include", "torch", "csrc", "autograd", "python_variable.h"),
+              os.path.join(sysconfig.get_paths()["include"], "Python.h"))
+    return root if all(os.path.exists(f) for f in needed) and shutil.which("g++") else None
+
+
+def build_facts() -> None:
+    """Compile the tensor_facts extension against the installed torch; without its headers the binding asks in Python."""
+    root = torch_headers()
+    if root is None:
+        return
+    tmp = FACTS + ".tmp.%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(root, "include"),
+           "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(CSRC, "tensor_facts.cpp"), "-o", tmp,
+           "-L" + os.path.join(root, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath," + os.path.join(root, "lib")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for tensor_facts.cpp:\n%s\n%s" % (" ".join(cmd), r.stderr))
+    os.replace(tmp, FACTS)
+
+
 def _inputs():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h"))]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h", ".cpp"))]
     files += [os.path.join(INCLUDE, f) for f in ("gemm.h", "serving.h")]
     files.append(os.path.abspath(__file__))
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    outputs = [LIB] + ([FACTS] if torch_headers() else [])
+    if not all(os.path.exists(f) for f in outputs):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(f) for f in outputs)
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -63,8 +95,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             raise RuntimeError("nvcc failed for %s:\n%s\n%s" % (src, " ".join(cmd), r.stderr))
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        facts = ex.submit(build_facts)
         results = list(ex.map(compile_one, SOURCES))
+        facts.result()
     if verbose or ptxas_verbose:
         for _, log in results:
             if log:

@@ -45,9 +45,7 @@ struct RopeParams {
     qk_norm_rope_grads_t g;
     int32_t rows_per_group;     // head rows of one token a lane group takes
     uint32_t q_groups, k_groups;    // lane groups per token for queries; for keys (and for values, with a cache)
-    uint32_t groups;            // lane groups per token
-    uint32_t items;             // forward: tokens x groups, below 2^31
-    uint32_t q_blocks;          // backward: blocks [0, q_blocks) take queries, the rest keys
+    uint32_t q_blocks, k_blocks;    // blocks [0, q_blocks) take queries, the next k_blocks keys, the rest values
     float* partials;            // backward: [block][kMaxHeadDim]
 };
 
@@ -172,122 +170,129 @@ struct RowLane {
     }
 };
 
-template <typename T, int LANES, int PAIRS>
-__global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const __grid_constant__ RopeParams p) {
+// One kind's rows of the forward pass; a block takes one kind only, so that nothing in the row loop asks for it.
+template <typename T, int LANES, int PAIRS, int KIND>
+__device__ __forceinline__ void forward_rows(const RopeParams& p, uint32_t block, float* srow) {
     constexpr int kAhead = 4;   // rows whose loads are in flight
-    __shared__ float scratch[PAIRS == kPairsAny ? (kRopeThreads / LANES) * LANES * 8 : 1];
-    griddep_wait();
-    griddep_launch_dependents();
     const qk_norm_rope_args_t& a = p.a;
     const RowLane<LANES, PAIRS> me(a);
-    const int e0 = me.e0;
-    float* srow = scratch + (PAIRS == kPairsAny ? (threadIdx.x / LANES) * LANES * 8 : 0);
-    const uint32_t item = blockIdx.x * (uint32_t)(kRopeThreads / LANES) + threadIdx.x / LANES;
-    const bool valid = item < p.items;
-    const int token = valid ? (int)(item / p.groups) : 0;
-    const uint32_t part = valid ? item % p.groups : 0;
-    const RowKind kind = part < p.q_groups ? kQueries : (part < p.q_groups + p.k_groups ? kKeys : kValues);
-    const int h0 = (int)(part - (kind == kQueries ? 0 : p.q_groups + (kind == kKeys ? 0 : p.k_groups))) * p.rows_per_group;
-    const int rows = valid && me.act ? min(p.rows_per_group, (kind == kQueries ? a.heads : a.kv_heads) - h0) : 0;
+    const int e0 = me.act ? me.e0 : 0;      // lanes past the row read its start and store nothing
+    const uint32_t groups = KIND == kQueries ? p.q_groups : p.k_groups;
+    const uint32_t items = (uint32_t)a.tokens * groups;
+    const uint32_t item = block * (uint32_t)(kRopeThreads / LANES) + threadIdx.x / LANES;
+    const bool valid = item < items;
+    const int token = valid ? (int)(item / groups) : 0;
+    const int h0 = valid ? (int)(item % groups) * p.rows_per_group : 0;
+    const int rows = min(p.rows_per_group, (KIND == kQueries ? a.heads : a.kv_heads) - h0);      // at least one
+    const bool stores = valid && me.act;
 
-    const T* src;
-    int64_t src_step;
+    const T* src = static_cast<const T*>(KIND == kQueries ? a.q : (KIND == kKeys ? a.k : a.v)) + e0;
+    int32_t src_step;
     T* dst = nullptr;
-    int64_t dst_step = 0;
-    if (kind == kQueries) {
-        src = static_cast<const T*>(a.q) + token * a.q_token + h0 * a.q_head + e0;
-        src_step = a.q_head;
+    int32_t dst_step = 0;
+    if constexpr (KIND == kQueries) {
+        src += token * a.q_token + h0 * a.q_head;
+        src_step = (int32_t)a.q_head;
         dst = static_cast<T*>(a.q_out) + token * a.q_out_token + h0 * a.q_out_head + e0;
-        dst_step = a.q_out_head;
-    } else if (kind == kKeys) {
-        src = static_cast<const T*>(a.k) + token * a.k_token + h0 * a.k_head + e0;
-        src_step = a.k_head;
+        dst_step = (int32_t)a.q_out_head;
+    } else if constexpr (KIND == kKeys) {
+        src += token * a.k_token + h0 * a.k_head;
+        src_step = (int32_t)a.k_head;
         if (a.k_out) {
             dst = static_cast<T*>(a.k_out) + token * a.k_out_token + h0 * a.k_out_head + e0;
-            dst_step = a.k_out_head;
+            dst_step = (int32_t)a.k_out_head;
         }
     } else {
-        src = static_cast<const T*>(a.v) + token * a.v_token + h0 * a.v_head + e0;
-        src_step = a.v_head;
+        src += token * a.v_token + h0 * a.v_head;
+        src_step = (int32_t)a.v_head;
     }
     // the cache rows of this token
     const bool fp8 = a.dtype_cache == GEMM_E4M3;
     uint8_t* slot_row = nullptr;
-    int64_t slot_step = 0;
+    int32_t slot_step = 0;
     float slot_scale = 1.f;
-    if (a.k_cache && kind != kQueries) {
+    if (KIND != kQueries && a.k_cache) {
         const int slot = a.slots[token];
         if (slot >= 0 && slot < a.num_pages * a.page_size) {
             const int page = slot / a.page_size, place = slot % a.page_size;
             const int es = fp8 ? 1 : 2;
-            const int64_t at = kind == kKeys ? page * a.k_page + place * a.k_place + h0 * a.k_chead
+            const int64_t at = KIND == kKeys ? page * a.k_page + place * a.k_place + h0 * a.k_chead
                                              : page * a.v_page + place * a.v_place + h0 * a.v_chead;
-            slot_row = static_cast<uint8_t*>(kind == kKeys ? a.k_cache : a.v_cache) + (at + e0) * es;
-            slot_step = (kind == kKeys ? a.k_chead : a.v_chead) * es;
-            slot_scale = kind == kKeys ? a.k_scale : a.v_scale;
+            slot_row = static_cast<uint8_t*>(KIND == kKeys ? a.k_cache : a.v_cache) + (at + e0) * es;
+            slot_step = (int32_t)(KIND == kKeys ? a.k_chead : a.v_chead) * es;
+            slot_scale = KIND == kKeys ? a.k_scale : a.v_scale;
         }
     }
-    auto append = [&](const float (&y)[8]) {
+    auto append = [&](int r, const float (&y)[8]) {
+        uint8_t* at = slot_row + (int64_t)r * slot_step;
         if (fp8) {
             uint2 w;
             w.x = e4m3x4(__fdiv_rn(y[0], slot_scale), __fdiv_rn(y[1], slot_scale), __fdiv_rn(y[2], slot_scale), __fdiv_rn(y[3], slot_scale));
             w.y = e4m3x4(__fdiv_rn(y[4], slot_scale), __fdiv_rn(y[5], slot_scale), __fdiv_rn(y[6], slot_scale), __fdiv_rn(y[7], slot_scale));
-            *reinterpret_cast<uint2*>(slot_row) = w;
+            *reinterpret_cast<uint2*>(at) = w;
         } else {
-            *reinterpret_cast<uint4*>(slot_row) = round8<T>(y);
-        }
-    };
-    uint4 raw[kAhead];
-    auto load_batch = [&](int b) {
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            raw[u] = make_uint4(0, 0, 0, 0);
-            if (b + u < rows) raw[u] = load_row16(src);
-            src += src_step;
+            *reinterpret_cast<uint4*>(at) = round8<T>(y);
         }
     };
     float own[8], other[8];
-    const T* weight = a.norm ? static_cast<const T*>(kind == kQueries ? a.q_weight : a.k_weight) : nullptr;
-    if (kind != kValues)
-        load_factors<T, PAIRS>(a, weight, token, e0, me.act, me.live, 1.f, own, other);
+    if constexpr (KIND != kValues)
+        load_factors<T, PAIRS>(a, a.norm ? static_cast<const T*>(KIND == kQueries ? a.q_weight : a.k_weight) : nullptr, token, me.e0,
+                               me.act, me.live, 1.f, own, other);
     const float inv_d = 1.f / (float)a.head_dim;
-    // every lane of a warp runs the same number of batches (the shuffles need them all)
+    // Every lane of a warp runs the same number of batches (the shuffles need them all); rows past a group's last one are
+    // its last one again, not stored.
     for (int b = 0; b < p.rows_per_group; b += kAhead) {
-        load_batch(b);
+        uint4 raw[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) raw[u] = load_row16(src + (int64_t)min(b + u, rows - 1) * src_step);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            if (b + u >= p.rows_per_group) break;
-            const bool on = b + u < rows;
-            float x[8];
-            unpack8<T>(raw[u], x);
-            if (__all_sync(0xffffffffu, kind == kValues)) {      // a warp of values: copied
-                if (on && slot_row) append(x);
-                if (slot_row) slot_row += slot_step;
-                continue;
-            }
-            float inv = 1.f;
-            if (a.norm) {
-                float sum = 0.f;
+            const int r = b + u;
+            const bool on = stores && r < rows;
+            if constexpr (KIND == kValues) {
+                if (on && slot_row) {
+                    if (fp8) {
+                        float y[8];
+                        unpack8<T>(raw[u], y);
+                        append(r, y);
+                    } else {
+                        *reinterpret_cast<uint4*>(slot_row + (int64_t)r * slot_step) = raw[u];
+                    }
+                }
+            } else {
+                float x[8], z[8];
+                unpack8<T>(raw[u], x);
+                float inv = 1.f;
+                if (a.norm) {
+                    float sum = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
+                    for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
+                    if (!me.act) sum = 0.f;
 #pragma unroll
-                for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                inv = rsqrtf(fmaf(sum, inv_d, a.eps));
-            }
-            float z[8];
-            partners<T, PAIRS>(a, e0, me.live, me.mate, srow, raw[u], x, z);
-            if (kind != kValues) {
+                    for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    inv = rsqrtf(fmaf(sum, inv_d, a.eps));
+                }
+                partners<T, PAIRS>(a, me.e0, me.live, me.mate, srow, raw[u], x, z);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = inv * fmaf(z[i], other[i], x[i] * own[i]);
+                if (on) {
+                    if (KIND == kQueries || dst) *reinterpret_cast<uint4*>(dst + (int64_t)r * dst_step) = round8<T>(x);
+                    if (KIND == kKeys && slot_row) append(r, x);
+                }
             }
-            if (on) {
-                if (dst) *reinterpret_cast<uint4*>(dst) = round8<T>(x);
-                if (slot_row) append(x);
-            }
-            if (dst) dst += dst_step;
-            if (slot_row) slot_row += slot_step;
         }
     }
+}
+
+template <typename T, int LANES, int PAIRS>
+__global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const __grid_constant__ RopeParams p) {
+    __shared__ float scratch[PAIRS == kPairsAny ? (kRopeThreads / LANES) * LANES * 8 : 1];
+    griddep_wait();
+    griddep_launch_dependents();
+    float* srow = scratch + (PAIRS == kPairsAny ? (threadIdx.x / LANES) * LANES * 8 : 0);
+    if (blockIdx.x < p.q_blocks) forward_rows<T, LANES, PAIRS, kQueries>(p, blockIdx.x, srow);
+    else if (blockIdx.x < p.q_blocks + p.k_blocks) forward_rows<T, LANES, PAIRS, kKeys>(p, blockIdx.x - p.q_blocks, srow);
+    else forward_rows<T, LANES, PAIRS, kValues>(p, blockIdx.x - p.q_blocks - p.k_blocks, srow);
 }
 
 // Backward: with g the incoming gradient turned back, n = x r, r = rsqrt(mean x^2 + eps):
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_backward_kernel(con
     const qk_norm_rope_args_t& a = p.a;
     const qk_norm_rope_grads_t& gr = p.g;
     const RowLane<LANES, PAIRS> me(a);
-    const int e0 = me.e0;
+    const int e0 = me.act ? me.e0 : 0;      // lanes past the row read its start and store nothing
     float* srow = scratch + (PAIRS == kPairsAny ? (threadIdx.x / LANES) * LANES * 8 : 0);
     const bool is_q = blockIdx.x < p.q_blocks;
     const uint32_t block = is_q ? blockIdx.x : blockIdx.x - p.q_blocks, blocks = is_q ? p.q_blocks : gridDim.x - p.q_blocks;
@@ -318,6 +323,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_backward_kernel(con
     const int64_t x_token = is_q ? a.q_token : a.k_token, x_head = is_q ? a.q_head : a.k_head;
     const int64_t g_token = is_q ? gr.dq_out_token : gr.dk_out_token, g_head = is_q ? gr.dq_out_head : gr.dk_out_head;
     const int64_t d_token = is_q ? gr.dq_token : gr.dk_token, d_head = is_q ? gr.dq_head : gr.dk_head;
+    const int32_t x_step = (int32_t)x_head, g_step = (int32_t)g_head, d_step = (int32_t)d_head;
     const T* weight = a.norm ? static_cast<const T*>(is_q ? a.q_weight : a.k_weight) : nullptr;
     float w[8], dw[8];
 #pragma unroll
@@ -336,34 +342,32 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_backward_kernel(con
         const bool valid = item < items;
         const int token = valid ? (int)(item / groups) : 0;
         const int h0 = valid ? (int)(item % groups) * p.rows_per_group : 0;
-        const int rows = valid && me.act ? min(p.rows_per_group, heads - h0) : 0;
+        const int rows = min(p.rows_per_group, heads - h0);       // at least one
+        const bool stores = valid && me.act;
         const T* xs = x_base + token * x_token + h0 * x_head;
         const T* gs = g_base + token * g_token + h0 * g_head;
         T* ds = d_base + token * d_token + h0 * d_head;
         uint4 rx[kAhead], rg[kAhead];
+        // rows past the group's last one are its last one again, neither stored nor summed
         auto load_batch = [&](int b) {
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                rx[u] = rg[u] = make_uint4(0, 0, 0, 0);
-                if (b + u < rows) {
-                    rx[u] = load_row16(xs);
-                    rg[u] = load_row16(gs);
-                }
-                xs += x_head;
-                gs += g_head;
+                const int r = min(b + u, rows - 1);
+                rx[u] = load_row16(xs + (int64_t)r * x_step);
+                rg[u] = load_row16(gs + (int64_t)r * g_step);
             }
         };
         load_batch(0);       // on the way while the factors' chain of loads (position, table) runs
         float own[8], other[8];
-        load_factors<T, PAIRS>(a, nullptr, token, e0, me.act, me.live, -1.f, own, other);
+        load_factors<T, PAIRS>(a, nullptr, token, me.e0, me.act, me.live, -1.f, own, other);
         for (int b = 0; b < p.rows_per_group; b += kAhead) {
             if (b > 0) load_batch(b);
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                if (b + u >= p.rows_per_group) break;
+                const bool on = stores && b + u < rows;
                 float g[8], z[8];
                 unpack8<T>(rg[u], g);
-                partners<T, PAIRS>(a, e0, me.live, me.mate, srow, rg[u], g, z);
+                partners<T, PAIRS>(a, me.e0, me.live, me.mate, srow, rg[u], g, z);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) g[i] = fmaf(z[i], other[i], g[i] * own[i]);
                 if (a.norm) {
@@ -375,6 +379,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_backward_kernel(con
                         sq = fmaf(x[i], x[i], sq);
                         dot = fmaf(g[i] * w[i], x[i], dot);
                     }
+                    if (!me.act) sq = dot = 0.f;
 #pragma unroll
                     for (int o = LANES / 2; o > 0; o >>= 1) {
                         sq += __shfl_xor_sync(0xffffffffu, sq, o);
@@ -382,14 +387,14 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_backward_kernel(con
                     }
                     const float inv = rsqrtf(fmaf(sq, inv_d, a.eps));
                     const float k = inv * inv * dot * inv_d;
+                    const float counted = on ? inv : 0.f;       // a repeated row adds nothing to the weight's gradient
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        dw[i] = fmaf(g[i] * inv, x[i], dw[i]);      // rows past the end hold zeros
+                        dw[i] = fmaf(g[i] * counted, x[i], dw[i]);
                         g[i] = inv * fmaf(-x[i], k, g[i] * w[i]);
                     }
                 }
-                if (b + u < rows) *reinterpret_cast<uint4*>(ds) = round8<T>(g);
-                ds += d_head;
+                if (on) *reinterpret_cast<uint4*>(ds + (int64_t)(b + u) * d_step) = round8<T>(g);
             }
         }
     }
@@ -399,7 +404,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_backward_kernel(con
     for (int i = 0; i < 8; ++i) {
 #pragma unroll
         for (int o = LANES; o < 32; o <<= 1) dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], o);
-        if ((threadIdx.x & 31) < LANES) sums[threadIdx.x / 32][e0 + i] = dw[i];
+        if ((threadIdx.x & 31) < LANES) sums[threadIdx.x / 32][me.e0 + i] = dw[i];
     }
     __syncthreads();
     for (int e = threadIdx.x; e < LANES * 8; e += kRopeThreads) {
@@ -438,6 +443,13 @@ namespace {
 
 constexpr int64_t kWorkspaceBytes = (int64_t)kBackwardMaxBlocks * kMaxHeadDim * sizeof(float);
 
+// Strides between heads are held in 32 bits (those between tokens and pages in 64).
+bool small_steps(std::initializer_list<int64_t> steps) {
+    for (int64_t v : steps)
+        if (v < -(int64_t(1) << 29) || v > (int64_t(1) << 29)) return false;
+    return true;
+}
+
 gemm_status_t check_rope(const qk_norm_rope_args_t& a, bool forward) {
     if (a.tokens < 0 || a.heads < 0 || a.kv_heads < 0 || a.head_dim < 1 || a.rot_dim < 0 || a.rot_dim > a.head_dim || (a.rot_dim & 1))
         return GEMM_ERR_INVALID_ARG;
@@ -449,7 +461,9 @@ gemm_status_t check_rope(const qk_norm_rope_args_t& a, bool forward) {
     if ((a.heads > 0 && !a.q) || (a.kv_heads > 0 && !a.k)) return GEMM_ERR_INVALID_ARG;
     if (!all_aligned(16, {a.q, a.k, a.q_weight, a.k_weight, a.table})) return GEMM_ERR_ALIGNMENT;
     if (!all_multiples(8, {a.q_token, a.q_head, a.k_token, a.k_head})) return GEMM_ERR_ALIGNMENT;
+    if (!small_steps({a.q_head, a.k_head})) return GEMM_ERR_UNSUPPORTED;
     if (!forward) return GEMM_OK;
+    if (!small_steps({a.q_out_head, a.k_out_head, a.v_head, a.k_chead, a.v_chead})) return GEMM_ERR_UNSUPPORTED;
     const bool cache = a.k_cache || a.v_cache;
     if (a.heads > 0 && !a.q_out) return GEMM_ERR_INVALID_ARG;
     if (a.kv_heads > 0 && !a.k_out && !cache) return GEMM_ERR_INVALID_ARG;
@@ -495,18 +509,17 @@ cudaError_t with_kernel(const qk_norm_rope_args_t& a, F&& f) {
 }
 
 // Cut the rows of every token into lane groups of at most `per_group` rows of one kind.
-void cut_rows(RopeParams& p, int64_t per_group, bool values) {
+void cut_rows(RopeParams& p, int64_t per_group) {
     const int64_t most = std::max(p.a.heads, p.a.kv_heads);
     per_group = std::min<int64_t>(std::max<int64_t>(per_group, 1), most);
     for (;;) {
         p.rows_per_group = (int32_t)per_group;
         p.q_groups = (uint32_t)((p.a.heads + per_group - 1) / per_group);
         p.k_groups = (uint32_t)((p.a.kv_heads + per_group - 1) / per_group);
-        p.groups = p.q_groups + p.k_groups * (values ? 2 : 1);
-        if ((int64_t)p.a.tokens * p.groups <= INT32_MAX - kRopeThreads || per_group >= most) break;
+        // numbers of items stay below 2^31
+        if ((int64_t)p.a.tokens * std::max(p.q_groups, p.k_groups) <= INT32_MAX - kRopeThreads || per_group >= most) break;
         per_group *= 2;
     }
-    p.items = (uint32_t)p.a.tokens * p.groups;
 }
 
 struct LaunchForward {
@@ -520,8 +533,12 @@ struct LaunchForward {
         const bool values = p.a.k_cache != nullptr;
         const int64_t total = (int64_t)p.a.tokens * (p.a.heads + p.a.kv_heads * (values ? 2 : 1));
         const int64_t resident = (int64_t)sms * 4 * kRopeThreads / LANES, want = (total + resident - 1) / resident;
-        cut_rows(p, want <= 1 ? 1 : (want <= 2 ? 2 : (want <= 4 ? 4 : 8)), values);
-        const int64_t blocks = ((int64_t)p.items * LANES + kRopeThreads - 1) / kRopeThreads;
+        cut_rows(p, want <= 1 ? 1 : (want <= 2 ? 2 : (want <= 4 ? 4 : 8)));
+        constexpr int64_t kPerBlock = kRopeThreads / LANES;
+        const int64_t q = ((int64_t)p.a.tokens * p.q_groups + kPerBlock - 1) / kPerBlock, k = ((int64_t)p.a.tokens * p.k_groups + kPerBlock - 1) / kPerBlock;
+        const int64_t blocks = q + k * (values ? 2 : 1);
+        p.q_blocks = (uint32_t)q;
+        p.k_blocks = (uint32_t)k;
         return launch_dependent(norm_rope_kernel<T, LANES, PAIRS>, dim3((unsigned)blocks), dim3(kRopeThreads), 0, stream, p);
     }
 };
@@ -534,7 +551,7 @@ struct LaunchBackward {
     cudaError_t operator()() {
         const int64_t total = (int64_t)p.a.tokens * (p.a.heads + p.a.kv_heads);
         const int64_t resident = (int64_t)sms * 2 * kRopeThreads / LANES, want = (total + resident - 1) / resident;
-        cut_rows(p, want <= 1 ? 1 : (want <= 2 ? 2 : (want <= 16 ? 4 : 8)), false);
+        cut_rows(p, want <= 1 ? 1 : (want <= 2 ? 2 : (want <= 16 ? 4 : 8)));
         // blocks in proportion to the rows, two to an SM (what their registers allow) at most
         constexpr int64_t kPerBlock = kRopeThreads / LANES;
         const int64_t most = std::min<int64_t>(2 * (int64_t)sms, kBackwardMaxBlocks);
@@ -597,6 +614,7 @@ gemm_status_t qk_norm_rope_backward(const qk_norm_rope_args_t* args, const qk_no
     if (!all_aligned(16, {g.dq_out, g.dk_out, g.dq, g.dk, g.workspace})) return GEMM_ERR_ALIGNMENT;
     if (!all_multiples(8, {g.dq_out_token, g.dq_out_head, g.dk_out_token, g.dk_out_head, g.dq_token, g.dq_head, g.dk_token, g.dk_head}))
         return GEMM_ERR_ALIGNMENT;
+    if (!small_steps({g.dq_out_head, g.dk_out_head, g.dq_head, g.dk_head})) return GEMM_ERR_UNSUPPORTED;
     DeviceFacts dev;
     if ((s = device_facts(&dev)) != GEMM_OK) return s;
     RopeParams p{};

@@ -1,0 +1,109 @@
+// tensor_facts.cpp -- what the binding asks of torch tensors on every call, in
+// one native call instead of several attribute look-ups per tensor (on the
+// GB300 host: 12 tensors' shapes, strides, types and devices 0.3 instead of
+// 3.2 us, and a small operator's GPU time is 3 us).
+//
+//   facts(*tensors) -> bytes   type, device, sizes and strides of each (None allowed): equal for equal layouts
+//   fill(buffer, offsets, *tensors)   writes each tensor's data address (None: 0) at its byte offset of `buffer`
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <cstdint>
+#include <cstring>
+#include <exception>
+
+#include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
+
+namespace {
+
+constexpr Py_ssize_t kRoom = 4096;
+
+PyObject* facts(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    char key[kRoom];
+    Py_ssize_t at = 0;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        if (at + 4 + 16 * 16 > kRoom) {
+            PyErr_SetString(PyExc_ValueError, "too many tensors");
+            return nullptr;
+        }
+        if (args[i] == Py_None) {
+            key[at++] = (char)0xFF;
+            continue;
+        }
+        if (!THPVariable_Check(args[i])) {
+            PyErr_Format(PyExc_TypeError, "a tensor expected, got %s", Py_TYPE(args[i])->tp_name);
+            return nullptr;
+        }
+        try {       // sparse tensors have no strides: torch throws
+            const at::Tensor& t = THPVariable_Unpack(args[i]);
+            const auto sizes = t.sizes(), strides = t.strides();
+            if (sizes.size() > 8) {
+                PyErr_SetString(PyExc_ValueError, "a tensor of more than eight dimensions");
+                return nullptr;
+            }
+            key[at++] = (char)t.scalar_type();
+            key[at++] = (char)t.device().type();
+            key[at++] = (char)t.device().index();
+            key[at++] = (char)sizes.size();
+            std::memcpy(key + at, sizes.data(), sizes.size() * 8);
+            at += (Py_ssize_t)sizes.size() * 8;
+            std::memcpy(key + at, strides.data(), strides.size() * 8);
+            at += (Py_ssize_t)strides.size() * 8;
+        } catch (const std::exception& e) {
+            PyErr_SetString(PyExc_TypeError, "a dense tensor expected");
+            return nullptr;
+        }
+    }
+    return PyBytes_FromStringAndSize(key, at);
+}
+
+PyObject* fill(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    if (n < 2 || !PyTuple_Check(args[1]) || PyTuple_GET_SIZE(args[1]) != n - 2) {
+        PyErr_SetString(PyExc_TypeError, "fill(buffer, offsets, *tensors): one offset per tensor");
+        return nullptr;
+    }
+    Py_buffer buf;
+    if (PyObject_GetBuffer(args[0], &buf, PyBUF_WRITABLE) != 0) return nullptr;
+    for (Py_ssize_t i = 2; i < n; ++i) {
+        const Py_ssize_t off = PyLong_AsSsize_t(PyTuple_GET_ITEM(args[1], i - 2));
+        if (off < 0 || off + 8 > buf.len) {
+            PyBuffer_Release(&buf);
+            if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "offset outside the buffer");
+            return nullptr;
+        }
+        uint64_t p = 0;
+        if (args[i] != Py_None) {
+            if (!THPVariable_Check(args[i])) {
+                PyBuffer_Release(&buf);
+                PyErr_Format(PyExc_TypeError, "a tensor expected, got %s", Py_TYPE(args[i])->tp_name);
+                return nullptr;
+            }
+            try {
+                p = (uint64_t) reinterpret_cast<uintptr_t>(THPVariable_Unpack(args[i]).data_ptr());
+            } catch (const std::exception& e) {
+                PyBuffer_Release(&buf);
+                PyErr_SetString(PyExc_RuntimeError, e.what());
+                return nullptr;
+            }
+        }
+        std::memcpy(static_cast<char*>(buf.buf) + off, &p, 8);
+    }
+    PyBuffer_Release(&buf);
+    Py_RETURN_NONE;
+}
+
+PyMethodDef kMethods[] = {
+    {"facts", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(facts)), METH_FASTCALL, nullptr},
+    {"fill", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(fill)), METH_FASTCALL, nullptr},
+    {nullptr, nullptr, 0, nullptr}};
+
+PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_tensor_facts", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__tensor_facts(void) {
+    PyObject* m = PyModule_Create(&kModule);
+    if (m) PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION);
+    return m;
+}

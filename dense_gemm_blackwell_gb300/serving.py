@@ -105,6 +105,7 @@ def _lib():
                            ("paged_attn_run", [_PTR, ref(PagedAttnArgs), _PTR]), ("paged_attn_plan_destroy", [_PTR])):
             f = getattr(L, name)
             f.argtypes, f.restype = args, ctypes.c_int
+        _use_native_facts()
         L.qk_norm_rope_backward_workspace.argtypes, L.qk_norm_rope_backward_workspace.restype = [], _I64
         _declared = L
     return _declared
@@ -115,13 +116,34 @@ def _check(status, where):
         raise GemmError(status, where)
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _facts(*tensors):
+def _python_facts(*tensors):
     """What a call's checks depend on: everything about its tensors but their addresses and contents."""
     return tuple([None if t is None else (t.shape, t.stride(), t.dtype, t.get_device()) for t in tensors])
+
+
+def _python_fill(args, offsets, *tensors):
+    """Writes each tensor's data address (None: 0) at its byte offset of a ctypes structure."""
+    for off, t in zip(offsets, tensors):
+        _PTR.from_buffer(args, off).value = None if t is None else t.data_ptr()
+
+
+_facts, _fill = _python_facts, _python_fill
+
+
+def _use_native_facts():
+    """Takes the two functions above from the compiled extension, when it was built for this torch."""
+    global _facts, _fill
+    import torch
+    try:
+        from . import _tensor_facts as native
+    except ImportError:
+        return
+    if native.torch_version == torch.__version__.split("+")[0]:
+        _facts, _fill = native.facts, native.fill
+
+
+def _offsets(cls, *names):
+    return tuple([getattr(cls, n).offset for n in names])
 
 
 def _need(cond, text):
@@ -216,11 +238,10 @@ class LoraPlan(_Plan):
         if checked is None:
             checked = self._args[key] = self._checked(x, w, a, b, adapter, y, scale)
         g = LoraArgs.from_buffer_copy(checked)
-        g.x, g.w, g.a, g.b, g.adapter, g.y = (x.data_ptr(), w.data_ptr(), a.data_ptr(), b.data_ptr(), adapter.data_ptr(),
-                                              y.data_ptr())
-        if scale is not None:
-            g.scale = scale.data_ptr()
-        _check(_lib().lora_run(self.handle, ctypes.byref(g), current_stream_handle() if stream is None else stream), "lora_run")
+        _fill(g, _LORA_PTRS, x, w, a, b, adapter, scale, y)
+        status = _declared.lora_run(self.handle, ctypes.byref(g), current_stream_handle() if stream is None else stream)
+        if status:
+            raise GemmError(status, "lora_run")
         return y
 
     def sync_status(self, stream=None):
@@ -230,6 +251,7 @@ class LoraPlan(_Plan):
         return s, rec
 
 
+_LORA_PTRS = _offsets(LoraArgs, "x", "w", "a", "b", "adapter", "scale", "y")
 _lora_plans = {}
 
 
@@ -376,6 +398,9 @@ def _checked_rope(q, k, positions, table, q_weight, k_weight, eps, interleaved, 
     return g
 
 
+_ROPE_PTRS = _offsets(QkNormRopeArgs, "q", "k", "positions", "table", "q_weight", "k_weight", "q_out", "k_out", "v", "k_cache", "v_cache",
+                      "slots")
+_GRAD_PTRS = _offsets(QkNormRopeGrads, "dq_out", "dk_out", "dq", "dk")
 _rope_checked = {}
 _rope_backward_checked = {}
 _rope_workspaces = {}
@@ -392,26 +417,22 @@ def qk_norm_rope(q, k, positions, table, *, q_weight=None, k_weight=None, eps=1e
     With k_cache, v_cache [pages, page_size, kv_heads, head_dim] the keys and v's values also go to slots [tokens] (int32:
     page * page_size + place, negative: nowhere); a float8_e4m3fn cache holds them divided by k_scale / v_scale.
     """
-    import torch
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = q.new_empty(q.shape)
     if k_out is None and k_cache is None and k is not None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        k_out = k.new_empty(k.shape)
     key = (eps, interleaved, norm, _facts(q, k, positions, table, q_weight, k_weight, q_out, k_out, v, k_cache, v_cache, slots))
     checked = _rope_checked.get(key)
     if checked is None:
         checked = _rope_checked[key] = _checked_rope(q, k, positions, table, q_weight, k_weight, eps, interleaved, norm, q_out,
                                                      k_out, v, k_cache, v_cache, slots)
     g = QkNormRopeArgs.from_buffer_copy(checked)
-    g.table, g.positions, g.q, g.q_out = table.data_ptr(), positions.data_ptr(), q.data_ptr(), q_out.data_ptr()
-    if k is not None:
-        g.k, g.k_out = k.data_ptr(), _ptr(k_out)
-    if norm:
-        g.q_weight, g.k_weight = _ptr(q_weight), _ptr(k_weight)
+    _fill(g, _ROPE_PTRS, q, k, positions, table, q_weight, k_weight, q_out, k_out, v, k_cache, v_cache, slots)
     if k_cache is not None:
-        g.v, g.k_cache, g.v_cache, g.slots = v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr()
         g.k_scale, g.v_scale = k_scale, v_scale
-    _check(_lib().qk_norm_rope_run(ctypes.byref(g), current_stream_handle() if stream is None else stream), "qk_norm_rope")
+    status = (_declared or _lib()).qk_norm_rope_run(ctypes.byref(g), current_stream_handle() if stream is None else stream)
+    if status:
+        raise GemmError(status, "qk_norm_rope")
     return q_out, k_out
 
 
@@ -438,30 +459,26 @@ def qk_norm_rope_backward(dq, dk, q, k, positions, table, *, q_weight=None, k_we
     """
     import torch
     if dq_out is None:
-        dq_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        dq_out = q.new_empty(q.shape)
     if dk_out is None and k is not None:
-        dk_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        dk_out = k.new_empty(k.shape)
     key = (eps, interleaved, norm, _facts(dq, dk, q, k, positions, table, q_weight, k_weight, dq_out, dk_out))
     checked = _rope_backward_checked.get(key)
     if checked is None:
         checked = _rope_backward_checked[key] = _checked_rope_backward(dq, dk, q, k, positions, table, q_weight, k_weight, eps,
                                                                        interleaved, norm, dq_out, dk_out)
     g, d = QkNormRopeArgs.from_buffer_copy(checked[0]), QkNormRopeGrads.from_buffer_copy(checked[1])
-    g.table, g.positions, g.q = table.data_ptr(), positions.data_ptr(), q.data_ptr()
-    d.dq_out, d.dq = dq.data_ptr(), dq_out.data_ptr()
-    if k is not None:
-        g.k, d.dk_out, d.dk = k.data_ptr(), dk.data_ptr(), dk_out.data_ptr()
+    _fill(g, _ROPE_PTRS[:6], q, k, positions, table, q_weight, k_weight)
+    _fill(d, _GRAD_PTRS, dq, dk, dq_out, dk_out)
     dqw = dkw = None
     if norm and (q_weight is not None or k_weight is not None):
         if stream is None:
             stream = current_stream_handle()
         n, device = q.shape[2], q.device
         if q_weight is not None:
-            g.q_weight = q_weight.data_ptr()
             dqw = torch.empty(n, dtype=torch.float32, device=device)
             d.dq_weight = dqw.data_ptr()
         if k_weight is not None and k is not None:
-            g.k_weight = k_weight.data_ptr()
             dkw = torch.empty(n, dtype=torch.float32, device=device)
             d.dk_weight = dkw.data_ptr()
         # the library's workspace: one per device and stream (a stream's calls follow one another), or the graph's own
@@ -479,6 +496,9 @@ def qk_norm_rope_backward(dq, dk, q, k, positions, table, *, q_weight=None, k_we
 
 
 # ---------------------------------------------------------------- attention of one token over a paged cache
+
+_ATTN_PTRS = _offsets(PagedAttnArgs, "q", "k_cache", "v_cache", "block_table", "lengths", "out", "lse")
+
 
 class PagedAttentionPlan(_Plan):
     """softmax(scale q K^T) V of one new token per sequence over a paged cache.
@@ -546,11 +566,10 @@ class PagedAttentionPlan(_Plan):
         if checked is None:
             checked = self._args[key] = self._checked(q, k_cache, v_cache, block_table, lengths, out, lse)
         g = PagedAttnArgs.from_buffer_copy(checked)
-        g.q, g.k_cache, g.v_cache, g.block_table = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr()
-        g.lengths, g.out = lengths.data_ptr(), out.data_ptr()
-        if lse is not None:
-            g.lse = lse.data_ptr()
+        _fill(g, _ATTN_PTRS, q, k_cache, v_cache, block_table, lengths, out, lse)
         g.scale = self.desc.head_dim ** -0.5 if scale is None else scale
         g.k_scale, g.v_scale = k_scale, v_scale
-        _check(_lib().paged_attn_run(self.handle, ctypes.byref(g), current_stream_handle() if stream is None else stream), "paged_attn_run")
+        status = _declared.paged_attn_run(self.handle, ctypes.byref(g), current_stream_handle() if stream is None else stream)
+        if status:
+            raise GemmError(status, "paged_attn_run")
         return out

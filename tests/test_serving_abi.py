@@ -183,6 +183,35 @@ def test_python_layer_refuses_host_tensors():
         dg.qk_norm_rope(x, None, torch.zeros(4, dtype=torch.int32), torch.zeros(8, 2, 32))
 
 
+def test_native_tensor_facts_agree_with_the_python_ones():
+    """Both tell the same layouts apart and write the same addresses."""
+    serving._lib()
+    native = pytest.importorskip("dense_gemm_blackwell_gb300._tensor_facts")
+    a = torch.zeros(4, 6, 8)
+    kinds = [a, a.clone(), a[1:], a[:, ::2], a.transpose(0, 1), a.half(), torch.zeros(4, 6, 8, 1), torch.zeros(()), None,
+             torch.zeros(24, 8), a.double(), torch.zeros(4, 6, 8, dtype=torch.int32)]
+    for x in kinds:
+        for y in kinds:
+            for rest in ((), (a, None)):
+                same = serving._python_facts(x, *rest) == serving._python_facts(y, *rest)
+                assert (native.facts(x, *rest) == native.facts(y, *rest)) == same
+    assert native.facts(a, None) != native.facts(None, a)
+    assert native.facts(a) != native.facts(a.to("meta"))
+    offsets = serving._LORA_PTRS
+    one, two = serving.LoraArgs(), serving.LoraArgs()
+    tensors = (a, a[2:], None, torch.zeros(0), a.half(), None, a[:, 1:])
+    native.fill(one, offsets, *tensors)
+    serving._python_fill(two, offsets, *tensors)
+    assert bytes(one) == bytes(two) and one.w == a[2:].data_ptr() and one.scale is None
+    for bad in (lambda: native.facts(3), lambda: native.facts("x", a), lambda: native.facts(a.to_sparse()), lambda: native.fill(one, (0,), 3),
+                lambda: native.fill(one, (0, 8), a), lambda: native.fill(one)):
+        with pytest.raises(TypeError):
+            bad()
+    for off in (-1, ctypes.sizeof(one), 1 << 40):
+        with pytest.raises(ValueError):
+            native.fill(one, (off,), a)
+
+
 # ---------------------------------------------------------------- rope_table
 
 def plain_table(positions, freq, gain=1.0):
