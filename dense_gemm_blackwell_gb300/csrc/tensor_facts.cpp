@@ -35,8 +35,12 @@ PyObject* facts(PyObject*, PyObject* const* args, Py_ssize_t n) {
             PyErr_Format(PyExc_TypeError, "a tensor expected, got %s", Py_TYPE(args[i])->tp_name);
             return nullptr;
         }
-        try {       // sparse tensors have no strides: torch throws
+        try {
             const at::Tensor& t = THPVariable_Unpack(args[i]);
+            if (t.layout() != at::kStrided) {
+                PyErr_SetString(PyExc_TypeError, "a dense tensor expected");
+                return nullptr;
+            }
             const auto sizes = t.sizes(), strides = t.strides();
             if (sizes.size() > 8) {
                 PyErr_SetString(PyExc_ValueError, "a tensor of more than eight dimensions");
@@ -50,8 +54,8 @@ PyObject* facts(PyObject*, PyObject* const* args, Py_ssize_t n) {
             at += (Py_ssize_t)sizes.size() * 8;
             std::memcpy(key + at, strides.data(), strides.size() * 8);
             at += (Py_ssize_t)strides.size() * 8;
-        } catch (const std::exception& e) {
-            PyErr_SetString(PyExc_TypeError, "a dense tensor expected");
+        } catch (const std::exception& e) {     // nothing of torch's is thrown through Python
+            PyErr_SetString(PyExc_TypeError, e.what());
             return nullptr;
         }
     }
