@@ -17,8 +17,7 @@
 // sums are fp32, added in a fixed order.
 //
 // Two forms of the first kernel:
-//   gather_kernel, up to kGatherTokens tokens (decode batches, each adapter
-//   with few rows): a CTA per token, of which every eighth of an adapter goes
+//   gather_kernel, for decode batches (each adapter with few rows): a CTA per token, of which every eighth of an adapter goes
 //   on, with its row and the adapter's next seven.  Its time is latency,
 //   so nothing is staged: eight warps split K and load 16-byte pieces of A_i
 //   and of the rows straight into matrix fragments, many at once;
@@ -402,8 +401,12 @@ static cudaError_t launch_stream_typed(const ShrinkParams& p, dim3 grid, cudaStr
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-// Whether the plan's first kernel gathers rows (see the top of this file).  A rank above 128 does not fit its registers.
-static bool gathers(const lora_desc_t& d) { return d.tokens <= kGatherTokens && d.rank <= 128; }
+// Whether the plan's first kernel gathers rows (see the top of this file): always for a decode batch; up to 1024 tokens where
+// an adapter has few of them on average (GB300, 400 x 4096 x 4096 with 64 adapters: 34 us against 62 streamed; 777 x 1543 x
+// 1001 with 5: 15.6 against 12.9).  A rank above 128 does not fit its registers.
+static bool gathers(const lora_desc_t& d) {
+    return d.rank <= 128 && (d.tokens <= kGatherTokens || (d.tokens <= 1024 && d.tokens <= 16 * (int64_t)d.adapters));
+}
 
 template <typename T>
 static cudaError_t launch_shrink(const ShrinkParams& p, bool gather, dim3 grid, cudaStream_t stream) {
@@ -459,14 +462,16 @@ gemm_status_t check_desc(const lora_desc_t& d) {
 
 // Tiles and K split of the few-tile kernel; false: the persistent kernel.  On GB300 up to 256 tokens ran 1.3 to 1.9 times
 // faster in one wave of this kernel than in the persistent one (4 x 4096 x 4096: 12.8 against 21.9 us; 200 x 4096 x 4096:
-// 20.6 against 30.0), 512 tokens 1.1 times, 777 x 1543 x 1001 slower (17.7 against 12.7).  Clusters of eight leave SMs
+// 20.6 against 30.0); up to 512 tokens it still pays on long K (300 x 1024 x 4096: 14.8 against 18.5; 512 x 4096 x 4096: 27.6
+// against 29.5), and not on short K or with more tiles (777 x 1543 x 1001: 17.7 against 12.7).  Clusters of eight leave SMs
 // without a place in one (128 CTAs of 96 x 4096 x 4096: 38.5 us, in fours 24.9), and a second wave costs as much as the
 // first.  Within that: the least time a CTA takes to bring in its operands (about 50 bytes a cycle into an SM and 100
 // cycles a stage) and, in a cluster, to join (2,000 cycles and a tenth of one per element).
 bool plan_skinny(const lora_desc_t& d, const DeviceFacts& dev, lora_plan_s* p) {
     // a forced choice of the persistent kernel's parameters keeps it
-    if (d.flags || d.tile_n || d.stages || d.max_ctas || d.tokens > 256) return false;
+    if (d.flags || d.tile_n || d.stages || d.max_ctas) return false;
     const int64_t m_blocks = (d.tokens + 127) / 128, k_blocks = (d.k + 63) / 64;
+    if (d.tokens > 256 && (d.tokens > 512 || d.k < 2048 || m_blocks * ((d.n + 127) / 128) > dev.sms)) return false;
     const int64_t box_m = up(std::min<int64_t>(d.tokens, 128), 8);
     double best = 0;
     for (int64_t tile_n = 32; tile_n <= 256; tile_n *= 2)

@@ -142,29 +142,8 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
         const int t = tiles_of<S::kTile>(first, length);
         return t > 0 ? (int64_t)(t + kAttnSegmentCost) * HV : 0;
     };
-    const int64_t first_units = units_of(threadIdx.x);
-    int64_t mine = first_units;
-    for (int b = threadIdx.x + kAttnThreads; b < B; b += kAttnThreads) mine += units_of(b);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) scan_part[warp] = mine;
-    __syncthreads();
-    int64_t total = 0;
-#pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) total += scan_part[w];
-    // Small problems leave CTAs idle rather than cut segments finely.
-    const int ctas = (int)min((int64_t)gridDim.x, (total + kAttnMinUnits - 1) / kAttnMinUnits);
-    if ((int)blockIdx.x >= ctas) {
-        write_empty();
-        return;
-    }
-    auto range_start = [&](int c) { return total * c / ctas; };
-    const int64_t range0 = range_start(blockIdx.x), range1 = range_start(blockIdx.x + 1);
-    // The sequence that holds unit range0: scan 128 sequences at a time.
-    int64_t before = 0;
-    for (int base = 0; base < B; base += kAttnThreads) {
-        const int b = base + threadIdx.x;
-        const int64_t v = base == 0 ? first_units : units_of(b);
+    // Units before this thread's sequence among 128 of them, and all of them's.
+    auto scan = [&](int64_t v, int64_t& all) {
         int64_t incl = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -174,19 +153,45 @@ __global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kern
         __syncthreads();
         if (lane == 31) scan_part[warp] = incl;
         __syncthreads();
-        int64_t lo = before + incl - v;
-        int64_t all = 0;
+        int64_t lo = incl - v;
+        all = 0;
 #pragma unroll
         for (int w = 0; w < kAttnWarps; ++w) {
             if (w < warp) lo += scan_part[w];
             all += scan_part[w];
         }
-        if (range0 >= lo && range0 < lo + v) {
-            found_b = b;
-            found_rest = range0 - lo;
+        return lo;
+    };
+    int64_t v = units_of(threadIdx.x), all;
+    int64_t lo = scan(v, all);                   // the first 128 sequences
+    int64_t total = all;
+    if (B > kAttnThreads) {
+        int64_t rest = 0;
+        for (int b = threadIdx.x + kAttnThreads; b < B; b += kAttnThreads) rest += units_of(b);
+        int64_t more;
+        scan(rest, more);
+        total += more;
+    }
+    // Small problems leave CTAs idle rather than cut segments finely.
+    const int ctas = (int)min((int64_t)gridDim.x, (total + kAttnMinUnits - 1) / kAttnMinUnits);
+    if ((int)blockIdx.x >= ctas) {
+        write_empty();
+        return;
+    }
+    auto range_start = [&](int c) { return total * c / ctas; };
+    const int64_t range0 = range_start(blockIdx.x), range1 = range_start(blockIdx.x + 1);
+    // The sequence that holds unit range0: 128 sequences at a time.
+    int64_t before = 0;
+    for (int base = 0;;) {
+        if (range0 >= before + lo && range0 < before + lo + v) {
+            found_b = base + threadIdx.x;
+            found_rest = range0 - before - lo;
         }
         before += all;
-        if (before > range0) break;
+        base += kAttnThreads;
+        if (before > range0 || base >= B) break;
+        v = units_of(base + threadIdx.x);
+        lo = scan(v, all);
     }
     __syncthreads();
 
