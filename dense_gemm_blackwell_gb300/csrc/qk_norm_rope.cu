@@ -300,9 +300,17 @@ __global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const __grid
 // The two row sums (x^2 and g w x) are reduced side by side.  A block takes queries or keys only, so that one weight and
 // one weight gradient stay in registers while its lane groups walk the tokens; it adds its groups' gradients in a fixed
 // order and leaves one partial for weight_grad_kernel.
+//
+// A lane group's work is a sequence of batches of four rows.  While one batch is computed the next one's x, dy and the
+// token's cosines and sines come by asynchronous copies into this thread's own places of shared memory (no barriers): held in
+// registers instead, the loads of a batch were waited for before its arithmetic began (8192 tokens: 55 us).
+constexpr int kGradAhead = 4;                            // rows of a batch
+constexpr int kGradPieces = 2 * kGradAhead + 4;          // 16-byte pieces of a thread's stage: x, dy, table
+constexpr int kGradSmem = 2 * kGradPieces * kRopeThreads * 16;
+
 template <typename T, int LANES, int PAIRS>
 __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_backward_kernel(const __grid_constant__ RopeParams p) {
-    constexpr int kAhead = 4;
+    extern __shared__ __align__(16) uint4 staged[];      // [stage][piece][thread]
     __shared__ float scratch[PAIRS == kPairsAny ? (kRopeThreads / LANES) * LANES * 8 : 1];
     __shared__ float sums[kRopeThreads / 32][LANES * 8];
     griddep_wait();
@@ -336,68 +344,154 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_backward_kernel(con
 
     const uint32_t step = blocks * (uint32_t)(kRopeThreads / LANES);
     const uint32_t warp_first = block * (uint32_t)(kRopeThreads / LANES) + (threadIdx.x & ~31) / LANES;
-    // warp-uniform trip count: the warp's first group has the most items
-    for (uint32_t base = warp_first; base < items; base += step) {
-        const uint32_t item = base + (threadIdx.x & 31) / LANES;
-        const bool valid = item < items;
-        const int token = valid ? (int)(item / groups) : 0;
-        const int h0 = valid ? (int)(item % groups) * p.rows_per_group : 0;
-        const int rows = min(p.rows_per_group, heads - h0);       // at least one
-        const bool stores = valid && me.act;
-        const T* xs = x_base + token * x_token + h0 * x_head;
-        const T* gs = g_base + token * g_token + h0 * g_head;
-        T* ds = d_base + token * d_token + h0 * d_head;
-        uint4 rx[kAhead], rg[kAhead];
-        // rows past the group's last one are its last one again, neither stored nor summed
-        auto load_batch = [&](int b) {
+    // A place in this lane group's sequence of batches.  `base`, the warp's first group's item, is the same in the whole
+    // warp (its first group has the most items), so every lane runs the same number of batches.
+    struct Place {
+        uint32_t base;
+        int batch, token, h0, rows;
+        bool valid;
+    };
+    auto enter = [&](Place& at) {        // an item's rows; the last rows of the list stand in for items that do not exist
+        const uint32_t item = at.base + (threadIdx.x & 31) / LANES;
+        at.valid = item < items;
+        at.token = at.valid ? (int)(item / groups) : 0;
+        at.h0 = at.valid ? (int)(item % groups) * p.rows_per_group : 0;
+        at.rows = min(p.rows_per_group, heads - at.h0);       // at least one
+        at.batch = 0;
+    };
+    auto advance = [&](Place& at) {
+        at.batch += kGradAhead;
+        if (at.batch < p.rows_per_group) return;
+        at.base += step;
+        if (at.base < items) enter(at);
+    };
+    const uint32_t place0 = smem_u32(staged) + threadIdx.x * 16u;
+    auto piece = [&](int stage, int i) { return place0 + (uint32_t)(stage * kGradPieces + i) * (kRopeThreads * 16u); };
+    const int half = a.rot_dim / 2;
+    int position = 0;                    // of the token that is copied next; fetched a batch ahead
+    auto fetch_position = [&](const Place& at) {
+        if (PAIRS != kPairsAny && me.live && at.base < items && at.batch == 0)
+            position = min(max(a.positions[at.token], 0), a.table_rows - 1);
+    };
+    auto copy = [&](const Place& at, int stage) {
+        if (at.base < items) {
+            const T* xs = x_base + at.token * x_token + at.h0 * x_head;
+            const T* gs = g_base + at.token * g_token + at.h0 * g_head;
+            // rows past the group's last one are its last one again, neither stored nor summed
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int r = min(b + u, rows - 1);
-                rx[u] = load_row16(xs + (int64_t)r * x_step);
-                rg[u] = load_row16(gs + (int64_t)r * g_step);
+            for (int u = 0; u < kGradAhead; ++u) {
+                const int r = min(at.batch + u, at.rows - 1);
+                cp_async_16(piece(stage, 2 * u), xs + (int64_t)r * x_step);
+                cp_async_16(piece(stage, 2 * u + 1), gs + (int64_t)r * g_step);
             }
-        };
-        load_batch(0);       // on the way while the factors' chain of loads (position, table) runs
-        float own[8], other[8];
-        load_factors<T, PAIRS>(a, nullptr, token, me.e0, me.act, me.live, -1.f, own, other);
-        for (int b = 0; b < p.rows_per_group; b += kAhead) {
-            if (b > 0) load_batch(b);
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const bool on = stores && b + u < rows;
-                float g[8], z[8];
-                unpack8<T>(rg[u], g);
-                partners<T, PAIRS>(a, me.e0, me.live, me.mate, srow, rg[u], g, z);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) g[i] = fmaf(z[i], other[i], g[i] * own[i]);
-                if (a.norm) {
-                    float x[8];
-                    unpack8<T>(rx[u], x);
-                    float sq = 0.f, dot = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        sq = fmaf(x[i], x[i], sq);
-                        dot = fmaf(g[i] * w[i], x[i], dot);
-                    }
-                    if (!me.act) sq = dot = 0.f;
-#pragma unroll
-                    for (int o = LANES / 2; o > 0; o >>= 1) {
-                        sq += __shfl_xor_sync(0xffffffffu, sq, o);
-                        dot += __shfl_xor_sync(0xffffffffu, dot, o);
-                    }
-                    const float inv = rsqrtf(fmaf(sq, inv_d, a.eps));
-                    const float k = inv * inv * dot * inv_d;
-                    const float counted = on ? inv : 0.f;       // a repeated row adds nothing to the weight's gradient
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        dw[i] = fmaf(g[i] * counted, x[i], dw[i]);
-                        g[i] = inv * fmaf(-x[i], k, g[i] * w[i]);
-                    }
+            if (PAIRS != kPairsAny && me.live && at.batch == 0) {
+                const float* row = a.table + (size_t)position * a.rot_dim;
+                if constexpr (PAIRS == kPairsHalves) {
+                    const int i0 = me.e0 >= half ? me.e0 - half : me.e0;
+                    cp_async_16(piece(stage, 2 * kGradAhead), row + i0);
+                    cp_async_16(piece(stage, 2 * kGradAhead + 1), row + i0 + 4);
+                    cp_async_16(piece(stage, 2 * kGradAhead + 2), row + half + i0);
+                    cp_async_16(piece(stage, 2 * kGradAhead + 3), row + half + i0 + 4);
+                } else {
+                    cp_async_16(piece(stage, 2 * kGradAhead), row + me.e0 / 2);
+                    cp_async_16(piece(stage, 2 * kGradAhead + 1), row + half + me.e0 / 2);
                 }
-                if (on) *reinterpret_cast<uint4*>(ds + (int64_t)(b + u) * d_step) = round8<T>(g);
             }
         }
+        cp_async_commit();
+    };
+
+    Place now, ahead;
+    now.base = warp_first;
+    if (now.base < items) enter(now);
+    ahead = now;
+    fetch_position(ahead);
+    copy(ahead, 0);
+    if (ahead.base < items) advance(ahead);
+    fetch_position(ahead);
+    int stage = 0;
+    float own[8], other[8];
+    while (now.base < items) {
+        copy(ahead, stage ^ 1);
+        if (ahead.base < items) advance(ahead);
+        fetch_position(ahead);
+        cp_async_wait<1>();
+        auto staged_piece = [&](int i) { return staged[(stage * kGradPieces + i) * kRopeThreads + threadIdx.x]; };
+        if (now.batch == 0) {
+            // the turn back: the sines' signs are the forward's negated
+            if constexpr (PAIRS == kPairsAny) {
+                load_factors<T, PAIRS>(a, nullptr, now.token, me.e0, me.act, me.live, -1.f, own, other);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    own[i] = 1.f;
+                    other[i] = 0.f;
+                }
+                if (me.live) {
+                    if constexpr (PAIRS == kPairsHalves) {
+                        const uint4 c[2] = {staged_piece(2 * kGradAhead), staged_piece(2 * kGradAhead + 1)};
+                        const uint4 t[2] = {staged_piece(2 * kGradAhead + 2), staged_piece(2 * kGradAhead + 3)};
+                        const float sg = me.e0 >= half ? -1.f : 1.f;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            own[4 * i] = __uint_as_float(c[i].x); own[4 * i + 1] = __uint_as_float(c[i].y);
+                            own[4 * i + 2] = __uint_as_float(c[i].z); own[4 * i + 3] = __uint_as_float(c[i].w);
+                            other[4 * i] = sg * __uint_as_float(t[i].x); other[4 * i + 1] = sg * __uint_as_float(t[i].y);
+                            other[4 * i + 2] = sg * __uint_as_float(t[i].z); other[4 * i + 3] = sg * __uint_as_float(t[i].w);
+                        }
+                    } else {
+                        const uint4 c = staged_piece(2 * kGradAhead), t = staged_piece(2 * kGradAhead + 1);
+                        const uint32_t cw[4] = {c.x, c.y, c.z, c.w}, tw[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            own[2 * i] = own[2 * i + 1] = __uint_as_float(cw[i]);
+                            other[2 * i] = __uint_as_float(tw[i]);
+                            other[2 * i + 1] = -__uint_as_float(tw[i]);
+                        }
+                    }
+                }
+            }
+        }
+        T* ds = d_base + now.token * d_token + now.h0 * d_head;
+        const bool stores = now.valid && me.act;
+#pragma unroll
+        for (int u = 0; u < kGradAhead; ++u) {
+            const bool on = stores && now.batch + u < now.rows;
+            const uint4 rg = staged_piece(2 * u + 1);
+            float g[8], z[8];
+            unpack8<T>(rg, g);
+            partners<T, PAIRS>(a, me.e0, me.live, me.mate, srow, rg, g, z);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = fmaf(z[i], other[i], g[i] * own[i]);
+            if (a.norm) {
+                float x[8];
+                unpack8<T>(staged_piece(2 * u), x);
+                float sq = 0.f, dot = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    sq = fmaf(x[i], x[i], sq);
+                    dot = fmaf(g[i] * w[i], x[i], dot);
+                }
+                if (!me.act) sq = dot = 0.f;
+#pragma unroll
+                for (int o = LANES / 2; o > 0; o >>= 1) {
+                    sq += __shfl_xor_sync(0xffffffffu, sq, o);
+                    dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                }
+                const float inv = rsqrtf(fmaf(sq, inv_d, a.eps));
+                const float k = inv * inv * dot * inv_d;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (on) dw[i] = fmaf(g[i] * inv, x[i], dw[i]);
+                    g[i] = inv * fmaf(-x[i], k, g[i] * w[i]);
+                }
+            }
+            if (on) *reinterpret_cast<uint4*>(ds + (int64_t)(now.batch + u) * d_step) = round8<T>(g);
+        }
+        advance(now);
+        stage ^= 1;
     }
+    cp_async_wait<0>();
     if (!(is_q ? gr.dq_weight : gr.dk_weight)) return;
     // groups of a warp, then warps of the block, in a fixed order
 #pragma unroll
@@ -427,8 +521,16 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const float* partials
     float* out = keys ? dk_weight : dq_weight;
     const int e = blockIdx.x * 32 + col;
     float v = 0.f;
-    if (out && e < head_dim)
-        for (int b = (keys ? q_blocks : 0) + s; b < (keys ? blocks : q_blocks); b += 32) v += partials[(size_t)b * kMaxHeadDim + e];
+    if (out && e < head_dim) {
+        const int end = keys ? blocks : q_blocks;
+        for (int b = (keys ? q_blocks : 0) + s; b < end; b += 32 * 8) {
+            float x[8];      // eight loads on the way at once
+#pragma unroll
+            for (int u = 0; u < 8; ++u) x[u] = b + 32 * u < end ? partials[(size_t)(b + 32 * u) * kMaxHeadDim + e] : 0.f;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v += x[u];
+        }
+    }
     strip[s][col] = v;
     __syncthreads();
     if (s == 0 && out && e < head_dim) {
@@ -565,8 +667,11 @@ struct LaunchBackward {
         p.q_blocks = (uint32_t)q;
         const bool weights = p.g.dq_weight || p.g.dk_weight;
         p.partials = static_cast<float*>(p.g.workspace);
-        cudaError_t e = launch_dependent(norm_rope_backward_kernel<T, LANES, PAIRS>, dim3((unsigned)(q + k)), dim3(kRopeThreads), 0,
-                                         stream, p);
+        static std::atomic<int> smem_set[kMaxDevices];
+        auto kern = norm_rope_backward_kernel<T, LANES, PAIRS>;
+        cudaError_t e = ensure_smem_limit(kern, kGradSmem, smem_set);
+        if (e != cudaSuccess) return e;
+        e = launch_dependent(kern, dim3((unsigned)(q + k)), dim3(kRopeThreads), kGradSmem, stream, p);
         if (e != cudaSuccess || !weights) return e;
         return launch_dependent(weight_grad_kernel, dim3((unsigned)((p.a.head_dim + 31) / 32), 2), dim3(1024), 0, stream,
                                 (const float*)p.partials, (int)q, (int)(q + k), (int)p.a.head_dim, p.g.dq_weight, p.g.dk_weight);
