@@ -157,6 +157,15 @@ def test_clusters_split_k_and_steps():
     check_exact(20, 64, 64, 16, 20, "mixed")
 
 
+@pytest.mark.parametrize("tokens,n,k,adapters,kind", [
+    (257, 200, 2056, 4, "runs"), (300, 1030, 2100, 3, "one"), (512, 136, 2100, 40, "mixed"), (511, 4100, 2048, 60, "wild"),       # few tiles, long K
+    (513, 136, 2100, 4, "runs"), (1000, 520, 136, 200, "mixed"), (1024, 300, 4200, 64, "mixed"), (1025, 300, 200, 64, "mixed"),   # persistent, gathered or streamed
+    (777, 2100, 3200, 300, "wild")])
+def test_middle_sizes(tokens, n, k, adapters, kind):
+    """Around the token counts at which the kernels of both launches change."""
+    check_exact(tokens, n, k, 24, adapters, kind, out=torch.bfloat16)
+
+
 def test_workspace_carries_nothing_over():
     """One plan, adapters that change from run to run: rows that had an adapter's T must be zero for it now."""
     for tokens in (60, 500):
