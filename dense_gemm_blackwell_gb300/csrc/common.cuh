@@ -157,6 +157,12 @@ struct LoraTail {
     int32_t max_adapters;     // slots per m block
     int32_t steps;            // K = 16 steps per adapter
     int32_t b_steps;          // of which this many cover B's columns (steps = b_steps, or twice that for two-term T)
+    // one token's factors, for lora_repair.cuh
+    const void *x, *w, *b, *t;
+    const int32_t* adapter;
+    int64_t ldx, ldw, ldb, stride_b;
+    int32_t k, rank;
+    int32_t bf16;             // inputs bf16, otherwise f16
 };
 constexpr uint32_t kTailRowBytes = 32;           // one row of one step's B
 constexpr uint32_t kTailAtomBytes = 128 * 128;   // four steps of T: 128 rows of one 128-byte atom

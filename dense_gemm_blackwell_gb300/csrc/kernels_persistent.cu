@@ -54,6 +54,7 @@
 #include "ptx.cuh"
 #include "common.cuh"
 #include "launch.h"
+#include "lora_repair.cuh"
 #include "pipeline.cuh"
 
 namespace dgb {
@@ -569,6 +570,7 @@ __device__ __forceinline__ void persistent_body(const PersistentParams& p, const
                 if (staged) fence_proxy_async_smem();
             }
             const float4* part = reinterpret_cast<const float4*>(p.sk_partials) + part_base;
+            uint32_t spoiled = 0;   // TAIL: chunks in which this thread's row has a value that is not finite
             // Chunks that hold at least one in-range column of an in-range row; the
             // rest of the tile (padding beyond M or N) is neither read nor stored.
             const int n_valid = (m0 < p.M) ? min(nchunks, (p.N - n0 + kChunkCols - 1) / kChunkCols) : 0;
@@ -653,6 +655,12 @@ __device__ __forceinline__ void persistent_body(const PersistentParams& p, const
                             }
                         };
                         const int x = n0 + c * kChunkCols;
+                        if constexpr (TAIL) {
+                            float z = 0.f;
+#pragma unroll
+                            for (int h = 0; h < kSub; ++h) z = finite_probe(r[cc * kSub + h], z);
+                            if (z != 0.f && m0 + lane < p.M) spoiled |= 1u << c;
+                        }
                         if (p.direct_store || chunk_needs_clipped_store<kOutBytes>(x, kChunkCols, p.N)) {
                             // This thread's row: 128 contiguous bytes, streaming stores
                             // (element by element past N at a ragged right edge).
@@ -692,6 +700,21 @@ __device__ __forceinline__ void persistent_body(const PersistentParams& p, const
                 }
             }
             if (lost) break;
+            if constexpr (TAIL) {
+                if (__any_sync(0xffffffffu, spoiled != 0)) {
+                    // the tile's TMA stores are complete, then visible to every lane
+                    if (lane == 0) bulk_wait_group<0>();
+                    fence_proxy_async_all();
+                    __syncwarp();
+                    const int row = m0 + lane;
+                    if (row < p.M)
+                        for (uint32_t left = spoiled; left; left &= left - 1) {
+                            const int x = n0 + (__ffs(left) - 1) * kChunkCols;
+                            repair_row<OUT>(*tail, row, mb, x, min(x + kChunkCols, p.N),
+                                            static_cast<uint8_t*>(p.d_ptr) + ((size_t)row * p.ldd + x) * kOutBytes);
+                        }
+                }
+            }
             if (++acc == TS) { acc = 0; acc_phase ^= 1u; }
         }
         if (lane == 0) bulk_wait_group<0>();

@@ -372,7 +372,12 @@ __global__ void __launch_bounds__(kShrinkThreads) stream_kernel(const __grid_con
                 v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
                 v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
             }
-            store_t<T>(p, dst + (size_t)r * p.pitch + c, v, scale);
+            // a row of another adapter has to stay zero, also where A_i holds infinities or NaN
+            if (row_id[r] != id) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = 0.f;
+            }
+            store_t<T>(p, dst + (size_t)r * p.pitch + c, v, row_id[r] == id ? scale : 1.f);
         }
         cluster_sync();     // the sums are read; the next slot may overwrite them and the ring
     }
@@ -664,6 +669,18 @@ gemm_status_t lora_run(lora_plan_t plan, const lora_args_t* args, gemm_stream_t 
     tail.max_adapters = q.max_adapters;
     tail.steps = q.cols / 16;
     tail.b_steps = q.rank16 / 16;
+    tail.x = a.x;
+    tail.w = a.w;
+    tail.b = a.b;
+    tail.t = q.t;
+    tail.adapter = a.adapter;
+    tail.ldx = d.ldx;
+    tail.ldw = ldw;
+    tail.ldb = a.ldb;
+    tail.stride_b = a.stride_b;
+    tail.k = q.K;
+    tail.rank = d.rank;
+    tail.bf16 = d.dtype == GEMM_BF16;
     SkinnyParams sk;
     PersistentParams p;
     if (plan->skinny) {

@@ -27,6 +27,7 @@
 #include "common.cuh"
 #include "elem.cuh"
 #include "lora_list.cuh"
+#include "lora_repair.cuh"
 #include "lora_skinny.h"
 #include "pipeline.cuh"
 #include "ptx.cuh"
@@ -255,6 +256,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1) skinny_kernel(const __grid_
         const int pieces = p.tile_n / 4, all = rows * pieces;
         const int i1 = all * (r + 1) / KS;
         const uint32_t mine = smem_u32(ring);
+        float probe = 0.f;
         constexpr int kAhead = 4;      // pieces of a thread whose loads are in flight
         for (int i0 = all * r / KS + (int)threadIdx.x; i0 < i1; i0 += kAhead * kSkinnyThreads) {
             float4 x[kAhead][kSkinnyMaxSplit];
@@ -285,6 +287,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1) skinny_kernel(const __grid_
                 if (n >= p.N) continue;
                 const int64_t o = (int64_t)(m0 + row) * p.ldy + n;
                 const float f[4] = {v.x, v.y, v.z, v.w};
+                probe = fmaf(v.x, 0.f, fmaf(v.y, 0.f, fmaf(v.z, 0.f, fmaf(v.w, 0.f, probe))));
                 if constexpr (OUT == GEMM_F32) {
                     float* y = static_cast<float*>(p.y) + o;
                     if (n + 4 <= p.N) {
@@ -304,6 +307,12 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1) skinny_kernel(const __grid_
                 }
             }
         }
+        if (probe != 0.f)       // one of this thread's values is not finite
+            for (int i = all * r / KS + (int)threadIdx.x; i < i1; i += kSkinnyThreads) {
+                const int row = i / pieces, n = n0 + (i - row * pieces) * 4;
+                repair_row<OUT>(tail, m0 + row, mb, n, min(n + 4, p.N),
+                                static_cast<uint8_t*>(p.y) + ((int64_t)(m0 + row) * p.ldy + n) * (OUT == GEMM_F32 ? 4 : 2));
+            }
     }
     if (KS > 1) cluster_sync_relaxed(); else __syncthreads();     // peers have read this CTA's sums
     if (warp == 1) {

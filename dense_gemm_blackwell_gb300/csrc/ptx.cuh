@@ -94,6 +94,10 @@ __device__ __forceinline__ void fence_mbar_init() {
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
+// The same for every state space (global writes of TMA stores, read back with plain loads).
+__device__ __forceinline__ void fence_proxy_async_all() {
+    asm volatile("fence.proxy.async;" ::: "memory");
+}
 
 // 16-byte asynchronous copy global -> shared (L2 only, no L1 allocation): many
 // copies in flight per thread without holding registers.  The thread sees the

@@ -200,6 +200,32 @@ def test_one_token_s_nan_stays_its_own(tokens):
     assert torch.isnan(y[5]).all() and not torch.isfinite(y[11]).all()
 
 
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tokens,n,k,rank,kw", [
+    (20, 96, 128, 16, {}), (200, 264, 2056, 24, {}), (300, 1030, 2100, 16, {}), (300, 250, 96, 136, {}),
+    (700, 520, 200, 16, dict(flags=dg.GEMM_FLAG_CTA_GROUP_1)), (700, 520, 200, 16, dict(flags=dg.GEMM_FLAG_CTA_GROUP_2)),
+    (40, 300, 8200, 16, dict(tile_n=64)), (600, 1100, 1030, 16, dict(tile_n=512, flags=dg.GEMM_FLAG_CTA_GROUP_2))])
+def test_one_adapter_s_nan_stays_its_own(tokens, n, k, rank, kw, out):
+    """Infinities and NaN in an adapter reach the tokens that use it and no others, though they share its tiles: columns of B,
+    one whole A, and their neighbours with neither."""
+    (x, w, a, b, adapter, scale), want = make_exact(tokens, n, k, rank, 5, "mixed", 3, torch.bfloat16)
+    b[2, 3], b[2, n - 1, 1], b[4, ::7], a[1] = NAN, float("inf"), -float("inf"), NAN
+    y = padded(torch.empty(tokens, n, dtype=out, device="cuda"))
+    with dg.LoraPlan(tokens, n, k, rank=rank, adapters=5, dtype_y=CODE[out], ldx=x.stride(0), ldw=w.stride(0), ldy=y.stride(0),
+                     **kw) as plan:
+        for _ in range(2):
+            y.fill_(7)
+            plan.run(x, w, a, b, adapter, y, scale=scale)
+            assert plan.sync_status()[0] == dg.GEMM_OK
+            same = y == want.to(out)
+            hit = torch.zeros(5, n, dtype=torch.bool, device="cuda")       # columns of an adapter's tokens that may differ
+            hit[1], hit[2, 3], hit[2, n - 1], hit[4, ::7] = True, True, True, True
+            may = (adapter >= 0)[:, None] & hit[adapter.clamp(min=0).long()]
+            assert same[~may].all()
+            assert torch.isnan(y[adapter == 1]).all() and torch.isnan(y[adapter == 2, 3]).all()
+            assert not torch.isfinite(y[adapter == 4][:, ::7]).any()
+
+
 @pytest.mark.parametrize("tokens,n,k,rank,adapters,kind,dtype,out", [
     (1, 4096, 4096, 16, 8, "one", torch.bfloat16, torch.bfloat16), (77, 1000, 2048, 32, 40, "mixed", torch.bfloat16, torch.bfloat16),
     (200, 777, 3001, 64, 6, "mixed", torch.float16, torch.float16), (1500, 1024, 1024, 16, 3, "runs", torch.bfloat16, torch.float32),
