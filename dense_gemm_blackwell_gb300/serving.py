@@ -142,6 +142,14 @@ def _use_native_facts():
         _facts, _fill = native.facts, native.fill
 
 
+def _keep(table, key, value):
+    """table[key] = value; a table of checked layouts stays small however many there are."""
+    if len(table) >= 1024:
+        table.clear()
+    table[key] = value
+    return value
+
+
 def _offsets(cls, *names):
     return tuple([getattr(cls, n).offset for n in names])
 
@@ -236,7 +244,7 @@ class LoraPlan(_Plan):
         key = _facts(x, w, a, b, adapter, y, scale)
         checked = self._args.get(key)
         if checked is None:
-            checked = self._args[key] = self._checked(x, w, a, b, adapter, y, scale)
+            checked = _keep(self._args, key, self._checked(x, w, a, b, adapter, y, scale))
         g = LoraArgs.from_buffer_copy(checked)
         _fill(g, _LORA_PTRS, x, w, a, b, adapter, scale, y)
         status = _declared.lora_run(self.handle, ctypes.byref(g), current_stream_handle() if stream is None else stream)
@@ -424,8 +432,8 @@ def qk_norm_rope(q, k, positions, table, *, q_weight=None, k_weight=None, eps=1e
     key = (eps, interleaved, norm, _facts(q, k, positions, table, q_weight, k_weight, q_out, k_out, v, k_cache, v_cache, slots))
     checked = _rope_checked.get(key)
     if checked is None:
-        checked = _rope_checked[key] = _checked_rope(q, k, positions, table, q_weight, k_weight, eps, interleaved, norm, q_out,
-                                                     k_out, v, k_cache, v_cache, slots)
+        checked = _keep(_rope_checked, key, _checked_rope(q, k, positions, table, q_weight, k_weight, eps, interleaved, norm, q_out,
+                                                          k_out, v, k_cache, v_cache, slots))
     g = QkNormRopeArgs.from_buffer_copy(checked)
     _fill(g, _ROPE_PTRS, q, k, positions, table, q_weight, k_weight, q_out, k_out, v, k_cache, v_cache, slots)
     if k_cache is not None:
@@ -465,8 +473,8 @@ def qk_norm_rope_backward(dq, dk, q, k, positions, table, *, q_weight=None, k_we
     key = (eps, interleaved, norm, _facts(dq, dk, q, k, positions, table, q_weight, k_weight, dq_out, dk_out))
     checked = _rope_backward_checked.get(key)
     if checked is None:
-        checked = _rope_backward_checked[key] = _checked_rope_backward(dq, dk, q, k, positions, table, q_weight, k_weight, eps,
-                                                                       interleaved, norm, dq_out, dk_out)
+        checked = _keep(_rope_backward_checked, key, _checked_rope_backward(dq, dk, q, k, positions, table, q_weight, k_weight, eps,
+                                                                            interleaved, norm, dq_out, dk_out))
     g, d = QkNormRopeArgs.from_buffer_copy(checked[0]), QkNormRopeGrads.from_buffer_copy(checked[1])
     _fill(g, _ROPE_PTRS[:6], q, k, positions, table, q_weight, k_weight)
     _fill(d, _GRAD_PTRS, dq, dk, dq_out, dk_out)
@@ -564,7 +572,7 @@ class PagedAttentionPlan(_Plan):
         key = _facts(q, k_cache, v_cache, block_table, lengths, out, lse)
         checked = self._args.get(key)
         if checked is None:
-            checked = self._args[key] = self._checked(q, k_cache, v_cache, block_table, lengths, out, lse)
+            checked = _keep(self._args, key, self._checked(q, k_cache, v_cache, block_table, lengths, out, lse))
         g = PagedAttnArgs.from_buffer_copy(checked)
         _fill(g, _ATTN_PTRS, q, k_cache, v_cache, block_table, lengths, out, lse)
         g.scale = self.desc.head_dim ** -0.5 if scale is None else scale
