@@ -50,7 +50,13 @@ __host__ __device__ constexpr int next_pow2(int v) { return v <= 1 ? 1 : 2 * nex
 template <int KD, bool FP8, int NH>
 struct AttnShape {
     static constexpr int kHeads = 8 * NH;
-    static constexpr int kStages = 3;                    // steps in flight per warp
+    // CTAs an SM holds, and steps in the pipeline of a warp.  E4M3 rows of up to 80 bytes: a step's instructions (the
+    // conversions), not its bytes, are the longer part, and more warps count for more than a deeper pipeline: 64 sequences
+    // of 100 to 8192 positions, 8 kv heads of 64, take 36.4 us so and 40.1 with two CTAs and three stages; longer rows
+    // want the loads in flight (two sequences of 100,000, heads of 128: 92.4 so and 87.4).
+    static constexpr bool kManyCtas = FP8 && NH == 1 && KD <= 5;
+    static constexpr int kCtas = kManyCtas ? 3 : (KD <= 8 ? 2 : 1);
+    static constexpr int kStages = kManyCtas ? 2 : 3;
     static constexpr int kDim = KD * 16;                 // head elements held (head_dim rounded up)
     static constexpr int kBytes = FP8 ? 1 : 2;
     static constexpr int kChunks = KD * kBytes;          // 16-byte chunks of a row
@@ -89,7 +95,7 @@ __device__ __forceinline__ int tiles_of(int first, int length) {
 }
 
 template <typename T, typename TQ, bool FP8, int KD, int NH>
-__global__ void __launch_bounds__(kAttnThreads, KD <= 8 ? 2 : 1) paged_attn_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kAttnThreads, AttnShape<KD, FP8, NH>::kCtas) paged_attn_kernel(const __grid_constant__ AttnParams p) {
     using S = AttnShape<KD, FP8, NH>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t scan_part[kAttnWarps];
