@@ -49,6 +49,51 @@ __device__ __forceinline__ uint4 round8(const float (&f)[8]) {
     return make_uint4(round2<T>(f[0], f[1]), round2<T>(f[2], f[3]), round2<T>(f[4], f[5]), round2<T>(f[6], f[7]));
 }
 
+// Two fp32 values in a pair of registers, and arithmetic on both by one instruction (each rounded as usual).
+struct Pair {
+    unsigned long long v;
+};
+__device__ __forceinline__ Pair pair_of(float lo, float hi) {
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ Pair pair_of(float both) { return pair_of(both, both); }
+__device__ __forceinline__ float2 halves(Pair a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4& v, Pair (&f)[4]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 t = unpack2<T>(w[i]);
+        f[i] = pair_of(t.x, t.y);
+    }
+}
+template <typename T>
+__device__ __forceinline__ uint4 round8(const Pair (&f)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 t = halves(f[i]);
+        w[i] = round2<T>(t.x, t.y);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Four E4M3 codes (one 32-bit word) of f[0..3], saturated to +-448.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);

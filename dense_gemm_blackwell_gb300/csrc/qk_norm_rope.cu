@@ -126,7 +126,7 @@ __device__ __forceinline__ void load_factors(const qk_norm_rope_args_t& a, const
 // group's shared row.  Called by every lane of the warp.
 template <typename T, int PAIRS>
 __device__ __forceinline__ void partners(const qk_norm_rope_args_t& a, int e0, bool live, int mate, float* row, const uint4& raw,
-                                         const float (&x)[8], float (&z)[8]) {
+                                         const Pair (&x)[4], Pair (&z)[4]) {
     if constexpr (PAIRS == kPairsHalves) {
         uint4 r;
         r.x = __shfl_sync(0xffffffffu, raw.x, mate);
@@ -137,22 +137,39 @@ __device__ __forceinline__ void partners(const qk_norm_rope_args_t& a, int e0, b
         unpack8<T>(r, z);
     } else if constexpr (PAIRS == kPairsNeighbours) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = live ? x[i ^ 1] : 0.f;
+        for (int i = 0; i < 4; ++i) {
+            const float2 t = halves(x[i]);
+            z[i] = live ? pair_of(t.y, t.x) : pair_of(0.f);
+        }
     } else {
         const int half = a.rot_dim / 2;
         __syncwarp();
         if (live) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) row[e0 + i] = x[i];
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<float2*>(row + e0 + 2 * i) = halves(x[i]);
         }
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int e = e0 + i;
-            const int at = a.interleaved ? (e ^ 1) : (e < half ? e + half : e - half);
-            z[i] = e < a.rot_dim ? row[at] : 0.f;
+        for (int i = 0; i < 4; ++i) {
+            float t[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int e = e0 + 2 * i + j;
+                const int at = a.interleaved ? (e ^ 1) : (e < half ? e + half : e - half);
+                t[j] = e < a.rot_dim ? row[at] : 0.f;
+            }
+            z[i] = pair_of(t[0], t[1]);
         }
     }
+}
+
+__device__ __forceinline__ void as_pairs(const float (&f)[8], Pair (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pair_of(f[2 * i], f[2 * i + 1]);
+}
+__device__ __forceinline__ float sum_of(Pair a) {
+    const float2 t = halves(a);
+    return t.x + t.y;
 }
 
 template <int LANES, int PAIRS>
@@ -206,6 +223,14 @@ __device__ __forceinline__ void forward_rows(const RopeParams& p, uint32_t block
         src += token * a.v_token + h0 * a.v_head;
         src_step = (int32_t)a.v_head;
     }
+    // Every lane of a warp runs the same number of batches (the shuffles need them all); rows past a group's last one are
+    // its last one again, not stored.  The first batch is on its way while positions, table and slots are looked up.
+    uint4 raw[kAhead];
+    auto load = [&](int b) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) raw[u] = load_row16(src + (int64_t)min(b + u, rows - 1) * src_step);
+    };
+    load(0);
     // the cache rows of this token
     const bool fp8 = a.dtype_cache == GEMM_E4M3;
     uint8_t* slot_row = nullptr;
@@ -223,28 +248,35 @@ __device__ __forceinline__ void forward_rows(const RopeParams& p, uint32_t block
             slot_scale = KIND == kKeys ? a.k_scale : a.v_scale;
         }
     }
-    auto append = [&](int r, const float (&y)[8]) {
+    auto append = [&](int r, const Pair (&v)[4]) {
         uint8_t* at = slot_row + (int64_t)r * slot_step;
         if (fp8) {
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 t = halves(v[i]);
+                y[2 * i] = t.x;
+                y[2 * i + 1] = t.y;
+            }
             uint2 w;
             w.x = e4m3x4(__fdiv_rn(y[0], slot_scale), __fdiv_rn(y[1], slot_scale), __fdiv_rn(y[2], slot_scale), __fdiv_rn(y[3], slot_scale));
             w.y = e4m3x4(__fdiv_rn(y[4], slot_scale), __fdiv_rn(y[5], slot_scale), __fdiv_rn(y[6], slot_scale), __fdiv_rn(y[7], slot_scale));
             *reinterpret_cast<uint2*>(at) = w;
         } else {
-            *reinterpret_cast<uint4*>(at) = round8<T>(y);
+            *reinterpret_cast<uint4*>(at) = round8<T>(v);
         }
     };
-    float own[8], other[8];
-    if constexpr (KIND != kValues)
+    Pair own[4], other[4];
+    if constexpr (KIND != kValues) {
+        float c[8], s[8];
         load_factors<T, PAIRS>(a, a.norm ? static_cast<const T*>(KIND == kQueries ? a.q_weight : a.k_weight) : nullptr, token, me.e0,
-                               me.act, me.live, 1.f, own, other);
+                               me.act, me.live, 1.f, c, s);
+        as_pairs(c, own);
+        as_pairs(s, other);
+    }
     const float inv_d = 1.f / (float)a.head_dim;
-    // Every lane of a warp runs the same number of batches (the shuffles need them all); rows past a group's last one are
-    // its last one again, not stored.
     for (int b = 0; b < p.rows_per_group; b += kAhead) {
-        uint4 raw[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) raw[u] = load_row16(src + (int64_t)min(b + u, rows - 1) * src_step);
+        if (b) load(b);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int r = b + u;
@@ -252,7 +284,7 @@ __device__ __forceinline__ void forward_rows(const RopeParams& p, uint32_t block
             if constexpr (KIND == kValues) {
                 if (on && slot_row) {
                     if (fp8) {
-                        float y[8];
+                        Pair y[4];
                         unpack8<T>(raw[u], y);
                         append(r, y);
                     } else {
@@ -260,13 +292,14 @@ __device__ __forceinline__ void forward_rows(const RopeParams& p, uint32_t block
                     }
                 }
             } else {
-                float x[8], z[8];
+                Pair x[4], z[4];
                 unpack8<T>(raw[u], x);
                 float inv = 1.f;
                 if (a.norm) {
-                    float sum = 0.f;
+                    Pair sq = x[0] * x[0];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
+                    for (int i = 1; i < 4; ++i) sq = fma2(x[i], x[i], sq);
+                    float sum = sum_of(sq);
                     if (!me.act) sum = 0.f;
 #pragma unroll
                     for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -274,7 +307,7 @@ __device__ __forceinline__ void forward_rows(const RopeParams& p, uint32_t block
                 }
                 partners<T, PAIRS>(a, me.e0, me.live, me.mate, srow, raw[u], x, z);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = inv * fmaf(z[i], other[i], x[i] * own[i]);
+                for (int i = 0; i < 4; ++i) x[i] = pair_of(inv) * fma2(z[i], other[i], x[i] * own[i]);
                 if (on) {
                     if (KIND == kQueries || dst) *reinterpret_cast<uint4*>(dst + (int64_t)r * dst_step) = round8<T>(x);
                     if (KIND == kKeys && slot_row) append(r, x);
@@ -286,7 +319,7 @@ __device__ __forceinline__ void forward_rows(const RopeParams& p, uint32_t block
 
 template <typename T, int LANES, int PAIRS>
 __global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const __grid_constant__ RopeParams p) {
-    __shared__ float scratch[PAIRS == kPairsAny ? (kRopeThreads / LANES) * LANES * 8 : 1];
+    __shared__ __align__(16) float scratch[PAIRS == kPairsAny ? (kRopeThreads / LANES) * LANES * 8 : 1];
     griddep_wait();
     griddep_launch_dependents();
     float* srow = scratch + (PAIRS == kPairsAny ? (threadIdx.x / LANES) * LANES * 8 : 0);
@@ -311,8 +344,8 @@ constexpr int kGradSmem = 2 * kGradPieces * kRopeThreads * 16;
 template <typename T, int LANES, int PAIRS>
 __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_backward_kernel(const __grid_constant__ RopeParams p) {
     extern __shared__ __align__(16) uint4 staged[];      // [stage][piece][thread]
-    __shared__ float scratch[PAIRS == kPairsAny ? (kRopeThreads / LANES) * LANES * 8 : 1];
-    __shared__ float sums[kRopeThreads / 32][LANES * 8];
+    __shared__ __align__(16) float scratch[PAIRS == kPairsAny ? (kRopeThreads / LANES) * LANES * 8 : 1];
+    __shared__ __align__(16) float sums[kRopeThreads / 32][LANES * 8];
     griddep_wait();
     griddep_launch_dependents();
     const qk_norm_rope_args_t& a = p.a;
@@ -333,11 +366,11 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_backward_kernel(con
     const int64_t d_token = is_q ? gr.dq_token : gr.dk_token, d_head = is_q ? gr.dq_head : gr.dk_head;
     const int32_t x_step = (int32_t)x_head, g_step = (int32_t)g_head, d_step = (int32_t)d_head;
     const T* weight = a.norm ? static_cast<const T*>(is_q ? a.q_weight : a.k_weight) : nullptr;
-    float w[8], dw[8];
+    Pair w[4], dw[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        w[i] = 1.f;
-        dw[i] = 0.f;
+    for (int i = 0; i < 4; ++i) {
+        w[i] = pair_of(1.f);
+        dw[i] = pair_of(0.f);
     }
     if (weight && me.act) unpack8<T>(*reinterpret_cast<const uint4*>(weight + e0), w);
     const float inv_d = 1.f / (float)a.head_dim;
@@ -348,21 +381,28 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_backward_kernel(con
     // warp (its first group has the most items), so every lane runs the same number of batches.
     struct Place {
         uint32_t base;
-        int batch, token, h0, rows;
+        int batch, token, group, h0, rows;
         bool valid;
     };
-    auto enter = [&](Place& at) {        // an item's rows; the last rows of the list stand in for items that do not exist
-        const uint32_t item = at.base + (threadIdx.x & 31) / LANES;
-        at.valid = item < items;
-        at.token = at.valid ? (int)(item / groups) : 0;
-        at.h0 = at.valid ? (int)(item % groups) * p.rows_per_group : 0;
+    // an item's rows; the first rows of the list stand in for items that do not exist
+    auto enter = [&](Place& at) {
+        at.valid = at.base + (threadIdx.x & 31) / LANES < items;
+        if (!at.valid) at.token = at.group = 0;
+        at.h0 = at.group * p.rows_per_group;
         at.rows = min(p.rows_per_group, heads - at.h0);       // at least one
         at.batch = 0;
     };
+    const int token_step = (int)(step / groups), group_step = (int)(step % groups);
     auto advance = [&](Place& at) {
         at.batch += kGradAhead;
         if (at.batch < p.rows_per_group) return;
         at.base += step;
+        at.token += token_step;
+        at.group += group_step;
+        if (at.group >= (int)groups) {
+            at.group -= (int)groups;
+            ++at.token;
+        }
         if (at.base < items) enter(at);
     };
     const uint32_t place0 = smem_u32(staged) + threadIdx.x * 16u;
@@ -403,6 +443,12 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_backward_kernel(con
 
     Place now, ahead;
     now.base = warp_first;
+    now.token = now.group = 0;
+    if (groups) {
+        const uint32_t item = warp_first + (threadIdx.x & 31) / LANES;
+        now.token = (int)(item / groups);
+        now.group = (int)(item % groups);
+    }
     if (now.base < items) enter(now);
     ahead = now;
     fetch_position(ahead);
@@ -410,9 +456,10 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_backward_kernel(con
     if (ahead.base < items) advance(ahead);
     fetch_position(ahead);
     int stage = 0;
-    float own[8], other[8];
+    Pair own[4], other[4];
     while (now.base < items) {
         copy(ahead, stage ^ 1);
+        const Place after = ahead;
         if (ahead.base < items) advance(ahead);
         fetch_position(ahead);
         cp_async_wait<1>();
@@ -420,33 +467,35 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_backward_kernel(con
         if (now.batch == 0) {
             // the turn back: the sines' signs are the forward's negated
             if constexpr (PAIRS == kPairsAny) {
-                load_factors<T, PAIRS>(a, nullptr, now.token, me.e0, me.act, me.live, -1.f, own, other);
+                float c[8], t[8];
+                load_factors<T, PAIRS>(a, nullptr, now.token, me.e0, me.act, me.live, -1.f, c, t);
+                as_pairs(c, own);
+                as_pairs(t, other);
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    own[i] = 1.f;
-                    other[i] = 0.f;
+                for (int i = 0; i < 4; ++i) {
+                    own[i] = pair_of(1.f);
+                    other[i] = pair_of(0.f);
                 }
                 if (me.live) {
                     if constexpr (PAIRS == kPairsHalves) {
                         const uint4 c[2] = {staged_piece(2 * kGradAhead), staged_piece(2 * kGradAhead + 1)};
                         const uint4 t[2] = {staged_piece(2 * kGradAhead + 2), staged_piece(2 * kGradAhead + 3)};
-                        const float sg = me.e0 >= half ? -1.f : 1.f;
+                        const Pair sg = pair_of(me.e0 >= half ? -1.f : 1.f);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            own[4 * i] = __uint_as_float(c[i].x); own[4 * i + 1] = __uint_as_float(c[i].y);
-                            own[4 * i + 2] = __uint_as_float(c[i].z); own[4 * i + 3] = __uint_as_float(c[i].w);
-                            other[4 * i] = sg * __uint_as_float(t[i].x); other[4 * i + 1] = sg * __uint_as_float(t[i].y);
-                            other[4 * i + 2] = sg * __uint_as_float(t[i].z); other[4 * i + 3] = sg * __uint_as_float(t[i].w);
+                            own[2 * i] = pair_of(__uint_as_float(c[i].x), __uint_as_float(c[i].y));
+                            own[2 * i + 1] = pair_of(__uint_as_float(c[i].z), __uint_as_float(c[i].w));
+                            other[2 * i] = sg * pair_of(__uint_as_float(t[i].x), __uint_as_float(t[i].y));
+                            other[2 * i + 1] = sg * pair_of(__uint_as_float(t[i].z), __uint_as_float(t[i].w));
                         }
                     } else {
                         const uint4 c = staged_piece(2 * kGradAhead), t = staged_piece(2 * kGradAhead + 1);
                         const uint32_t cw[4] = {c.x, c.y, c.z, c.w}, tw[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            own[2 * i] = own[2 * i + 1] = __uint_as_float(cw[i]);
-                            other[2 * i] = __uint_as_float(tw[i]);
-                            other[2 * i + 1] = -__uint_as_float(tw[i]);
+                            own[i] = pair_of(__uint_as_float(cw[i]));
+                            other[i] = pair_of(__uint_as_float(tw[i]), -__uint_as_float(tw[i]));
                         }
                     }
                 }
@@ -454,51 +503,74 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_backward_kernel(con
         }
         T* ds = d_base + now.token * d_token + now.h0 * d_head;
         const bool stores = now.valid && me.act;
+        // kSide rows side by side: their chains of shuffles overlap
+        constexpr int kSide = 2;
 #pragma unroll
-        for (int u = 0; u < kGradAhead; ++u) {
-            const bool on = stores && now.batch + u < now.rows;
-            const uint4 rg = staged_piece(2 * u + 1);
-            float g[8], z[8];
-            unpack8<T>(rg, g);
-            partners<T, PAIRS>(a, me.e0, me.live, me.mate, srow, rg, g, z);
+        for (int u0 = 0; u0 < kGradAhead; u0 += kSide) {
+            Pair g[kSide][4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] = fmaf(z[i], other[i], g[i] * own[i]);
+            for (int v = 0; v < kSide; ++v) {
+                const uint4 rg = staged_piece(2 * (u0 + v) + 1);
+                Pair z[4];
+                unpack8<T>(rg, g[v]);
+                partners<T, PAIRS>(a, me.e0, me.live, me.mate, srow, rg, g[v], z);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) g[v][i] = fma2(z[i], other[i], g[v][i] * own[i]);
+            }
             if (a.norm) {
-                float x[8];
-                unpack8<T>(staged_piece(2 * u), x);
-                float sq = 0.f, dot = 0.f;
+                Pair x[kSide][4];
+                float sq[kSide], dot[kSide];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    sq = fmaf(x[i], x[i], sq);
-                    dot = fmaf(g[i] * w[i], x[i], dot);
+                for (int v = 0; v < kSide; ++v) {
+                    unpack8<T>(staged_piece(2 * (u0 + v)), x[v]);
+                    Pair squares = x[v][0] * x[v][0], products = (g[v][0] * w[0]) * x[v][0];
+#pragma unroll
+                    for (int i = 1; i < 4; ++i) {
+                        squares = fma2(x[v][i], x[v][i], squares);
+                        products = fma2(g[v][i] * w[i], x[v][i], products);
+                    }
+                    sq[v] = me.act ? sum_of(squares) : 0.f;
+                    dot[v] = me.act ? sum_of(products) : 0.f;
                 }
-                if (!me.act) sq = dot = 0.f;
 #pragma unroll
-                for (int o = LANES / 2; o > 0; o >>= 1) {
-                    sq += __shfl_xor_sync(0xffffffffu, sq, o);
-                    dot += __shfl_xor_sync(0xffffffffu, dot, o);
-                }
-                const float inv = rsqrtf(fmaf(sq, inv_d, a.eps));
-                const float k = inv * inv * dot * inv_d;
+                for (int o = LANES / 2; o > 0; o >>= 1)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (on) dw[i] = fmaf(g[i] * inv, x[i], dw[i]);
-                    g[i] = inv * fmaf(-x[i], k, g[i] * w[i]);
+                    for (int v = 0; v < kSide; ++v) {
+                        sq[v] += __shfl_xor_sync(0xffffffffu, sq[v], o);
+                        dot[v] += __shfl_xor_sync(0xffffffffu, dot[v], o);
+                    }
+#pragma unroll
+                for (int v = 0; v < kSide; ++v) {
+                    const bool on = stores && now.batch + u0 + v < now.rows;
+                    const float inv = rsqrtf(fmaf(sq[v], inv_d, a.eps));
+                    const Pair r = pair_of(inv), k = pair_of(-inv * inv * dot[v] * inv_d);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (on) dw[i] = fma2(g[v][i] * r, x[v][i], dw[i]);
+                        g[v][i] = r * fma2(x[v][i], k, g[v][i] * w[i]);
+                    }
                 }
             }
-            if (on) *reinterpret_cast<uint4*>(ds + (int64_t)(now.batch + u) * d_step) = round8<T>(g);
+#pragma unroll
+            for (int v = 0; v < kSide; ++v)
+                if (stores && now.batch + u0 + v < now.rows)
+                    *reinterpret_cast<uint4*>(ds + (int64_t)(now.batch + u0 + v) * d_step) = round8<T>(g[v]);
         }
-        advance(now);
+        now = after;
         stage ^= 1;
     }
     cp_async_wait<0>();
     if (!(is_q ? gr.dq_weight : gr.dk_weight)) return;
     // groups of a warp, then warps of the block, in a fixed order
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
+        float2 v = halves(dw[i]);
 #pragma unroll
-        for (int o = LANES; o < 32; o <<= 1) dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], o);
-        if ((threadIdx.x & 31) < LANES) sums[threadIdx.x / 32][me.e0 + i] = dw[i];
+        for (int o = LANES; o < 32; o <<= 1) {
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+        }
+        if ((threadIdx.x & 31) < LANES) *reinterpret_cast<float2*>(&sums[threadIdx.x / 32][me.e0 + 2 * i]) = v;
     }
     __syncthreads();
     for (int e = threadIdx.x; e < LANES * 8; e += kRopeThreads) {
