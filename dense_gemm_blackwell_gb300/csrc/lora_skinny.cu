@@ -9,7 +9,10 @@
 // memory in rank order and every CTA of the cluster writes its part of the
 // tile.  Against a split through global memory (partial tiles, flags, one
 // finisher) the join costs a few hundred nanoseconds instead of microseconds
-// and the adapter steps are shared out too.
+// and the adapter steps are shared out too (96 tokens x 4096 x 4096, 80
+// adapters: 17.6 us here, 31.6 in the persistent kernel; 4 tokens: 11.1 and
+// 21.5).  W comes by TMA: with asynchronous 16-byte copies by four warps the
+// 96 tokens took 2.4 us longer.
 //
 // Only the tokens that exist are loaded: X boxes are round_up(tokens, 8) rows
 // high, and the matrix instruction's other rows read whatever lies behind
@@ -18,9 +21,9 @@
 //
 // Roles: warp 0 TMA producer, warp 1 tensor memory and MMA issue, warps 2..5
 // first list the tile's adapters (the producer then fetches their B before T is
-// ready) and at the end read the accumulator (32 rows each).  Waits are bounded as in the persistent
-// kernel; on expiry the CTA records GEMM_ERR_TIMEOUT and still takes part in
-// the cluster's barriers.
+// ready) and at the end read the accumulator (32 rows each).  Waits are bounded
+// as in the persistent kernel; on expiry the CTA records GEMM_ERR_TIMEOUT and
+// still takes part in the cluster's barriers.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
