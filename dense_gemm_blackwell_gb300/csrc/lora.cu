@@ -33,8 +33,9 @@
 // 6.8 TB/s of a plain copy is the chain of steps around the stream: T (7 to 9
 // us beside the stream of W), the adapter steps that wait for it (1.7), the
 // join of the cluster and the stores (2 to 3).  Many tokens: the tensor cores,
-// 8192 x 8192 x 8192 with prompts of 12 requests and rank 64: 620 us, 1.80
-// PFLOP/s at the power cap, where the same product without adapters takes 595.
+// 8192 x 8192 x 8192 with prompts of 12 requests and rank 64: 624 us, 1.79
+// PFLOP/s at the power cap, of which T takes 44; the same product without
+// adapters takes 595.
 #include <algorithm>
 #include <cstring>
 #include <new>
@@ -72,10 +73,11 @@ struct ShrinkParams {
 
 template <int NT>
 struct StreamShape {
-    static constexpr int kStages = NT > 16 ? 3 : 4;
+    static constexpr int kStages = 3;
     static constexpr int kStageBytes = (kShrinkRows + NT * 8) * 128;
-    static constexpr int kSumPitch = NT * 8 + 4;      // floats
-    static constexpr int kSmemBytes = kStages * kStageBytes + kShrinkRows * kSumPitch * 4;
+    static constexpr int kSumPitch = NT * 8 + 4;      // floats; the sums lie over the ring
+    static constexpr int kSmemBytes = kStages * kStageBytes;
+    static_assert(kShrinkRows * kSumPitch * 4 <= kSmemBytes, "");
 };
 
 __device__ __forceinline__ float4 load_cluster_f4(uint32_t addr) {
@@ -274,18 +276,18 @@ __global__ void __launch_bounds__(kShrinkThreads) stream_kernel(const __grid_con
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ AdapterList adapters;
     __shared__ int32_t row_id[kShrinkRows];
-    float* sums = reinterpret_cast<float*>(smem + S::kStages * S::kStageBytes);
+    float* sums = reinterpret_cast<float*>(smem);
 
     griddep_wait();
     griddep_launch_dependents();
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ks = blockIdx.x, num_ks = gridDim.x;            // cluster rank and size: ranges of K
-    const int row0 = blockIdx.z * kShrinkRows;
+    const int row0 = blockIdx.y * kShrinkRows;
     const int tile = row0 / p.tile_rows, in_tile = row0 % p.tile_rows;
     const int count = find_adapters(p.a.adapter, p.adapters, p.M, tile * p.tile_rows, p.tile_rows, adapters, row_id, in_tile, kShrinkRows,
                                     threadIdx.x, kShrinkThreads, [] { __syncthreads(); });
-    if (ks == 0 && blockIdx.y == 0 && in_tile == 0) publish_adapters(p, tile, adapters, count);
+    if (ks == 0 && blockIdx.z == 0 && in_tile == 0) publish_adapters(p, tile, adapters, count);
 
     const int chunks = (p.K + 63) / 64;
     const int c_begin = min(ks * p.chunks_per_cta, chunks), c_end = min(c_begin + p.chunks_per_cta, chunks);
@@ -293,7 +295,7 @@ __global__ void __launch_bounds__(kShrinkThreads) stream_kernel(const __grid_con
     const T* X = static_cast<const T*>(p.a.x);
     const T* A = static_cast<const T*>(p.a.a);
 
-    for (int slot = blockIdx.y; slot < count; slot += gridDim.y) {
+    for (int slot = blockIdx.z; slot < count; slot += gridDim.z) {
         const int id = adapters.list[slot];
         T* dst = static_cast<T*>(p.t) + ((size_t)tile * p.tile_rows + in_tile) * p.pitch + slot * p.cols;
         const bool here = __syncthreads_or(threadIdx.x < kShrinkRows && row_id[threadIdx.x] == id);
@@ -359,6 +361,7 @@ __global__ void __launch_bounds__(kShrinkThreads) stream_kernel(const __grid_con
             if (++stage == S::kStages) stage = 0;
         }
         cp_async_wait<0>();
+        __syncthreads();        // the ring is idle
         // this CTA's sums over its range of K
         {
             const int r = warp * 16 + (lane >> 2), c = (lane & 3) * 2;
@@ -469,7 +472,7 @@ gemm_status_t check_desc(const lora_desc_t& d) {
     if (d.dtype != GEMM_BF16 && d.dtype != GEMM_F16) return GEMM_ERR_UNSUPPORTED;
     if (d.dtype_y != GEMM_F32 && d.dtype_y != GEMM_BF16 && d.dtype_y != GEMM_F16) return GEMM_ERR_UNSUPPORTED;
     if (d.rank % 8 != 0 || d.rank > 256 || d.adapters > kMaxAdapters) return GEMM_ERR_UNSUPPORTED;
-    if (d.tokens > 65535ll * kShrinkRows) return GEMM_ERR_UNSUPPORTED;      // the shrink grid's z extent
+    if (d.tokens > 65535ll * kShrinkRows) return GEMM_ERR_UNSUPPORTED;      // the shrink grid's y extent
     const uint32_t known = GEMM_FLAG_CTA_GROUP_1 | GEMM_FLAG_CTA_GROUP_2 | GEMM_FLAG_NO_STREAM_K | GEMM_FLAG_STAGE_K1 | GEMM_FLAG_STAGE_K2;
     if (d.flags & ~known) return GEMM_ERR_UNSUPPORTED;
     return GEMM_OK;
@@ -599,15 +602,17 @@ gemm_status_t lora_plan_create(lora_plan_t* out, const lora_desc_t* desc) {
             p->info.shrink_k_split = 1;
             p->shrink_grid = dim3((unsigned)std::min<int64_t>(d.tokens, p->tile_rows), (unsigned)p->m_blocks, 1);
         } else {
-            // clusters split K while that fills the device twice over and leaves every CTA four chunks of K; then CTAs
-            // share out the slots
+            // Clusters split K, up to four ways while that fills the device four times over (8192 rows of 8192, rank 64: 44
+            // us, two ways 56), up to eight while it does so twice (beyond, starts outweigh it), and every CTA keeps four
+            // chunks of K.  Then CTAs share out the slots; those of a block's first slots come first in the grid, as most
+            // blocks of prompts have no others.
             const int64_t row_blocks = (d.tokens + kShrinkRows - 1) / kShrinkRows, chunks = (d.k + 63) / 64;
             int64_t ks = 1;
-            while (ks < 8 && row_blocks * ks * 2 <= 2 * dev.sms && chunks >= 4 * ks * 2) ks *= 2;
+            while (ks < 8 && row_blocks * ks * 2 <= (ks < 4 ? 4 : 2) * dev.sms && chunks >= 4 * ks * 2) ks *= 2;
             p->chunks_per_cta = (int32_t)((chunks + ks - 1) / ks);
             p->info.shrink_k_split = (int32_t)ks;
-            p->shrink_grid = dim3((unsigned)ks, (unsigned)std::min<int64_t>(slots, std::max<int64_t>(1, 4 * dev.sms / (row_blocks * ks))),
-                                  (unsigned)row_blocks);
+            p->shrink_grid = dim3((unsigned)ks, (unsigned)row_blocks,
+                                  (unsigned)std::min<int64_t>(slots, std::max<int64_t>(1, 8 * dev.sms / (row_blocks * ks))));
         }
         p->info.shrink_grid = (int32_t)(p->shrink_grid.x * p->shrink_grid.y * p->shrink_grid.z);
         p->t_bytes = up((int64_t)p->m_blocks * slots * p->tile_rows * p->cols * 2, 256);
