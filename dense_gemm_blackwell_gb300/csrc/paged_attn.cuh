@@ -276,13 +276,15 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<KD, FP8, NH>::kCtas) p
         const int next_page = next.page, next_place = next.place, next_head = next.head;
         if (next.live) {
             const bool have = next_page >= 0 && next_page < p.a.num_pages;
-            const int page0 = __shfl_sync(0xffffffffu, next_page, 0);
+            const int page0 = __shfl_sync(0xffffffffu, next_page, 0), first_place = __shfl_sync(0xffffffffu, next_place, 0);
             const uint32_t mask = __ballot_sync(0xffffffffu, have) & kFull;
             if (lane == 0) stage_mask[warp][stage] = mask;
             const uint32_t dst = copy_dst + stage * S::kStageBytes;
-            if (mask == kFull && __all_sync(0xffffffffu, next_page == page0)) {
-                // one page holds all rows (the common case): they lie one place stride apart
-                const int64_t place0 = __shfl_sync(0xffffffffu, next_place, 0) + copy_row;
+            // The places have to follow one another too: neighbouring columns of the block table may name the same page.
+            const bool in_line = next_page == page0 && next_place == first_place + (lane & (kTokens - 1));
+            if (mask == kFull && __all_sync(0xffffffffu, in_line)) {
+                // one column's page holds all rows (the common case): they lie one place stride apart
+                const int64_t place0 = first_place + copy_row;
                 const uint8_t* kp = kbase + (page0 * p.a.k_page + next_head * p.a.k_head) * S::kBytes + place0 * k_place;
                 const uint8_t* vp = vbase + (page0 * p.a.v_page + next_head * p.a.v_head) * S::kBytes + place0 * v_place;
                 if (copies) {

@@ -209,6 +209,23 @@ def test_infinite_scores():
     assert torch.equal(out[1], torch.zeros_like(out[1]))
 
 
+@pytest.mark.parametrize("page", [1, 2, 7, 8, 16, 24])
+@pytest.mark.parametrize("window", [0, 21])
+@pytest.mark.parametrize("dim,dtype,cache", [(64, torch.bfloat16, torch.bfloat16), (128, torch.float16, torch.float16), (64, torch.bfloat16, E4M3),
+                                             (128, torch.float16, E4M3)])
+def test_a_page_named_by_neighbouring_columns(dim, dtype, cache, window, page):
+    """Columns that name one page: each position reads its own place of it, the cache's last page among them."""
+    gen = torch.Generator(device="cuda").manual_seed(page)
+    pages, width = 5, -(-150 // page)
+    kc, vc = ((torch.randn(pages, page, 2, dim, generator=gen, device="cuda") * (30 if cache == E4M3 else 1)).to(cache) for _ in range(2))
+    q = torch.randn(4, 8, dim, generator=gen, device="cuda").to(dtype)
+    col = torch.arange(width, device="cuda")
+    last = torch.full_like(col, pages - 1)
+    table = torch.stack((last, col // 2 % pages, torch.where(col < 3, 1, last), torch.where(col % 2 == 0, last, 0))).to(torch.int32)
+    lengths = torch.tensor([150, 149, 96, 32], dtype=torch.int32, device="cuda")
+    check(q, kc, vc, table, lengths, window=window, ks=0.02 if cache == E4M3 else 1.0, vs=0.03 if cache == E4M3 else 1.0)
+
+
 def test_large_scores():
     """Softmax far from its mean: one key dominates by hundreds."""
     q, kc, vc, table, lengths = make([500, 64], 4, 2, 128, 16, torch.bfloat16, torch.bfloat16)
