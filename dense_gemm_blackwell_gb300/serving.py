@@ -163,6 +163,12 @@ def _rows_ok(t, name):
     _need(t.shape[-1] <= 1 or t.stride(-1) == 1, "%s: the last dimension must be contiguous" % name)
 
 
+def _apart(t, dim, name):
+    """A stride that the library takes 0 of for "packed": a tensor that repeats one row or matrix is refused."""
+    _need(t.shape[dim] <= 1 or t.stride(dim) != 0, "%s: dimension %d is expanded (stride 0); a copy is needed" % (name, dim))
+    return t.stride(dim)
+
+
 class _Plan:
     """A created plan (owns the C handle); use as a context manager or call close()."""
 
@@ -198,7 +204,8 @@ class LoraPlan(_Plan):
     """Y = X W^T + scale_i (X A_i^T) B_i^T with i = adapter[token]; a negative i: the projection alone.
 
     X [tokens, k], W [n, k], A [adapters, rank, k], B [adapters, n, rank], Y [tokens, n]; X, W, A and B of one 16-bit
-    type.  Rows may be padded (ldx, ldw, ldy in elements, 0 = packed; A's and B's strides are taken from the tensors).
+    type.  Rows may be padded (ldx, ldw, ldy in elements, 0 = packed; A's and B's strides are taken from the tensors, which must not
+    be expanded).
     """
 
     _destroy = "lora_plan_destroy"
@@ -236,7 +243,7 @@ class LoraPlan(_Plan):
         for name, t, ld, cols in (("x", x, d.ldx, d.k), ("w", w, d.ldw, d.k), ("y", y, d.ldy, d.n)):
             _need(t.shape[0] <= 1 or t.stride(0) == (ld or cols), "%s: rows %d apart, the plan has %d" % (name, t.stride(0), ld or cols))
         g = LoraArgs()
-        g.lda, g.stride_a, g.ldb, g.stride_b = a.stride(1), a.stride(0), b.stride(1), b.stride(0)
+        g.lda, g.stride_a, g.ldb, g.stride_b = _apart(a, 1, "a"), _apart(a, 0, "a"), _apart(b, 1, "b"), _apart(b, 0, "b")
         return g
 
     def run(self, x, w, a, b, adapter, y, scale=None, stream=None):

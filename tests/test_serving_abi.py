@@ -183,6 +183,50 @@ def test_python_layer_refuses_host_tensors():
         dg.qk_norm_rope(x, None, torch.zeros(4, dtype=torch.int32), torch.zeros(8, 2, 32))
 
 
+class Layout:
+    """What the binding's checks ask of a tensor on CUDA device `device`; nothing is allocated."""
+
+    def __init__(self, shape, dtype, stride=None, device=0):
+        self.shape, self.dtype, self.device_index = tuple(shape), dtype, device
+        self.strides = tuple(torch.empty(shape, device="meta").stride() if stride is None else stride)
+        self.is_cuda = True
+
+    def stride(self, dim=None):
+        return self.strides if dim is None else self.strides[dim]
+
+    def dim(self):
+        return len(self.shape)
+
+    def get_device(self):
+        return self.device_index
+
+    def is_contiguous(self):
+        return self.strides == torch.empty(self.shape, device="meta").stride()
+
+
+def lora_layouts(tokens=16, n=64, k=128, rank=16, adapters=4, **other):
+    """(a plan that owns nothing, the layouts of one run's tensors), with the tensors in `other` in place of the packed ones."""
+    plan = object.__new__(dg.LoraPlan)
+    plan.desc = serving.LoraDesc(tokens=tokens, n=n, k=k, rank=rank, adapters=adapters, dtype=dg.GEMM_BF16, dtype_y=dg.GEMM_BF16)
+    half = torch.bfloat16
+    kinds = dict(x=Layout((tokens, k), half), w=Layout((n, k), half), a=Layout((adapters, rank, k), half), b=Layout((adapters, n, rank), half),
+                 adapter=Layout((tokens,), torch.int32), y=Layout((tokens, n), half), scale=Layout((adapters,), torch.float32))
+    return plan, {**kinds, **other}
+
+
+def test_lora_refuses_expanded_adapters():
+    """A stride of 0 would count as packed in the library, which then reads past the one matrix there is."""
+    half = torch.bfloat16
+    plan, good = lora_layouts()
+    assert plan._checked(**good).stride_a == 16 * 128
+    for bad in (dict(a=Layout((4, 16, 128), half, (0, 128, 1))), dict(a=Layout((4, 16, 128), half, (128, 0, 1))),
+                dict(b=Layout((4, 64, 16), half, (0, 16, 1))), dict(b=Layout((4, 64, 16), half, (16, 0, 1)))):
+        with pytest.raises(ValueError):
+            plan._checked(**{**good, **bad})
+    plan, one = lora_layouts(adapters=1)            # one adapter: nothing is repeated
+    plan._checked(**one)
+
+
 def test_native_tensor_facts_agree_with_the_python_ones():
     """Both tell the same layouts apart and write the same addresses."""
     serving._lib()
