@@ -833,6 +833,16 @@ namespace dgb {
 
 gemm_status_t status_of(cudaError_t e) { return e == cudaSuccess ? GEMM_OK : cuda_fail(e); }
 
+cudaError_t clear_now(void* mem, size_t bytes) {
+    cudaStream_t s;
+    cudaError_t e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+    if (e != cudaSuccess) return e;
+    e = cudaMemsetAsync(mem, 0, bytes, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    const cudaError_t d = cudaStreamDestroy(s);
+    return e != cudaSuccess ? e : d;
+}
+
 gemm_status_t device_facts(DeviceFacts* out) {
     // attributes of a device never change: looked up once (sms 0 = not yet)
     static std::atomic<int> sms[kMaxDevices], optin[kMaxDevices];
@@ -949,7 +959,7 @@ gemm_status_t gemm_plan_create(gemm_plan_t* out, const gemm_desc_t* desc) {
         delete p;
         return cuda_fail(e);
     }
-    if ((e = cudaMemset(mem, 0, 256 + (size_t)flag_bytes)) != cudaSuccess) {
+    if ((e = dgb::clear_now(mem, 256 + (size_t)flag_bytes)) != cudaSuccess) {
         cudaFree(mem);
         delete p;
         return cuda_fail(e);
@@ -1442,7 +1452,7 @@ gemm_status_t gemm_sync_status(gemm_plan_t plan, gemm_stream_t stream_, gemm_dev
     cudaError_t e;
     if ((e = cudaStreamSynchronize(stream)) != cudaSuccess) return cuda_fail(e);
     if ((e = cudaMemcpy(&rec, plan->status, sizeof(rec), cudaMemcpyDeviceToHost)) != cudaSuccess) return cuda_fail(e);
-    if (rec.code != 0 && (e = cudaMemset(plan->status, 0, sizeof(rec))) != cudaSuccess) return cuda_fail(e);
+    if (rec.code != 0 && (e = dgb::clear_now(plan->status, sizeof(rec))) != cudaSuccess) return cuda_fail(e);
     if (out) *out = rec;
     return rec.code == 0 ? GEMM_OK : (gemm_status_t)rec.code;
 }

@@ -13,6 +13,10 @@ namespace dgb {
 // Records the error for gemm_last_cuda_error.
 gemm_status_t status_of(cudaError_t e);
 
+// Zeroes device memory before it returns, whatever the legacy stream is busy with: cudaMemset waits in that stream's queue
+// and returns at once, and non-blocking streams do not wait for it.
+cudaError_t clear_now(void* mem, size_t bytes);
+
 struct DeviceFacts {
     int device = 0;
     int sms = 0;
