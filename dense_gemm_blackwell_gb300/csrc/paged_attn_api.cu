@@ -76,7 +76,7 @@ gemm_status_t paged_attn_plan_create(paged_attn_plan_t* out, const paged_attn_de
         delete p;
         return status_of(e);
     }
-    if ((e = cudaMemset(p->memory, 0, (size_t)p->counter_bytes)) != cudaSuccess) {
+    if ((e = clear_now(p->memory, (size_t)p->counter_bytes)) != cudaSuccess) {
         cudaFree(p->memory);
         delete p;
         return status_of(e);

@@ -86,3 +86,32 @@ def test_adapters_with_split_tiles():
     assert plans[0].info.product.stream_k_tiles > 0
     plans[0].close()
     assert torch.equal(y[0], want) and torch.equal(y[1], want)
+
+
+@pytest.mark.parametrize("length", [300, 20000])
+def test_attention_with_split_sequences(length):
+    """Values that are one in every element make the output one, whatever the probabilities are, if all parts are joined once."""
+    pages = -(-length // 16)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    q = torch.randn(2, 16, 128, generator=gen, device="cuda").to(torch.bfloat16)
+    kc = torch.randn(2 * pages, 16, 2, 128, generator=gen, device="cuda").to(torch.bfloat16)
+    vc = torch.ones_like(kc)
+    table = torch.arange(2 * pages, dtype=torch.int32, device="cuda").view(2, pages)
+    lengths = torch.tensor([length, length // 2], dtype=torch.int32, device="cuda")
+    out = torch.full((2, 2, 16, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((2, 2, 16), float("nan"), device="cuda")
+    leave_dirty_memory()
+    plans = []
+
+    def work():
+        plans.append(dg.PagedAttentionPlan(2, heads=16, kv_heads=2, head_dim=128, page_size=16))
+        for o, s in zip(out, lse):
+            plans[0].run(q, kc, vc, table, lengths, o, lse=s)
+
+    on_a_side_stream(work)
+    plans[0].run(q, kc, vc, table, lengths, out[0], lse=lse[0])        # the counters were left at zero
+    torch.cuda.synchronize()
+    plans[0].close()
+    assert torch.equal(lse[0], lse[1]) and torch.isfinite(lse).all()
+    # P is rounded to bf16 (2^-8 each) before its product with V, the sum of P is not
+    assert ((out.float() - 1).abs() <= 2.0 ** -7).all() and torch.equal(out[0], out[1])
