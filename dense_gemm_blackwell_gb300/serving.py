@@ -7,8 +7,8 @@
 
 As in the rest of the package this is argument marshalling: shapes, types, strides and devices are checked here, the
 work is enqueued by the CUDA library on torch's current stream (or the one given), and errors raise GemmError (from the
-library) or ValueError / TypeError (from these checks).  Outputs that are not given are allocated by torch on its current
-stream: pass them when `stream` is another one.  A plan's launches share its workspace, so launches of one plan (and graphs
+library) or ValueError / TypeError (from these checks).  Outputs that are not given, and scratch memory, are allocated by
+torch for the stream that the work goes to.  A plan's launches share its workspace, so launches of one plan (and graphs
 that captured it) must follow one another.
 """
 from __future__ import annotations
@@ -148,6 +148,13 @@ def _keep(table, key, value):
         table.clear()
     table[key] = value
     return value
+
+
+def _as_current(stream, device):
+    """Makes the stream of a handle torch's current one: what torch allocates meanwhile is that stream's, to be used again
+    only in its order, and in a capture of that stream the graph's."""
+    import torch
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device))
 
 
 def _offsets(cls, *names):
@@ -418,7 +425,6 @@ _ROPE_PTRS = _offsets(QkNormRopeArgs, "q", "k", "positions", "table", "q_weight"
 _GRAD_PTRS = _offsets(QkNormRopeGrads, "dq_out", "dk_out", "dq", "dk")
 _rope_checked = {}
 _rope_backward_checked = {}
-_rope_workspaces = {}
 
 
 def qk_norm_rope(q, k, positions, table, *, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, norm=True, q_out=None,
@@ -432,6 +438,11 @@ def qk_norm_rope(q, k, positions, table, *, q_weight=None, k_weight=None, eps=1e
     With k_cache, v_cache [pages, page_size, kv_heads, head_dim] the keys and v's values also go to slots [tokens] (int32:
     page * page_size + place, negative: nowhere); a float8_e4m3fn cache holds them divided by k_scale / v_scale.
     """
+    if stream is not None and (q_out is None or k_out is None and k_cache is None) and q.is_cuda and stream != current_stream_handle():
+        with _as_current(stream, q.device):
+            return qk_norm_rope(q, k, positions, table, q_weight=q_weight, k_weight=k_weight, eps=eps, interleaved=interleaved, norm=norm,
+                                q_out=q_out, k_out=k_out, v=v, k_cache=k_cache, v_cache=v_cache, slots=slots, k_scale=k_scale,
+                                v_scale=v_scale)
     if q_out is None:
         q_out = q.new_empty(q.shape)
     if k_out is None and k_cache is None and k is not None:
@@ -473,6 +484,10 @@ def qk_norm_rope_backward(dq, dk, q, k, positions, table, *, q_weight=None, k_we
     and k go (default: new tensors; may be dq and dk themselves).
     """
     import torch
+    if stream is not None and q.is_cuda and stream != current_stream_handle():
+        with _as_current(stream, q.device):
+            return qk_norm_rope_backward(dq, dk, q, k, positions, table, q_weight=q_weight, k_weight=k_weight, eps=eps,
+                                         interleaved=interleaved, norm=norm, dq_out=dq_out, dk_out=dk_out)
     if dq_out is None:
         dq_out = q.new_empty(q.shape)
     if dk_out is None and k is not None:
@@ -485,10 +500,9 @@ def qk_norm_rope_backward(dq, dk, q, k, positions, table, *, q_weight=None, k_we
     g, d = QkNormRopeArgs.from_buffer_copy(checked[0]), QkNormRopeGrads.from_buffer_copy(checked[1])
     _fill(g, _ROPE_PTRS[:6], q, k, positions, table, q_weight, k_weight)
     _fill(d, _GRAD_PTRS, dq, dk, dq_out, dk_out)
+    L = _declared or _lib()
     dqw = dkw = None
     if norm and (q_weight is not None or k_weight is not None):
-        if stream is None:
-            stream = current_stream_handle()
         n, device = q.shape[2], q.device
         if q_weight is not None:
             dqw = torch.empty(n, dtype=torch.float32, device=device)
@@ -496,16 +510,10 @@ def qk_norm_rope_backward(dq, dk, q, k, positions, table, *, q_weight=None, k_we
         if k_weight is not None and k is not None:
             dkw = torch.empty(n, dtype=torch.float32, device=device)
             d.dk_weight = dkw.data_ptr()
-        # the library's workspace: one per device and stream (a stream's calls follow one another), or the graph's own
-        place = (q.get_device(), stream)
-        capturing = torch.cuda.is_current_stream_capturing()
-        work = None if capturing else _rope_workspaces.get(place)
-        if work is None:
-            work = torch.empty(_lib().qk_norm_rope_backward_workspace(), dtype=torch.uint8, device=device)
-            if not capturing:
-                _rope_workspaces[place] = work
+        # of this call alone, so that calls of several threads and graphs do not meet in it
+        work = torch.empty(L.qk_norm_rope_backward_workspace(), dtype=torch.uint8, device=device)
         d.workspace, d.workspace_bytes = work.data_ptr(), work.numel()
-    _check(_lib().qk_norm_rope_backward(ctypes.byref(g), ctypes.byref(d), current_stream_handle() if stream is None else stream),
+    _check(L.qk_norm_rope_backward(ctypes.byref(g), ctypes.byref(d), current_stream_handle() if stream is None else stream),
            "qk_norm_rope_backward")
     return dq_out, dk_out, dqw, dkw
 

@@ -12,6 +12,7 @@ E4M3 cache entries: the fp32 value before rounding is off by at most 2^-18 m / s
 that interval: between the codes of its ends.
 """
 import math
+import threading
 
 import pytest
 import torch
@@ -321,6 +322,85 @@ def test_streams_and_graph():
     torch.cuda.synchronize()
     close(qo, *plain(q, wq, pos, table, False), U[torch.bfloat16])
     close(ko, *plain(k, wk, pos, table, False), U[torch.bfloat16])
+
+
+def backward_case(tokens=300, seed=0):
+    q, k, v, pos, table, wq, wk = make(tokens, 4, 2, 128, 128, torch.bfloat16, seed=seed)
+    gen = torch.Generator(device="cuda").manual_seed(seed + 1)
+    dq, dk = (torch.randn(t.shape, generator=gen, device="cuda").to(torch.bfloat16) for t in (q, k))
+    return (dq, dk, q, k, pos, table), dict(q_weight=wq, k_weight=wk, eps=EPS)
+
+
+def test_another_stream_than_the_current_one():
+    """What is allocated for a call on another stream may not be memory that earlier work of the current stream still writes."""
+    tensors, kw = backward_case()
+    want = dg.qk_norm_rope_backward(*tensors, **kw)
+    forward = dg.qk_norm_rope(*tensors[2:], **kw)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    freed = [torch.zeros(n, dtype=torch.uint8, device="cuda") for n in [512] * 8 + [1 << 20] * 3 + [1 << 19] * 3]
+    torch.cuda._sleep(400_000_000)
+    for t in freed:
+        t.fill_(77)
+    del freed, t
+    got = dg.qk_norm_rope_backward(*tensors, stream=side.cuda_stream, **kw)
+    rows = dg.qk_norm_rope(*tensors[2:], stream=side.cuda_stream, **kw)
+    torch.cuda.synchronize()
+    for a, b in zip(want + forward, got + rows):
+        assert torch.equal(a, b)
+    with torch.cuda.stream(side):                        # from the side to the default stream, whose handle is 0
+        got = dg.qk_norm_rope_backward(*tensors, stream=torch.cuda.default_stream().cuda_stream, **kw)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("explicit", [False, True])
+def test_backward_in_a_graph(explicit):
+    """A captured pass keeps scratch of its own: eager passes between replays change nothing; the stream may be given as well."""
+    tensors, kw = backward_case()
+    others, other_kw = backward_case(seed=5)
+    want = dg.qk_norm_rope_backward(*tensors, **kw)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        if explicit:
+            inner = torch.cuda.current_stream().cuda_stream
+            with torch.cuda.stream(torch.cuda.Stream()):
+                got = dg.qk_norm_rope_backward(*tensors, stream=inner, **kw)
+        else:
+            got = dg.qk_norm_rope_backward(*tensors, **kw)
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        dg.qk_norm_rope_backward(*others, **other_kw)
+        graph.replay()
+        dg.qk_norm_rope_backward(*others, **other_kw)
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+
+
+def test_backward_from_several_threads():
+    """Threads that share a stream: each pass is two launches, and another thread's may come between them."""
+    cases = [backward_case(200 + 37 * i, seed=i) for i in range(4)]
+    want = [dg.qk_norm_rope_backward(*t, **kw) for t, kw in cases]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        t, kw = cases[i]
+        for _ in range(40):
+            got = dg.qk_norm_rope_backward(*t, **kw)
+            if not all(torch.equal(a, b) for a, b in zip(want[i], got)):
+                wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
 
 
 def test_refusals():
