@@ -450,6 +450,7 @@ struct lora_plan_s {
     lora_desc_t desc;
     lora_plan_info_t info;
     gemm_plan_t product = nullptr;
+    int device = 0;
     void* memory = nullptr;       // T, counts, ids
     int64_t t_bytes = 0, count_bytes = 0;
     int32_t m_blocks = 0, rank16 = 0, cols = 0;
@@ -558,6 +559,7 @@ gemm_status_t lora_plan_create(lora_plan_t* out, const lora_desc_t* desc) {
     lora_plan_s* p = new (std::nothrow) lora_plan_s();
     if (!p) return GEMM_ERR_RESOURCES;
     p->desc = d;
+    p->device = dev.device;
     if (p->desc.ldx == 0) p->desc.ldx = d.k;
     p->skinny = d.tokens > 0 && plan_skinny(d, dev, p);
     // the product's plan also holds the device error record, which both kernels use
@@ -640,6 +642,8 @@ gemm_status_t lora_run(lora_plan_t plan, const lora_args_t* args, gemm_stream_t 
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     const lora_desc_t& d = plan->desc;
     if (d.tokens == 0) return GEMM_OK;
+    gemm_status_t s;
+    if ((s = check_device(plan->device)) != GEMM_OK) return s;
     ShrinkParams q;
     std::memset(&q, 0, sizeof(q));
     q.a = *args;
@@ -654,7 +658,6 @@ gemm_status_t lora_run(lora_plan_t plan, const lora_args_t* args, gemm_stream_t 
     if (!all_aligned(16, {a.x, a.w, a.a, a.b, a.y})) return GEMM_ERR_ALIGNMENT;
     if (!all_multiples(8, {d.ldx, ldw, a.lda, a.stride_a, a.ldb, a.stride_b}) || ldy * y_bytes % 16 != 0) return GEMM_ERR_ALIGNMENT;
     const gemm_plan_info_t& info = plan->info.product;
-    gemm_status_t s;
     char* mem = static_cast<char*>(plan->memory);
     q.ldx = d.ldx;
     q.M = (int32_t)d.tokens;

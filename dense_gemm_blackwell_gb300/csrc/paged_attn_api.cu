@@ -97,6 +97,8 @@ gemm_status_t paged_attn_run(paged_attn_plan_t plan, const paged_attn_args_t* ar
     const paged_attn_args_t& a = *args;
     if (a.batch < 0 || a.batch > d.max_batch || a.table_width < 0 || a.num_pages < 0) return GEMM_ERR_INVALID_ARG;
     if (a.batch == 0) return GEMM_OK;
+    const gemm_status_t here = check_device(plan->device);
+    if (here != GEMM_OK) return here;
     if (!a.q || !a.out || !a.lengths) return GEMM_ERR_INVALID_ARG;
     if (a.table_width > 0 && (!a.block_table || !a.k_cache || !a.v_cache || a.table_stride < 0)) return GEMM_ERR_INVALID_ARG;
     if (!std::isfinite(a.scale) || !std::isfinite(a.k_scale) || !std::isfinite(a.v_scale)) return GEMM_ERR_INVALID_ARG;

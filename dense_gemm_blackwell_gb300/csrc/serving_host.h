@@ -26,6 +26,14 @@ struct DeviceFacts {
 // The current device's facts; GEMM_ERR_NO_DEVICE unless it is compute capability 10.3.
 gemm_status_t device_facts(DeviceFacts* out);
 
+// A plan's workspace lies on the device it was made on: GEMM_ERR_INVALID_ARG where another one is current.
+inline gemm_status_t check_device(int made_on) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return status_of(e);
+    return dev == made_on ? GEMM_OK : GEMM_ERR_INVALID_ARG;
+}
+
 inline bool all_aligned(uintptr_t bytes, std::initializer_list<const void*> ptrs) {
     for (const void* p : ptrs)
         if (reinterpret_cast<uintptr_t>(p) % bytes != 0) return false;

@@ -106,6 +106,7 @@ def _lib():
             f = getattr(L, name)
             f.argtypes, f.restype = args, ctypes.c_int
         _use_native_facts()
+        _use_device_query()
         L.qk_norm_rope_backward_workspace.argtypes, L.qk_norm_rope_backward_workspace.restype = [], _I64
         _declared = L
     return _declared
@@ -114,6 +115,20 @@ def _lib():
 def _check(status, where):
     if status != GEMM_OK:
         raise GemmError(status, where)
+
+
+def _no_device():
+    return -1
+
+
+_current_device = _no_device      # the device that work goes to (a stream handle does not tell); -1: there is none
+
+
+def _use_device_query():
+    global _current_device
+    import torch
+    if torch.cuda.is_available():
+        _current_device = torch._C._cuda_getDevice
 
 
 def _python_facts(*tensors):
@@ -177,10 +192,11 @@ def _apart(t, dim, name):
 
 
 class _Plan:
-    """A created plan (owns the C handle); use as a context manager or call close()."""
+    """A created plan (owns the C handle) of the device that was current; use as a context manager or call close()."""
 
     _destroy = None
     handle = None
+    device = -1
 
     def close(self):
         if self.handle is not None:
@@ -208,7 +224,7 @@ def _torch_types():
 
 
 class LoraPlan(_Plan):
-    """Y = X W^T + scale_i (X A_i^T) B_i^T with i = adapter[token]; a negative i: the projection alone.
+    """Y = X W^T + scale_i (X A_i^T) B_i^T with i = adapter[token]; a negative i: the projection alone.  Of the current device.
 
     X [tokens, k], W [n, k], A [adapters, rank, k], B [adapters, n, rank], Y [tokens, n]; X, W, A and B of one 16-bit
     type.  Rows may be padded (ldx, ldw, ldy in elements, 0 = packed; A's and B's strides are taken from the tensors, which must not
@@ -226,7 +242,7 @@ class LoraPlan(_Plan):
         d.flags, d.tile_n, d.stages, d.max_ctas, d.wait_timeout_ns = flags, tile_n, stages, max_ctas, wait_timeout_ns
         h = _PTR()
         _check(_lib().lora_plan_create(ctypes.byref(h), ctypes.byref(d)), "lora_plan_create")
-        self.handle, self.desc = h, d
+        self.handle, self.desc, self.device = h, d, _current_device()
         self.info = LoraPlanInfo()
         _check(_lib().lora_plan_info(h, ctypes.byref(self.info)), "lora_plan_info")
         self._args = {}
@@ -245,7 +261,7 @@ class LoraPlan(_Plan):
             if t.dtype != kind:
                 raise TypeError("%s: %s expected, got %s" % (name, kind, t.dtype))
             _need(tuple(t.shape) == shape, "%s: shape %s expected, got %s" % (name, shape, tuple(t.shape)))
-            _need(t.is_cuda and t.get_device() == x.get_device(), "%s: must be on x's CUDA device" % name)
+            _need(t.is_cuda and t.get_device() == self.device, "%s: must be on the plan's CUDA device, %d" % (name, self.device))
             _rows_ok(t, name)
         for name, t, ld, cols in (("x", x, d.ldx, d.k), ("w", w, d.ldw, d.k), ("y", y, d.ldy, d.n)):
             _need(t.shape[0] <= 1 or t.stride(0) == (ld or cols), "%s: rows %d apart, the plan has %d" % (name, t.stride(0), ld or cols))
@@ -287,6 +303,8 @@ def lora_matmul(x, w, a, b, adapter, *, scale=None, out=None, out_dtype=None):
     _need(x.dim() == 2 and w.dim() == 2 and a.dim() == 3 and b.dim() == 3, "x [M, K], w [N, K], a [L, R, K], b [L, N, R] expected")
     _rows_ok(x, "x")
     _rows_ok(w, "w")
+    _lib()
+    _need(x.is_cuda and x.get_device() == _current_device(), "x: must be on the current CUDA device")
     if out is None:
         out = torch.empty(x.shape[0], w.shape[0], dtype=out_dtype or x.dtype, device=x.device)
     stream = current_stream_handle()
@@ -348,12 +366,13 @@ def _check_rows(name, t, tokens, dim, kind, device):
     _rows_ok(t, name)
 
 
-def _rope_args(q, k, positions, table, q_weight, k_weight, eps, interleaved, norm):
-    """The fields forward and backward share, checked; everything but addresses."""
+def _rope_args(here, q, k, positions, table, q_weight, k_weight, eps, interleaved, norm):
+    """The fields forward and backward share, checked; everything but addresses.  here: the current device."""
     import torch
     _need(q.dim() == 3 and q.is_cuda, "q: [tokens, heads, head_dim] on a CUDA device expected")
     tokens, heads, dim = q.shape
     dev = q.get_device()
+    _need(dev == here, "q: on CUDA device %d, the current one is %d" % (dev, here))
     if q.dtype not in (torch.bfloat16, torch.float16):
         raise TypeError("q: bfloat16 or float16 expected, got %s" % q.dtype)
     _check_rows("q", q, tokens, dim, q.dtype, dev)
@@ -389,9 +408,9 @@ def _check_cache(name, cache, kv_heads, dim, like, device):
     _rows_ok(cache, name)
 
 
-def _checked_rope(q, k, positions, table, q_weight, k_weight, eps, interleaved, norm, q_out, k_out, v, k_cache, v_cache, slots):
+def _checked_rope(here, q, k, positions, table, q_weight, k_weight, eps, interleaved, norm, q_out, k_out, v, k_cache, v_cache, slots):
     import torch
-    g = _rope_args(q, k, positions, table, q_weight, k_weight, eps, interleaved, norm)
+    g = _rope_args(here, q, k, positions, table, q_weight, k_weight, eps, interleaved, norm)
     dev = q.get_device()
     _check_rows("q_out", q_out, g.tokens, g.head_dim, q.dtype, dev)
     _need(q_out.shape == q.shape, "q_out: q's shape expected")
@@ -447,23 +466,25 @@ def qk_norm_rope(q, k, positions, table, *, q_weight=None, k_weight=None, eps=1e
         q_out = q.new_empty(q.shape)
     if k_out is None and k_cache is None and k is not None:
         k_out = k.new_empty(k.shape)
-    key = (eps, interleaved, norm, _facts(q, k, positions, table, q_weight, k_weight, q_out, k_out, v, k_cache, v_cache, slots))
+    L = _declared or _lib()
+    here = _current_device()
+    key = (here, eps, interleaved, norm, _facts(q, k, positions, table, q_weight, k_weight, q_out, k_out, v, k_cache, v_cache, slots))
     checked = _rope_checked.get(key)
     if checked is None:
-        checked = _keep(_rope_checked, key, _checked_rope(q, k, positions, table, q_weight, k_weight, eps, interleaved, norm, q_out,
+        checked = _keep(_rope_checked, key, _checked_rope(here, q, k, positions, table, q_weight, k_weight, eps, interleaved, norm, q_out,
                                                           k_out, v, k_cache, v_cache, slots))
     g = QkNormRopeArgs.from_buffer_copy(checked)
     _fill(g, _ROPE_PTRS, q, k, positions, table, q_weight, k_weight, q_out, k_out, v, k_cache, v_cache, slots)
     if k_cache is not None:
         g.k_scale, g.v_scale = k_scale, v_scale
-    status = (_declared or _lib()).qk_norm_rope_run(ctypes.byref(g), current_stream_handle() if stream is None else stream)
+    status = L.qk_norm_rope_run(ctypes.byref(g), current_stream_handle() if stream is None else stream)
     if status:
         raise GemmError(status, "qk_norm_rope")
     return q_out, k_out
 
 
-def _checked_rope_backward(dq_out, dk_out, q, k, positions, table, q_weight, k_weight, eps, interleaved, norm, dq, dk):
-    g = _rope_args(q, k, positions, table, q_weight, k_weight, eps, interleaved, norm)
+def _checked_rope_backward(here, dq_out, dk_out, q, k, positions, table, q_weight, k_weight, eps, interleaved, norm, dq, dk):
+    g = _rope_args(here, q, k, positions, table, q_weight, k_weight, eps, interleaved, norm)
     d = QkNormRopeGrads()
     _need((dk_out is None) == (k is None), "dk goes with k")
     for name, t, like in (("dq", dq_out, q), ("dk", dk_out, k), ("dq_out", dq, q), ("dk_out", dk, k)):
@@ -492,15 +513,16 @@ def qk_norm_rope_backward(dq, dk, q, k, positions, table, *, q_weight=None, k_we
         dq_out = q.new_empty(q.shape)
     if dk_out is None and k is not None:
         dk_out = k.new_empty(k.shape)
-    key = (eps, interleaved, norm, _facts(dq, dk, q, k, positions, table, q_weight, k_weight, dq_out, dk_out))
+    L = _declared or _lib()
+    here = _current_device()
+    key = (here, eps, interleaved, norm, _facts(dq, dk, q, k, positions, table, q_weight, k_weight, dq_out, dk_out))
     checked = _rope_backward_checked.get(key)
     if checked is None:
-        checked = _keep(_rope_backward_checked, key, _checked_rope_backward(dq, dk, q, k, positions, table, q_weight, k_weight, eps,
+        checked = _keep(_rope_backward_checked, key, _checked_rope_backward(here, dq, dk, q, k, positions, table, q_weight, k_weight, eps,
                                                                             interleaved, norm, dq_out, dk_out))
     g, d = QkNormRopeArgs.from_buffer_copy(checked[0]), QkNormRopeGrads.from_buffer_copy(checked[1])
     _fill(g, _ROPE_PTRS[:6], q, k, positions, table, q_weight, k_weight)
     _fill(d, _GRAD_PTRS, dq, dk, dq_out, dk_out)
-    L = _declared or _lib()
     dqw = dkw = None
     if norm and (q_weight is not None or k_weight is not None):
         n, device = q.shape[2], q.device
@@ -538,7 +560,7 @@ class PagedAttentionPlan(_Plan):
         d.dtype, d.dtype_cache, d.window, d.max_ctas = dtype, dtype if dtype_cache is None else dtype_cache, window, max_ctas
         h = _PTR()
         _check(_lib().paged_attn_plan_create(ctypes.byref(h), ctypes.byref(d)), "paged_attn_plan_create")
-        self.handle, self.desc = h, d
+        self.handle, self.desc, self.device = h, d, _current_device()
         self.info = PagedAttnPlanInfo()
         _check(_lib().paged_attn_plan_info(h, ctypes.byref(self.info)), "paged_attn_plan_info")
         self._args = {}
@@ -549,6 +571,7 @@ class PagedAttentionPlan(_Plan):
         types = _torch_types()
         _need(q.dim() == 3 and q.is_cuda, "q: [batch, heads, head_dim] on a CUDA device expected")
         batch, dev = q.shape[0], q.get_device()
+        _need(dev == self.device, "q: must be on the plan's CUDA device, %d" % self.device)
         _need(batch <= d.max_batch, "q: %d sequences, the plan holds %d" % (batch, d.max_batch))
         for name, t in (("q", q), ("out", out)):
             if t.dtype != types[d.dtype]:

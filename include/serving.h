@@ -15,7 +15,9 @@
  * only enqueue work (no allocation, no synchronisation), so they may be
  * captured into a CUDA graph; unsupported requests fail with
  * GEMM_ERR_UNSUPPORTED, never a silent fallback.  Strides and leading
- * dimensions count elements.  A plan may be run on one stream, from one host
+ * dimensions count elements.  Work goes to the current device; a plan runs on
+ * the device it was made on (GEMM_ERR_INVALID_ARG where another one is current),
+ * and all buffers lie there.  A plan may be run on one stream, from one host
  * thread, at a time (its launches share its workspace); launches of one plan
  * on several streams must be ordered by events.
  *

@@ -208,6 +208,7 @@ def lora_layouts(tokens=16, n=64, k=128, rank=16, adapters=4, **other):
     """(a plan that owns nothing, the layouts of one run's tensors), with the tensors in `other` in place of the packed ones."""
     plan = object.__new__(dg.LoraPlan)
     plan.desc = serving.LoraDesc(tokens=tokens, n=n, k=k, rank=rank, adapters=adapters, dtype=dg.GEMM_BF16, dtype_y=dg.GEMM_BF16)
+    plan.device = 0
     half = torch.bfloat16
     kinds = dict(x=Layout((tokens, k), half), w=Layout((n, k), half), a=Layout((adapters, rank, k), half), b=Layout((adapters, n, rank), half),
                  adapter=Layout((tokens,), torch.int32), y=Layout((tokens, n), half), scale=Layout((adapters,), torch.float32))
@@ -225,6 +226,73 @@ def test_lora_refuses_expanded_adapters():
             plan._checked(**{**good, **bad})
     plan, one = lora_layouts(adapters=1)            # one adapter: nothing is repeated
     plan._checked(**one)
+
+
+def attn_layouts(batch=3, heads=8, kv=2, dim=64, page=16, **other):
+    """The same for the attention."""
+    plan = object.__new__(dg.PagedAttentionPlan)
+    plan.desc = serving.PagedAttnDesc(max_batch=batch, heads=heads, kv_heads=kv, head_dim=dim, page_size=page, dtype=dg.GEMM_BF16,
+                                      dtype_cache=dg.GEMM_BF16)
+    plan.device = 0
+    half = torch.bfloat16
+    kinds = dict(q=Layout((batch, heads, dim), half), k_cache=Layout((9, page, kv, dim), half), v_cache=Layout((9, page, kv, dim), half),
+                 block_table=Layout((batch, 4), torch.int32), lengths=Layout((batch,), torch.int32), out=Layout((batch, heads, dim), half),
+                 lse=Layout((batch, heads), torch.float32))
+    return plan, {**kinds, **other}
+
+
+def rope_layouts(tokens=5, heads=8, kv=2, dim=64, **other):
+    """The tensors and options of a forward pass's checks."""
+    half = torch.bfloat16
+    kinds = dict(q=Layout((tokens, heads, dim), half), k=Layout((tokens, kv, dim), half), positions=Layout((tokens,), torch.int32),
+                 table=Layout((32, 2, dim // 2), torch.float32), q_weight=None, k_weight=None, eps=1e-6, interleaved=False, norm=True,
+                 q_out=Layout((tokens, heads, dim), half), k_out=Layout((tokens, kv, dim), half), v=None, k_cache=None, v_cache=None, slots=None)
+    return {**kinds, **other}
+
+
+def test_plans_refuse_tensors_of_another_device():
+    """All tensors of a call on one device, but not on the one that the plan's workspace and the stream belong to."""
+    for plan, good in (lora_layouts(), attn_layouts()):
+        plan._checked(**good)
+        for t in good.values():
+            t.device_index = 1
+        with pytest.raises(ValueError):
+            plan._checked(**good)
+
+
+def test_head_norms_refuse_tensors_of_another_device_than_the_current_one():
+    good = rope_layouts()
+    assert serving._checked_rope(0, **good).tokens == 5
+    with pytest.raises(ValueError):
+        serving._checked_rope(1, **good)
+    shared = {n: good[n] for n in ("q", "k", "positions", "table", "q_weight", "k_weight", "eps", "interleaved", "norm")}
+    grads = dict(dq_out=good["q"], dk_out=good["k"], dq=good["q_out"], dk=good["k_out"])
+    serving._checked_rope_backward(0, **shared, **grads)
+    with pytest.raises(ValueError):
+        serving._checked_rope_backward(1, **shared, **grads)
+
+
+def test_the_current_device_is_part_of_what_is_checked(monkeypatch):
+    """Checks are kept by layout and current device: the same layouts under another one are checked again."""
+    current = [0]
+
+    def check(here, *rest):
+        raise KeyError(here)
+
+    good = rope_layouts()
+    names = ("q", "k", "positions", "table", "q_weight", "k_weight", "q_out", "k_out", "v", "k_cache", "v_cache", "slots")
+    kept = (0, 1e-6, False, True, serving._python_facts(*[good[n] for n in names]))
+    serving._lib()
+    monkeypatch.setattr(serving, "_facts", serving._python_facts)
+    monkeypatch.setattr(serving, "_current_device", lambda: current[0])
+    monkeypatch.setattr(serving, "_rope_checked", {kept: "found"})
+    monkeypatch.setattr(serving, "_checked_rope", check)
+    run = lambda: dg.qk_norm_rope(good["q"], good["k"], good["positions"], good["table"], q_out=good["q_out"], k_out=good["k_out"])  # noqa: E731
+    with pytest.raises(TypeError):          # found: text is no structure to copy
+        run()
+    current[0] = 1
+    with pytest.raises(KeyError):           # checked
+        run()
 
 
 def test_native_tensor_facts_agree_with_the_python_ones():
