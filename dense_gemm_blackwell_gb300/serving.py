@@ -14,9 +14,11 @@ that captured it) must follow one another.
 from __future__ import annotations
 
 import ctypes
+import itertools
 import math
 import os
 import re
+import threading
 
 from . import (GEMM_BF16, GEMM_E4M3, GEMM_F16, GEMM_F32, GEMM_OK, GemmDeviceError, GemmError, GemmPlanInfo, _dtype_code,
                current_stream_handle, lib)
@@ -232,6 +234,8 @@ class LoraPlan(_Plan):
     """
 
     _destroy = "lora_plan_destroy"
+    captured = False      # lora_matmul: used while its stream was captured,
+    last_use = 0          # and when
 
     def __init__(self, tokens, n, k, *, rank, adapters, dtype=GEMM_BF16, dtype_y=None, ldx=0, ldw=0, ldy=0, flags=0,
                  tile_n=0, stages=0, max_ctas=0, wait_timeout_ns=0):
@@ -271,13 +275,15 @@ class LoraPlan(_Plan):
 
     def run(self, x, w, a, b, adapter, y, scale=None, stream=None):
         """Enqueue on `stream` (default: torch's current stream)."""
-        key = _facts(x, w, a, b, adapter, y, scale)
+        return self._run(_facts(x, w, a, b, adapter, y, scale), x, w, a, b, adapter, y, scale, current_stream_handle() if stream is None else stream)
+
+    def _run(self, key, x, w, a, b, adapter, y, scale, stream):
         checked = self._args.get(key)
         if checked is None:
             checked = _keep(self._args, key, self._checked(x, w, a, b, adapter, y, scale))
         g = LoraArgs.from_buffer_copy(checked)
         _fill(g, _LORA_PTRS, x, w, a, b, adapter, scale, y)
-        status = _declared.lora_run(self.handle, ctypes.byref(g), current_stream_handle() if stream is None else stream)
+        status = _declared.lora_run(self.handle, ctypes.byref(g), stream)
         if status:
             raise GemmError(status, "lora_run")
         return y
@@ -290,32 +296,84 @@ class LoraPlan(_Plan):
 
 
 _LORA_PTRS = _offsets(LoraArgs, "x", "w", "a", "b", "adapter", "scale", "y")
+
+# lora_matmul's plans.  Their workspaces grow with the tokens (67 MB at 8192 tokens, 64 adapters and rank 64), so they are
+# bounded: those not used for longest go until the rest takes no more than this.
+_LORA_PLAN_BYTES = 1 << 30
+_LORA_PLAN_COUNT = 256
 _lora_plans = {}
+_lora_calls = {}          # the plan of a call's layouts
+_lora_uses = itertools.count(1)
+_lora_lock = threading.Lock()
+
+
+def _bound_lora_plans(newest):
+    """Gives up plans, but never the newest one nor those that a graph may replay."""
+    import torch
+    size = sum(p.info.workspace_bytes for p in _lora_plans.values())
+    count = len(_lora_plans)
+    idle = False
+    for key, plan in sorted(_lora_plans.items(), key=lambda item: item[1].last_use):
+        if size <= _LORA_PLAN_BYTES and count <= _LORA_PLAN_COUNT:
+            return
+        if plan.captured or plan is newest:
+            continue
+        if not idle:
+            torch.cuda.synchronize()      # their last launches are done
+            idle = True
+        del _lora_plans[key]
+        size -= plan.info.workspace_bytes
+        count -= 1
+        plan.close()
+
+
+def _lora_plan_for(x, w, a, b, out, stream, capturing):
+    _need(x.dim() == 2 and w.dim() == 2 and a.dim() == 3 and b.dim() == 3 and out.dim() == 2,
+          "x [M, K], w [N, K], a [L, R, K], b [L, N, R], out [M, N] expected")
+    _rows_ok(x, "x")
+    _rows_ok(w, "w")
+    device = x.get_device()
+    _need(x.is_cuda and device == _current_device(), "x: must be on the current CUDA device")
+    (m, k), n = x.shape, w.shape[0]
+    ld = lambda t: max(t.stride(0), t.shape[1])  # noqa: E731  (a single row's stride says nothing)
+    key = (device, stream, x.shape, w.shape, a.shape, x.dtype, out.dtype, ld(x), ld(w), ld(out))
+    plan = _lora_plans.get(key)
+    if plan is None:
+        plan = LoraPlan(m, n, k, rank=a.shape[1], adapters=a.shape[0], dtype=_dtype_code(x.dtype), dtype_y=_dtype_code(out.dtype),
+                        ldx=ld(x), ldw=ld(w), ldy=ld(out))
+        _lora_plans[key] = plan
+        if not capturing:
+            _bound_lora_plans(plan)
+    return plan
 
 
 def lora_matmul(x, w, a, b, adapter, *, scale=None, out=None, out_dtype=None):
     """Y = X W^T + scale_i (X A_i^T) B_i^T (see LoraPlan).
 
-    Plans are kept per shape, layout, device and stream: graphs captured on one stream share them, so replay those one
-    after the other (or give each a LoraPlan of its own).
+    Plans are kept per shape, layout, device and stream, up to 1 GiB of workspaces: the first call of a shape, or of one that
+    was given up since, allocates and may wait for the device (a server with few batch sizes makes LoraPlans instead).  Plans
+    that a capture used are kept for good; graphs captured on one stream share them, so replay those one after the other (or
+    give each a LoraPlan of its own).  Calls may come from several threads.
     """
     import torch
-    _need(x.dim() == 2 and w.dim() == 2 and a.dim() == 3 and b.dim() == 3, "x [M, K], w [N, K], a [L, R, K], b [L, N, R] expected")
-    _rows_ok(x, "x")
-    _rows_ok(w, "w")
-    _lib()
-    _need(x.is_cuda and x.get_device() == _current_device(), "x: must be on the current CUDA device")
+    if _declared is None:
+        _lib()
     if out is None:
+        _need(x.dim() == 2 and w.dim() == 2, "x [M, K], w [N, K] expected")
         out = torch.empty(x.shape[0], w.shape[0], dtype=out_dtype or x.dtype, device=x.device)
     stream = current_stream_handle()
-    ld = lambda t: max(t.stride(0), t.shape[1])  # noqa: E731  (a single row's stride says nothing)
-    key = (x.get_device(), stream, x.shape, w.shape, a.shape, x.dtype, out.dtype, ld(x), ld(w), ld(out))
-    plan = _lora_plans.get(key)
-    if plan is None:
-        plan = _lora_plans[key] = LoraPlan(x.shape[0], w.shape[0], x.shape[1], rank=a.shape[1], adapters=a.shape[0],
-                                           dtype=_dtype_code(x.dtype), dtype_y=_dtype_code(out.dtype), ldx=ld(x),
-                                           ldw=ld(w), ldy=ld(out))
-    return plan.run(x, w, a, b, adapter, out, scale=scale, stream=stream)
+    capturing = torch._C._cuda_isCurrentStreamCapturing()
+    facts = _facts(x, w, a, b, adapter, out, scale)
+    key = (_current_device(), stream, facts)
+    # A call is two launches that share the plan's workspace: no other thread's come between them.
+    with _lora_lock:
+        plan = _lora_calls.get(key)
+        if plan is None or plan.handle is None:
+            plan = _keep(_lora_calls, key, _lora_plan_for(x, w, a, b, out, stream, capturing))
+        plan.last_use = next(_lora_uses)
+        if capturing:
+            plan.captured = True
+        return plan._run(facts, x, w, a, b, adapter, out, scale, stream)
 
 
 # ---------------------------------------------------------------- head norms and rotary positions

@@ -11,6 +11,8 @@ Random cases: with S = sum |x||w| + s sum_r (sum_k |x||a|) |b| the sum of all ma
                                            for fp32 outputs T is two terms: u^2
              + u_out (|Y64| + the above)   the output's rounding.
 """
+import threading
+
 import pytest
 import torch
 
@@ -308,6 +310,52 @@ def test_lora_matmul_and_empty_batches():
     assert torch.equal(dg.lora_matmul(x[:1], w, a, b, adapter[:1], scale=scale, out_dtype=torch.float32), want.float()[:1])
     none = dg.lora_matmul(x[:0], w, a, b, adapter[:0], scale=scale)
     assert tuple(none.shape) == (0, 64)
+
+
+def test_lora_matmul_with_ever_new_token_counts(monkeypatch):
+    """Plans come and go; a graph's plan stays."""
+    from dense_gemm_blackwell_gb300 import serving
+    monkeypatch.setattr(serving, "_LORA_PLAN_COUNT", 3)
+    (x, w, a, b, adapter, scale), want = make_exact(80, 264, 328, 16, 7, "mixed", 2, torch.bfloat16)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out = torch.empty(33, 264, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        dg.lora_matmul(x[:33], w, a, b, adapter[:33], scale=scale, out=out)
+        side.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            dg.lora_matmul(x[:33], w, a, b, adapter[:33], scale=scale, out=out)
+    torch.cuda.synchronize()
+    for tokens in (1, 80, 17, 9, 64, 80, 2, 50):
+        y = dg.lora_matmul(x[:tokens], w, a, b, adapter[:tokens], scale=scale, out_dtype=torch.float32)
+        assert torch.equal(y, want.float()[:tokens])
+    assert len(serving._lora_plans) <= 4
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want.float()[:33])
+
+
+@pytest.mark.parametrize("tokens", [40, 700])
+def test_lora_matmul_from_several_threads(tokens):
+    """Threads that share a stream and a shape, each with inputs of its own."""
+    cases = [make_exact(tokens, 264, 328, 16, 7, "mixed", 10 + i, torch.bfloat16) for i in range(4)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        (x, w, a, b, adapter, scale), want = cases[i]
+        for _ in range(50):
+            if not torch.equal(dg.lora_matmul(x, w, a, b, adapter, scale=scale, out_dtype=torch.float32), want.float()):
+                wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
 
 
 def test_refusals():

@@ -6,6 +6,8 @@ import math
 import os
 import shutil
 import subprocess
+import threading
+import time
 
 import numpy as np
 import pytest
@@ -293,6 +295,102 @@ def test_the_current_device_is_part_of_what_is_checked(monkeypatch):
     current[0] = 1
     with pytest.raises(KeyError):           # checked
         run()
+
+
+class StandInPlan:
+    """Counts as a LoraPlan of 300 bytes."""
+
+    made = []
+    captured, last_use = False, 0
+
+    def __init__(self, tokens, n, k, **kw):
+        self.info = type("Info", (), {"workspace_bytes": 300})
+        self.tokens, self.handle = tokens, 1
+        StandInPlan.made.append(self)
+
+    def _run(self, facts, x, *rest):
+        assert self.handle and self.tokens == x.shape[0]
+        return x.shape[0]
+
+    def close(self):
+        self.handle = None
+
+    @property
+    def open(self):
+        return self.handle is not None
+
+
+@pytest.fixture
+def stand_in_plans(monkeypatch):
+    """(call lora_matmul for a number of tokens, a list whose last element says whether the stream is captured)"""
+    state, waited = [False], []
+    monkeypatch.setattr(StandInPlan, "made", [])
+    monkeypatch.setattr(serving, "LoraPlan", StandInPlan)
+    monkeypatch.setattr(serving, "_current_device", lambda: 0)
+    monkeypatch.setattr(serving, "current_stream_handle", lambda: 7)
+    monkeypatch.setattr(serving, "_facts", serving._python_facts)
+    monkeypatch.setattr(serving, "_lora_plans", {})
+    monkeypatch.setattr(serving, "_lora_calls", {})
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: state[-1], raising=False)
+    serving._lib()
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda *a: waited.append([p.open for p in StandInPlan.made]))
+
+    def call(tokens):
+        half = torch.bfloat16
+        x, w, y = Layout((tokens, 64), half), Layout((32, 64), half), Layout((tokens, 32), half)
+        assert dg.lora_matmul(x, w, Layout((2, 8, 64), half), Layout((2, 32, 8), half), Layout((tokens,), torch.int32), out=y) == tokens
+
+    return call, state, waited
+
+
+def test_lora_matmul_bounds_its_plans(stand_in_plans, monkeypatch):
+    """Ever new token counts: the oldest plans are given up once the device is idle, those that a graph may replay are not."""
+    call, state, waited = stand_in_plans
+    monkeypatch.setattr(serving, "_LORA_PLAN_BYTES", 1000)
+    for tokens in (1, 2, 3, 1, 4):
+        call(tokens)
+    assert [p.tokens for p in StandInPlan.made if p.open] == [1, 3, 4]           # 2 was used least recently
+    assert waited == [[True] * 4]                                                # the wait came before the first was closed
+    state.append(True)
+    call(3)                                                                      # captured: nothing is freed or waited for
+    call(5)
+    assert len(waited) == 1 and [p.tokens for p in StandInPlan.made if p.open] == [1, 3, 4, 5]
+    state.append(False)
+    for tokens in range(6, 12):
+        call(tokens)
+    still = [p.tokens for p in StandInPlan.made if p.open]
+    assert still == [3, 5, 11] and [p.tokens for p in serving._lora_plans.values()] == still
+    call(4)                                                                      # given up before: made anew, and 11 goes for it
+    assert len(StandInPlan.made) == 12 and [p.tokens for p in StandInPlan.made if p.open] == [3, 5, 4]
+    monkeypatch.setattr(serving, "_LORA_PLAN_BYTES", 100)                        # the last one stays even if it alone is too much
+    call(12)
+    assert [p.tokens for p in StandInPlan.made if p.open] == [3, 5, 12]
+    monkeypatch.setattr(serving, "_LORA_PLAN_BYTES", 1 << 30)
+    monkeypatch.setattr(serving, "_LORA_PLAN_COUNT", 4)
+    for tokens in range(13, 20):
+        call(tokens)
+    assert [p.tokens for p in StandInPlan.made if p.open] == [3, 5, 18, 19]
+
+
+def test_lora_matmul_s_launches_of_one_call_stay_together(stand_in_plans, monkeypatch):
+    """No other thread runs a plan while one thread does."""
+    call, _, _ = stand_in_plans
+    inside, worst = [0], [0]
+
+    def run(self, facts, x, *rest):
+        inside[0] += 1
+        worst[0] = max(worst[0], inside[0])
+        time.sleep(0.002)
+        inside[0] -= 1
+        return x.shape[0]
+
+    monkeypatch.setattr(StandInPlan, "_run", run)
+    threads = [threading.Thread(target=lambda: [call(t) for t in (1, 2, 3)]) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert worst[0] == 1 and len(StandInPlan.made) == 3
 
 
 def test_native_tensor_facts_agree_with_the_python_ones():
