@@ -187,10 +187,15 @@ def _rows_ok(t, name):
     _need(t.shape[-1] <= 1 or t.stride(-1) == 1, "%s: the last dimension must be contiguous" % name)
 
 
+def _steps(t, *dims):
+    """Strides of a tensor's dimensions; that of one element is never used and may be anything, so it counts as 0."""
+    return [t.stride(d) if t.shape[d] > 1 else 0 for d in dims]
+
+
 def _apart(t, dim, name):
     """A stride that the library takes 0 of for "packed": a tensor that repeats one row or matrix is refused."""
     _need(t.shape[dim] <= 1 or t.stride(dim) != 0, "%s: dimension %d is expanded (stride 0); a copy is needed" % (name, dim))
-    return t.stride(dim)
+    return _steps(t, dim)[0]
 
 
 class _Plan:
@@ -450,9 +455,9 @@ def _rope_args(here, q, k, positions, table, q_weight, k_weight, eps, interleave
     g = QkNormRopeArgs()
     g.tokens, g.heads, g.kv_heads, g.head_dim, g.rot_dim = tokens, heads, 0 if k is None else k.shape[1], dim, 2 * table.shape[2]
     g.interleaved, g.norm, g.dtype, g.eps, g.table_rows = int(interleaved), int(norm), _dtype_code(q.dtype), eps, table.shape[0]
-    g.q_token, g.q_head = q.stride(0), q.stride(1)
+    g.q_token, g.q_head = _steps(q, 0, 1)
     if k is not None:
-        g.k_token, g.k_head = k.stride(0), k.stride(1)
+        g.k_token, g.k_head = _steps(k, 0, 1)
     return g
 
 
@@ -472,11 +477,11 @@ def _checked_rope(here, q, k, positions, table, q_weight, k_weight, eps, interle
     dev = q.get_device()
     _check_rows("q_out", q_out, g.tokens, g.head_dim, q.dtype, dev)
     _need(q_out.shape == q.shape, "q_out: q's shape expected")
-    g.q_out_token, g.q_out_head = q_out.stride(0), q_out.stride(1)
+    g.q_out_token, g.q_out_head = _steps(q_out, 0, 1)
     if k_out is not None:
         _need(k is not None and k_out.shape == k.shape, "k_out: k's shape expected")
         _check_rows("k_out", k_out, g.tokens, g.head_dim, q.dtype, dev)
-        g.k_out_token, g.k_out_head = k_out.stride(0), k_out.stride(1)
+        g.k_out_token, g.k_out_head = _steps(k_out, 0, 1)
     if k_cache is not None:
         _need(k is not None and v is not None and v_cache is not None and slots is not None, "a cache append needs k, v, k_cache, v_cache and slots")
         _check_rows("v", v, g.tokens, g.head_dim, q.dtype, dev)
@@ -487,9 +492,9 @@ def _checked_rope(here, q, k, positions, table, q_weight, k_weight, eps, interle
         if slots.dtype != torch.int32:
             raise TypeError("slots: int32 expected, got %s" % slots.dtype)
         _need(tuple(slots.shape) == (g.tokens,) and slots.is_contiguous() and slots.get_device() == dev, "slots: [tokens], contiguous, on q's device")
-        g.v_token, g.v_head = v.stride(0), v.stride(1)
-        g.k_page, g.k_place, g.k_chead = k_cache.stride()[:3]
-        g.v_page, g.v_place, g.v_chead = v_cache.stride()[:3]
+        g.v_token, g.v_head = _steps(v, 0, 1)
+        g.k_page, g.k_place, g.k_chead = _steps(k_cache, 0, 1, 2)
+        g.v_page, g.v_place, g.v_chead = _steps(v_cache, 0, 1, 2)
         g.num_pages, g.page_size, g.dtype_cache = k_cache.shape[0], k_cache.shape[1], _dtype_code(k_cache.dtype)
     else:
         _need(v is None and v_cache is None and slots is None, "v, v_cache and slots go with k_cache")
@@ -549,9 +554,9 @@ def _checked_rope_backward(here, dq_out, dk_out, q, k, positions, table, q_weigh
         if like is not None:
             _check_rows(name, t, g.tokens, g.head_dim, q.dtype, q.get_device())
             _need(t.shape == like.shape, "%s: the forward input's shape expected" % name)
-    d.dq_out_token, d.dq_out_head, d.dq_token, d.dq_head = dq_out.stride(0), dq_out.stride(1), dq.stride(0), dq.stride(1)
+    d.dq_out_token, d.dq_out_head, d.dq_token, d.dq_head = _steps(dq_out, 0, 1) + _steps(dq, 0, 1)
     if k is not None:
-        d.dk_out_token, d.dk_out_head, d.dk_token, d.dk_head = dk_out.stride(0), dk_out.stride(1), dk.stride(0), dk.stride(1)
+        d.dk_out_token, d.dk_out_head, d.dk_token, d.dk_head = _steps(dk_out, 0, 1) + _steps(dk, 0, 1)
     return g, d
 
 
@@ -651,10 +656,10 @@ class PagedAttentionPlan(_Plan):
                 raise TypeError("lse: float32 expected, got %s" % lse.dtype)
             _need(tuple(lse.shape) == (batch, d.heads) and lse.is_contiguous() and lse.get_device() == dev, "lse: [batch, heads], contiguous, on q's device")
         g = PagedAttnArgs()
-        g.batch, g.table_width, g.table_stride = batch, block_table.shape[1], block_table.stride(0)
-        g.q_batch, g.q_head, g.out_batch, g.out_head = q.stride(0), q.stride(1), out.stride(0), out.stride(1)
-        g.k_page, g.k_place, g.k_head = k_cache.stride()[:3]
-        g.v_page, g.v_place, g.v_head = v_cache.stride()[:3]
+        g.batch, g.table_width, g.table_stride = batch, block_table.shape[1], _steps(block_table, 0)[0]
+        g.q_batch, g.q_head, g.out_batch, g.out_head = _steps(q, 0, 1) + _steps(out, 0, 1)
+        g.k_page, g.k_place, g.k_head = _steps(k_cache, 0, 1, 2)
+        g.v_page, g.v_place, g.v_head = _steps(v_cache, 0, 1, 2)
         g.num_pages = k_cache.shape[0]
         return g
 

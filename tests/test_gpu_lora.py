@@ -358,6 +358,14 @@ def test_lora_matmul_from_several_threads(tokens):
     assert not wrong
 
 
+def test_strides_of_single_elements_do_not_matter():
+    (x, w, a, b, adapter, scale), want = make_exact(2, 1, 128, 16, 1, "one", 3, torch.bfloat16)
+    y = torch.empty(2, 8, device="cuda")[:, :1]
+    with dg.LoraPlan(2, 1, 128, rank=16, adapters=1, dtype_y=dg.GEMM_F32, ldx=x.stride(0), ldy=8) as plan:
+        plan.run(x, w.as_strided((1, 128), (1, 1)), a.as_strided(a.shape, (1, a.stride(1), 1)), b.as_strided(b.shape, (1, 3, 1)), adapter, y, scale=scale)
+    assert torch.equal(y, want.float())
+
+
 def test_refusals():
     x, w = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(32, 64, dtype=torch.bfloat16, device="cuda")
     a, b = torch.zeros(2, 16, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, 32, 16, dtype=torch.bfloat16, device="cuda")

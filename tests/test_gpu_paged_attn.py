@@ -252,6 +252,14 @@ def test_cache_beyond_32_bits():
     check(q, kc, vc, table, torch.tensor([77, 80], dtype=torch.int32, device="cuda"))
 
 
+def test_strides_of_single_elements_do_not_matter():
+    q, kc, vc, table, lengths = make([77], 4, 1, 64, 16, torch.bfloat16, torch.bfloat16)
+    want = check(q, kc, vc, table, lengths)
+    odd = lambda t, *strides: t.as_strided(t.shape, strides)  # noqa: E731
+    q, kc, vc = odd(q.contiguous(), 1, 64, 1), odd(kc, 1024, 64, 3, 1), odd(vc, 1024, 64, 1, 1)
+    assert torch.equal(check(q, kc, vc, odd(table, 1, 1), lengths), want)
+
+
 def test_streams_and_graph():
     q, kc, vc, table, lengths = make([500, 64, 0, 1000], 8, 2, 128, 16, torch.bfloat16, torch.bfloat16)
     plan = dg.PagedAttentionPlan(4, heads=8, kv_heads=2, head_dim=128, page_size=16)

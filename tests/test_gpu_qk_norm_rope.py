@@ -324,6 +324,16 @@ def test_streams_and_graph():
     close(ko, *plain(k, wk, pos, table, False), U[torch.bfloat16])
 
 
+def test_strides_of_single_elements_do_not_matter():
+    q, k, v, pos, table, wq, wk = make(1, 3, 1, 64, 64, torch.bfloat16)
+    odd = lambda t: t.contiguous().as_strided(t.shape, (1, 64 if t.shape[1] > 1 else 5, 1))  # noqa: E731
+    kw = dict(q_weight=wq, k_weight=wk, eps=EPS)
+    for a, b in zip(dg.qk_norm_rope(q, k, pos, table, **kw), dg.qk_norm_rope(odd(q), odd(k), pos, table, **kw)):
+        assert torch.equal(a, b)
+    for a, b in zip(dg.qk_norm_rope_backward(q, k, q, k, pos, table, **kw), dg.qk_norm_rope_backward(odd(q), odd(k), odd(q), odd(k), pos, table, **kw)):
+        assert torch.equal(a, b)
+
+
 def backward_case(tokens=300, seed=0):
     q, k, v, pos, table, wq, wk = make(tokens, 4, 2, 128, 128, torch.bfloat16, seed=seed)
     gen = torch.Generator(device="cuda").manual_seed(seed + 1)

@@ -297,6 +297,27 @@ def test_the_current_device_is_part_of_what_is_checked(monkeypatch):
         run()
 
 
+def test_strides_of_single_elements_do_not_matter():
+    """A dimension of one element may have any stride (tensors from other libraries often say 1): it is never used, and must
+    not fail the checks of alignment."""
+    half = torch.bfloat16
+    plan, args = attn_layouts(batch=1, heads=1, kv=1, page=1, q=Layout((1, 1, 64), half, (1, 1, 1)), out=Layout((1, 1, 64), half, (3, 5, 1)),
+                              k_cache=Layout((9, 1, 1, 64), half, (64, 1, 1, 1)), v_cache=Layout((9, 1, 1, 64), half, (64, 7, 7, 1)),
+                              block_table=Layout((1, 4), torch.int32, (-1, 1)))
+    g = plan._checked(**args)
+    names = ("q_batch", "q_head", "out_batch", "out_head", "k_place", "k_head", "v_place", "v_head", "table_stride")
+    assert [getattr(g, n) for n in names] == [0] * len(names) and g.k_page == 64
+    row = Layout((1, 1, 64), half, (1, 1, 1))
+    g = serving._checked_rope(0, **rope_layouts(tokens=1, heads=1, kv=1, q=row, k=row, q_out=row, k_out=row, v=row,
+                                                k_cache=Layout((9, 1, 1, 64), half, (64, 1, 1, 1)), v_cache=Layout((9, 1, 1, 64), half, (64, 1, 1, 1)),
+                                                slots=Layout((1,), torch.int32)))
+    assert not any(getattr(g, n) for n in ("q_token", "q_head", "k_token", "k_head", "v_token", "v_head", "q_out_token", "k_out_head", "k_place", "v_chead"))
+    plan, args = lora_layouts(tokens=1, n=1, adapters=1, x=Layout((1, 128), half, (1, 1)), w=Layout((1, 128), half, (1, 1)),
+                              a=Layout((1, 16, 128), half, (1, 128, 1)), b=Layout((1, 1, 16), half, (1, 1, 1)), y=Layout((1, 1), half, (1, 1)))
+    g = plan._checked(**args)
+    assert (g.stride_a, g.lda, g.stride_b, g.ldb) == (0, 128, 0, 0)
+
+
 class StandInPlan:
     """Counts as a LoraPlan of 300 bytes."""
 
