@@ -91,7 +91,8 @@ __device__ __forceinline__ void publish_adapters(const ShrinkParams& p, int tile
     for (int i = threadIdx.x; i < count; i += kShrinkThreads) p.ids[(size_t)tile * p.max_adapters + i] = l.list[i];
 }
 
-// Eight scaled sums as T's row piece: one term, or for fp32 outputs the rounded value and what the rounding left.
+// Eight scaled sums as T's row piece: one term, or for fp32 outputs the rounded value and what the rounding left.  Nothing is
+// left of an infinity (an f16 sum past 65504 among them): the difference would be a NaN.
 template <typename T>
 __device__ __forceinline__ void store_t(const ShrinkParams& p, T* at, float (&v)[8], float scale) {
 #pragma unroll
@@ -102,7 +103,7 @@ __device__ __forceinline__ void store_t(const ShrinkParams& p, T* at, float (&v)
         float back[8];
         unpack8<T>(first, back);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] -= back[j];
+        for (int j = 0; j < 8; ++j) v[j] = back[j] - back[j] == 0.f ? v[j] - back[j] : 0.f;
         *reinterpret_cast<uint4*>(at + p.rank16) = round8<T>(v);
     }
 }

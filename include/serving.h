@@ -40,7 +40,8 @@ extern "C" {
 /* Y[m, n] = sum_k X[m, k] W[n, k] + scale[i] sum_r T[m, r] B_i[n, r],
  * T[m, r] = sum_k X[m, k] A_i[r, k], i = adapter[m]; a token with i < 0 (or i >= adapters) takes the projection alone.
  * All sums are fp32, Y is rounded once.  scale[i] T is rounded to the input type before its product with B_i (the tensor
- * core multiplies 16-bit operands); for fp32 outputs it is carried as the sum of two such values.  Infinities and NaN of
+ * core multiplies 16-bit operands); for fp32 outputs it is carried as the sum of two such values.  For f16 inputs a scale[i] T
+ * past 65504 so becomes an infinity, and the token's outputs with it.  Infinities and NaN of
  * a token or of A_i and B_i stay with that token and the tokens of adapter i; many of them in B_i are slow, as the
  * outputs of other tokens beside them are computed twice. */
 typedef struct {

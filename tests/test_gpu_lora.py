@@ -358,6 +358,27 @@ def test_lora_matmul_from_several_threads(tokens):
     assert not wrong
 
 
+@pytest.mark.parametrize("out", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("tokens", [5, 300, 700])
+def test_a_sum_past_f16_is_an_infinity(tokens, out):
+    """scale T is rounded to f16: what does not fit is an infinity of its sign in any output type, for its own token only."""
+    (x, w, a, b, adapter, scale), _ = make_exact(tokens, 40, 72, 16, 2, "one", 6, torch.float16)
+    a.zero_()
+    a[:, 0, 0] = 1024.0
+    b.copy_(b.abs())
+    b[:, :, 0] = 1.0
+    x[:, 0] = torch.randint(-2, 3, (tokens,), device="cuda").half()
+    x[3, 0], x[4, 0] = 1024.0, -1024.0
+    scale.fill_(1.0)
+    want = plain(x.double(), w.double(), a.double(), b.double(), adapter.long(), scale.double())
+    want[3], want[4] = float("inf"), float("-inf")
+    y = torch.empty(tokens, 40, dtype=out, device="cuda")
+    with dg.LoraPlan(tokens, 40, 72, rank=16, adapters=2, dtype=dg.GEMM_F16, dtype_y=CODE[out], ldx=x.stride(0), ldw=w.stride(0)) as plan:
+        plan.run(x, w, a, b, adapter, y, scale=scale)
+        assert plan.sync_status()[0] == dg.GEMM_OK
+    assert torch.equal(y, want.to(out))
+
+
 def test_strides_of_single_elements_do_not_matter():
     (x, w, a, b, adapter, scale), want = make_exact(2, 1, 128, 16, 1, "one", 3, torch.bfloat16)
     y = torch.empty(2, 8, device="cuda")[:, :1]
