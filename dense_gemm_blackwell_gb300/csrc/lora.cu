@@ -47,6 +47,7 @@
 #include "launch.h"
 #include "lora_list.cuh"
 #include "lora_skinny.h"
+#include "ptx.cuh"
 #include "serving.h"
 #include "serving_host.h"
 
@@ -79,12 +80,6 @@ struct StreamShape {
     static constexpr int kSmemBytes = kStages * kStageBytes;
     static_assert(kShrinkRows * kSumPitch * 4 <= kSmemBytes, "");
 };
-
-__device__ __forceinline__ float4 load_cluster_f4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-    return v;
-}
 
 __device__ __forceinline__ void publish_adapters(const ShrinkParams& p, int tile, const AdapterList& l, int count) {
     if (threadIdx.x == 0) p.counts[tile] = count;
@@ -154,25 +149,10 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
     const uint32_t ballot = __ballot_sync(0xffffffffu, mine == id);
     if (lane == 0) same[warp] = ballot;
     __syncthreads();
-    if (lead == 0) {
+    if (lead == 0 && warp == 0) {
         // the m block's list of adapters, for the product
-        if (warp == 0) {
-            int done = 0;
-            for (int base = 0; base < words; base += 32) {
-                uint32_t word = base + lane < words ? bits[base + lane] : 0u;
-                int at = __popc(word);
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int t = __shfl_up_sync(0xffffffffu, at, o);
-                    if (lane >= o) at += t;
-                }
-                const int all = __shfl_sync(0xffffffffu, at, 31);
-                at += done - __popc(word);
-                for (; word; word &= word - 1) p.ids[(size_t)tile * p.max_adapters + at++] = (base + lane) * 32 + __ffs(word) - 1;
-                done += all;
-            }
-            if (lane == 0) p.counts[tile] = done;
-        }
+        const int count = list_bits(bits, words, lane, p.ids + (size_t)tile * p.max_adapters);
+        if (lane == 0) p.counts[tile] = count;
     }
     if (id < 0) return;
     // This row leads a group if the number of its adapter's rows before it is a multiple of eight.

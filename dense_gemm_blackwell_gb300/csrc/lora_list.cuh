@@ -15,6 +15,25 @@ struct AdapterList {
     int32_t count;
 };
 
+// Writes the numbers of the set bits of `words` words to `list`, ascending; returns how many.  Called by a whole warp.
+__device__ __forceinline__ int list_bits(const uint32_t* bits, int words, int lane, int32_t* list) {
+    int done = 0;
+    for (int base = 0; base < words; base += 32) {
+        uint32_t word = base + lane < words ? bits[base + lane] : 0u;
+        int at = __popc(word);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, at, o);
+            if (lane >= o) at += t;
+        }
+        const int all = __shfl_sync(0xffffffffu, at, 31);
+        at += done - __popc(word);
+        for (; word; word &= word - 1) list[at++] = (base + lane) * 32 + __ffs(word) - 1;
+        done += all;
+    }
+    return done;
+}
+
 // Fills `out` from the adapters of rows [row0, row0 + rows) (rows past M and numbers outside [0, adapters) have none), and
 // row_ids[i] (-1: none) for the rows i of [first, first + num) among them.  Called by `threads` threads, the first
 // warp of them whole, numbered `tid`; `sync` is their barrier.
@@ -32,21 +51,8 @@ __device__ __forceinline__ int find_adapters(const int32_t* adapter, int adapter
     }
     sync();
     if (tid < 32) {
-        int done = 0;
-        for (int base = 0; base < words; base += 32) {
-            uint32_t word = base + lane < words ? out.bits[base + lane] : 0u;
-            int at = __popc(word);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int t = __shfl_up_sync(0xffffffffu, at, o);
-                if (lane >= o) at += t;
-            }
-            const int all = __shfl_sync(0xffffffffu, at, 31);
-            at += done - __popc(word);
-            for (; word; word &= word - 1) out.list[at++] = (base + lane) * 32 + __ffs(word) - 1;
-            done += all;
-        }
-        if (lane == 0) out.count = done;
+        const int count = list_bits(out.bits, words, lane, out.list);
+        if (lane == 0) out.count = count;
     }
     sync();
     return out.count;

@@ -40,12 +40,6 @@ namespace dgb {
 
 constexpr int kSkinnyThreads = 192;
 
-__device__ __forceinline__ float4 peer_f4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
-    return v;
-}
-
 template <int OUT>
 __global__ void __launch_bounds__(kSkinnyThreads, 1) skinny_kernel(const __grid_constant__ SkinnyParams p,
                                                                    const __grid_constant__ LoraTail tail) {
@@ -270,7 +264,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1) skinny_kernel(const __grid_
                 const uint32_t at = mine + (uint32_t)(i / pieces * p.sum_pitch + i % pieces * 4) * 4u;
 #pragma unroll
                 for (int q = 0; q < kSkinnyMaxSplit; ++q)
-                    if (q < KS) x[u][q] = peer_f4(KS > 1 ? map_to_cta(at, (uint32_t)q) : at);
+                    if (q < KS) x[u][q] = load_cluster_f4(KS > 1 ? map_to_cta(at, (uint32_t)q) : at);
             }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {

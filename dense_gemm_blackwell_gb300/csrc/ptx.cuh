@@ -73,6 +73,14 @@ __device__ __forceinline__ void cluster_sync_relaxed() {
                  "barrier.cluster.wait.aligned;" ::: "memory");
 }
 
+// Four floats of the cluster's shared memory (an address of map_to_cta or this CTA's own); ordered against the CTAs' stores by
+// the cluster's barriers around it.
+__device__ __forceinline__ float4 load_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
+}
+
 // Address of the same shared-memory offset in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t map_to_cta(uint32_t smem_addr, uint32_t rank) {
     uint32_t r;
