@@ -340,7 +340,10 @@ def _lora_plan_for(x, w, a, b, out, stream, capturing):
     device = x.get_device()
     _need(x.is_cuda and device == _current_device(), "x: must be on the current CUDA device")
     (m, k), n = x.shape, w.shape[0]
-    ld = lambda t: max(t.stride(0), t.shape[1])  # noqa: E731  (a single row's stride says nothing)
+
+    def ld(t):      # a single row's stride is never used: any that is a multiple of 16 bytes
+        return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+
     key = (device, stream, x.shape, w.shape, a.shape, x.dtype, out.dtype, ld(x), ld(w), ld(out))
     plan = _lora_plans.get(key)
     if plan is None:

@@ -379,6 +379,14 @@ def test_a_sum_past_f16_is_an_infinity(tokens, out):
     assert torch.equal(y, want.to(out))
 
 
+@pytest.mark.parametrize("n,k", [(1543, 1001), (1, 1001), (7, 3)])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_lora_matmul_takes_single_rows_of_any_width(n, k, out):
+    (x, w, a, b, adapter, scale), want = make_exact(1, n, k, 16, 2, "one", 5, torch.bfloat16)
+    y = dg.lora_matmul(x.contiguous(), w, a, b, adapter, scale=scale, out_dtype=out)
+    assert torch.equal(y, want.to(out))
+
+
 def test_strides_of_single_elements_do_not_matter():
     (x, w, a, b, adapter, scale), want = make_exact(2, 1, 128, 16, 1, "one", 3, torch.bfloat16)
     y = torch.empty(2, 8, device="cuda")[:, :1]

@@ -325,6 +325,7 @@ class StandInPlan:
     captured, last_use = False, 0
 
     def __init__(self, tokens, n, k, **kw):
+        self.kw = kw
         self.info = type("Info", (), {"workspace_bytes": 300})
         self.tokens, self.handle = tokens, 1
         StandInPlan.made.append(self)
@@ -362,6 +363,14 @@ def stand_in_plans(monkeypatch):
         assert dg.lora_matmul(x, w, Layout((2, 8, 64), half), Layout((2, 32, 8), half), Layout((tokens,), torch.int32), out=y) == tokens
 
     return call, state, waited
+
+
+def test_lora_matmul_takes_single_rows_of_any_width(stand_in_plans):
+    """A row alone has no neighbour to be 16 bytes apart from."""
+    half = torch.bfloat16
+    x, w, y = Layout((1, 1001), half), Layout((1543, 1001), half, (1008, 1)), Layout((1, 1543), half)
+    dg.lora_matmul(x, w, Layout((2, 8, 1001), half, (8064, 1008, 1)), Layout((2, 1543, 8), half), Layout((1,), torch.int32), out=y)
+    assert [StandInPlan.made[0].kw[n] for n in ("ldx", "ldw", "ldy")] == [1008, 1008, 1544]
 
 
 def test_lora_matmul_bounds_its_plans(stand_in_plans, monkeypatch):
