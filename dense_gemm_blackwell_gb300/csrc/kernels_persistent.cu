@@ -737,7 +737,9 @@ __global__ void __launch_bounds__(kThreads, 1) persistent_kernel(const __grid_co
 
 // The product with a tail of adapter steps after each tile's K blocks (lora.cu): rank / 16 more K = 16 instructions per
 // adapter among the tile's rows.  Bound like the product by the tensor cores: 8192^3 bf16, 512-wide pair tiles, prompts of
-// 12 requests with rank 64: 556 us a launch on a cool device, 2.0 PFLOP/s.
+// 12 requests with rank 64: 556 us a launch on a cool device, 2.0 PFLOP/s.  fp32 outputs: two terms of T, and the repair's
+// bookkeeping beside 32 fp32 values does not fit the registers (104 bytes stored, 304 to 312 loaded a thread, once per tile
+// row): 667 us a call where bf16 outputs take 638.
 template <int CG, int OUT>
 __global__ void __launch_bounds__(kThreads, 1) adapters_kernel(const __grid_constant__ PersistentParams p,
                                                                const __grid_constant__ LoraTail tail) {

@@ -28,14 +28,24 @@
 //   and add their sums through distributed shared memory.
 //
 // Bounds, GB300.  Few tokens: the bytes of W and the adapters, 34 MB for 4
-// tokens x 4096 x 4096 with two adapters of rank 16: 11.1 us, 3.1 TB/s; 56 MB
-// for 96 tokens with 80 adapters: 17.6 us, 3.2 TB/s.  What keeps it from the
-// 6.8 TB/s of a plain copy is the chain of steps around the stream: T (7 to 9
-// us beside the stream of W), the adapter steps that wait for it (1.7), the
-// join of the cluster and the stores (2 to 3).  Many tokens: the tensor cores,
-// 8192 x 8192 x 8192 with prompts of 12 requests and rank 64: 624 us, 1.79
-// PFLOP/s at the power cap, of which T takes 44; the same product without
-// adapters takes 595.
+// tokens x 4096 x 4096 with two adapters of rank 16: 11.0 us, 3.1 TB/s; 56 MB
+// for 96 tokens with 80 adapters: 17.5 us, 3.2 TB/s (8.6 and 10.6 with no
+// token's adapter set).  What keeps it from the 6.8 TB/s of a plain copy is the
+// chain of steps around the stream: T (7 to 9 us beside the stream of W), the
+// adapter steps that wait for it (1.7), the join of the cluster and the stores
+// (2 to 3).  Above rank 32 also that the two kernels no longer share an SM (see
+// plan_skinny): 96 tokens with 80 adapters of rank 64 take 48 us at a floor of
+// 18, of rank 128 72 at 30.  Many tokens: the tensor cores, 8192 x 8192 x 8192
+// with prompts of 12 requests and rank 64: 619 us on a cool device, 638 on a warm
+// one (power cap), 1.75 to 1.80 PFLOP/s, of which T takes 44; the plain product
+// in the same minute 612.  Between those, T is what stands out: it is complete
+// before the adapter steps begin and does not shrink with the product (1024 x
+// 2048 x 2048 with 8 adapters of rank 16: 19.2 us, 15.4 with no adapter set, the
+// plain product 10.8), and where the rows of a 64-row block have many adapters
+// the streamed form multiplies all 64 rows for each of them (4096 x 4096 x 4096,
+// 32 adapters of rank 16 mixed token by token: 239 us, the plain product 82).
+// fp32 outputs run twice the adapter steps and, in the persistent kernel, spill
+// (104 bytes stored a thread): 96 tokens 20.2 us, 8192^3 667.
 #include <algorithm>
 #include <cstring>
 #include <new>
@@ -401,7 +411,7 @@ static cudaError_t launch_stream_typed(const ShrinkParams& p, dim3 grid, cudaStr
 }
 
 // Whether the plan's first kernel gathers rows (see the top of this file): always for a decode batch; up to 1024 tokens where
-// an adapter has few of them on average (GB300, 400 x 4096 x 4096 with 64 adapters: 34 us against 62 streamed; 777 x 1543 x
+// an adapter has few of them on average (GB300, 400 x 4096 x 4096 with 64 adapters: 33 to 34 us against 62 streamed; 777 x 1543 x
 // 1001 with 5: 15.6 against 12.9).  A rank above 128 does not fit its registers.
 static bool gathers(const lora_desc_t& d) {
     return d.rank <= 128 && (d.tokens <= kGatherTokens || (d.tokens <= 1024 && d.tokens <= 16 * (int64_t)d.adapters));
@@ -499,7 +509,8 @@ bool plan_skinny(const lora_desc_t& d, const DeviceFacts& dev, lora_plan_s* p) {
     // the last stage's matrix instruction reads 128 rows from its X box on: 16 KB behind the ring
     const int64_t stage = (box_m + q.tile_n) * 128, slack = 128 * 128 + 1024;
     const int64_t most = dev.smem_optin - 4096 - slack;       // 4096: the kernel's static shared memory, rounded up
-    // room beside it for a CTA of gather_kernel (8 KB), so that the two kernels overlap on an SM
+    // Room beside it for a CTA of gather_kernel, so that the two kernels overlap on an SM: 5.6 KB up to rank 16, 9.6 up to 32.
+    // At ranks up to 64 and 128 it takes 17.6 and 33.6 KB, and where the ring fills its share its CTAs come first.
     const int64_t room = most - (12 << 10);
     q.stages = (int32_t)std::min<int64_t>(kSkinnyMaxStages, room / stage);
     const int64_t ring = std::max<int64_t>(q.stages * stage, std::min<int64_t>(d.tokens, 128) * q.sum_pitch * 4);
@@ -586,7 +597,8 @@ gemm_status_t lora_plan_create(lora_plan_t* out, const lora_desc_t* desc) {
             p->shrink_grid = dim3((unsigned)std::min<int64_t>(d.tokens, p->tile_rows), (unsigned)p->m_blocks, 1);
         } else {
             // Clusters split K, up to four ways while that fills the device four times over (8192 rows of 8192, rank 64: 44
-            // us, two ways 56), up to eight while it does so twice (beyond, starts outweigh it), and every CTA keeps four
+            // us, two ways 56; the mixed 4096 x 4096 x 4096 above as a whole: 241 so, up to 304 with the other splits tried),
+            // up to eight while it does so twice (beyond, starts outweigh it), and every CTA keeps four
             // chunks of K.  Then CTAs share out the slots; those of a block's first slots come first in the grid, as most
             // blocks of prompts have no others.
             const int64_t row_blocks = (d.tokens + kShrinkRows - 1) / kShrinkRows, chunks = (d.k + 63) / 64;

@@ -10,7 +10,7 @@
 // tile.  Against a split through global memory (partial tiles, flags, one
 // finisher) the join costs a few hundred nanoseconds instead of microseconds
 // and the adapter steps are shared out too (96 tokens x 4096 x 4096, 80
-// adapters: 17.6 us here, 31.6 in the persistent kernel; 4 tokens: 11.1 and
+// adapters: 17.5 us here, 31.6 in the persistent kernel; 4 tokens: 11.0 and
 // 21.5).  W comes by TMA: with asynchronous 16-byte copies by four warps the
 // 96 tokens took 2.4 us longer.
 //

@@ -11,15 +11,28 @@
 // 8-column side the query heads, so up to eight shared heads waste nothing; the
 // heads as the 16 rows would take twice the instructions a step.
 //
-// GB300: two sequences of 130,001 and 131,072 positions, 8 kv heads of 128 and
-// 64 query heads: 184 us for 1.07 GB, 5.8 TB/s, 86% of a plain copy's rate
-// (with the arithmetic left out 178: the loads, and SMs that do not finish
-// together, are the bound).  64 sequences of 0 to 8192 positions, 32 query
-// heads: 48.5 us for 253 MB, 5.2 TB/s; some 11 us of it are the start (list of
-// lengths, page numbers, the first rows) and the ends of segments.  E4M3 caches
-// are bound by the conversions' instructions until lengths are large: 33
-// windows of up to 2001 positions, 4 kv heads of 80: 19.1 us for 36 MB; two
-// sequences of 100,000, 8 kv heads of 128: 85 us for 410 MB.
+// GB300 (one device to the next 2% apart): two sequences of 130,001 and 131,072
+// positions, 8 kv heads of 128 and 64 query heads: 184 to 188 us for 1.07 GB,
+// 5.7 to 5.8 TB/s, 84 to 86% of a plain copy's rate (with the arithmetic left out
+// 178: the loads, and SMs that do not finish together, are the bound).  64
+// sequences of 0 to 8192 positions, 32 query heads: 49.5 to 50.7 us for 253 MB,
+// 5.0 to 5.1 TB/s; some 11 us of it are the start (list of lengths, page
+// numbers, the first rows) and the ends of segments, and moderate batches pay
+// the same: 4 sequences of 2000 13.5 us at a floor of 4.8, 16 of 100 to 4000
+// 21.9 at 10.9.  E4M3 caches: short rows are bound by the conversions'
+// instructions (33 windows of up to 2001 positions, 4 kv heads of 80: 19.1 us
+// for 36 MB; 64 sequences of 100 to 8192, 8 kv heads of 64: 36.7 at a floor of
+// 18.2, of 80: 50 to 57 at 23); long ones by their loads (two sequences of
+// 100,000, 8 kv heads of 128: 80 to 85 us for 410 MB, and 82 of 85 with the
+// arithmetic left out, 5.0 TB/s; the 16-bit cache of the same positions 140 us
+// for 820 MB, 5.9 TB/s).
+//
+// Nine to 16 query heads a kv head take two tiles of heads, in 217 to 255
+// registers: 16 sequences of 100 to 8192, 4 kv heads of 128 with 16 query heads
+// each, 40 us at a floor of 9.7.  Heads of 256 with two tiles spill (416 to 472
+// bytes stored a thread): 64 such sequences, 2 kv heads, 92 us at 36.5, where
+// one tile takes 55.  Head sizes from 136 to 248 run as 256, one CTA an SM: 8
+// kv heads of 192 133 us at 109, of 136 135 at 77.
 //
 // Work.  A segment is one (sequence, kv head, group of 8 or 16 query heads);
 // its positions are cut into tiles of four warps' steps.  All segments' tiles,
@@ -63,7 +76,7 @@ struct AttnShape {
     static constexpr int kHeads = 8 * NH;
     // CTAs an SM holds, and steps in the pipeline of a warp.  E4M3 rows of up to 80 bytes: a step's instructions (the
     // conversions), not its bytes, are the longer part, and more warps count for more than a deeper pipeline: 64 sequences
-    // of 100 to 8192 positions, 8 kv heads of 64, take 36.4 us so and 40.1 with two CTAs and three stages; longer rows
+    // of 100 to 8192 positions, 8 kv heads of 64, took 36.4 us so and 40.1 with two CTAs and three stages; longer rows
     // want the loads in flight (two sequences of 100,000, heads of 128: 92.4 so and 87.4).
     static constexpr bool kManyCtas = FP8 && NH == 1 && KD <= 5;
     static constexpr int kCtas = kManyCtas ? 3 : (KD <= 8 ? 2 : 1);

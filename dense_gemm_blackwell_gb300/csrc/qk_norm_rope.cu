@@ -9,8 +9,8 @@
 // group takes several rows of one kind (queries, keys or values) of one token
 // and prepares their common factors once, and fp32 arithmetic goes two values
 // to an instruction.  GB300, heads of 128, 32 of queries and 8 of keys: 16384
-// tokens forward with the cache append 70.3 us, 411 MB, 5.8 TB/s, 86% of a plain
-// copy's rate; 8192 tokens backward 52.0 us, 256 MB, 4.9 TB/s; 16 tokens forward
+// tokens forward with the cache append 69.9 us, 411 MB, 5.9 TB/s, 87% of a plain
+// copy's rate; 8192 tokens backward 51.7 us, 256 MB, 4.9 TB/s; 16 tokens forward
 // 3.0 us, which is a launch.
 //
 // With the pairs' rotation y_a' = y_a c - y_b s, y_b' = y_a s + y_b c and
@@ -39,7 +39,10 @@ constexpr int kMaxHeadDim = 256;
 enum RopePairs {
     kPairsHalves = 0,      // elements (i, i + rot/2), rot a multiple of 16: one other lane holds all eight partners
     kPairsNeighbours = 1,  // elements (2i, 2i + 1), rot a multiple of 8
-    kPairsAny = 2          // either layout, any even rot: through shared memory
+    // Either layout, any even rot: through shared memory.  Bound by its instructions, not by memory (spills of 96 bytes stored,
+    // 244 loaded a thread forward): 16384 tokens, 24 of 128 elements rotated as halves, 84.7 us, 20 as neighbours 97.4, where
+    // the whole head takes 69.9; 8192 tokens backward, 24 of 128, 71.2 and 51.7.
+    kPairsAny = 2
 };
 
 enum RowKind { kQueries = 0, kKeys = 1, kValues = 2 };

@@ -9,7 +9,8 @@ As in the rest of the package this is argument marshalling: shapes, types, strid
 work is enqueued by the CUDA library on torch's current stream (or the one given), and errors raise GemmError (from the
 library) or ValueError / TypeError (from these checks).  Outputs that are not given, and scratch memory, are allocated by
 torch for the stream that the work goes to.  A plan's launches share its workspace, so launches of one plan (and graphs
-that captured it) must follow one another.
+that captured it) must follow one another.  None of these calls enters torch's autograd graph: training calls
+qk_norm_rope_backward itself, from an autograd function of its own for instance.
 """
 from __future__ import annotations
 
@@ -231,11 +232,11 @@ def _torch_types():
 
 
 class LoraPlan(_Plan):
-    """Y = X W^T + scale_i (X A_i^T) B_i^T with i = adapter[token]; a negative i: the projection alone.  Of the current device.
+    """Y = X W^T + scale_i (X A_i^T) B_i^T with i = adapter[token]; a negative i: the projection alone.
 
-    X [tokens, k], W [n, k], A [adapters, rank, k], B [adapters, n, rank], Y [tokens, n]; X, W, A and B of one 16-bit
-    type.  Rows may be padded (ldx, ldw, ldy in elements, 0 = packed; A's and B's strides are taken from the tensors, which must not
-    be expanded).
+    X [tokens, k], W [n, k], A [adapters, rank, k], B [adapters, n, rank], Y [tokens, n]; X, W, A and B of one 16-bit type;
+    every run has exactly `tokens` tokens, on the device that was current when the plan was made.  Rows may be padded (ldx,
+    ldw, ldy in elements, 0 = packed; A's and B's strides are taken from the tensors, which must not be expanded).
     """
 
     _destroy = "lora_plan_destroy"
@@ -390,13 +391,15 @@ def rope_table(positions, rot_dim, *, base=10000.0, factor=1.0, scaling="linear"
                beta_slow=1.0, attention_factor=None, device="cuda"):
     """cos and sin of every position below `positions`: [positions, 2, rot_dim / 2] fp32, computed in fp64.
 
-    Pair i turns by position * f_i, f_i = base^(-2i / rot_dim).  `factor` > 1 stretches the table to longer contexts:
-      "linear"  positions are divided by the factor;
+    Pair i turns by position * f_i, f_i = base^(-2i / rot_dim) (Su et al., "RoFormer").  `factor` > 1 stretches the table to
+    longer contexts, by the published rules:
+      "linear"  positions are divided by the factor (Chen et al., position interpolation);
       "base"    the base becomes base * factor^(rot_dim / (rot_dim - 2)): the fastest pair keeps its frequency, the
-                slowest is divided by the factor;
+                slowest is divided by the factor (known as NTK-aware scaling);
       "blend"   pairs that turn at least beta_fast times within original_positions keep f_i, those that turn at most
                 beta_slow times get f_i / factor, and those between are blended linearly over the pair index; cos and
-                sin are multiplied by attention_factor (default 0.1 ln(factor) + 1), which scales q . k by its square.
+                sin are multiplied by attention_factor (default 0.1 ln(factor) + 1), which scales q . k by its square
+                (Peng et al., "YaRN", whose bounds and defaults these are).
     """
     import torch
     _need(rot_dim > 0 and rot_dim % 2 == 0 and positions > 0, "rot_dim must be even and positive, positions positive")

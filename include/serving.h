@@ -192,7 +192,12 @@ gemm_status_t paged_attn_plan_info(paged_attn_plan_t plan, paged_attn_plan_info_
  * to [0, table_width * page_size]); position j lies in page block_table[b][j / page_size].  K_j and V_j are the cache's
  * values times k_scale and v_scale.  lse[b, h] (NULL: not wanted) = log sum_j exp(scale q . K_j).  n = 0 gives zeros and
  * lse -inf.  Cache contents past n, or before the window, are not read into the result whatever they hold.  A page
- * number outside [0, num_pages) makes its positions count as masked. */
+ * number outside [0, num_pages) makes its positions count as masked; columns may name one page more than once.
+ * Scores, the softmax's statistics and all sums are fp32; out is rounded once.  The tensor core multiplies 16-bit
+ * operands, so the probabilities are rounded before their product with V: to bf16, or to f16 (2^15 times the
+ * probability) for f16 queries and for E4M3 caches, whose values are exact in f16.  bf16 queries over an E4M3 cache
+ * are scaled per head by a power of two to f16: elements under 2^-14 of the head's largest lose bits, at most 2^-24 of
+ * that largest each. */
 typedef struct {
     int32_t batch;
     int32_t table_width;        /* columns of the block table */
