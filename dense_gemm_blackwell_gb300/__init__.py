@@ -454,3 +454,5 @@ def matmul(a, b, *, out=None, out_dtype=None, scale_a=None, scale_b=None, flags=
 
 from .serving import (LoraPlan, PagedAttentionPlan, lora_matmul, qk_norm_rope, qk_norm_rope_backward,  # noqa: E402
                       rope_table, serving_header_functions)
+from .feedforward import (GatedPlan, add_rms_norm, add_rms_norm_backward, feedforward_header_functions, int4_matmul,  # noqa: E402
+                          int4_quantize)

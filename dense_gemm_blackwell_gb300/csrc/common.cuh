@@ -164,6 +164,17 @@ struct LoraTail {
     int32_t k, rank;
     int32_t bf16;             // inputs bf16, otherwise f16
 };
+// A gated pair of projections (gated.cu): the product's tiles hold gates and ups side by side, and the epilogue writes
+// act(gate) * up.
+struct GatedTail {
+    CUtensorMap tmap_gate;    // what the backward pass keeps: (features, M) of both sums, box (64, 32)
+    CUtensorMap tmap_up;
+    int32_t features;         // columns of the output
+    int32_t act;              // gated_activation_t
+    int32_t keep;             // 1: write both sums too
+    int32_t reserved0;
+};
+
 constexpr uint32_t kTailRowBytes = 32;           // one row of one step's B
 constexpr uint32_t kTailAtomBytes = 128 * 128;   // four steps of T: 128 rows of one 128-byte atom
 

@@ -21,6 +21,11 @@ cudaError_t launch_persistent(const PersistentParams& p, int cta_group, int dtyp
 cudaError_t launch_adapters(const PersistentParams& p, const LoraTail& tail, int cta_group, int dtype_d, int grid,
                             size_t smem_bytes, cudaStream_t stream);
 
+// The persistent kernel for a gated pair of projections (GatedTail): p.N counts gates and ups, tmap_b has boxes of
+// min(tile_n, 256) / 2 rows, tmap_d is the output's.
+cudaError_t launch_gated(const PersistentParams& p, const GatedTail& q, int cta_group, int dtype, int grid, size_t smem_bytes,
+                         cudaStream_t stream);
+
 // The launch parameters of a plan's product on these operands (gemm_api.cu).
 gemm_status_t product_params(gemm_plan_t plan, const void* A, const void* B, void* D, PersistentParams* out);
 

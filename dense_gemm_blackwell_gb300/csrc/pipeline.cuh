@@ -17,6 +17,9 @@
 
 namespace dgb {
 
+constexpr uint32_t kStagingBytes = 32 * 128;  // one warp's output chunk: 32 rows x 128 B
+constexpr int kEpilogueWarps = 8;             // two per TMEM lane quarter, one half of the chunks each
+
 // Float4 index, inside one (slot, rank) partial, of 16-byte piece j (0..7) of
 // thread `lane` of epilogue warp wq for 32-column chunk c32: a warp's pieces
 // j are 512 contiguous bytes, so partial stores and loads are coalesced.
@@ -156,10 +159,14 @@ constexpr uint32_t kPartA = 1u, kPartB0 = 2u, kPartB1 = 4u, kPartsAll = 7u;
 // right-half repeats), the tile's adapter steps (LoraTail), 4 * ATOMS of them to
 // a stage: T as one 128-byte K atom per four steps, like A; step j's rows of B
 // at j times their size of the B area (of each half's share of it).
-template <int CG, int ATOMS = 1, int HALVES = 1, uint32_t PARTS = kPartsAll, bool kSerpentine = false, bool kTail = false>
+// kGated: B is W = [gates; ups] of `features` rows each (gated.cu), and a tile is tile_n / 2 columns of the output: its B rows
+// are, in every half of a 512-wide tile by itself, those columns' gates and then their ups.  In an SM pair the even CTA loads
+// the gates and the odd one the ups; a lone CTA takes both.
+template <int CG, int ATOMS = 1, int HALVES = 1, uint32_t PARTS = kPartsAll, bool kSerpentine = false, bool kTail = false,
+          bool kGated = false>
 __device__ void producer_loop(const PersistentParams& p, uint8_t* ring, uint32_t stage_bytes, int tile_k,
                               uint32_t full0, uint32_t empty0, volatile uint32_t* abort_flag, uint32_t rank,
-                              int cluster_id, int num_clusters, const LoraTail* tail = nullptr) {
+                              int cluster_id, int num_clusters, const LoraTail* tail = nullptr, int features = 0) {
     constexpr uint32_t parts = PARTS;
     const int S = p.stages;
     const bool leader = rank == 0;
@@ -270,7 +277,20 @@ __device__ void producer_loop(const PersistentParams& p, uint8_t* ring, uint32_t
                     if constexpr ((parts & kPartA) != 0)
                         load_operand<CG, ATOMS>(sa, &p.tmap_a, fb, p.mn_major_a != 0, 128, a_row, kx, b,
                                                 p.batched != 0, keep_a, pol_a, atom_k, 0, mn_elems, mn_box_bytes);
-                    if constexpr (HALVES == 1) {
+                    if constexpr (kGated) {
+                        const int rows = p.tile_n / (2 * HALVES);       // of one kind and half
+#pragma unroll
+                        for (int h = 0; h < HALVES; ++h) {
+                            if ((parts & (kPartB0 << h)) == 0 || (halves & (1 << h)) == 0) continue;
+#pragma unroll
+                            for (int q = 0; q < (CG == 1 ? 2 : 1); ++q) {
+                                const int kind = CG == 1 ? q : (int)rank;
+                                load_operand<CG, ATOMS>(sb + (uint32_t)((h * (b_rows / HALVES) + q * rows) * 128), &p.tmap_b, fb, false, rows,
+                                                        kind * features + (nb * HALVES + h) * rows, kx, b, false, false, pol_a, atom_k,
+                                                        (uint32_t)b_rows * 128u);
+                            }
+                        }
+                    } else if constexpr (HALVES == 1) {
                         if constexpr ((parts & kPartB0) != 0)
                             load_operand<CG, ATOMS>(sb, &p.tmap_b, fb, p.mn_major_b != 0, b_rows, b_row, kx, b,
                                                     p.batched != 0, false, pol_a, atom_k, 0, mn_elems, mn_box_bytes);
