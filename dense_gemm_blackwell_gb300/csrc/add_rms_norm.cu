@@ -2,11 +2,13 @@
 // (include/feedforward.h), in 16 bits or as E4M3 codes with the scales that the
 // block-scaled products read, and the backward pass.
 //
-// A row is held in registers by the threads that share it, eight elements (one
-// 16-byte load) a vector: it is read once, its sum of squares is reduced by
-// shuffles and one exchange through shared memory, and it is written once.  A
-// scale block of 128 (32) columns is 16 (4) neighbouring lanes, so its largest
-// magnitude needs shuffles only.  Bound by memory.
+// A row is shared by up to 32 warps, eight elements (16 bytes) a vector, a few
+// vectors a thread.  Bound by memory: a block takes row after row, and every
+// thread keeps its vectors of the next rows on the way by asynchronous copies into
+// places of shared memory that it alone reads, so that no barrier waits for them; a
+// row's sums take shuffles and one exchange.  A scale block of 128 (32) columns is
+// 16 (4) neighbouring lanes, so its largest magnitude needs shuffles only.  Few
+// rows take one vector a thread (the time is latency), many rows more.
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
@@ -23,22 +25,23 @@ namespace dgb {
 constexpr int kNormMaxHidden = 32768;
 constexpr float kE4M3Max = 448.f;
 
-// Vector v of a row of n elements, those past its end as zeros.
-__device__ __forceinline__ uint4 load_vector(const void* row, int v, int n) {
+// Vector v of the weights, zeros past the row's end.
+__device__ __forceinline__ uint4 load_weights(const void* weight, int v, int n) {
     const int left = n - 8 * v;
-    if (left >= 8) return __ldcs(static_cast<const uint4*>(row) + v);
+    if (left >= 8) return __ldg(static_cast<const uint4*>(weight) + v);
+    if (left <= 0) return make_uint4(0u, 0u, 0u, 0u);
     uint32_t w[4] = {0u, 0u, 0u, 0u};
-    const uint16_t* e = static_cast<const uint16_t*>(row) + 8 * v;
+    const uint16_t* e = static_cast<const uint16_t*>(weight) + 8 * v;
 #pragma unroll
     for (int i = 0; i < 7; ++i)
         if (i < left) w[i >> 1] |= (uint32_t)e[i] << (16 * (i & 1));
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Vector v of the weights, which every row reads again.
-__device__ __forceinline__ uint4 load_weights(const void* weight, int v, int n) {
-    if (n - 8 * v >= 8) return __ldg(static_cast<const uint4*>(weight) + v);
-    return load_vector(weight, v, n);
+// Vector v of a row of n elements to shared memory, zeros past its end (which are not read).
+__device__ __forceinline__ void fetch_vector(uint32_t dst, const uint16_t* row, int v, int n) {
+    const int bytes = min(16, 2 * (n - 8 * v));
+    cp_async_16_zfill(dst, row + (bytes > 0 ? 8 * v : 0), (uint32_t)max(0, bytes));
 }
 
 __device__ __forceinline__ void store_vector(void* row, int v, int n, const uint4& q) {
@@ -73,18 +76,6 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// The sum of `v` over a row's `warps` warps, the same in each of its threads.  `part` [rows][warps] of the block, not in use by
-// an earlier call that threads may still read.  Every thread of the block calls it.
-__device__ __forceinline__ float row_sum(float v, int warps, float* part, int row, int warp) {
-    v = warp_sum(v);
-    if (warps == 1) return v;
-    if ((threadIdx.x & 31) == 0) part[row * warps + warp] = v;
-    __syncthreads();
-    float s = 0.f;
-    for (int i = 0; i < warps; ++i) s += part[row * warps + i];
-    return s;
-}
-
 // Exponent byte of the least power of two s >= 2^-126 with top <= 448 s (448 = 1.75 * 2^8); top is not negative.
 __device__ __forceinline__ uint32_t e8m0_of(float top) {
     const uint32_t bits = __float_as_uint(top);
@@ -92,132 +83,177 @@ __device__ __forceinline__ uint32_t e8m0_of(float top) {
     return (uint32_t)max(1, min(e, 254));
 }
 
+// The word of the scales' tiles that holds the four blocks of vectors v .. v + 15 of a row.
+__device__ __forceinline__ uint32_t* scale_word(const add_rms_norm_args_t& a, int row, int v) {
+    const int64_t tile = (int64_t)(row / 128) * ((a.hidden + 127) / 128) + v / 16;
+    return reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.scales) + tile * 512) + (row % 32) * 4 + row / 32 % 4;
+}
+
 struct NormParams {
     add_rms_norm_args_t a;
     int32_t warps;          // of a row
-    int32_t rows;           // of a block
+    int32_t rows;           // of a block at a time
     int32_t all_rows;       // tokens, or for tiled scales the tiles' rows
     float over_hidden;      // 1 / hidden
 };
 
 constexpr int kOutSame = 0, kOutBlock128 = 1, kOutMx = 2;
 
-template <typename T, int OUT, int VPT>
+// Rows of a thread on the way or in use: two, but for rows past 16384 elements one, as two of theirs may not fit.  (Three and four
+// are no faster: 8192 x 8192 with a residual to codes 79 and 93 us where two take 79.)
+template <int VPT>
+__host__ __device__ constexpr int norm_stages() { return VPT == 4 ? 1 : 2; }
+
+// Instructions count beside the bytes, so the loops over a thread's vectors have no branches: vectors past the row are zeros, and
+// only their stores are left out.  n weight = (h weight) r: the product that does not wait for r, and the largest magnitude of a
+// scale block, come before the exchange.
+template <typename T, int OUT, int VPT, bool RES>
 __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const __grid_constant__ NormParams p) {
-    __shared__ float part[32];
+    constexpr int S = norm_stages<VPT>(), kKinds = RES ? 2 : 1;
+    __shared__ float part[2][32];
+    extern __shared__ uint4 ring[];         // [S][x, residual][VPT][threads]
     griddep_wait();
     griddep_launch_dependents();
     const add_rms_norm_args_t& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = warp / p.warps, rw = warp - sub * p.warps;
-    const int n = a.hidden, row = blockIdx.x * p.rows + sub;
+    const int n = a.hidden;
     const int first = rw * 32 + lane, step = p.warps * 32;     // this thread's vectors: first, first + step, ...
-    const bool live = row < a.tokens;
-    uint4 h[VPT], weight[VPT];      // the row as it is kept, 16 bits an element
-    float squares = 0.f;
-    if (live) {
-        const uint16_t* x = static_cast<const uint16_t*>(a.x) + (int64_t)row * a.ldx;
-        const uint16_t* res = static_cast<const uint16_t*>(a.residual) + (a.residual ? (int64_t)row * a.ld_residual : 0);
-        uint16_t* sum = static_cast<uint16_t*>(a.sum) + (a.sum ? (int64_t)row * a.ld_sum : 0);
-        uint4 qr[VPT];
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int v = first + j * step;
-            if (8 * v >= n) break;
-            h[j] = load_vector(x, v, n);
-            if (a.residual) qr[j] = load_vector(res, v, n);
-        }
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int v = first + j * step;
-            if (8 * v >= n) break;
-            if (a.weight) weight[j] = load_weights(a.weight, v, n);
-        }
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int v = first + j * step;
-            if (8 * v >= n) break;
-            float f[8];
-            unpack8<T>(h[j], f);
-            if (a.residual) {
-                float r[8];
-                unpack8<T>(qr[j], r);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] += r[i];
-                // the sum is rounded once, and the norm is that of the rounded sum, which is what the backward pass and the
-                // next layer have
-                h[j] = round8<T>(f);
-                unpack8<T>(h[j], f);
-            }
-            if (a.sum) store_vector(sum, v, n, h[j]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) squares = fmaf(f[i], f[i], squares);
-        }
-    }
-    const float r = rsqrtf(row_sum(squares, p.warps, part, sub, rw) * p.over_hidden + a.eps);
-    if (OUT != kOutMx && !live) return;
-    if (row >= p.all_rows) return;
+    const int stride = gridDim.x * p.rows, threads = blockDim.x;
+    int bytes[VPT];
+    Pair weight[VPT][4];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int v = first + j * step;
-        if (8 * (v - lane) >= n) break;            // whole warps: the lanes' largest magnitudes are exchanged
-        const bool in = live && 8 * v < n;
-        float y[8];
-        if (in) {
-            unpack8<T>(h[j], y);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] *= r;
-            if (a.weight) {
-                float w[8];
-                unpack8<T>(weight[j], w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] *= w[i];
-            }
+        bytes[j] = max(0, min(16, 2 * (n - 8 * v)));
+        if (a.weight) {
+            unpack8<T>(load_weights(a.weight, v, n), weight[j]);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = 0.f;
+            for (int i = 0; i < 4; ++i) weight[j][i] = pair_of(1.f);
         }
-        if constexpr (OUT == kOutSame) {
-            if (in) store_vector(static_cast<uint16_t*>(a.y) + (int64_t)row * a.ldy, v, n, round8<T>(y));
-        } else {
-            float top = 0.f;
+    }
+    auto fetch = [&](int row, int s) {
+        if (row < a.tokens) {
+            const uint16_t* x = static_cast<const uint16_t*>(a.x) + (int64_t)row * a.ldx;
+            const uint16_t* res = RES ? static_cast<const uint16_t*>(a.residual) + (int64_t)row * a.ld_residual : nullptr;
+            const uint32_t dst = smem_u32(ring + s * (kKinds * VPT) * threads + threadIdx.x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(y[i]));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            for (int j = 0; j < VPT; ++j) {
+                const int at = bytes[j] > 0 ? 8 * (first + j * step) : 0;
+                cp_async_16_zfill(dst + j * threads * 16, x + at, (uint32_t)bytes[j]);
+                if constexpr (RES) cp_async_16_zfill(dst + (VPT + j) * threads * 16, res + at, (uint32_t)bytes[j]);
+            }
+        }
+        cp_async_commit();
+    };
+    int row0 = blockIdx.x * p.rows;
+#pragma unroll
+    for (int s = 0; s < S; ++s) fetch(row0 + sub + s * stride, s);
+    int slot = 0;
+    for (int turn = 0; row0 < p.all_rows; row0 += stride, turn ^= 1) {      // the same turns in the whole block
+        const int row = row0 + sub;
+        const bool live = row < a.tokens;
+        Pair y[VPT][4];             // h, then h weight
+        float top[VPT];
+        Pair squares = pair_of(0.f);
+        cp_async_wait<S - 1>();
+        const uint4* mine = ring + slot * (kKinds * VPT) * threads + threadIdx.x;
+        uint16_t* sum = static_cast<uint16_t*>(a.sum) + (int64_t)row * a.ld_sum;
+        if (live) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int v = first + j * step;
+                uint4 q = mine[j * threads];
+                unpack8<T>(q, y[j]);
+                if constexpr (RES) {
+                    Pair r[4];
+                    unpack8<T>(mine[(VPT + j) * threads], r);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[j][i] = y[j][i] + r[i];
+                    // the sum is rounded once, and the norm is that of the rounded sum, which is what the backward pass and
+                    // the next layer have
+                    q = round8<T>(y[j]);
+                    unpack8<T>(q, y[j]);
+                }
+                if (a.sum && bytes[j] > 0) store_vector(sum, v, n, q);
+                top[j] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    squares = fma2(y[j][i], y[j][i], squares);
+                    y[j][i] = y[j][i] * weight[j][i];
+                    if constexpr (OUT != kOutSame) top[j] = fmaxf(top[j], fmaxf(fabsf(halves(y[j][i]).x), fabsf(halves(y[j][i]).y)));
+                }
+                if constexpr (OUT != kOutSame) {
+#pragma unroll
+                    for (int o = 1; o < (OUT == kOutMx ? 4 : 16); o *= 2) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+                }
+            }
+        }
+        float total = warp_sum(halves(squares).x + halves(squares).y);
+        if (p.warps > 1) {
+            // two turns' places: a warp may be a turn ahead of those that still read
+            if (lane == 0) part[turn][warp] = total;
+            __syncthreads();
+            total = 0.f;
+            for (int i = 0; i < p.warps; ++i) total += part[turn][sub * p.warps + i];
+        }
+        fetch(row + S * stride, slot);
+        if (++slot == S) slot = 0;
+        if (!live) {
+            if (OUT == kOutMx && row < p.all_rows) {
+                // the tiles' rows past the matrix: scales of 0
+#pragma unroll
+                for (int j = 0; j < VPT; ++j)
+                    if ((lane & 15) == 0 && bytes[j] > 0) *scale_word(a, row, first + j * step) = 0u;
+            }
+            continue;
+        }
+        const float r = rsqrtf(total * p.over_hidden + a.eps);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int v = first + j * step;
+            const bool in = bytes[j] > 0;
             float inverse;
             if constexpr (OUT == kOutBlock128) {
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                const float s = fmaxf(top / kE4M3Max, 0x1p-100f);
-                inverse = 1.f / s;
+                const float s = fmaxf(top[j] * r * (1.f / kE4M3Max), 0x1p-100f);
+                inverse = __fdividef(1.f, s);
                 if (in && (lane & 15) == 0) static_cast<float*>(a.scales)[(int64_t)row * a.ld_scales + v / 16] = s;
-            } else {
-                const uint32_t e = e8m0_of(top);
-                inverse = __uint_as_float((254u - e) << 23);        // 2^(127 - e); 0 for e = 254, which finite rows do not reach
+            }
+            if constexpr (OUT == kOutMx) {
+                const uint32_t e = e8m0_of(top[j] * r);
+                inverse = __uint_as_float((254u - e) << 23);            // 2^(127 - e); 0 for e = 254, which finite rows do not reach
                 // four blocks are one 32-bit word of a tile; blocks past the matrix are 0
                 uint32_t word = in ? e : 0u;
                 word |= __shfl_down_sync(0xffffffffu, word, 4) << 8;
                 word |= __shfl_down_sync(0xffffffffu, word, 8) << 16;
-                if ((lane & 15) == 0 && 8 * v < n) {
-                    const int64_t tile = (int64_t)(row / 128) * ((n + 127) / 128) + v / 16;
-                    reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.scales) + tile * 512)[(row % 32) * 4 + row / 32 % 4] = word;
-                }
+                if (in && (lane & 15) == 0) *scale_word(a, row, v) = word;
             }
-            if (in) {
-                // the scale's reciprocal and its product with y are rounded in fp32: next to the code's 4 bits nothing
-                const uint2 q = make_uint2(e4m3x4(y[0] * inverse, y[1] * inverse, y[2] * inverse, y[3] * inverse),
-                                           e4m3x4(y[4] * inverse, y[5] * inverse, y[6] * inverse, y[7] * inverse));
-                store_codes(static_cast<uint8_t*>(a.y) + (int64_t)row * a.ldy, v, n, q);
+            const Pair both = pair_of(r);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[j][i] = y[j][i] * both;
+            if (!in) continue;
+            if constexpr (OUT == kOutSame) {
+                store_vector(static_cast<uint16_t*>(a.y) + (int64_t)row * a.ldy, v, n, round8<T>(y[j]));
+            } else {
+                // the scale's reciprocal and its products are rounded in fp32: next to the code's 4 bits nothing
+                const Pair scale = pair_of(inverse);
+                float2 c[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) c[i] = halves(y[j][i] * scale);
+                store_codes(static_cast<uint8_t*>(a.y) + (int64_t)row * a.ldy, v, n,
+                            make_uint2(e4m3x4(c[0].x, c[0].y, c[1].x, c[1].y), e4m3x4(c[2].x, c[2].y, c[3].x, c[3].y)));
             }
         }
     }
+    cp_async_wait<0>();
 }
 
 // ------------------------------------------------------------------ backward
 
+constexpr int kNormGradStages = 2;
 constexpr int kNormGradBlocks = 608;       // partial weight gradients in the workspace, one a block
-constexpr int kNormJoinColumns = 32, kNormJoinRows = 16;
+constexpr int kNormJoinThreads = 512, kNormJoinColumns = 32, kNormJoinRows = kNormJoinThreads / (kNormJoinColumns / 4);
 
 struct NormGradParams {
     add_rms_norm_grads_t a;
@@ -227,13 +263,11 @@ struct NormGradParams {
 };
 
 // dh = d_sum + r dy w - h r^3 mean(dy w h): one exchange for both sums of a row.  A thread keeps the same columns in every row
-// that its block takes and sums their weight gradients, in registers, or for wide rows (SHARED: registers hold the row) in
-// shared memory, each thread its own words.
-template <typename T, int VPT, bool SHARED>
-__global__ void __launch_bounds__(SHARED ? 1024 : 512, SHARED ? 1 : 2)
-add_rms_norm_backward_kernel(const __grid_constant__ NormGradParams p) {
-    __shared__ float2 part[2][32];
-    extern __shared__ float4 sums_smem[];       // [rows of the block][padded hidden], fp32
+// that its block takes and sums their weight gradients in registers.
+template <typename T, int VPT, int S>
+__global__ void __launch_bounds__(512) add_rms_norm_backward_kernel(const __grid_constant__ NormGradParams p) {
+    __shared__ float2 part[2][16];
+    extern __shared__ uint4 ring[];         // [S][h, dy, d_sum][VPT][threads]; at the end the rows' weight gradients
     griddep_wait();
     griddep_launch_dependents();
     const add_rms_norm_grads_t& a = p.a;
@@ -241,60 +275,56 @@ add_rms_norm_backward_kernel(const __grid_constant__ NormGradParams p) {
     const int sub = warp / p.warps, rw = warp - sub * p.warps;
     const int n = a.hidden, pitch = (n + 7) & ~7;
     const int first = rw * 32 + lane, step = p.warps * 32;
-    float4* mine = sums_smem + sub * (pitch / 4);
-    float dw[SHARED ? 1 : VPT][8];
+    const int kinds = a.d_sum ? 3 : 2, stride = gridDim.x * p.rows;
+    auto place = [&](int s, int kind, int j) { return ring + ((s * kinds + kind) * VPT + j) * blockDim.x + threadIdx.x; };
+    auto fetch = [&](int row, int s) {
+        if (row < a.tokens) {
+            const uint16_t* h = static_cast<const uint16_t*>(a.h) + (int64_t)row * a.ld_h;
+            const uint16_t* g = static_cast<const uint16_t*>(a.dy) + (int64_t)row * a.ld_dy;
+            const uint16_t* d = static_cast<const uint16_t*>(a.d_sum) + (a.d_sum ? (int64_t)row * a.ld_d_sum : 0);
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int v = first + j * step;
+                fetch_vector(smem_u32(place(s, 0, j)), h, v, n);
+                fetch_vector(smem_u32(place(s, 1, j)), g, v, n);
+                if (a.d_sum) fetch_vector(smem_u32(place(s, 2, j)), d, v, n);
+            }
+        }
+        cp_async_commit();
+    };
+    int row0 = blockIdx.x * p.rows;
+#pragma unroll
+    for (int s = 0; s < S; ++s) fetch(row0 + sub + s * stride, s);
+    uint4 weight[VPT];
+    Pair dw[VPT][4];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int v = first + j * step;
-        if constexpr (SHARED) {
-            if (p.partials && 8 * v < n) mine[2 * v] = mine[2 * v + 1] = make_float4(0.f, 0.f, 0.f, 0.f);
-        } else {
+        if (a.weight) weight[j] = load_weights(a.weight, v, n);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
-        }
+        for (int i = 0; i < 4; ++i) dw[j][i] = pair_of(0.f);
     }
-    const int stride = gridDim.x * p.rows;
-    int turn = 0;
-    for (int row0 = blockIdx.x * p.rows; row0 < a.tokens; row0 += stride, turn ^= 1) {       // the same turns in the whole block
+    int slot = 0, turn = 0;
+    for (; row0 < a.tokens; row0 += stride, turn ^= 1) {       // the same turns in the whole block
         const int row = row0 + sub;
         const bool live = row < a.tokens;
-        uint4 qh[VPT], qg[VPT], qs[SHARED ? 1 : VPT];
-        const uint16_t* ds = static_cast<const uint16_t*>(a.d_sum) + (a.d_sum && live ? (int64_t)row * a.ld_d_sum : 0);
-        float2 sums = make_float2(0.f, 0.f);
+        Pair hh = pair_of(0.f), gh = pair_of(0.f);
+        cp_async_wait<S - 1>();
         if (live) {
-            const uint16_t* h = static_cast<const uint16_t*>(a.h) + (int64_t)row * a.ld_h;
-            const uint16_t* g = static_cast<const uint16_t*>(a.dy) + (int64_t)row * a.ld_dy;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const int v = first + j * step;
-                if (8 * v >= n) break;
-                qh[j] = load_vector(h, v, n);
-                qg[j] = load_vector(g, v, n);
-                if constexpr (!SHARED)
-                    if (a.d_sum) qs[j] = load_vector(ds, v, n);
-            }
+                Pair h[4], g[4], w[4];
+                unpack8<T>(*place(slot, 0, j), h);
+                unpack8<T>(*place(slot, 1, j), g);
+                if (a.weight) unpack8<T>(weight[j], w);
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                const int v = first + j * step;
-                if (8 * v >= n) break;
-                float x[8], g8[8];
-                unpack8<T>(qh[j], x);
-                unpack8<T>(qg[j], g8);
-                if (a.weight) {
-                    float w[8];
-                    unpack8<T>(load_weights(a.weight, v, n), w);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) g8[i] *= w[i];
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    sums.x = fmaf(x[i], x[i], sums.x);
-                    sums.y = fmaf(g8[i], x[i], sums.y);
+                for (int i = 0; i < 4; ++i) {
+                    hh = fma2(h[i], h[i], hh);
+                    gh = fma2(a.weight ? g[i] * w[i] : g[i], h[i], gh);
                 }
             }
         }
-        sums.x = warp_sum(sums.x);
-        sums.y = warp_sum(sums.y);
+        float2 sums = make_float2(warp_sum(halves(hh).x + halves(hh).y), warp_sum(halves(gh).x + halves(gh).y));
         if (p.warps > 1) {
             // two turns' places: a warp may be a turn ahead of those that still read
             if (lane == 0) part[turn][warp] = sums;
@@ -306,74 +336,52 @@ add_rms_norm_backward_kernel(const __grid_constant__ NormGradParams p) {
                 sums.y += o.y;
             }
         }
-        if (!live) continue;
-        const float r = rsqrtf(sums.x * p.over_hidden + a.eps);
-        const float c = r * r * r * (sums.y * p.over_hidden);
-        uint16_t* dh = static_cast<uint16_t*>(a.dh) + (int64_t)row * a.ld_dh;
+        if (live) {
+            const float r = rsqrtf(sums.x * p.over_hidden + a.eps);
+            const Pair both = pair_of(r), c = pair_of(-r * r * r * (sums.y * p.over_hidden));
+            uint16_t* dh = static_cast<uint16_t*>(a.dh) + (int64_t)row * a.ld_dh;
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int v = first + j * step;
-            if (8 * v >= n) break;
-            float x[8], g8[8], o[8];
-            unpack8<T>(qh[j], x);
-            unpack8<T>(qg[j], g8);
+            for (int j = 0; j < VPT; ++j) {
+                const int v = first + j * step;
+                Pair h[4], g[4], w[4];
+                unpack8<T>(*place(slot, 0, j), h);
+                unpack8<T>(*place(slot, 1, j), g);
+                if (a.weight) unpack8<T>(weight[j], w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) g8[i] *= r;
-            if constexpr (SHARED) {
-                if (p.partials) {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        float4 t = mine[2 * v + q];
-                        t.x = fmaf(g8[4 * q], x[4 * q], t.x);
-                        t.y = fmaf(g8[4 * q + 1], x[4 * q + 1], t.y);
-                        t.z = fmaf(g8[4 * q + 2], x[4 * q + 2], t.z);
-                        t.w = fmaf(g8[4 * q + 3], x[4 * q + 3], t.w);
-                        mine[2 * v + q] = t;
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    g[i] = g[i] * both;
+                    dw[j][i] = fma2(g[i], h[i], dw[j][i]);
+                    if (a.weight) g[i] = g[i] * w[i];
+                    g[i] = fma2(c, h[i], g[i]);
                 }
-            } else {
+                if (a.d_sum) {
+                    Pair d[4];
+                    unpack8<T>(*place(slot, 2, j), d);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) dw[j][i] = fmaf(g8[i], x[i], dw[j][i]);
+                    for (int i = 0; i < 4; ++i) g[i] = g[i] + d[i];
+                }
+                if (8 * v < n) store_vector(dh, v, n, round8<T>(g));
             }
-            if (a.weight) {
-                float w[8];
-                unpack8<T>(load_weights(a.weight, v, n), w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) g8[i] *= w[i];
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = fmaf(-c, x[i], g8[i]);
-            if (a.d_sum) {
-                float d[8];
-                if constexpr (SHARED) unpack8<T>(load_vector(ds, v, n), d);
-                else unpack8<T>(qs[j], d);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] += d[i];
-            }
-            store_vector(dh, v, n, round8<T>(o));
         }
+        fetch(row + S * stride, slot);
+        if (++slot == S) slot = 0;
     }
+    cp_async_wait<0>();
     if (p.partials == nullptr) return;
     float* to = p.partials + (int64_t)blockIdx.x * pitch;
+    float* all = reinterpret_cast<float*>(ring);
+    if (p.rows > 1) __syncthreads();        // the ring is free
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int v = first + j * step;
         if (8 * v >= n) break;
-        float4 lo, hi;
-        if constexpr (SHARED) {
-            lo = mine[2 * v];
-            hi = mine[2 * v + 1];
-        } else {
-            lo = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
-            hi = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
-        }
-        float4* q = p.rows > 1 ? mine : reinterpret_cast<float4*>(to);
-        q[2 * v] = lo;
-        q[2 * v + 1] = hi;
+        float4* q = reinterpret_cast<float4*>(p.rows > 1 ? all + sub * pitch : to) + 2 * v;
+        const float2 b0 = halves(dw[j][0]), b1 = halves(dw[j][1]), b2 = halves(dw[j][2]), b3 = halves(dw[j][3]);
+        q[0] = make_float4(b0.x, b0.y, b1.x, b1.y);
+        q[1] = make_float4(b2.x, b2.y, b3.x, b3.y);
     }
     if (p.rows > 1) {
         __syncthreads();
-        const float* all = reinterpret_cast<const float*>(sums_smem);
         for (int i = threadIdx.x; i < pitch; i += blockDim.x) {
             float s = 0.f;
             for (int q = 0; q < p.rows; ++q) s += all[q * pitch + i];
@@ -383,24 +391,33 @@ add_rms_norm_backward_kernel(const __grid_constant__ NormGradParams p) {
 }
 
 // The blocks' partial weight gradients, added in an order that depends on their number alone.
-__global__ void __launch_bounds__(kNormJoinColumns* kNormJoinRows) add_rms_norm_join_kernel(const float* partials, int blocks, int n,
-                                                                                            float* d_weight) {
-    __shared__ float part[kNormJoinRows][kNormJoinColumns + 1];
+__global__ void __launch_bounds__(kNormJoinThreads) add_rms_norm_join_kernel(const float* partials, int blocks, int n, float* d_weight) {
+    __shared__ float4 part[kNormJoinRows][kNormJoinColumns / 4];
     griddep_wait();
     griddep_launch_dependents();
-    const int lane = threadIdx.x % kNormJoinColumns, slice = threadIdx.x / kNormJoinColumns;
-    const int i = blockIdx.x * kNormJoinColumns + lane, pitch = (n + 7) & ~7;
-    float s = 0.f;
-    if (i < n)
-        for (int b = slice; b < blocks; b += kNormJoinRows) s += partials[(int64_t)b * pitch + i];
+    constexpr int kLanes = kNormJoinColumns / 4;
+    const int lane = threadIdx.x % kLanes, slice = threadIdx.x / kLanes;
+    const int i = blockIdx.x * kNormJoinColumns + 4 * lane, pitch = (n + 7) & ~7;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float4& o) { s = make_float4(s.x + o.x, s.y + o.y, s.z + o.z, s.w + o.w); };
+    if (i < pitch) {
+#pragma unroll 4
+        for (int b = slice; b < blocks; b += kNormJoinRows) add(__ldcg(reinterpret_cast<const float4*>(partials + (int64_t)b * pitch + i)));
+    }
     part[slice][lane] = s;
     __syncthreads();
-    if (slice == 0 && i < n) {
-        s = 0.f;
-#pragma unroll
-        for (int q = 0; q < kNormJoinRows; ++q) s += part[q][lane];
-        d_weight[i] = s;
+    for (int half = kNormJoinRows / 2; half > 0; half /= 2) {
+        if (slice < half) {
+            add(part[slice + half][lane]);
+            part[slice][lane] = s;
+        }
+        __syncthreads();
     }
+    if (slice != 0) return;
+    const float f[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (i + q < n) d_weight[i + q] = f[q];
 }
 
 // ------------------------------------------------------------------ host
@@ -413,35 +430,74 @@ static bool settle(int64_t& ld, int64_t least) {
     return ld >= least;
 }
 
-template <typename T, int OUT>
-static cudaError_t launch_norm(const NormParams& p, int vpt, unsigned blocks, unsigned threads, cudaStream_t stream) {
-    switch (vpt) {
-    case 1: return launch_dependent(add_rms_norm_kernel<T, OUT, 1>, dim3(blocks), dim3(threads), 0, stream, p);
-    case 2: return launch_dependent(add_rms_norm_kernel<T, OUT, 2>, dim3(blocks), dim3(threads), 0, stream, p);
-    default: return launch_dependent(add_rms_norm_kernel<T, OUT, 4>, dim3(blocks), dim3(threads), 0, stream, p);
-    }
+// How rows are laid on threads and blocks.
+struct NormShape {
+    int vpt, warps, rows, stages;
+    unsigned threads;
+    size_t smem;
+    int per_sm;             // blocks that an SM holds
+};
+
+constexpr size_t kNormSmem = 224 * 1024;
+
+// `resident`: threads that an SM holds by their registers.
+static NormShape norm_shape(int vectors, int vpt, int kinds, int stages, unsigned resident) {
+    NormShape s;
+    s.vpt = vpt;
+    s.warps = (vectors + 32 * vpt - 1) / (32 * vpt);
+    s.rows = std::max(1, 4 / s.warps);
+    s.threads = (unsigned)(s.rows * s.warps * 32);
+    const size_t row = (size_t)s.threads * vpt * kinds * 16;
+    s.stages = stages * row <= kNormSmem ? stages : 1;
+    s.smem = s.stages * row;
+    s.per_sm = (int)std::max<size_t>(1, std::min<size_t>(kNormSmem / (s.smem + 1280), resident / s.threads));
+    return s;
 }
 
-template <typename T>
-static cudaError_t launch_norm_out(const NormParams& p, int vpt, unsigned blocks, unsigned threads, cudaStream_t stream) {
-    switch (p.a.scale_mode) {
-    case GEMM_SCALE_NONE: return launch_norm<T, kOutSame>(p, vpt, blocks, threads, stream);
-    case GEMM_SCALE_BLOCK_1x128_128x128: return launch_norm<T, kOutBlock128>(p, vpt, blocks, threads, stream);
-    default: return launch_norm<T, kOutMx>(p, vpt, blocks, threads, stream);
-    }
-}
-
-constexpr int kNormGradNarrow = 8192;      // the widest rows whose weight gradients a thread sums in registers
-
-template <typename T>
-static cudaError_t launch_backward(const NormGradParams& p, int vpt, unsigned blocks, unsigned threads, size_t smem, cudaStream_t stream) {
-    switch (vpt) {
-    case 1: return launch_dependent(add_rms_norm_backward_kernel<T, 1, false>, dim3(blocks), dim3(threads), smem, stream, p);
-    case 2: return launch_dependent(add_rms_norm_backward_kernel<T, 2, false>, dim3(blocks), dim3(threads), smem, stream, p);
-    }
+template <typename T, int OUT, int VPT, bool RES>
+static cudaError_t launch_norm(const NormParams& p, const NormShape& s, unsigned blocks, cudaStream_t stream) {
     static std::atomic<int> smem_set[kMaxDevices];
-    const cudaError_t e = ensure_smem_limit(add_rms_norm_backward_kernel<T, 4, true>, smem, smem_set);
-    return e != cudaSuccess ? e : launch_dependent(add_rms_norm_backward_kernel<T, 4, true>, dim3(blocks), dim3(threads), smem, stream, p);
+    auto kern = add_rms_norm_kernel<T, OUT, VPT, RES>;
+    const cudaError_t e = ensure_smem_limit(kern, s.smem, smem_set);
+    return e != cudaSuccess ? e : launch_dependent(kern, dim3(blocks), dim3(s.threads), s.smem, stream, p);
+}
+
+template <typename T, int OUT>
+static cudaError_t launch_norm_vpt(const NormParams& p, const NormShape& s, unsigned blocks, cudaStream_t stream) {
+    const bool res = p.a.residual != nullptr;
+    switch (s.vpt) {
+    case 1: return res ? launch_norm<T, OUT, 1, true>(p, s, blocks, stream) : launch_norm<T, OUT, 1, false>(p, s, blocks, stream);
+    case 2: return res ? launch_norm<T, OUT, 2, true>(p, s, blocks, stream) : launch_norm<T, OUT, 2, false>(p, s, blocks, stream);
+    default: return res ? launch_norm<T, OUT, 4, true>(p, s, blocks, stream) : launch_norm<T, OUT, 4, false>(p, s, blocks, stream);
+    }
+}
+
+template <typename T>
+static cudaError_t launch_norm_out(const NormParams& p, const NormShape& s, unsigned blocks, cudaStream_t stream) {
+    switch (p.a.scale_mode) {
+    case GEMM_SCALE_NONE: return launch_norm_vpt<T, kOutSame>(p, s, blocks, stream);
+    case GEMM_SCALE_BLOCK_1x128_128x128: return launch_norm_vpt<T, kOutBlock128>(p, s, blocks, stream);
+    default: return launch_norm_vpt<T, kOutMx>(p, s, blocks, stream);
+    }
+}
+
+template <typename T, int VPT>
+static cudaError_t launch_grad(const NormGradParams& p, const NormShape& s, unsigned blocks, cudaStream_t stream) {
+    static std::atomic<int> smem_one[kMaxDevices], smem_ring[kMaxDevices];
+    const bool one = s.stages == 1;
+    auto kern = one ? add_rms_norm_backward_kernel<T, VPT, 1> : add_rms_norm_backward_kernel<T, VPT, kNormGradStages>;
+    const cudaError_t e = one ? ensure_smem_limit(kern, s.smem, smem_one) : ensure_smem_limit(kern, s.smem, smem_ring);
+    return e != cudaSuccess ? e : launch_dependent(kern, dim3(blocks), dim3(s.threads), s.smem, stream, p);
+}
+
+template <typename T>
+static cudaError_t launch_backward(const NormGradParams& p, const NormShape& s, unsigned blocks, cudaStream_t stream) {
+    switch (s.vpt) {
+    case 1: return launch_grad<T, 1>(p, s, blocks, stream);
+    case 2: return launch_grad<T, 2>(p, s, blocks, stream);
+    case 4: return launch_grad<T, 4>(p, s, blocks, stream);
+    default: return launch_grad<T, 8>(p, s, blocks, stream);
+    }
 }
 
 }  // namespace dgb
@@ -475,15 +531,16 @@ gemm_status_t add_rms_norm_run(const add_rms_norm_args_t* args, gemm_stream_t st
     if (s != GEMM_OK) return s;
     const int vectors = (int)((n + 7) / 8);
     p.all_rows = tiled ? (a.tokens + 127) / 128 * 128 : a.tokens;
-    int vpt = 1;
-    while (vpt < 4 && (vectors + 32 * vpt - 1) / (32 * vpt) > 32) vpt *= 2;
-    p.warps = (vectors + 32 * vpt - 1) / (32 * vpt);
-    p.rows = std::max(1, 8 / p.warps);
+    // one vector a thread while there are few rows, two while a row fits a block so
+    int vpt = p.all_rows > 2 * dev.sms && vectors > 32 ? 2 : 1;
+    while ((vectors + 32 * vpt - 1) / (32 * vpt) > 32) vpt *= 2;
+    const NormShape shape = norm_shape(vectors, vpt, a.residual ? 2 : 1, vpt == 4 ? norm_stages<4>() : norm_stages<2>(), 1024);
+    p.warps = shape.warps;
+    p.rows = shape.rows;
     p.over_hidden = 1.f / (float)n;
-    const unsigned blocks = (unsigned)((p.all_rows + p.rows - 1) / p.rows), threads = (unsigned)(p.rows * p.warps * 32);
+    const unsigned blocks = (unsigned)std::min((p.all_rows + p.rows - 1) / p.rows, dev.sms * shape.per_sm);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return status_of(a.dtype == GEMM_BF16 ? launch_norm_out<__nv_bfloat16>(p, vpt, blocks, threads, st)
-                                          : launch_norm_out<__half>(p, vpt, blocks, threads, st));
+    return status_of(a.dtype == GEMM_BF16 ? launch_norm_out<__nv_bfloat16>(p, shape, blocks, st) : launch_norm_out<__half>(p, shape, blocks, st));
 }
 
 int64_t add_rms_norm_backward_workspace(int32_t hidden) {
@@ -510,21 +567,21 @@ gemm_status_t add_rms_norm_backward(const add_rms_norm_grads_t* args, gemm_strea
     gemm_status_t s = device_facts(&dev);
     if (s != GEMM_OK) return s;
     const int vectors = (int)((n + 7) / 8);
-    const bool wide = n > kNormGradNarrow;
-    const int vpt = wide ? 4 : vectors > 128 ? 2 : 1;
-    p.warps = (vectors + 32 * vpt - 1) / (32 * vpt);
-    p.rows = std::max(1, 8 / p.warps);
+    int vpt = vectors > 32 ? 2 : 1;
+    while ((vectors + 32 * vpt - 1) / (32 * vpt) > 16) vpt *= 2;
+    NormShape shape = norm_shape(vectors, vpt, a.d_sum ? 3 : 2, kNormGradStages, vpt > 1 ? 512 : 1024);
+    p.warps = shape.warps;
+    p.rows = shape.rows;
     p.over_hidden = 1.f / (float)n;
     p.partials = a.d_weight ? static_cast<float*>(a.workspace) : nullptr;
-    const unsigned threads = (unsigned)(p.rows * p.warps * 32);
+    if (p.partials && p.rows > 1) shape.smem = std::max(shape.smem, (size_t)p.rows * (size_t)((n + 7) / 8 * 8) * sizeof(float));
     const int groups = (a.tokens + p.rows - 1) / p.rows;
-    const int blocks = std::min({groups, kNormGradBlocks, dev.sms * (wide ? 1 : threads <= 256 ? 4 : 2)});
-    const size_t smem = p.partials && (wide || p.rows > 1) ? (size_t)p.rows * (size_t)((n + 7) / 8 * 8) * sizeof(float) : 0;
-    cudaError_t e = a.dtype == GEMM_BF16 ? launch_backward<__nv_bfloat16>(p, vpt, (unsigned)blocks, threads, smem, st)
-                                         : launch_backward<__half>(p, vpt, (unsigned)blocks, threads, smem, st);
+    const int blocks = std::min({groups, kNormGradBlocks, dev.sms * shape.per_sm});
+    cudaError_t e = a.dtype == GEMM_BF16 ? launch_backward<__nv_bfloat16>(p, shape, (unsigned)blocks, st)
+                                         : launch_backward<__half>(p, shape, (unsigned)blocks, st);
     if (e == cudaSuccess && a.d_weight)
         e = launch_dependent(add_rms_norm_join_kernel, dim3((unsigned)((n + kNormJoinColumns - 1) / kNormJoinColumns)),
-                             dim3(kNormJoinColumns * kNormJoinRows), 0, st, static_cast<const float*>(p.partials), blocks, (int)n, a.d_weight);
+                             dim3(kNormJoinThreads), 0, st, static_cast<const float*>(p.partials), blocks, (int)n, a.d_weight);
     return status_of(e);
 }
 
