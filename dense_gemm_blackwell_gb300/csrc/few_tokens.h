@@ -8,6 +8,8 @@
 namespace dgb {
 
 constexpr int kFewTokensMax = 16;
+constexpr int kFewWarps = 8;
+constexpr int kFewRowBytes = 256;       // a stage: so many bytes of each of a tile's 16 rows
 
 struct FewParams {
     const void* x;              // [tokens][k], 16 bits
@@ -20,8 +22,13 @@ struct FewParams {
     int64_t ldx, ldw_bytes, ld_scales, ld_zeros, ldy, ld_gate_up;
     int32_t tokens, k, n;       // n: columns of y
     int32_t group;              // 4-bit weights: a multiple of 32
-    int32_t k_split;            // CTAs (one cluster) that share K
     int32_t act;                // gated
+    // filled in by shape_few
+    int32_t k_split_log;        // CTAs (one cluster) that share K
+    int32_t k_warps_log;        // warps of a CTA that share a tile's part of K
+    int32_t rounds;             // tiles that a warp goes through
+    uint32_t group_magic;       // 4-bit weights: floor(2^32 / (group / 32)), at most 2^32 - 1
+    int32_t grid, smem;
 };
 
 // vec: 0 = 16-bit weights; otherwise 4-bit words a lane loads at once (1, 2 or 4; group a multiple of 32 vec).  gated: w's
@@ -29,7 +36,7 @@ struct FewParams {
 cudaError_t launch_few_bf16(const FewParams& p, int vec, bool gated, cudaStream_t stream);
 cudaError_t launch_few_f16(const FewParams& p, int vec, bool gated, cudaStream_t stream);
 
-// CTAs of a cluster that share K, for `n` columns.
-int few_k_split(int64_t n, int64_t k, bool gated, bool four_bits, int sms);
+// Lays a product (tokens, n and k are set) on a device: false where its tokens do not fit shared memory.
+bool shape_few(FewParams* p, bool gated, bool four_bits, int sms);
 
 }  // namespace dgb

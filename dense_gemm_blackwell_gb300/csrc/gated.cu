@@ -60,13 +60,36 @@ __global__ void __launch_bounds__(kSlopeThreads) gated_slope_kernel(const __grid
     }
 }
 
-// Streamed tiles are 16 pairs or 32 rows; a cluster shares K while the tiles fill the device less than twice and every warp keeps
-// a stage of its own (128 bytes of a row).
-int few_k_split(int64_t n, int64_t k, bool gated, bool four_bits, int sms) {
-    const int64_t tiles = (n + (gated ? 15 : 31)) / (gated ? 16 : 32), stages = (k + (four_bits ? 255 : 63)) / (four_bits ? 256 : 64);
-    int ks = 1;
-    while (ks < 8 && tiles * ks * 2 <= 2 * sms && stages >= 16 * ks) ks *= 2;
-    return ks;
+// A tile is 16 rows of W, a stage 256 bytes of each.  Clusters share K as often as X (in whole stages, 8 or 16 tokens) needs for two
+// blocks to fit an SM, and further while that leaves no more blocks than fit the device and every warp a stage.  Then as many warps
+// share a tile as leaves a block the fewest stages in sequence, a tile's end counted as half a stage.
+bool shape_few(FewParams* p, bool gated, bool four_bits, int sms) {
+    constexpr int64_t kSmemMax = 112 * 1024;
+    const int64_t tiles = ((int64_t)p->n + (gated ? 7 : 15)) / (gated ? 8 : 16);
+    const int64_t stage_k = four_bits ? 2 * kFewRowBytes : kFewRowBytes / 2, stages = (p->k + stage_k - 1) / stage_k;
+    const int64_t tokens = p->tokens > 8 ? 16 : 8, sums = 2 * kFewWarps * tokens * 17 * 4;
+    auto x_bytes = [&](int64_t ks) { return (stages + ks - 1) / ks * stage_k * tokens * 2; };
+    int ks = 0;
+    while (ks <= 3 && sums + x_bytes(1 << ks) > kSmemMax) ++ks;
+    if (ks > 3) return false;
+    while (ks < 3 && (tiles << (ks + 1)) <= 2 * sms && stages >= (2 * kFewWarps) << ks) ++ks;
+    const int64_t clusters = (2 * sms) >> ks, mine = (stages + (1 << ks) - 1) >> ks;
+    int64_t best = INT64_MAX;
+    for (int kw = 0; (1 << kw) <= kFewWarps; ++kw) {
+        const int64_t at_once = clusters * (kFewWarps >> kw), rounds = (tiles + at_once - 1) / at_once;
+        const int64_t cost = rounds * (2 * ((mine + (1 << kw) - 1) >> kw) + 1);
+        if (cost < best) {
+            best = cost;
+            p->k_warps_log = kw;
+        }
+    }
+    const int per_round = kFewWarps >> p->k_warps_log;
+    const int64_t blocks = std::min<int64_t>((tiles + per_round - 1) / per_round, clusters);
+    p->k_split_log = ks;
+    p->rounds = (int)((tiles + per_round * blocks - 1) / (per_round * blocks));
+    p->grid = (int)(blocks << ks);
+    p->smem = (int)(sums + x_bytes(1 << ks));
+    return true;
 }
 
 static cudaError_t launch_few(const FewParams& p, int dtype, int vec, bool gated, cudaStream_t stream) {
@@ -84,6 +107,7 @@ struct gated_plan_s {
     gemm_plan_t forward = nullptr, dx = nullptr, dw = nullptr;
     PersistentParams params;        // of the pointers below
     GatedTail tail;
+    FewParams few{};                // streamed: what does not change from run to run
     const void* ptrs[4] = {nullptr, nullptr, nullptr, nullptr};
     bool params_valid = false;
 };
@@ -144,10 +168,14 @@ gemm_status_t gated_plan_create(gated_plan_t* out, const gated_desc_t* desc) {
     g.dtype_a = g.dtype_b = d.dtype;
     g.wait_timeout_ns = d.wait_timeout_ns;
     const bool forced = d.flags != 0 || d.tile_n != 0 || d.stages != 0 || d.max_ctas != 0;
-    p->info.streamed = d.tokens <= kFewTokensMax && !forced;
-    if (p->info.streamed) {
-        p->info.k_split = few_k_split(d.features, d.k, true, false, dev.sms);
-    } else {
+    if (d.tokens <= kFewTokensMax && !forced) {
+        p->few.tokens = (int32_t)d.tokens;
+        p->few.k = (int32_t)d.k;
+        p->few.n = (int32_t)d.features;
+        p->info.streamed = shape_few(&p->few, true, false, dev.sms);
+        if (p->info.streamed) p->info.k_split = 1 << p->few.k_split_log;
+    }
+    if (!p->info.streamed) {
         gemm_desc_t f = g;
         f.M = d.tokens;
         f.N = 2 * d.features;
@@ -208,7 +236,7 @@ gemm_status_t gated_run(gated_plan_t plan, const void* x, const void* w, void* h
     if (!all_aligned(16, {x, w, h, gate_up})) return GEMM_ERR_ALIGNMENT;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (plan->info.streamed) {
-        FewParams f{};
+        FewParams f = plan->few;
         f.x = x;
         f.w = w;
         f.y = h;
@@ -218,10 +246,6 @@ gemm_status_t gated_run(gated_plan_t plan, const void* x, const void* w, void* h
         f.ldw_bytes = 2 * d.ldw;
         f.ldy = d.ldh;
         f.ld_gate_up = d.ld_gate_up;
-        f.tokens = (int32_t)d.tokens;
-        f.k = (int32_t)d.k;
-        f.n = (int32_t)d.features;
-        f.k_split = plan->info.k_split;
         f.act = d.activation;
         return status_of(launch_few(f, d.dtype, 0, true, st));
     }
@@ -344,8 +368,9 @@ gemm_status_t int4_matmul_run(const int4_matmul_args_t* args, gemm_stream_t stre
     f.k = a.k;
     f.n = a.n;
     f.group = a.group;
-    f.k_split = few_k_split(a.n, a.k, gated, true, dev.sms);
     f.act = a.activation;
+    f.group_magic = (uint32_t)std::min<uint64_t>(UINT32_MAX, (1ull << 32) / (uint32_t)(a.group / 32));
+    if (!shape_few(&f, gated, true, dev.sms)) return GEMM_ERR_UNSUPPORTED;
     const int vec = a.group % 128 == 0 ? 4 : a.group % 64 == 0 ? 2 : 1;
     return status_of(launch_few(f, a.dtype, vec, gated, reinterpret_cast<cudaStream_t>(stream)));
 }
