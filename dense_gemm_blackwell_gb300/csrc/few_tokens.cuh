@@ -126,9 +126,6 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_tokens_kernel(const __grid
     auto row_of = [&](int tile, int i) {
         return GATED ? (int64_t)i * p.n + min(tile * kOut + g, p.n - 1) : (int64_t)min(tile * kOut + 8 * i + g, p.n - 1);
     };
-    griddep_wait();
-    griddep_launch_dependents();
-
     // ---------------------------------------------------------------- weights, a stage ahead in registers
     int load_round = 0, load_at = 0;
     bool load_tile = false;
@@ -139,6 +136,12 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_tokens_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             from[i] = static_cast<const uint8_t*>(p.w) + row_of(tile, i) * p.ldw_bytes + (int64_t)(s0 + share) * kFewRowBytes + 4 * kWords * t;
+    };
+    // The lines of the stage that is loaded next into L2, four lanes a row pair's four lines: its loads are issued a stage later and
+    // used a stage after that, which alone does not cover DRAM's latency under load.
+    auto prefetch = [&] {
+        if (load_tile && load_at < own && s0 + share + (load_at << p.k_warps_log) < whole)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"((t & 1 ? from[1] : from[0]) + (128 * (t >> 1) - 4 * kWords * t)));
     };
     auto load = [&](uint32_t (&w)[2][kRowWords]) {
         if (load_tile && load_at < own) {
@@ -182,6 +185,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_tokens_kernel(const __grid
             ++load_round;
             set_rows();
         }
+        prefetch();
     };
     // ---------------------------------------------------------------- scales and zero points, a stage ahead in registers
     // A lane of row g (and g + 8) has the stage's groups t, t + 4, ...; they stay as loaded until the stage comes, as whatever uses
@@ -235,27 +239,34 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_tokens_kernel(const __grid
 
     uint32_t now[2][kRowWords], next[2][kRowWords];
     set_rows();
+    prefetch();         // while the kernel before this one may still run: it returns nothing, so it does not matter who writes W
+    griddep_wait();
+    griddep_launch_dependents();
     load(next);
     if constexpr (kCodes) set_looks();
     look();
-    // X of this CTA's part of K: zeros past K and past the last token
+    // X of this CTA's part of K, a warp an instruction pair's 32 lanes at a time: zeros past K and past the last token
     constexpr int kBatch = 4;       // loads of a thread on the way
-    const int x_all = s_count * (kStageVectors * NB * 32);
-    for (int e0 = threadIdx.x; e0 < x_all; e0 += kBatch * kFewThreads) {
-        uint4 q[kBatch];
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int e = e0 + b * kFewThreads, l = e % 32, nb = e / 32 % NB, cv = e / (32 * NB), m = nb * 8 + l / 4;
-            const int k = s0 * kStageK + (cv / kVectors) * kChunkK + 8 * (kVectors * (l % 4) + cv % kVectors);
-            q[b] = make_uint4(0u, 0u, 0u, 0u);
-            if (m < p.tokens && e < x_all) q[b] = load_clipped16(static_cast<const uint16_t*>(p.x) + (int64_t)m * p.ldx + k, 2 * (p.k - k));
-        }
+    for (int nb = 0; nb < NB; ++nb) {
+        const int m = nb * 8 + g, k_left = m < p.tokens ? p.k - s0 * kStageK - 8 * kVectors * t : 0;
+        const uint16_t* x = static_cast<const uint16_t*>(p.x) + (int64_t)min(m, p.tokens - 1) * p.ldx + s0 * kStageK + 8 * kVectors * t;
+        for (int v0 = warp; v0 < s_count * kStageVectors; v0 += kBatch * kFewWarps) {
+            uint4 q[kBatch];
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            if constexpr (kCodes)      // elements j and j + 4 of a word of codes lie 16 bits apart
-                q[b] = make_uint4(__byte_perm(q[b].x, q[b].z, 0x5410), __byte_perm(q[b].x, q[b].z, 0x7632),
-                                  __byte_perm(q[b].y, q[b].w, 0x5410), __byte_perm(q[b].y, q[b].w, 0x7632));
-            if (e0 + b * kFewThreads < x_all) x_smem[e0 + b * kFewThreads] = q[b];
+            for (int b = 0; b < kBatch; ++b) {
+                const int v = v0 + b * kFewWarps, k = v / kVectors * kChunkK + v % kVectors * 8;
+                q[b] = make_uint4(0u, 0u, 0u, 0u);
+                if (v < s_count * kStageVectors && k < k_left) q[b] = load_clipped16(x + k, 2 * (k_left - k));
+            }
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const int v = v0 + b * kFewWarps;
+                if constexpr (kCodes)      // elements j and j + 4 of a word of codes lie 16 bits apart
+                    q[b] = make_uint4(__byte_perm(q[b].x, q[b].z, 0x5410), __byte_perm(q[b].x, q[b].z, 0x7632),
+                                      __byte_perm(q[b].y, q[b].w, 0x5410), __byte_perm(q[b].y, q[b].w, 0x7632));
+                if (v < s_count * kStageVectors) x_smem[(v * NB + nb) * 32 + lane] = q[b];
+            }
         }
     }
     __syncthreads();
@@ -370,40 +381,42 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_tokens_kernel(const __grid
             for (int w = 1; w < KW; ++w) v += tile_sums[(w * kTokens + m) * kFewPitch + c];
             return v;
         };
-        int e0 = 0, e1 = p.tokens * kOut;
+        int m0 = 0, m1 = p.tokens;
         if (KS > 1) {
             // in the place of the first warp's sums; each is read and written by one thread
             for (int e = thread; e < p.tokens * 16; e += threads) tile_sums[e / 16 * kFewPitch + e % 16] = add_warps(e / 16, e % 16);
             // a CTA that passes has everyone's sums of this round, and everyone has read those of the round before
             cluster_sync();
-            const int all = e1;
-            e0 = all * rank / KS;
-            e1 = all * (rank + 1) / KS;
+            m0 = p.tokens * rank >> p.k_split_log;
+            m1 = p.tokens * (rank + 1) >> p.k_split_log;
         }
-        auto total = [&](int m, int c) {
-            if (KS == 1) return add_warps(m, c);
-            const uint32_t from = smem_u32(tile_sums + m * kFewPitch + c);
+        for (int e0 = m0 * 16; e0 < m1 * 16; e0 += threads) {
+            const int e = e0 + thread, m = min(e / 16, m1 - 1), c = e % 16;
             float v = 0.f;
-            for (int o = 0; o < KS; ++o) {
-                float s;
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(s) : "r"(map_to_cta(from, (uint32_t)o)));
-                v += s;
-            }
-            return v;
-        };
-        for (int e = e0 + thread; e < e1; e += threads) {
-            const int c = e % kOut, m = e / kOut, n = tile_of(r) * kOut + c;
-            if (n >= p.n) continue;
-            float v = total(m, c);
-            if constexpr (GATED) {
-                const float u = total(m, 8 + c);
-                if (p.gate) {
-                    static_cast<T*>(p.gate)[(int64_t)m * p.ld_gate_up + n] = (T)v;
-                    static_cast<T*>(p.up)[(int64_t)m * p.ld_gate_up + n] = (T)u;
+            if (KS == 1) {
+                v = add_warps(m, c);
+            } else {
+                const uint32_t part = smem_u32(tile_sums + m * kFewPitch + c);
+                for (int o = 0; o < KS; ++o) {
+                    float s;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(s) : "r"(map_to_cta(part, (uint32_t)o)));
+                    v += s;
                 }
-                v = activate(p.act, v) * u;
             }
-            static_cast<T*>(p.y)[(int64_t)m * p.ldy + n] = (T)v;
+            const int n = tile_of(r) * kOut + c % kOut;
+            const bool there = e < m1 * 16 && n < p.n;
+            if constexpr (GATED) {
+                const float u = __shfl_down_sync(0xffffffffu, v, 8);       // the column's other sum
+                if (there && c < 8) {
+                    if (p.gate) {
+                        static_cast<T*>(p.gate)[(int64_t)m * p.ld_gate_up + n] = (T)v;
+                        static_cast<T*>(p.up)[(int64_t)m * p.ld_gate_up + n] = (T)u;
+                    }
+                    static_cast<T*>(p.y)[(int64_t)m * p.ldy + n] = (T)(activate(p.act, v) * u);
+                }
+            } else if (there) {
+                static_cast<T*>(p.y)[(int64_t)m * p.ldy + n] = (T)v;
+            }
         }
         ++r;
         tile_here = tile_of(r) < tiles;
