@@ -25,8 +25,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["kernels_single.cu", "kernels_persistent.cu", "kernels_fp8.cu", "kernels_mx.cu", "gemm_api.cu",
            "schedule_model.cu", "lora.cu", "lora_skinny.cu", "qk_norm_rope.cu", "paged_attn_api.cu", "paged_attn_bf16.cu", "paged_attn_f16.cu",
-           "paged_attn_bf16_e4m3.cu", "paged_attn_f16_e4m3.cu", "add_rms_norm.cu", "gated.cu", "kernels_gated.cu", "few_tokens_bf16.cu",
-           "few_tokens_f16.cu"]
+           "paged_attn_bf16_e4m3.cu", "paged_attn_f16_e4m3.cu", "add_rms_norm.cu", "gated.cu", "gated_few.cu", "kernels_gated.cu", "int4_matmul.cu",
+           "int4_matmul_bf16.cu", "int4_matmul_f16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "-I" + INCLUDE, "-I" + CSRC]

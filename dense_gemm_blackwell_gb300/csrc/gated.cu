@@ -1,10 +1,9 @@
-// gated.cu -- a gated pair of projections (include/feedforward.h): plans, the
-// pass over the kept sums that begins the backward pass, and the 4-bit products'
-// entry point, which shares the streaming kernel.
+// gated.cu -- a gated pair of projections (include/feedforward.h): plans and the
+// pass over the kept sums that begins the backward pass.
 //
-// Forward, more than kFewTokensMax tokens: the persistent pipeline on W's 2 x
-// features rows (kernels_gated.cu).  Up to that many: one stream over W
-// (few_tokens.cuh).  Backward: d_gate_up = [dH U act'(G), dH act(G)] in one pass
+// Forward, up to 128 tokens: one wave of CTAs over W, columns dealt out evenly
+// (gated_few.cu).  More: the persistent pipeline on W's 2 x features rows
+// (kernels_gated.cu).  Backward: d_gate_up = [dH U act'(G), dH act(G)] in one pass
 // over memory, then two of the library's products, d_gate_up W (W as an N-major
 // operand, K = 2 features) and d_gate_up^T X (both operands M- and N-major).
 #include <algorithm>
@@ -18,7 +17,7 @@
 #include "common.cuh"
 #include "elem.cuh"
 #include "feedforward.h"
-#include "few_tokens.h"
+#include "gated_few.h"
 #include "launch.h"
 #include "serving_host.h"
 
@@ -60,42 +59,6 @@ __global__ void __launch_bounds__(kSlopeThreads) gated_slope_kernel(const __grid
     }
 }
 
-// A tile is 16 rows of W, a stage 256 bytes of each.  Clusters share K as often as X (in whole stages, 8 or 16 tokens) needs for two
-// blocks to fit an SM, and further while that leaves no more blocks than fit the device and every warp a stage.  Then as many warps
-// share a tile as leaves a block the fewest stages in sequence, a tile's end counted as half a stage.
-bool shape_few(FewParams* p, bool gated, bool four_bits, int sms) {
-    constexpr int64_t kSmemMax = 112 * 1024;
-    const int64_t tiles = ((int64_t)p->n + (gated ? 7 : 15)) / (gated ? 8 : 16);
-    const int64_t stage_k = four_bits ? 2 * kFewRowBytes : kFewRowBytes / 2, stages = (p->k + stage_k - 1) / stage_k;
-    const int64_t tokens = p->tokens > 8 ? 16 : 8, sums = 2 * kFewWarps * tokens * 17 * 4;
-    auto x_bytes = [&](int64_t ks) { return (stages + ks - 1) / ks * stage_k * tokens * 2; };
-    int ks = 0;
-    while (ks <= 3 && sums + x_bytes(1 << ks) > kSmemMax) ++ks;
-    if (ks > 3) return false;
-    while (ks < 3 && (tiles << (ks + 1)) <= 2 * sms && stages >= (2 * kFewWarps) << ks) ++ks;
-    const int64_t clusters = (2 * sms) >> ks, mine = (stages + (1 << ks) - 1) >> ks;
-    int64_t best = INT64_MAX;
-    for (int kw = 0; (1 << kw) <= kFewWarps; ++kw) {
-        const int64_t at_once = clusters * (kFewWarps >> kw), rounds = (tiles + at_once - 1) / at_once;
-        const int64_t cost = rounds * (2 * ((mine + (1 << kw) - 1) >> kw) + 1);
-        if (cost < best) {
-            best = cost;
-            p->k_warps_log = kw;
-        }
-    }
-    const int per_round = kFewWarps >> p->k_warps_log;
-    const int64_t blocks = std::min<int64_t>((tiles + per_round - 1) / per_round, clusters);
-    p->k_split_log = ks;
-    p->rounds = (int)((tiles + per_round * blocks - 1) / (per_round * blocks));
-    p->grid = (int)(blocks << ks);
-    p->smem = (int)(sums + x_bytes(1 << ks));
-    return true;
-}
-
-static cudaError_t launch_few(const FewParams& p, int dtype, int vec, bool gated, cudaStream_t stream) {
-    return dtype == GEMM_BF16 ? launch_few_bf16(p, vec, gated, stream) : launch_few_f16(p, vec, gated, stream);
-}
-
 }  // namespace dgb
 
 using namespace dgb;
@@ -107,7 +70,9 @@ struct gated_plan_s {
     gemm_plan_t forward = nullptr, dx = nullptr, dw = nullptr;
     PersistentParams params;        // of the pointers below
     GatedTail tail;
-    FewParams few{};                // streamed: what does not change from run to run
+    GatedFewParams tiles{};         // few tiles: what does not change from run to run, and the maps of the pointers below
+    dim3 tiles_grid;
+    size_t tiles_smem = 0;
     const void* ptrs[4] = {nullptr, nullptr, nullptr, nullptr};
     bool params_valid = false;
 };
@@ -140,6 +105,83 @@ gemm_status_t resolve_gated(gated_desc_t* d) {
     return GEMM_OK;
 }
 
+// The kernel for few tokens takes up to 96, and up to 128 where the pipeline's tiles would cover less than half of the SMs: with more,
+// its sums on their way to the stores cost what its even wave gains (4096 x 2 x 12288: 1 token 31.4 us here, 52 there, 96 37.1 and 37.9,
+// 128 39.6 and 38.0; 4096 x 2 x 4096, 128 tokens: 17.4 and 23.8).  Columns and K are dealt out over one wave of clusters as costs the
+// least: an SM takes in about 50 bytes a cycle and 200 cycles a K block beside; a join costs a start and what its sums cost.  (One
+// wave: a 37th cluster of four CTAs, where the device held 36, doubled the time.)
+bool plan_few_tiles(const gated_desc_t& d, const DeviceFacts& dev, gated_plan_s* p) {
+    if (d.tokens > 128 || (d.tokens > 96 && 2 * d.features >= 128 * (int64_t)dev.sms)) return false;
+    const int64_t k_blocks = (d.k + 63) / 64, box_m = (d.tokens + 7) / 8 * 8;
+    GatedFewParams& q = p->tiles;
+    double best = 0;
+    for (int64_t ks = 1; ks <= kGatedFewMaxSplit && ks <= k_blocks; ks *= 2) {
+        const int64_t wave = gated_few_max_clusters(d.dtype, (int)ks, dev);
+        for (int64_t half = 8; half <= 128; half += 8) {
+            if ((d.features + half - 1) / half > wave) continue;
+            const double sums = (double)(box_m * 2 * half);
+            const double cost = (double)((k_blocks + ks - 1) / ks) * ((box_m + 2 * half) * 128 / 50 + 200) + 0.1 * sums +
+                                (ks > 1 ? 1000 + 0.1 * ks * sums : 0);
+            if (best > 0 && cost >= best) continue;
+            best = cost;
+            q.half = (int32_t)half;
+            q.k_split = (int32_t)ks;
+        }
+    }
+    if (best == 0) return false;
+    q.M = (int32_t)d.tokens;
+    q.features = (int32_t)d.features;
+    q.k_blocks = (int32_t)k_blocks;
+    q.box_m = (int32_t)box_m;
+    q.tmem_cols = 32;
+    while (q.tmem_cols < 2 * q.half) q.tmem_cols *= 2;
+    q.sum_pitch = 2 * q.half + 4;
+    q.ldy = d.ldh;
+    q.ld_gate_up = d.ld_gate_up;
+    q.act = d.activation;
+    q.timeout_ns = d.wait_timeout_ns ? d.wait_timeout_ns : 2000000000ull;
+    q.idesc = make_idesc(d.dtype == GEMM_BF16 ? 1u : 0u, 128u, 2u * q.half);
+    // the last stage's matrix instruction reads 128 rows from its X box on: 16 KB behind the ring
+    const int64_t stage = (box_m + 2 * q.half) * 128, slack = 128 * 128 + 1024, most = dev.smem_optin - 2048 - slack;
+    q.stages = (int32_t)std::max<int64_t>(2, std::min<int64_t>({most / stage, (int64_t)kGatedFewMaxStages, (k_blocks + q.k_split - 1) / q.k_split}));
+    // the sums lie over the ring
+    const int64_t bytes = std::max(q.stages * stage, d.tokens * q.sum_pitch * 4);
+    p->tiles_grid = dim3((unsigned)((d.features + q.half - 1) / q.half * q.k_split));
+    p->tiles_smem = (size_t)(bytes + slack);
+    return true;
+}
+
+// Tensor maps and pointers of a run, kept while the pointers stay the same.
+gemm_status_t few_tiles_params(gated_plan_s* plan, const void* x, const void* w, void* h, void* gate_up) {
+    const gated_desc_t& d = plan->desc;
+    GatedFewParams& q = plan->tiles;
+    gemm_status_t s = encode_rows_map(&q.tmap_x, d.dtype, x, d.k, d.tokens, d.ldx, q.box_m);
+    if (s == GEMM_OK) s = encode_rows_map(&q.tmap_w, d.dtype, w, d.k, 2 * d.features, d.ldw, q.half);
+    q.y = h;
+    q.gate = gate_up;
+    q.up = gate_up ? static_cast<uint16_t*>(gate_up) + d.features : nullptr;
+    q.status = device_record(plan->forward);
+    return s;
+}
+
+gemm_status_t pipeline_params(gated_plan_s* plan, const void* x, const void* w, void* h, void* gate_up) {
+    const gated_desc_t& d = plan->desc;
+    PersistentParams& p = plan->params;
+    GatedTail& q = plan->tail;
+    std::memset(&q, 0, sizeof(q));
+    gemm_status_t s = product_params(plan->forward, x, w, h, &p);
+    // W's rows of one kind; the output's columns
+    if (s == GEMM_OK) s = encode_rows_map(&p.tmap_b, d.dtype, w, d.k, 2 * d.features, d.ldw, std::min(p.tile_n, 256) / 2);
+    if (s == GEMM_OK) s = encode_rows_map(&p.tmap_d, d.dtype, h, d.features, d.tokens, d.ldh, 32);
+    if (s == GEMM_OK && gate_up) s = encode_rows_map(&q.tmap_gate, d.dtype, gate_up, d.features, d.tokens, d.ld_gate_up, 32);
+    if (s == GEMM_OK && gate_up)
+        s = encode_rows_map(&q.tmap_up, d.dtype, static_cast<uint16_t*>(gate_up) + d.features, d.features, d.tokens, d.ld_gate_up, 32);
+    q.features = (int32_t)d.features;
+    q.act = d.activation;
+    q.keep = gate_up != nullptr;
+    return s;
+}
+
 gemm_status_t make_product(gemm_plan_t* plan, gemm_plan_info_t* info, const gemm_desc_t& g) {
     const gemm_status_t s = gemm_plan_create(plan, &g);
     return s == GEMM_OK ? gemm_plan_info(*plan, info) : s;
@@ -168,26 +210,39 @@ gemm_status_t gated_plan_create(gated_plan_t* out, const gated_desc_t* desc) {
     g.dtype_a = g.dtype_b = d.dtype;
     g.wait_timeout_ns = d.wait_timeout_ns;
     const bool forced = d.flags != 0 || d.tile_n != 0 || d.stages != 0 || d.max_ctas != 0;
-    if (d.tokens <= kFewTokensMax && !forced) {
-        p->few.tokens = (int32_t)d.tokens;
-        p->few.k = (int32_t)d.k;
-        p->few.n = (int32_t)d.features;
-        p->info.streamed = shape_few(&p->few, true, false, dev.sms);
-        if (p->info.streamed) p->info.k_split = 1 << p->few.k_split_log;
-    }
-    if (!p->info.streamed) {
-        gemm_desc_t f = g;
-        f.M = d.tokens;
-        f.N = 2 * d.features;
-        f.K = d.k;
-        f.dtype_d = d.dtype;
-        f.lda = d.ldx;
-        f.ldb = d.ldw;
-        f.flags = d.flags | GEMM_FLAG_NO_SINGLE_CTA;
-        f.tile_n = d.tile_n == 0 && d.features < 128 ? 128 : d.tile_n;     // tiles hold whole 64-column chunks of both kinds
-        f.stages = d.stages;
-        f.max_ctas = d.max_ctas;
-        s = make_product(&p->forward, &p->info.product, f);
+    gemm_desc_t f = g;
+    f.M = d.tokens;
+    f.N = 2 * d.features;
+    f.K = d.k;
+    f.dtype_d = d.dtype;
+    f.lda = d.ldx;
+    f.ldb = d.ldw;
+    p->info.few_tiles = d.tokens > 0 && !forced && plan_few_tiles(d, dev, p);
+    f.flags = d.flags | GEMM_FLAG_NO_SINGLE_CTA;
+    if (p->info.few_tiles) f.flags |= GEMM_FLAG_NO_STREAM_K;       // the product's plan holds the error record only
+    f.tile_n = d.tile_n == 0 && d.features < 128 ? 128 : d.tile_n;     // tiles hold whole 64-column chunks of both kinds
+    f.stages = d.stages;
+    f.max_ctas = d.max_ctas;
+    s = make_product(&p->forward, &p->info.product, f);
+    if (s == GEMM_OK && p->info.few_tiles) {
+        // what runs instead
+        gemm_plan_info_t& info = p->info.product;
+        const GatedFewParams& q = p->tiles;
+        info.cta_group = 1;
+        info.tile_m = 128;
+        info.tile_n = 2 * q.half;
+        info.tile_k = 64;
+        info.stages = q.stages;
+        info.tmem_stages = 1;
+        info.tmem_cols = q.tmem_cols;
+        info.grid = (int32_t)p->tiles_grid.x;
+        info.block_threads = 192;
+        info.num_tiles = p->tiles_grid.x / q.k_split;
+        info.stage_bytes = (q.box_m + 2 * q.half) * 128;
+        info.pipeline_bytes = info.stages * info.stage_bytes + 8 * (2 * info.stages + 1) + 4;
+        info.smem_bytes = (int64_t)p->tiles_smem;
+        info.epilogue = 1;
+        p->info.k_split = q.k_split;
     }
     if (s == GEMM_OK && d.gradients) {
         gemm_desc_t x = g;      // d_x [tokens, k] = d_gate_up [tokens, 2 features] * W, W's rows the contraction
@@ -235,42 +290,15 @@ gemm_status_t gated_run(gated_plan_t plan, const void* x, const void* w, void* h
     if (!x || !w || !h) return GEMM_ERR_INVALID_ARG;
     if (!all_aligned(16, {x, w, h, gate_up})) return GEMM_ERR_ALIGNMENT;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (plan->info.streamed) {
-        FewParams f = plan->few;
-        f.x = x;
-        f.w = w;
-        f.y = h;
-        f.gate = gate_up;
-        f.up = gate_up ? static_cast<uint16_t*>(gate_up) + d.features : nullptr;
-        f.ldx = d.ldx;
-        f.ldw_bytes = 2 * d.ldw;
-        f.ldy = d.ldh;
-        f.ld_gate_up = d.ld_gate_up;
-        f.act = d.activation;
-        return status_of(launch_few(f, d.dtype, 0, true, st));
-    }
     const void* now[4] = {x, w, h, gate_up};
     if (!plan->params_valid || std::memcmp(now, plan->ptrs, sizeof(now)) != 0) {
         plan->params_valid = false;
-        if ((s = product_params(plan->forward, x, w, h, &plan->params)) != GEMM_OK) return s;
-        PersistentParams& p = plan->params;
-        GatedTail& q = plan->tail;
-        std::memset(&q, 0, sizeof(q));
-        // W's rows of one kind; the output's columns
-        s = encode_rows_map(&p.tmap_b, d.dtype, w, d.k, 2 * d.features, d.ldw, std::min(p.tile_n, 256) / 2);
-        if (s == GEMM_OK) s = encode_rows_map(&p.tmap_d, d.dtype, h, d.features, d.tokens, d.ldh, 32);
-        if (s == GEMM_OK && gate_up) {
-            s = encode_rows_map(&q.tmap_gate, d.dtype, gate_up, d.features, d.tokens, d.ld_gate_up, 32);
-            if (s == GEMM_OK)
-                s = encode_rows_map(&q.tmap_up, d.dtype, static_cast<uint16_t*>(gate_up) + d.features, d.features, d.tokens, d.ld_gate_up, 32);
-        }
+        s = plan->info.few_tiles ? few_tiles_params(plan, x, w, h, gate_up) : pipeline_params(plan, x, w, h, gate_up);
         if (s != GEMM_OK) return s;
-        q.features = (int32_t)d.features;
-        q.act = d.activation;
-        q.keep = gate_up != nullptr;
         std::memcpy(plan->ptrs, now, sizeof(now));
         plan->params_valid = true;
     }
+    if (plan->info.few_tiles) return status_of(launch_gated_few(plan->tiles, d.dtype, plan->tiles_grid, plan->tiles_smem, st));
     return status_of(launch_gated(plan->params, plan->tail, plan->info.product.cta_group, d.dtype, plan->info.product.grid,
                                   (size_t)plan->info.product.smem_bytes, st));
 }
@@ -332,47 +360,6 @@ gemm_status_t gated_plan_destroy(gated_plan_t plan) {
     }
     delete plan;
     return worst;
-}
-
-gemm_status_t int4_matmul_run(const int4_matmul_args_t* args, gemm_stream_t stream) {
-    if (!args) return GEMM_ERR_INVALID_ARG;
-    int4_matmul_args_t a = *args;
-    if (a.tokens < 0 || a.n < 1 || a.k < 1 || a.group < 1) return GEMM_ERR_INVALID_ARG;
-    if (a.activation < GATED_SILU || a.activation > GATED_NONE) return GEMM_ERR_INVALID_ARG;
-    const bool gated = a.activation != GATED_NONE;
-    if (!type16(a.dtype) || a.tokens > kFewTokensMax || a.k % 2 != 0 || a.group % 32 != 0 || (gated && a.n > INT32_MAX / 2))
-        return GEMM_ERR_UNSUPPORTED;
-    const int64_t groups = ((int64_t)a.k + a.group - 1) / a.group;
-    if (!settle(a.ldx, a.k) || !settle(a.ld_codes, a.k / 2) || !settle(a.ld_scales, groups) || !settle(a.ld_zeros, groups) || !settle(a.ldy, a.n))
-        return GEMM_ERR_INVALID_ARG;
-    if (a.tokens == 0) return GEMM_OK;
-    if (!a.x || !a.codes || !a.scales || !a.y) return GEMM_ERR_INVALID_ARG;
-    if (!all_aligned(16, {a.x, a.codes}) || !all_aligned(2, {a.scales, a.y}) || (a.tokens > 1 && a.ldx % 8 != 0) ||
-        ((a.n > 1 || gated) && a.ld_codes % 16 != 0))
-        return GEMM_ERR_ALIGNMENT;
-    DeviceFacts dev;
-    const gemm_status_t s = device_facts(&dev);
-    if (s != GEMM_OK) return s;
-    FewParams f{};
-    f.x = a.x;
-    f.w = a.codes;
-    f.scales = a.scales;
-    f.zeros = a.zeros;
-    f.y = a.y;
-    f.ldx = a.ldx;
-    f.ldw_bytes = a.ld_codes;
-    f.ld_scales = a.ld_scales;
-    f.ld_zeros = a.ld_zeros;
-    f.ldy = a.ldy;
-    f.tokens = a.tokens;
-    f.k = a.k;
-    f.n = a.n;
-    f.group = a.group;
-    f.act = a.activation;
-    f.group_magic = (uint32_t)std::min<uint64_t>(UINT32_MAX, (1ull << 32) / (uint32_t)(a.group / 32));
-    if (!shape_few(&f, gated, true, dev.sms)) return GEMM_ERR_UNSUPPORTED;
-    const int vec = a.group % 128 == 0 ? 4 : a.group % 64 == 0 ? 2 : 1;
-    return status_of(launch_few(f, a.dtype, vec, gated, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

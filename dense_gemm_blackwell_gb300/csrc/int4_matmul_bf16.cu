@@ -1,0 +1,8 @@
+// int4_matmul_bf16.cu -- int4_matmul.cuh for bf16 tokens.
+#include "int4_matmul.cuh"
+
+namespace dgb {
+
+cudaError_t launch_int4_bf16(const Int4Params& p, bool gated, cudaStream_t stream) { return launch_int4<__nv_bfloat16>(p, gated, stream); }
+
+}  // namespace dgb

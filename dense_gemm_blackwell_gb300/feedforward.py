@@ -46,7 +46,7 @@ class GatedDesc(ctypes.Structure):
 
 
 class GatedPlanInfo(ctypes.Structure):
-    _fields_ = [("product", GemmPlanInfo), ("dx", GemmPlanInfo), ("dw", GemmPlanInfo), ("streamed", _I32), ("k_split", _I32),
+    _fields_ = [("product", GemmPlanInfo), ("dx", GemmPlanInfo), ("dw", GemmPlanInfo), ("few_tiles", _I32), ("k_split", _I32),
                 ("workspace_bytes", _I64)]
 
 

@@ -97,16 +97,16 @@ typedef struct {
     int64_t ld_dx, ld_dw;
     uint32_t flags;                 /* GEMM_FLAG_CTA_GROUP_1/2, _NO_STREAM_K, _STAGE_K1/K2 as in gemm.h */
     int32_t tile_n;                 /* gates and ups of a tile together: 128, 256 or 512; 0 = planner */
-    int32_t stages, max_ctas;       /* as in gemm.h; 0 = planner.  Any of these four or of the flags keeps to the pipeline where few
-                                       tokens would take the streaming kernel, and applies to the forward pass alone */
+    int32_t stages, max_ctas;       /* as in gemm.h; 0 = planner.  Any of these three or of the flags keeps to the persistent
+                                       pipeline, and applies to the forward pass alone */
     uint64_t wait_timeout_ns;       /* bound on every device-side wait; 0 = 2 s */
 } gated_desc_t;
 
 typedef struct {
-    gemm_plan_info_t product;       /* the forward pass in the pipeline (N = 2 features); zeros where it is streamed */
+    gemm_plan_info_t product;       /* the forward pass (N = 2 features) */
     gemm_plan_info_t dx, dw;        /* the backward pass's products; zeros without gradients */
-    int32_t streamed;               /* 1: few tokens, one stream over W (few_tokens.cuh) */
-    int32_t k_split;                /* streamed: CTAs (one cluster) that share K */
+    int32_t few_tiles;              /* 1: up to 128 tokens, one wave of CTAs (gated_few.cu); otherwise the persistent pipeline */
+    int32_t k_split;                /* few tiles: CTAs (one cluster) that share K */
     int64_t workspace_bytes;        /* device memory of the plan's products */
 } gated_plan_info_t;
 
@@ -142,8 +142,9 @@ gemm_status_t gated_plan_destroy(gated_plan_t plan);
 /* p[m, j] = sum over groups g of scales[j, g] * sum over k in g of x[m, k] (code[j, k] - zero[j, g]);  group g is K's elements
  * [g * group, (g + 1) * group), the last one cut short by k.  activation GATED_NONE: y = p (n columns of n weight rows).
  * Otherwise w has 2 n rows, gates first: y[m, j] = act(p[m, j]) * p[m, n + j].  Codes are 0..15, two a byte, element k in the
- * low half of byte k/2 when k is even.  Every code less its zero point is exact, sums and scaling are fp32, y is rounded once.
- * x and the scales may hold infinities and NaN; they stay with their token or weight row. */
+ * low half of byte k/2 when k is even.  Products of codes are exact; their sums, the zero points' part, which is taken off a group's sum, and the scaling are fp32; y is rounded once.
+ * Infinities and NaN of x and of the scales stay with their token or weight row (an infinite x gives NaN or infinities).  A bf16 x
+ * past 2^63 counts as infinite, and one under 2^-57 may lose bits. */
 typedef struct {
     int32_t tokens;             /* 0 (no-op) .. 16; more go through the product, with the weights in another form */
     int32_t n, k;               /* n >= 1; k even */
