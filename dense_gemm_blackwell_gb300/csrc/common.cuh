@@ -48,6 +48,7 @@ __host__ __device__ constexpr uint64_t smem_desc_sw128(uint32_t smem_addr) {
 // offset = 1024 B between groups of 8 k-rows.  One MMA spans 16 (K16) or 32
 // (K32) k-rows: +2048 or +4096 B per MMA.
 constexpr uint32_t kMNMajorBoxBytes = 64 * 128;
+constexpr int kMNMajorGrouped = 2;
 constexpr uint64_t kSmemDescSw128MNMajorBase =
     (uint64_t(kMNMajorBoxBytes >> 4) << 16) |   // LBO: next 64 elements of M/N
     (uint64_t(1024 >> 4) << 32) |                // SBO: next 8 k-rows
@@ -114,8 +115,8 @@ struct PersistentParams {
     int32_t tile_k;           // elements of K per ring stage (k_atoms 128-byte swizzle rows)
     int32_t k_atoms;          // 128-byte K atoms per stage (1 or 2; 2 only with K-major operands)
     uint32_t mma_kind;        // kMmaKindF16 or kMmaKindTF32 (16-bit kernel only)
-    int32_t mn_major_a;       // 1: A is M-contiguous (loaded as 64x64 boxes, MN-major descriptor)
-    int32_t mn_major_b;       // 1: B is N-contiguous
+    int32_t mn_major_a;       // 1: A is M-contiguous (loaded as 64x64 boxes, MN-major descriptor); kMNMajorGrouped: in one box
+    int32_t mn_major_b;       // the same of B, N-contiguous
     int32_t acc_f16;          // 1: the accumulator is fp16 (one per 32-bit TMEM column, low half)
     int32_t mn_box_elems;     // MN-major boxes: elements along M/N per 128-byte row (64 or 128)
     uint32_t idesc;

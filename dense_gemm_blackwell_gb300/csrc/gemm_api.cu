@@ -558,6 +558,24 @@ bool encode_map(CUtensorMap* m, int dt, const void* base, int64_t cols, int64_t 
     return r == CUDA_SUCCESS;
 }
 
+// An MN-major 16-bit operand (`k` rows of `mn` elements, a multiple of 64, `ld` apart) as groups of 64 elements: dimensions (64, k,
+// mn / 64), box (64, tile_k, groups), 128-byte swizzle.
+bool encode_groups_map(CUtensorMap* m, int dt, const void* base, int64_t mn, int64_t k, int64_t ld, int tile_k, int groups) {
+    EncodeTiledFn enc = get_encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {64, (cuuint64_t)k, (cuuint64_t)(mn / 64)};
+    cuuint64_t strides[2] = {(cuuint64_t)(ld * 2), 128};
+    cuuint32_t box[3] = {64, (cuuint32_t)tile_k, (cuuint32_t)groups};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, tma_dtype(dt), 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Whole groups of 64 (a group that M or N ends in would be read past the end of its last row) of one matrix.
+int mn_mode(bool mn_major, int dt, int64_t mn, int64_t batch) {
+    return !mn_major ? 0 : (is16(dt) && batch == 1 && mn % 64 == 0 ? dgb::kMNMajorGrouped : 1);
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Scale tiles of a matrix with `rows` rows as a 4-D map of 32-bit words: 128
@@ -767,14 +785,15 @@ static gemm_status_t persistent_params(gemm_plan_s* plan, const void* A, const v
         // K-major: (K, rows) boxes of one 128-byte atom x rows (k_atoms per
         // stage).  MN-major: (rows, K) boxes of 64 x tile_k.
         const int atom_k = (int)(128 / eb_a);
-        const bool ok_a = mn_a ? encode_map(&plan->maps[0], d.dtype_a, A, d.M, d.K, d.lda, batch_maps, d.stride_a,
-                                            (int)(128 / eb_a), info.tile_k)
-                               : encode_map(&plan->maps[0], d.dtype_a, A, d.K, d.M, d.lda, batch_maps, d.stride_a,
-                                            atom_k, 128);
-        const bool ok_b = mn_b ? encode_map(&plan->maps[1], d.dtype_b, B, d.N, d.K, d.ldb, batch_maps, d.stride_b,
-                                            (int)(128 / eb_b), info.tile_k)
-                               : encode_map(&plan->maps[1], d.dtype_b, B, d.K, d.N, d.ldb, batch_maps, d.stride_b,
-                                            atom_k, std::min(info.tile_n, 256) / cg);
+        const int b_rows = std::min(info.tile_n, 256) / cg;
+        const bool ok_a = !mn_a ? encode_map(&plan->maps[0], d.dtype_a, A, d.K, d.M, d.lda, batch_maps, d.stride_a, atom_k, 128)
+                          : mn_mode(mn_a, d.dtype_a, d.M, d.batch) == dgb::kMNMajorGrouped
+                              ? encode_groups_map(&plan->maps[0], d.dtype_a, A, d.M, d.K, d.lda, info.tile_k, 2)
+                              : encode_map(&plan->maps[0], d.dtype_a, A, d.M, d.K, d.lda, batch_maps, d.stride_a, (int)(128 / eb_a), info.tile_k);
+        const bool ok_b = !mn_b ? encode_map(&plan->maps[1], d.dtype_b, B, d.K, d.N, d.ldb, batch_maps, d.stride_b, atom_k, b_rows)
+                          : mn_mode(mn_b, d.dtype_b, d.N, d.batch) == dgb::kMNMajorGrouped
+                              ? encode_groups_map(&plan->maps[1], d.dtype_b, B, d.N, d.K, d.ldb, info.tile_k, b_rows / 64)
+                              : encode_map(&plan->maps[1], d.dtype_b, B, d.N, d.K, d.ldb, batch_maps, d.stride_b, (int)(128 / eb_b), info.tile_k);
         if (!ok_a || !ok_b ||
             !encode_map(&plan->maps[2], d.dtype_d, D, d.N, d.M, d.ldd, batch_maps, d.stride_d, 128 / eb_d, 32)) {
             g_last_cuda_error = (int)cudaErrorInvalidValue;
@@ -800,14 +819,14 @@ static gemm_status_t persistent_params(gemm_plan_s* plan, const void* A, const v
     p.k_atoms = (int32_t)(info.tile_k * eb_a / 128);   // 128-byte K atoms per stage
     p.mma_kind = d.dtype_a == GEMM_TF32 ? dgb::kMmaKindTF32 : dgb::kMmaKindF16;
     // A/B formats: kind::f16 0 = f16, 1 = bf16; kind::tf32 2 = tf32
-    p.mn_major_a = d.major_a == GEMM_MN_MAJOR;
+    p.mn_major_a = mn_mode(d.major_a == GEMM_MN_MAJOR, d.dtype_a, d.M, d.batch);
     p.mn_box_elems = (int32_t)(128 / eb_a);
-    p.mn_major_b = d.major_b == GEMM_MN_MAJOR;
+    p.mn_major_b = mn_mode(d.major_b == GEMM_MN_MAJOR, d.dtype_b, d.N, d.batch);
     // one MMA covers at most 256 columns (512-wide tiles issue two)
     const uint32_t fmt = d.dtype_a == GEMM_BF16 ? 1u : (d.dtype_a == GEMM_TF32 ? 2u : 0u);
     p.acc_f16 = (d.flags & GEMM_FLAG_ACCUM_F16) ? 1 : 0;
     p.idesc = dgb::make_idesc2(fmt, fmt, (uint32_t)info.tile_m, (uint32_t)std::min(info.tile_n, 256),
-                               (uint32_t)p.mn_major_a, (uint32_t)p.mn_major_b, p.acc_f16 ? 0u : 1u);
+                               p.mn_major_a != 0, p.mn_major_b != 0, p.acc_f16 ? 0u : 1u);
     p.stage_bytes_a = (uint32_t)(128 * info.tile_k * eb_a);
     p.stage_bytes_b = (uint32_t)((info.tile_n / cg) * info.tile_k * eb_b);
     p.flags = d.flags;

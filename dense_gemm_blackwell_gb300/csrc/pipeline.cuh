@@ -98,12 +98,24 @@ __device__ __forceinline__ void store_segment_clipped(uint8_t* dst, int valid, P
 // 128-byte swizzle atom column each, `atom_stride` bytes apart (default
 // rows x 128 B).  MN-major (ATOMS == 1): boxes of `mn_elems` contiguous M/N
 // elements (128 bytes) x tile_k k-rows, one per `mn_elems` rows, `mn_box_bytes`
-// apart.
+// apart; kMNMajorGrouped: the same bytes in the same places as one box of a map
+// that counts groups of mn_elems as a dimension of its own (a copy takes its warp
+// up to 290 cycles to issue, and two of them more than a stage's 512 of MMA).
 template <int CG, int ATOMS = 1>
-__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, uint32_t bar, bool mn_major,
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, uint32_t bar, int mn_major,
                                              int rows, int row0, int kx, int b, bool batched, bool hint,
                                              uint64_t policy, int atom_k = 0, uint32_t atom_stride = 0,
                                              int mn_elems = 64, uint32_t mn_box_bytes = kMNMajorBoxBytes) {
+    if (mn_major == kMNMajorGrouped) {
+        if constexpr (CG == 1) {
+            if (hint) tma_load_3d_hint(dst, map, bar, 0, kx, row0 / mn_elems, policy);
+            else tma_load_3d(dst, map, bar, 0, kx, row0 / mn_elems);
+        } else {
+            if (hint) tma_load_3d_pair_hint(dst, map, bar, 0, kx, row0 / mn_elems, policy);
+            else tma_load_3d_pair(dst, map, bar, 0, kx, row0 / mn_elems);
+        }
+        return;
+    }
     const int boxes = mn_major ? rows / mn_elems : ATOMS;
     const uint32_t a_stride = atom_stride ? atom_stride : (uint32_t)rows * 128u;
     for (int j = 0; j < boxes; ++j) {
@@ -275,7 +287,7 @@ __device__ void producer_loop(const PersistentParams& p, uint8_t* ring, uint32_t
                     const bool back = kSerpentine && u.role == kUnitWhole && (idx & 1);
                     const int kx = (back ? u.kb0 + u.kb1 - 1 - kb : kb) * tile_k;
                     if constexpr ((parts & kPartA) != 0)
-                        load_operand<CG, ATOMS>(sa, &p.tmap_a, fb, p.mn_major_a != 0, 128, a_row, kx, b,
+                        load_operand<CG, ATOMS>(sa, &p.tmap_a, fb, p.mn_major_a, 128, a_row, kx, b,
                                                 p.batched != 0, keep_a, pol_a, atom_k, 0, mn_elems, mn_box_bytes);
                     if constexpr (kGated) {
                         const int rows = p.tile_n / (2 * HALVES);       // of one kind and half
@@ -292,7 +304,7 @@ __device__ void producer_loop(const PersistentParams& p, uint8_t* ring, uint32_t
                         }
                     } else if constexpr (HALVES == 1) {
                         if constexpr ((parts & kPartB0) != 0)
-                            load_operand<CG, ATOMS>(sb, &p.tmap_b, fb, p.mn_major_b != 0, b_rows, b_row, kx, b,
+                            load_operand<CG, ATOMS>(sb, &p.tmap_b, fb, p.mn_major_b, b_rows, b_row, kx, b,
                                                     p.batched != 0, false, pol_a, atom_k, 0, mn_elems, mn_box_bytes);
                     } else {
                         constexpr int kHalfRows = 256 / CG;
