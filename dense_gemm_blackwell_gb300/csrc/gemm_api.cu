@@ -425,9 +425,9 @@ gemm_status_t plan(const gemm_desc_t& d, const gemm_device_props_t& props, gemm_
         if (tile_n == 256 && 2 * tiles256 < props.sm_count / cg) tile_n = 128;
     }
     // 512-wide tiles: two N = 256 MMAs per K step into one 512-column
-    // accumulator (K-major operands, one K atom per stage)
+    // accumulator (one K atom per stage; MN-major operands on request only)
     const bool wide = tile_n == 512;
-    if (wide && (mn_a || mn_b || (d.flags & GEMM_FLAG_STAGE_K2))) return GEMM_ERR_UNSUPPORTED;
+    if (wide && ((d.flags & GEMM_FLAG_STAGE_K2) || ((mn_a || mn_b) && !is16(d.dtype_a)))) return GEMM_ERR_UNSUPPORTED;
     if (!wide && (tile_n % 16 != 0 || tile_n < 16 || tile_n > 256)) return GEMM_ERR_UNSUPPORTED;
     if (tile_n % chunk_cols != 0) return GEMM_ERR_UNSUPPORTED;     // epilogue writes 128-byte column chunks
     if ((tile_n / cg) % 8 != 0) return GEMM_ERR_UNSUPPORTED;      // B half-tile rows form 8-row swizzle atoms

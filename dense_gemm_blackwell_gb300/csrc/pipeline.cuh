@@ -311,10 +311,10 @@ __device__ void producer_loop(const PersistentParams& p, uint8_t* ring, uint32_t
 #pragma unroll
                         for (int h = 0; h < HALVES; ++h)
                             if ((parts & (kPartB0 << h)) != 0 && (halves & (1 << h)) != 0)
-                                load_operand<CG, ATOMS>(sb + (uint32_t)(h * kHalfRows * 128), &p.tmap_b, fb, false,
+                                load_operand<CG, ATOMS>(sb + (uint32_t)(h * kHalfRows * 128), &p.tmap_b, fb, p.mn_major_b,
                                                         kHalfRows, nb * p.tile_n + h * 256 + (int)rank * kHalfRows,
                                                         kx, b, p.batched != 0, false, pol_a, atom_k,
-                                                        (uint32_t)b_rows * 128u);
+                                                        (uint32_t)b_rows * 128u, mn_elems, mn_box_bytes);
                     }
                 }
             }

@@ -134,7 +134,7 @@ typedef struct {
                                       (MX/NV tiles); 0 = packed */
     uint32_t flags;             /* GEMM_FLAG_* */
     int32_t tile_n;             /* N extent of one output tile: a multiple of 16 in 16..256, or 512 (16-bit/tf32
-                                   K-major operands: two N = 256 MMAs per K step, one 512-column accumulator);
+                                   operands: two N = 256 MMAs per K step, one 512-column accumulator);
                                    block-scaled fp8: 128 or 256; MX/NV: 256; 0 = planner */
     int32_t stages;             /* shared-memory ring depth (2..16); 0 = planner */
     int32_t max_ctas;           /* cap on persistent CTAs; 0 = all SMs */
