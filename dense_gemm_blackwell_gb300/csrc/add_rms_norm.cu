@@ -23,6 +23,7 @@
 namespace dgb {
 
 constexpr int kNormMaxHidden = 32768;
+constexpr int kNormMaxTokens = 1 << 30;     // rows a few turns ahead are counted in 32 bits
 constexpr float kE4M3Max = 448.f;
 
 // Vector v of the weights, zeros past the row's end.
@@ -338,7 +339,7 @@ __global__ void __launch_bounds__(512) add_rms_norm_backward_kernel(const __grid
         }
         if (live) {
             const float r = rsqrtf(sums.x * p.over_hidden + a.eps);
-            const Pair both = pair_of(r), c = pair_of(-r * r * r * (sums.y * p.over_hidden));
+            const Pair both = pair_of(r), c = pair_of(-(sums.y * p.over_hidden) * r * r * r);       // r^3 alone may overflow
             uint16_t* dh = static_cast<uint16_t*>(a.dh) + (int64_t)row * a.ld_dh;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
@@ -515,12 +516,12 @@ gemm_status_t add_rms_norm_run(const add_rms_norm_args_t* args, gemm_stream_t st
     if (!type16(a.dtype)) return GEMM_ERR_UNSUPPORTED;
     const bool tiled = a.scale_mode == GEMM_SCALE_MX_E8M0_32, blocks128 = a.scale_mode == GEMM_SCALE_BLOCK_1x128_128x128;
     if (a.scale_mode != GEMM_SCALE_NONE && !tiled && !blocks128) return GEMM_ERR_UNSUPPORTED;
-    if (a.hidden > kNormMaxHidden) return GEMM_ERR_UNSUPPORTED;
+    if (a.hidden > kNormMaxHidden || a.tokens > kNormMaxTokens) return GEMM_ERR_UNSUPPORTED;
     const int64_t n = a.hidden;
     if (!settle(a.ldx, n) || !settle(a.ld_residual, n) || !settle(a.ld_sum, n) || !settle(a.ldy, n)) return GEMM_ERR_INVALID_ARG;
     if (blocks128 ? !settle(a.ld_scales, (n + 127) / 128) : a.ld_scales != 0) return GEMM_ERR_INVALID_ARG;
     if (a.tokens == 0) return GEMM_OK;
-    if (!a.x || !a.y || (tiled || blocks128) != (a.scales != nullptr)) return GEMM_ERR_INVALID_ARG;
+    if (!a.x || !a.y || a.y == a.sum || (tiled || blocks128) != (a.scales != nullptr)) return GEMM_ERR_INVALID_ARG;
     if (!all_aligned(16, {a.x, a.residual, a.weight, a.sum, a.y}) || !all_aligned(tiled ? 16 : 4, {a.scales})) return GEMM_ERR_ALIGNMENT;
     // of a single row no leading dim is used
     if (a.tokens > 1 && (!all_multiples(8, {a.ldx, a.residual ? a.ld_residual : 0, a.sum ? a.ld_sum : 0}) ||
@@ -553,7 +554,7 @@ gemm_status_t add_rms_norm_backward(const add_rms_norm_grads_t* args, gemm_strea
     p.a = *args;
     add_rms_norm_grads_t& a = p.a;
     if (a.tokens < 0 || a.hidden < 1 || !(a.eps >= 0.f)) return GEMM_ERR_INVALID_ARG;
-    if (!type16(a.dtype) || a.hidden > kNormMaxHidden) return GEMM_ERR_UNSUPPORTED;
+    if (!type16(a.dtype) || a.hidden > kNormMaxHidden || a.tokens > kNormMaxTokens) return GEMM_ERR_UNSUPPORTED;
     const int64_t n = a.hidden;
     if (!settle(a.ld_dy, n) || !settle(a.ld_h, n) || !settle(a.ld_d_sum, n) || !settle(a.ld_dh, n)) return GEMM_ERR_INVALID_ARG;
     if (a.d_weight && (!a.workspace || a.workspace_bytes < add_rms_norm_backward_workspace(a.hidden))) return GEMM_ERR_INVALID_ARG;

@@ -42,7 +42,7 @@ extern "C" {
  * values).  Infinite h gives NaN at its place and zeros in the rest of the row.  Squares are summed in fp32: rows with |h| past
  * about 1e18 give zeros. */
 typedef struct {
-    int32_t tokens, hidden;     /* hidden 1..32768; tokens 0 = no-op */
+    int32_t tokens, hidden;     /* hidden 1..32768; tokens 0 (no-op) .. 2^30 */
     int32_t dtype;              /* GEMM_BF16 or GEMM_F16: x, residual, weight, sum and an unscaled y */
     int32_t scale_mode;
     float eps;

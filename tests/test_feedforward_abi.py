@@ -51,7 +51,8 @@ def test_structures_match_the_header(tmp_path):
 def norm_args(**kw):
     g = ff.AddRmsNormArgs()
     g.tokens, g.hidden, g.dtype, g.scale_mode, g.eps = 4, 64, dg.GEMM_BF16, dg.GEMM_SCALE_NONE, 1e-6
-    g.x = g.residual = g.sum = g.y = AT
+    g.x = g.residual = g.sum = AT
+    g.y = AT + 1024
     for name, value in kw.items():
         setattr(g, name, value)
     return g
@@ -64,7 +65,8 @@ BLOCK, MX = dg.GEMM_SCALE_BLOCK_1x128_128x128, dg.GEMM_SCALE_MX_E8M0_32
     (dict(tokens=-1), dg.GEMM_ERR_INVALID_ARG), (dict(hidden=0), dg.GEMM_ERR_INVALID_ARG), (dict(reserved0=1), dg.GEMM_ERR_INVALID_ARG),
     (dict(eps=-1.0), dg.GEMM_ERR_INVALID_ARG), (dict(eps=float("nan")), dg.GEMM_ERR_INVALID_ARG),
     (dict(dtype=dg.GEMM_F32), dg.GEMM_ERR_UNSUPPORTED), (dict(scale_mode=dg.GEMM_SCALE_NV_E4M3_16), dg.GEMM_ERR_UNSUPPORTED),
-    (dict(hidden=32769), dg.GEMM_ERR_UNSUPPORTED), (dict(ldx=63), dg.GEMM_ERR_INVALID_ARG), (dict(x=0), dg.GEMM_ERR_INVALID_ARG),
+    (dict(hidden=32769), dg.GEMM_ERR_UNSUPPORTED), (dict(tokens=2 ** 30 + 1), dg.GEMM_ERR_UNSUPPORTED),
+    (dict(y=AT + 64, sum=AT + 64), dg.GEMM_ERR_INVALID_ARG), (dict(ldx=63), dg.GEMM_ERR_INVALID_ARG), (dict(x=0), dg.GEMM_ERR_INVALID_ARG),
     (dict(y=0), dg.GEMM_ERR_INVALID_ARG), (dict(scales=AT), dg.GEMM_ERR_INVALID_ARG), (dict(scale_mode=MX), dg.GEMM_ERR_INVALID_ARG),
     (dict(scale_mode=MX, scales=AT, ld_scales=4), dg.GEMM_ERR_INVALID_ARG), (dict(scale_mode=BLOCK, scales=AT, hidden=129, ldx=136, ld_scales=1),
                                                                           dg.GEMM_ERR_INVALID_ARG),
@@ -83,7 +85,7 @@ def test_norm_of_nothing():
 
 @pytest.mark.parametrize("change,status", [
     (dict(tokens=-1), dg.GEMM_ERR_INVALID_ARG), (dict(hidden=0), dg.GEMM_ERR_INVALID_ARG), (dict(dtype=dg.GEMM_E4M3), dg.GEMM_ERR_UNSUPPORTED),
-    (dict(hidden=40000), dg.GEMM_ERR_UNSUPPORTED), (dict(dy=0), dg.GEMM_ERR_INVALID_ARG), (dict(ld_h=8), dg.GEMM_ERR_INVALID_ARG),
+    (dict(hidden=40000), dg.GEMM_ERR_UNSUPPORTED), (dict(tokens=2 ** 30 + 1), dg.GEMM_ERR_UNSUPPORTED), (dict(dy=0), dg.GEMM_ERR_INVALID_ARG), (dict(ld_h=8), dg.GEMM_ERR_INVALID_ARG),
     (dict(d_weight=AT), dg.GEMM_ERR_INVALID_ARG), (dict(d_weight=AT, workspace=AT, workspace_bytes=64), dg.GEMM_ERR_INVALID_ARG),
     (dict(dh=AT + 8), dg.GEMM_ERR_ALIGNMENT), (dict(ld_dy=65), dg.GEMM_ERR_ALIGNMENT), (dict(d_sum=AT, ld_d_sum=66), dg.GEMM_ERR_ALIGNMENT)])
 def test_norm_backward_refuses(change, status):

@@ -271,6 +271,15 @@ def test_backward_against_differences():
     assert abs((dw.double() * vw).sum() - slope) <= (dw.double() * vw).abs().sum() * 1e-5 + 1e-6
 
 
+def test_backward_of_tiny_rows_without_eps():
+    """r^3 is past fp32's range where r and the gradients are not."""
+    t, n, kind = 5, 200, torch.bfloat16
+    h, dy, w = rows(t, n, kind, 34) * 2.0 ** -50, rows(t, n, kind, 35), weights(n, kind)
+    dh, dw = dg.add_rms_norm_backward(dy, h, w, eps=0.0)
+    want, want_w = dg.add_rms_norm_backward(dy, h * 2.0 ** 50, w, eps=0.0)
+    assert want.isfinite().all() and torch.equal(dh * 2.0 ** -50, want) and torch.equal(dw, want_w)
+
+
 @pytest.mark.parametrize("n", [1000, 12000])
 def test_backward_in_place(n):
     t, kind = 40, torch.bfloat16
