@@ -52,9 +52,9 @@ __device__ __forceinline__ float2 activate_with_slope(int act, float g) {
     }
     const float u2 = 2.f * kSqrt2OverPi * fmaf(kTanhCubic * g * g, g, g);
     const float p = logistic(u2);
-    // (1 - tanh^2 u) / 2 = 2 p (1 - p)
-    const float du = kSqrt2OverPi * fmaf(3.f * kTanhCubic * g, g, 1.f);
-    return make_float2(g * p, fmaf(g * 2.f * p * (1.f - p), du, p));
+    // (1 - tanh^2 u) / 2 = 2 p (1 - p): 0 long before |g| = 64, past which du might overflow
+    const float near = fminf(fmaxf(g, -64.f), 64.f), du = kSqrt2OverPi * fmaf(3.f * kTanhCubic * near, near, 1.f);
+    return make_float2(g * p, fmaf(near * 2.f * p * (1.f - p), du, p));
 }
 
 }  // namespace dgb

@@ -171,6 +171,24 @@ def test_backward(t, f, k, act, dw_f32, kind):
         assert ((got.double() - want).abs() <= bound).all(), ((got.double() - want).abs() / bound).max().item()
 
 
+def test_far_slopes():
+    """Kept gates out to the ends of the types: slopes of 0 and 1, nothing of infinity times zero."""
+    for kind, far in ((torch.bfloat16, 1e38), (torch.float16, 6e4)):
+        t, f, k = 8, 8, 16
+        gates = torch.tensor([-far, -far ** 0.5, -100.0, -50.0, 50.0, 100.0, far ** 0.5, far], device="cuda").to(kind)
+        gate_up = torch.cat((gates.repeat(t, 1), torch.ones(t, f, dtype=kind, device="cuda")), 1)
+        one, x, w = torch.ones(t, f, dtype=kind, device="cuda"), rows(t, k, kind, 5), rows(2 * f, k, kind, 6)
+        for act in ("silu", "gelu", "gelu_tanh"):
+            with dg.GatedPlan(t, f, k, activation=act, dtype=CODE[kind], gradients=True) as p:
+                d = torch.empty(t, 2 * f, dtype=kind, device="cuda")
+                p.backward(one, x, w, gate_up, d_gate_up=d)
+                assert p.sync_status()[0] == dg.GEMM_OK
+            # silu, whose tails are the longest: |silu'(g) - [g > 0]| <= (|g| + 1) e^-|g| and |silu(g) - max(g, 0)| <= |g| e^-|g|, at
+            # |g| = 50 less than 51 * 1.93e-22 < 1e-20, far below the half step around 1 and 50
+            assert ((d[:, :f].float() - (gates > 0).float()).abs() <= 1e-20).all(), act
+            assert ((d[:, f:].float() - gates.float().clamp(min=0)).abs() <= 1e-20).all(), act
+
+
 def test_backward_against_differences():
     t, f, k, kind = 24, 40, 72, torch.bfloat16
     x, w, dh = rows(t, k, kind, 21), rows(2 * f, k, kind, 22, 0.2), rows(t, f, kind, 23)
