@@ -60,13 +60,14 @@ struct CodeScale<__half> {
     static __device__ __forceinline__ uint32_t operand(uint32_t x, bool) { return x; }
 };
 
-// `bytes` (may be over 16 or negative) bytes of p's 16, the rest as zeros; elements of 2 bytes.
+// `bytes` (may be over 16 or negative) bytes of p's 16, the rest as zeros; elements of 2 bytes.  Not by the read-only path: the
+// kernel before this one, which may still run when this one starts, may have written them.
 __device__ __forceinline__ uint4 load_clipped16(const void* p, int bytes) {
-    if (bytes >= 16) return __ldg(static_cast<const uint4*>(p));
+    if (bytes >= 16) return *static_cast<const uint4*>(p);
     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int i = 0; i < 7; ++i)
-        if (2 * i + 2 <= bytes) w[i >> 1] |= (uint32_t)__ldg(static_cast<const uint16_t*>(p) + i) << (16 * (i & 1));
+        if (2 * i + 2 <= bytes) w[i >> 1] |= (uint32_t)static_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 

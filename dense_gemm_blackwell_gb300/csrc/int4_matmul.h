@@ -8,6 +8,7 @@
 namespace dgb {
 
 constexpr int kInt4TokensMax = 16;
+constexpr int kInt4RowsMax = 1 << 30;     // of Y's columns: tiles past the last are counted too
 constexpr int kInt4Warps = 8;
 constexpr int kInt4RowBytes = 256;      // a stage: so many bytes of each of a tile's 16 rows
 

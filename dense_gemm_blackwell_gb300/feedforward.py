@@ -369,7 +369,8 @@ def int4_matmul(x, codes, scales, *, group=128, zeros=None, activation=None, out
 
     x [tokens, k], at most 16 tokens (more go through matmul with weights in another form); codes uint8 [rows, k / 2], rows a
     multiple of 16 bytes apart: column k in the low half of byte k / 2 when k is even, in the high half when it is odd; scales
-    [rows, ceil(k / group)] of x's type; zeros uint8, 0..127; group: a multiple of 32.
+    [rows, ceil(k / group)] of x's type; zeros uint8, 0..127; group: a multiple of 32.  k up to 94208 with at most 8 tokens, up
+    to 45056 with more.
     """
     if out is None:
         _need(x.dim() == 2 and codes.dim() == 2, "x [tokens, k], codes [rows, k / 2] expected")

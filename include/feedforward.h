@@ -142,12 +142,14 @@ gemm_status_t gated_plan_destroy(gated_plan_t plan);
 /* p[m, j] = sum over groups g of scales[j, g] * sum over k in g of x[m, k] (code[j, k] - zero[j, g]);  group g is K's elements
  * [g * group, (g + 1) * group), the last one cut short by k.  activation GATED_NONE: y = p (n columns of n weight rows).
  * Otherwise w has 2 n rows, gates first: y[m, j] = act(p[m, j]) * p[m, n + j].  Codes are 0..15, two a byte, element k in the
- * low half of byte k/2 when k is even.  Products of codes are exact; their sums, the zero points' part, which is taken off a group's sum, and the scaling are fp32; y is rounded once.
+ * low half of byte k/2 when k is even.  Products of codes are exact; their sums, the zero points'
+ * part, which is taken off a group's sum, and the scaling are fp32; y is rounded once.
  * Infinities and NaN of x and of the scales stay with their token or weight row (an infinite x gives NaN or infinities).  A bf16 x
  * past 2^63 counts as infinite, and one under 2^-57 may lose bits. */
 typedef struct {
     int32_t tokens;             /* 0 (no-op) .. 16; more go through the product, with the weights in another form */
-    int32_t n, k;               /* n >= 1; k even */
+    int32_t n, k;               /* n 1..2^30; k even, and such that X fits the shared memory of a cluster: 94208 and less does for up
+                                   to 8 tokens, 45056 and less for more */
     int32_t group;              /* a multiple of 32 */
     int32_t dtype;              /* GEMM_BF16 or GEMM_F16: x, scales and y */
     int32_t activation;         /* gated_activation_t */
@@ -159,8 +161,8 @@ typedef struct {
     int64_t ldx, ld_codes /* bytes */, ld_scales, ld_zeros, ldy;     /* 0 = packed */
 } int4_matmul_args_t;
 
-/* int4_matmul_run -- enqueue.  GEMM_OK, GEMM_ERR_INVALID_ARG, GEMM_ERR_UNSUPPORTED (17 tokens or more, odd k, a group that is no
- * multiple of 32), GEMM_ERR_ALIGNMENT, GEMM_ERR_NO_DEVICE or GEMM_ERR_CUDA. */
+/* int4_matmul_run -- enqueue.  GEMM_OK, GEMM_ERR_INVALID_ARG, GEMM_ERR_UNSUPPORTED (17 tokens or more, an odd or too long k, a group
+ * that is no multiple of 32), GEMM_ERR_ALIGNMENT, GEMM_ERR_NO_DEVICE or GEMM_ERR_CUDA. */
 gemm_status_t int4_matmul_run(const int4_matmul_args_t* args, gemm_stream_t stream);
 
 #ifdef __cplusplus

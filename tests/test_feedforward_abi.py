@@ -145,7 +145,7 @@ def int4_args(**kw):
     (dict(tokens=-1), dg.GEMM_ERR_INVALID_ARG), (dict(n=0), dg.GEMM_ERR_INVALID_ARG), (dict(group=0), dg.GEMM_ERR_INVALID_ARG),
     (dict(activation=4), dg.GEMM_ERR_INVALID_ARG), (dict(x=0), dg.GEMM_ERR_INVALID_ARG), (dict(scales=0), dg.GEMM_ERR_INVALID_ARG),
     (dict(ld_scales=3), dg.GEMM_ERR_INVALID_ARG), (dict(ld_codes=127), dg.GEMM_ERR_INVALID_ARG), (dict(ldy=63), dg.GEMM_ERR_INVALID_ARG),
-    (dict(tokens=17), dg.GEMM_ERR_UNSUPPORTED), (dict(k=255), dg.GEMM_ERR_UNSUPPORTED), (dict(group=48), dg.GEMM_ERR_UNSUPPORTED),
+    (dict(tokens=17), dg.GEMM_ERR_UNSUPPORTED), (dict(n=2 ** 30 + 1), dg.GEMM_ERR_UNSUPPORTED), (dict(k=255), dg.GEMM_ERR_UNSUPPORTED), (dict(group=48), dg.GEMM_ERR_UNSUPPORTED),
     (dict(dtype=dg.GEMM_F32), dg.GEMM_ERR_UNSUPPORTED), (dict(codes=AT + 8), dg.GEMM_ERR_ALIGNMENT), (dict(ldx=260), dg.GEMM_ERR_ALIGNMENT),
     (dict(ld_codes=136), dg.GEMM_ERR_ALIGNMENT), (dict(scales=AT + 1), dg.GEMM_ERR_ALIGNMENT), (dict(y=AT + 1), dg.GEMM_ERR_ALIGNMENT)])
 def test_int4_refuses(change, status):

@@ -76,6 +76,20 @@ def test_gated(t, n, k, group, act, kind):
     check(y, x, codes, scales, z, group, act)
 
 
+@pytest.mark.parametrize("t,n,k,group", [(16, 70, 28672, 128), (16, 33, 45056, 32), (8, 40, 49154, 64), (8, 33, 94208, 32), (1, 17, 94208, 256)])
+def test_long_k(t, n, k, group):
+    """X of a block takes a cluster of eight's shared memory, at last that of whole SMs."""
+    x, codes, scales, z = make(t, n, k, group, torch.bfloat16, True, seed=8)
+    check(dg.int4_matmul(x, codes, scales, group=group, zeros=z), x, codes, scales, z, group)
+
+
+def test_too_long_k_is_refused():
+    for t, k in ((1, 131072), (9, 65536)):
+        x, codes, scales, z = make(t, 8, k, 128, torch.bfloat16, False)
+        with pytest.raises(dg.GemmError):
+            dg.int4_matmul(x, codes, scales)
+
+
 def test_every_code_is_exact():
     """One element of x at a time picks a column of W out: scale times (code - zero), rounded once."""
     k, n = 64, 256
