@@ -2,48 +2,79 @@
 // (include/feedforward.h) and how a call is laid on the device.  The kernel:
 // int4_matmul.cuh.
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_runtime.h>
 
+#include "common.cuh"
 #include "feedforward.h"
 #include "int4_matmul.h"
 #include "serving_host.h"
 
 namespace dgb {
 
-// A tile is 16 rows of W, a stage 256 bytes of each.  Clusters may share K, warps of a block a tile; what is chosen costs the least
-// by a rough count of cycles: a stage takes a warp 1600 with one block on the SM and 2500 with two (twice that with groups of 32,
-// whose factors change every 32 elements; a third more with 16 tokens), a tile's end 600 and 800 more for every doubling of a
-// cluster; X comes into a block's shared memory at 24 bytes a cycle, and the shared memory it takes is missed as L1 cache.
-bool shape_int4(Int4Params* p, bool gated, int sms) {
+// The device's answer, asked for once.
+static int64_t resident(int k_split_log, int per_sm, int device) {
+    static std::atomic<int> known[kMaxDevices][4][3];
+    if (device >= kMaxDevices) return std::max(1, int4_resident(k_split_log, per_sm));
+    std::atomic<int>& at = known[device][k_split_log][per_sm];
+    int n = at.load(std::memory_order_relaxed);
+    if (n == 0) at.store(n = std::max(1, int4_resident(k_split_log, per_sm)), std::memory_order_relaxed);
+    return n;
+}
+
+// A tile is 16 rows of W, a stage 256 bytes of each.  The CTAs of a cluster may share K: X in each CTA's shared memory is what one of
+// them needs of it.  What is chosen costs the least by a count of cycles that was fitted to 560 times of 85 sizes (1, 8 and 16
+// tokens, 608 to 77824 rows, K from 512 to 28672; in the mean the choice takes 1.2 % more than the best one):
+// a stage takes a warp 4700 cycles where it shares the memory with all the others, 2900 where fewer than half of the device's warps
+// have one, a quarter more with groups of 64, 1.9 times with groups of 32, 7 % more with 16 tokens, and longer when the shared memory
+// leaves the L1 cache less room than the loads on their way take; X comes in at 13 bytes a cycle (of two CTAs an SM at less); a
+// tile's sums cost 38 cycles a token, more than twice that in a cluster, a doubling of the cluster 840; 16 warps meet later than 8.
+// Measured, 8 tokens x 4096 -> 4864 and 77824: two CTAs of 8 warps 8.5 and 37.7 us, in clusters of two 7.3 and 45.7, one CTA of 16
+// warps 7.6 and 37.1; 16 tokens -> 77824 in clusters of two 82, one CTA 51.
+bool shape_int4(Int4Params* p, bool gated, const DeviceFacts& dev) {
     constexpr int64_t kStageK = 2 * kInt4RowBytes;
     const int64_t tiles = ((int64_t)p->n + (gated ? 7 : 15)) / (gated ? 8 : 16), stages = (p->k + kStageK - 1) / kStageK;
-    const int64_t tokens = p->tokens > 8 ? 16 : 8, sums = 2 * kInt4Warps * tokens * 17 * 4;
+    const int64_t tokens = p->tokens > 8 ? 16 : 8, slot = tokens * 17 * 4;
     const int64_t chunks = p->group % 128 == 0 ? 4 : p->group % 64 == 0 ? 8 : 16;       // of a stage
-    const int64_t factors = kInt4Warps * chunks * 16 * 8;
-    const double stage_cost = (chunks == 4 ? 1.0 : chunks == 8 ? 1.3 : 2.0) * (tokens > 8 ? 1.35 : 1.0);
+    const double stage_cost = (chunks == 4 ? 1.0 : chunks == 8 ? 1.25 : 1.9) * (tokens > 8 ? 1.07 : 1.0);
     double best = 0;
-    // two blocks an SM, or, of X too long for that, one
-    for (int per_sm = 2; per_sm >= 1 && best == 0; --per_sm) {
+    // two CTAs of 8 warps an SM, one of 16 or, of X too long for its other places, one of 8
+    for (int choice = 0; choice < (best > 0 ? 2 : 3); ++choice) {
+        const int per_sm = choice == 0 ? 2 : 1;
+        const int64_t room = kInt4Room / per_sm, warps = choice == 1 ? 16 : 8;
         for (int ks = 0; ks <= 3 && (1 << ks) <= stages; ++ks) {
-            const int64_t clusters = (per_sm * sms) >> ks, mine = (stages + (1 << ks) - 1) >> ks;
-            const int64_t smem = sums + factors + mine * (kStageK * tokens * 2 + chunks * tokens * 4);
-            if (smem > (per_sm == 2 ? 112 : 224) * 1024) continue;
-            for (int kw = 0; (1 << kw) <= kInt4Warps; ++kw) {
-                const int64_t per_round = kInt4Warps >> kw, blocks = std::min((tiles + per_round - 1) / per_round, clusters);
-                const int64_t rounds = (tiles + per_round * blocks - 1) / (per_round * blocks), per_tile = (mine + (1 << kw) - 1) >> kw;
-                const double beside = (blocks << ks) > sms ? 1.0 : 0.5;        // how full an SM is
-                const double cost = (double)rounds * (per_tile * stage_cost * (700 + 1800 * beside) + 600 + 800 * ks) +
-                                    (double)(mine * kStageK * 2) * (p->tokens / 24.0 + tokens / 60.0);
-                if (best > 0 && cost >= best) continue;
-                best = cost;
-                p->k_split_log = ks;
-                p->k_warps_log = kw;
-                p->rounds = (int)rounds;
-                p->grid = (int)(blocks << ks);
-                p->smem = (int)smem;
+            const int64_t mine = (stages + (1 << ks) - 1) >> ks;
+            const int64_t base = warps * chunks * 16 * 8 + mine * (kStageK * tokens * 2 + chunks * tokens * 4);
+            const int64_t clusters = std::min<int64_t>(tiles, ks == 0 ? per_sm * dev.sms : resident(ks, per_sm, dev.device));
+            const int64_t all = (tiles + clusters - 1) / clusters;      // tiles of a cluster
+            int64_t slots = 2 * warps, round_tiles = all;
+            if (ks > 0) {
+                const int64_t most = kInt4RoundTiles * 8 / tokens;
+                slots = warps - 1 + all;
+                if (all > most || base + slots * slot > room) {
+                    const int64_t fit = std::min(((room - base) / slot) / 2 - (warps - 1), most / 2);
+                    if (fit < 1) continue;
+                    const int64_t rounds = (all + fit - 1) / fit;
+                    round_tiles = (all + rounds - 1) / rounds;
+                    slots = 2 * (warps - 1 + round_tiles);
+                }
             }
+            const int64_t smem = base + slots * slot, units = all * mine, beside = (clusters << ks) > dev.sms ? 2 : 1;
+            if (smem > room) continue;
+            const double cache = std::max(8.0, 256.0 - beside * (double)(smem + 1536) / 1024), full = units * (clusters << ks) > 8 * dev.sms;
+            const double cost = (double)((units + warps - 1) / warps) * stage_cost * (full ? 4700 : 2900) * (1 + 0.44 * std::max(0.0, 64 / cache - 0.89)) +
+                                (double)(mine * kStageK * 2 * p->tokens) / 13 * (beside > 1 ? 2.2 : 1) + 38.0 * all * p->tokens * (ks > 0 ? 2.2 : 1) +
+                                840 * ks + (choice == 1 ? 1000 : 0);
+            if (best > 0 && cost >= best) continue;
+            best = cost;
+            p->k_split_log = ks;
+            p->grid = (int)(clusters << ks);
+            p->round_tiles = (int)round_tiles;
+            p->slots = (int)slots;
+            p->warps_log = warps == 8 ? 3 : 4;
+            p->smem = (int)smem;
         }
     }
     p->tokens_log = 0;
@@ -101,7 +132,7 @@ gemm_status_t int4_matmul_run(const int4_matmul_args_t* args, gemm_stream_t stre
     f.group = a.group;
     f.act = a.activation;
     f.group_magic = (uint32_t)std::min<uint64_t>(UINT32_MAX, (1ull << 32) / (uint32_t)(a.group / 32));
-    if (!shape_int4(&f, gated, dev.sms)) return GEMM_ERR_UNSUPPORTED;       // X does not fit
+    if (!shape_int4(&f, gated, dev)) return GEMM_ERR_UNSUPPORTED;       // X does not fit
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return status_of(a.dtype == GEMM_BF16 ? launch_int4_bf16(f, gated, st) : launch_int4_f16(f, gated, st));
 }

@@ -6,12 +6,23 @@
 // side, straight from global memory: which 16 of K's elements one instruction takes is
 // free as long as both operands agree, so each lane loads consecutive ones of its two
 // rows, 16 of every 64 bytes (four lanes exchange words where groups are shorter than
-// what they load together), and no weight passes through shared memory.  X lies there, laid out once per block so that a lane's part of an
-// instruction pair is one 16-byte load.  A block's warps share a tile's K (several
-// tiles where K is short); a block goes from tile to tile with the next stage's weights
-// on the way, across tiles too, and two blocks an SM cover each other's joins.  The CTAs
-// of a cluster share K when there are few tiles or X does not fit.  All sums are fp32 in
-// a fixed order, so a column's sum never depends on timing.
+// what they load together), and no weight passes through shared memory.  X lies there,
+// laid out once per block so that a lane's part of an instruction pair is one 16-byte
+// load.  (Up to 16 tokens a 128-row tcgen05 tile would be seven eighths empty.)
+//
+// A block's tiles are laid end to end in stages of 512 codes a row and every warp takes
+// an equal run of them, whatever K is: a tile inside a run is stored by its warp, one
+// that runs share after the block's only barrier.  (Tiles dealt out whole, or their
+// stages in turn, need a barrier a tile: 109 us where runs take 94 at 16 x 4096 x
+// 155648.)  The next stage's weights are on the way in registers, across tiles too, and
+// the lines of the one after that into L2.  The CTAs of a cluster share K when there are
+// few tiles or X does not fit, and join once in a few tiles.  All sums are fp32 in an
+// order that the sizes alone decide.
+//
+// Bound by memory at first and by latency at the listed sizes: 8 tokens, 4096 -> 77824
+// columns of a pair 36.9 us (4.5 TB/s, 155648 5.2), 24576 17.1 us (3.1 TB/s: 2.2 of a
+// launch, about 3 of bringing X to 304 blocks, and 5 or 6 tiles a block); one token 4096 x
+// 4096 4.9 us, of which 1.3 are the bytes.  16 tokens: instructions (195 TFLOP/s).
 //
 // A code is a 16-bit float as it stands: the integers 0..255 in the low bits of an f16 are
 // the multiples of its least step 2^-24, of a bf16 those of 2^-133 (subnormal numbers and
@@ -37,7 +48,7 @@
 
 namespace dgb {
 
-constexpr int kInt4Threads = 32 * kInt4Warps;
+constexpr int kInt4MaxThreads = 512;
 constexpr int kInt4Pitch = 17;           // floats between tokens of a warp's sums: 16 rows
 
 // What the sums of code * x are multiplied by when they are complete, its reciprocal, and x as the instructions take it.
@@ -123,7 +134,7 @@ __device__ __forceinline__ int chunk_rank(int t) { return VEC == 2 ? (t & 1) * 2
 
 // VEC: consecutive 32-bit words of a row (eight codes each) that a lane takes: four lanes' make a chunk, which lies in one group.
 template <typename T, int VEC, int NB, bool GATED>
-__global__ void __launch_bounds__(kInt4Threads, 2) int4_matmul_kernel(const __grid_constant__ Int4Params p) {
+__global__ void __launch_bounds__(kInt4MaxThreads, 1) int4_matmul_kernel(const __grid_constant__ Int4Params p) {
     constexpr int kRowWords = kInt4RowBytes / 16;            // of a stage and lane
     constexpr int kChunks = kRowWords / VEC, kChunkK = 32 * VEC, kStageK = kChunks * kChunkK;
     constexpr int kTokens = 8 * NB;
@@ -131,130 +142,123 @@ __global__ void __launch_bounds__(kInt4Threads, 2) int4_matmul_kernel(const __gr
     constexpr int kOut = GATED ? 8 : 16;                    // columns of Y of a tile
 
     extern __shared__ uint4 int4_smem[];
-    float* sums = reinterpret_cast<float*>(int4_smem);       // [2][warp][token][kInt4Pitch]
+    __shared__ int tail_tile[kInt4MaxThreads / 32];      // the tile that a warp's run begins and another's ends, or -1
+    __shared__ int tile_warps[2][2][kInt4RoundTiles / NB];       // of a cluster's round: the tiles' first and last warps
+    const int W = 1 << p.warps_log;
+    float* sums = reinterpret_cast<float*>(int4_smem);       // [p.slots][token][kInt4Pitch]
     // [warp][group of the stage][row]: scale and zero point
-    float2* factors = reinterpret_cast<float2*>(sums + 2 * kInt4Warps * kTokens * kInt4Pitch) + (threadIdx.x >> 5) * (4 * kFactors * 16);
-    float* x_sums = sums + 2 * kInt4Warps * kTokens * kInt4Pitch + kInt4Warps * 4 * kFactors * 16 * 2;      // [chunk][token]: sum of X, in steps
+    float2* factors = reinterpret_cast<float2*>(sums + p.slots * kTokens * kInt4Pitch) + (threadIdx.x >> 5) * (4 * kFactors * 16);
+    float* x_sums = sums + p.slots * kTokens * kInt4Pitch + W * 4 * kFactors * 16 * 2;      // [chunk][token]: sum of X, in steps
     // [stage][word][NB][lane]
 
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int KS = 1 << p.k_split_log, rank = KS > 1 ? (int)cluster_ctarank() : 0;
-    const int KW = 1 << p.k_warps_log, share = warp & (KW - 1), sub = warp >> p.k_warps_log;    // of the warps that share a tile; which of the block's tiles
-    const int per_round = kInt4Warps >> p.k_warps_log;                   // tiles of a block at a time
     const int clusters = (int)gridDim.x >> p.k_split_log, cluster = (int)blockIdx.x >> p.k_split_log;
 
     const int stages = (p.k + kStageK - 1) / kStageK, whole = p.k / kStageK;
     const int s0 = (int)(((int64_t)stages * rank) >> p.k_split_log), s_count = (int)(((int64_t)stages * (rank + 1)) >> p.k_split_log) - s0;
-    const int per_tile = (s_count + KW - 1) >> p.k_warps_log;           // stages of a warp in a tile
-    const int own = s_count > share ? (s_count - share + KW - 1) >> p.k_warps_log : 0;     // of which this one has so many, the rest lie past the end
-    const int tiles = (p.n + kOut - 1) / kOut;
-    const int rounds = p.rounds;
+    const int tiles = (p.n + kOut - 1) / kOut, my_tiles = (tiles - 1 - cluster) / clusters + 1;     // cluster, cluster + clusters, ...
     uint4* x_smem = reinterpret_cast<uint4*>(x_sums + s_count * kChunks * kTokens);
-    // The warp's tile in round r; there may be none.  Its stages in this CTA's part of K: share, share + KW, ...
-    auto tile_of = [&](int r) { return (r * clusters + cluster) * per_round + sub; };
+    // Every warp has an equal run of all tiles' stages, tile after tile.  In a cluster: of a round's, up to p.round_tiles tiles with
+    // their stages in this CTA's part of K.
+    auto tiles_of = [&](int r) { return min(p.round_tiles, my_tiles - r * p.round_tiles); };
+    auto units_to = [&](int all, int w) { return all * w >> p.warps_log; };
     // Row g + 8 i of a tile; rows past the last are that one again and are not stored.
     auto row_of = [&](int tile, int i) {
         return GATED ? (int64_t)i * p.n + min(tile * kOut + g, p.n - 1) : (int64_t)min(tile * kOut + 8 * i + g, p.n - 1);
     };
-    // ---------------------------------------------------------------- weights, a stage ahead in registers
-    int load_round = 0, load_at = 0;
-    bool load_tile = false;
+    // ---------------------------------------------------------------- weights, scales and zero points, a stage ahead in registers
+    // A lane of row g (and g + 8) has 16 bytes of every 64 of the row's codes and the scales of the stage's groups t, t + 4, ...; they
+    // stay as loaded until the stage comes, as whatever uses them would wait for them.
+    int a_round = 0, a_left = 0, a_tile = 0, a_stage = 0;       // what is loaded next: a tile of the round and a stage; a_left: 0 = nothing
     const uint8_t* from[2];
-    auto set_rows = [&] {
-        const int tile = tile_of(load_round);
-        load_tile = load_round < rounds && tile < tiles;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            from[i] = static_cast<const uint8_t*>(p.w) + row_of(tile, i) * p.ldw_bytes + (int64_t)(s0 + share) * kInt4RowBytes + 16 * t;
-    };
-    // The lines of the stage that is loaded next into L2, four lanes a row pair's four lines: its loads are issued a stage later and
-    // used a stage after that, which alone does not cover DRAM's latency under load.
-    auto prefetch = [&] {
-        if (load_tile && load_at < own && s0 + share + (load_at << p.k_warps_log) < whole)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"((t & 1 ? from[1] : from[0]) + (128 * (t >> 1) - 16 * t)));
-    };
-    auto load = [&](uint4 (&w)[2][kRowWords / 4]) {       // 16 bytes of every 64 of a row
-        if (load_tile && load_at < own) {
-            const int stage = s0 + share + (load_at << p.k_warps_log);
-            if (stage < whole) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int s = 0; s < kRowWords / 4; ++s) w[i][s] = load_once16(from[i] + 64 * s);
-            } else {
-                const int left = p.k / 2 - stage * kInt4RowBytes - 16 * t;
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int s = 0; s < kRowWords / 4; ++s) w[i][s] = load_clipped_bytes(from[i] + 64 * s, left - 64 * s);
-            }
-        }
-        if (++load_at < per_tile) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) from[i] += KW * kInt4RowBytes;
-        } else {
-            load_at = 0;
-            ++load_round;
-            set_rows();
-        }
-        prefetch();
-    };
-    // ---------------------------------------------------------------- scales and zero points, a stage ahead in registers
-    // A lane of row g (and g + 8) has the stage's groups t, t + 4, ...; they stay as loaded until the stage comes, as whatever uses
-    // them would wait for them.
-    int look_round = 0, look_at = 0;
-    bool look_tile = false;
+    const uint16_t* scale_row[2];
+    const uint8_t* zero_row[2];
+    uint4 next[2][kRowWords / 4];
     uint16_t scale_next[2][kFactors] = {};
     uint8_t zero_next[2][kFactors] = {};
     int in_group_next = 0;      // where in its group the stage begins, in 32s
-    const uint16_t* scale_row[2];
-    const uint8_t* zero_row[2];
     const int last_group = (p.k - 1) / p.group, group_units = p.group / 32;
-    auto set_looks = [&] {
-        const int tile = tile_of(look_round);
-        look_tile = look_round < rounds && tile < tiles;
+    auto set_rows = [&] {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int64_t row = row_of(tile, i);
+            const int64_t row = row_of((a_round * p.round_tiles + a_tile) * clusters + cluster, i);
+            from[i] = static_cast<const uint8_t*>(p.w) + row * p.ldw_bytes + (int64_t)(s0 + a_stage) * kInt4RowBytes + 16 * t;
             scale_row[i] = static_cast<const uint16_t*>(p.scales) + row * p.ld_scales;
             zero_row[i] = p.zeros + (p.zeros ? row * p.ld_zeros : 0);
         }
     };
-    auto look = [&] {
-        if (look_tile && look_at < own) {
-            const uint32_t unit = (uint32_t)(s0 + share + (look_at << p.k_warps_log)) * (kStageK / 32);
-            int first = (int)__umulhi(unit, p.group_magic);
-            in_group_next = (int)unit - first * group_units;
-            if (in_group_next >= group_units) {
-                in_group_next -= group_units;
-                ++first;
-            }
-#pragma unroll
-            for (int h = 0; h < kFactors; ++h) {
-                const int gi = min(first + t + 4 * h, last_group);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    scale_next[i][h] = __ldg(scale_row[i] + gi);
-                    zero_next[i][h] = p.zeros ? __ldg(zero_row[i] + gi) : (uint8_t)8;
-                }
-            }
-        }
-        if (++look_at == per_tile) {
-            look_at = 0;
-            ++look_round;
-            set_looks();
+    auto seek = [&] {       // the warp's first from round a_round on
+        for (int count; (count = tiles_of(a_round)) > 0; ++a_round) {
+            const int all = count * s_count, u0 = units_to(all, warp);
+            if ((a_left = units_to(all, warp + 1) - u0) == 0) continue;
+            a_tile = (int)((unsigned)u0 / (unsigned)s_count);
+            a_stage = u0 - a_tile * s_count;
+            set_rows();
+            return;
         }
     };
+    // The lines of the stage that is loaded next into L2, four lanes a row pair's four lines: its loads are issued a stage later and
+    // used a stage after that, which alone does not cover DRAM's latency under load.
+    auto prefetch = [&] {
+        if (a_left > 0 && s0 + a_stage < whole)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"((t & 1 ? from[1] : from[0]) + (128 * (t >> 1) - 16 * t)));
+    };
+    auto load_codes = [&] {
+        if (a_left == 0) return;
+        const int stage = s0 + a_stage;
+        if (stage < whole) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int s = 0; s < kRowWords / 4; ++s) next[i][s] = load_once16(from[i] + 64 * s);
+        } else {
+            const int left = p.k / 2 - stage * kInt4RowBytes - 16 * t;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int s = 0; s < kRowWords / 4; ++s) next[i][s] = load_clipped_bytes(from[i] + 64 * s, left - 64 * s);
+        }
+    };
+    auto load_factors = [&] {       // and on to the next stage
+        if (a_left == 0) return;
+        const uint32_t unit = (uint32_t)(s0 + a_stage) * (kStageK / 32);
+        int first = (int)__umulhi(unit, p.group_magic);
+        in_group_next = (int)unit - first * group_units;
+        if (in_group_next >= group_units) {
+            in_group_next -= group_units;
+            ++first;
+        }
+#pragma unroll
+        for (int h = 0; h < kFactors; ++h) {
+            const int gi = min(first + t + 4 * h, last_group);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                scale_next[i][h] = __ldg(scale_row[i] + gi);
+                zero_next[i][h] = p.zeros ? __ldg(zero_row[i] + gi) : (uint8_t)8;
+            }
+        }
+        if (--a_left == 0) {
+            ++a_round;
+            seek();
+        } else if (++a_stage == s_count) {
+            a_stage = 0;
+            ++a_tile;
+            set_rows();
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) from[i] += kInt4RowBytes;
+        }
+        prefetch();
+    };
 
-    uint4 next[2][kRowWords / 4];
     uint32_t now[2][kRowWords];
-    set_rows();
+    seek();
     prefetch();         // while the kernel before this one may still run: it returns nothing, so it does not matter who writes W
     griddep_wait();
     griddep_launch_dependents();
-    load(next);
-    set_looks();
-    look();
+    load_codes();
+    load_factors();
     // X of this CTA's part of K and its sums over the chunks, a quarter of a token's chunk at a time; zeros past K.  What lies in the
     // places of tokens past the last is never stored: a column of the products depends on its own token alone.
     {
@@ -262,12 +266,12 @@ __global__ void __launch_bounds__(kInt4Threads, 2) int4_matmul_kernel(const __gr
         const int chunks = s_count * kChunks, quarters = (chunks * 4) << p.tokens_log;
         const uint16_t* x = static_cast<const uint16_t*>(p.x) + s0 * kStageK;
         const int k_left = p.k - s0 * kStageK;
-        for (int all0 = 0; all0 < quarters; all0 += kBatch * kInt4Threads) {       // the same turns in every lane: they exchange sums
+        for (int all0 = 0; all0 < quarters; all0 += kBatch * (int)blockDim.x) {       // the same turns in every lane: they exchange sums
             const int e0 = all0 + (int)threadIdx.x;
             uint4 q[kBatch][VEC];
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
-                const int e = e0 + b * kInt4Threads, m = (e >> 2) & ((1 << p.tokens_log) - 1), c = e >> (2 + p.tokens_log);
+                const int e = e0 + b * (int)blockDim.x, m = (e >> 2) & ((1 << p.tokens_log) - 1), c = e >> (2 + p.tokens_log);
                 const bool there = e < quarters && m < p.tokens;
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
@@ -278,8 +282,8 @@ __global__ void __launch_bounds__(kInt4Threads, 2) int4_matmul_kernel(const __gr
             }
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
-                const int e = e0 + b * kInt4Threads, m = (e >> 2) & ((1 << p.tokens_log) - 1), c = e >> (2 + p.tokens_log);
-                if (all0 + b * kInt4Threads >= quarters) break;
+                const int e = e0 + b * (int)blockDim.x, m = (e >> 2) & ((1 << p.tokens_log) - 1), c = e >> (2 + p.tokens_log);
+                if (all0 + b * (int)blockDim.x >= quarters) break;
                 float sum = 0.f;
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
@@ -301,39 +305,46 @@ __global__ void __launch_bounds__(kInt4Threads, 2) int4_matmul_kernel(const __gr
     }
     __syncthreads();
 
-    float acc[NB][4];
+    for (int r = 0, count; (count = tiles_of(r)) > 0; ++r) {
+        const int all = count * s_count;
+        float* round_sums = sums + (r & 1) * (p.slots / 2 * kTokens * kInt4Pitch);
+        int* first_warp = tile_warps[r & 1][0];
+        int* last_warp = tile_warps[r & 1][1];
+        const int u0 = units_to(all, warp), u1 = units_to(all, warp + 1);
+        int tile = (int)((unsigned)u0 / (unsigned)s_count), at = u0 - tile * s_count;      // of the round's tiles; of this CTA's stages
+        float acc[NB][4];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[nb][i] = 0.f;
-    int r = 0, at = 0;
-    bool tile_here = tile_of(0) < tiles;
-    const int all_stages = rounds * per_tile;
-    for (int f = 0; f < all_stages; ++f) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int s = 0; s < kRowWords / 4; ++s) {
-                uint32_t w[4] = {next[i][s].x, next[i][s].y, next[i][s].z, next[i][s].w};
-                deal_words<VEC>(w, t);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) now[i][4 * s + j] = w[j];
-            }
-        load(next);
-        __syncwarp();           // every lane is done with the stage before
-#pragma unroll
-        for (int h = 0; h < kFactors; ++h)
+            for (int i = 0; i < 4; ++i) acc[nb][i] = 0.f;
+        if (lane == 0) {
+            if (KS == 1) tail_tile[warp] = -1;
+            else if (at == 0 && u0 < u1) first_warp[tile] = warp;
+        }
+        bool begun = at == 0;       // this run has the tile's first stage
+        for (int u = u0; u < u1; ++u) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                factors[(t + 4 * h) * 16 + 8 * i + g] = make_float2(unpack2<T>(scale_next[i][h]).x, (float)zero_next[i][h]);
-        __syncwarp();
-        int in_group = in_group_next;
-        look();
-        if (tile_here && at < own) {
-            const int in = share + (at << p.k_warps_log);
-            const uint4* x = x_smem + (size_t)in * (kRowWords * NB * 32) + lane;
-            const float* sx = x_sums + in * (kChunks * kTokens) + 2 * t;
-            const int chunks = (p.k - (s0 + in) * kStageK + kChunkK - 1) / kChunkK;     // that K reaches
+#pragma unroll
+                for (int s = 0; s < kRowWords / 4; ++s) {
+                    uint32_t w[4] = {next[i][s].x, next[i][s].y, next[i][s].z, next[i][s].w};
+                    deal_words<VEC>(w, t);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) now[i][4 * s + j] = w[j];
+                }
+            load_codes();
+            __syncwarp();           // every lane is done with the stage before
+#pragma unroll
+            for (int h = 0; h < kFactors; ++h)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    factors[(t + 4 * h) * 16 + 8 * i + g] = make_float2(unpack2<T>(scale_next[i][h]).x, (float)zero_next[i][h]);
+            __syncwarp();
+            int in_group = in_group_next;
+            load_factors();
+            const uint4* x = x_smem + (size_t)at * (kRowWords * NB * 32) + lane;
+            const float* sx = x_sums + at * (kChunks * kTokens) + 2 * t;
+            const int chunks = (p.k - (s0 + at) * kStageK + kChunkK - 1) / kChunkK;     // that K reaches
             int gi = 0;
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
@@ -376,66 +387,120 @@ __global__ void __launch_bounds__(kInt4Threads, 2) int4_matmul_kernel(const __gr
                     ++gi;
                 }
             }
-        }
-        if (++at < per_tile) continue;
-        at = 0;
-
-        // ------------------------------------------------------------ a tile's end: the warps' sums, then the cluster's, then Y
-        float* mine = sums + (r & 1) * (kInt4Warps * kTokens * kInt4Pitch);
+            if (++at < s_count && u + 1 < u1) continue;
+            // the tile's or the run's end
+            const bool ended = at == s_count;
+            if (KS == 1 && begun && ended) {
+                const int n = ((tile * clusters) + cluster) * kOut + g;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+                for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                mine[(warp * kTokens + nb * 8 + 2 * t + (i & 1)) * kInt4Pitch + (i >> 1) * 8 + g] = acc[nb][i];
-                acc[nb][i] = 0.f;
+                    for (int i = 0; i < 2; ++i) {
+                        const int m = nb * 8 + 2 * t + i;
+                        const float v0 = acc[nb][i] * CodeScale<T>::back, v1 = acc[nb][2 + i] * CodeScale<T>::back;
+                        T* y = static_cast<T*>(p.y) + (int64_t)m * p.ldy + n;
+                        if (m < p.tokens && n < p.n) {
+                            if constexpr (GATED) *y = (T)(activate(p.act, v0) * v1);
+                            else *y = (T)v0;
+                        }
+                        if (!GATED && m < p.tokens && n + 8 < p.n) y[8] = (T)v1;
+                    }
+            } else {
+                // A run has two parts of tiles at most, of the tile that it does not begin and of the one that it does not end.  In a
+                // cluster all sums go this way: from one part to the next either the warp or the tile goes up by one, or both.
+                float* mine = round_sums + (KS == 1 ? 2 * warp + begun : warp + tile) * (kTokens * kInt4Pitch);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mine[(nb * 8 + 2 * t + (i & 1)) * kInt4Pitch + (i >> 1) * 8 + g] = acc[nb][i];
+                if (lane == 0) {
+                    if (KS == 1) {
+                        if (begun) tail_tile[warp] = tile;
+                    } else if (ended) {
+                        last_warp[tile] = warp;
+                        if (u + 1 < u1) first_warp[tile + 1] = warp;
+                    }
+                }
             }
-        // the tile's warps meet; a buffer is written again two rounds on, after all have met once more
-        const int threads = 32 * KW, thread = share * 32 + lane;
-        if (KW == 1) __syncwarp();
-        else asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "r"(threads) : "memory");
-        float* tile_sums = mine + sub * KW * kTokens * kInt4Pitch;
-        auto add_warps = [&](int m, int c) {
-            float v = tile_sums[m * kInt4Pitch + c];
-#pragma unroll 4
-            for (int w = 1; w < KW; ++w) v += tile_sums[(w * kTokens + m) * kInt4Pitch + c];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[nb][i] = 0.f;
+            at = 0;
+            begun = true;
+            ++tile;
+        }
+        __syncthreads();
+
+        // ------------------------------------------------------------ the warps' sums, then the cluster's, then Y
+        const int c = lane & 15, half = lane >> 4;       // a row of the tile; one of two tokens
+        auto finish = [&](int j, int m, bool mine, float v) {
+            v *= CodeScale<T>::back;
+            const int n = ((r * p.round_tiles + j) * clusters + cluster) * kOut + c % kOut;
+            if constexpr (GATED) {
+                const float u = __shfl_down_sync(0xffffffffu, v, 8);       // the column's other sum
+                if (mine && c < 8 && n < p.n) static_cast<T*>(p.y)[(int64_t)m * p.ldy + n] = (T)(activate(p.act, v) * u);
+            } else if (mine && n < p.n) {
+                static_cast<T*>(p.y)[(int64_t)m * p.ldy + n] = (T)v;
+            }
+        };
+        if (KS == 1) {
+            // tiles that a run begins and later ones end, two tokens of one at a time
+            const int pairs_log = max(0, p.tokens_log - 1);
+            for (int q = warp; q < W << pairs_log; q += W) {
+                const int w = q >> pairs_log, j = tail_tile[w], m = 2 * (q - (w << pairs_log)) + half;
+                if (j < 0) continue;
+                const bool mine = m < p.tokens;
+                float v = 0.f;
+                if (mine) {
+                    v = sums[((2 * w + 1) * kTokens + m) * kInt4Pitch + c];
+                    const int end = (j + 1) * s_count;
+                    for (int o0 = w + 1; o0 < W && units_to(all, o0) < end; o0 += 4)
+#pragma unroll
+                        for (int o = o0; o < o0 + 4; ++o) {
+                            const int from = units_to(all, o);
+                            if (o < W && from < end && from < units_to(all, o + 1)) v += sums[(2 * o * kTokens + m) * kInt4Pitch + c];
+                        }
+                }
+                finish(j, m, mine, v);
+            }
+            return;
+        }
+        // The first slot of tile j is its first warp's; warps without units have none.
+        auto add_warps = [&](int j, int m, int c) {
+            float v = 0.f;
+            for (int w = first_warp[j]; w <= last_warp[j]; ++w)
+                if (units_to(all, w) < units_to(all, w + 1)) v += round_sums[((w + j) * kTokens + m) * kInt4Pitch + c];
             return v;
         };
-        int m0 = 0, m1 = p.tokens;
-        if (KS > 1) {
-            // in the place of the first warp's sums; each is read and written by one thread
-            for (int e = thread; e < p.tokens * 16; e += threads) tile_sums[e / 16 * kInt4Pitch + e % 16] = add_warps(e / 16, e % 16);
-            // a CTA that passes has everyone's sums of this round, and everyone has read those of the round before
-            cluster_sync();
-            m0 = p.tokens * rank >> p.k_split_log;
-            m1 = p.tokens * (rank + 1) >> p.k_split_log;
+        const int rows = count << p.tokens_log;       // tile j's token m is row j << tokens_log | m
+        // in the place of the first warp's sums; each is read and written by one thread
+        for (int q = 2 * warp + half; q < rows; q += 2 * W) {
+            const int j = q >> p.tokens_log, m = q & ((1 << p.tokens_log) - 1);
+            if (m < p.tokens && first_warp[j] < last_warp[j]) round_sums[((first_warp[j] + j) * kTokens + m) * kInt4Pitch + c] = add_warps(j, m, c);
         }
-        for (int e0 = m0 * 16; e0 < m1 * 16; e0 += threads) {
-            const int e = e0 + thread, m = min(e / 16, m1 - 1), c = e % 16;
+        cluster_sync();
+        for (int q0 = 2 * warp; (q0 << p.k_split_log) < rows; q0 += 2 * W) {
+            const int q = ((q0 + half) << p.k_split_log) + rank, j = q >> p.tokens_log, m = q & ((1 << p.tokens_log) - 1);
+            const bool mine = q < rows && m < p.tokens;
             float v = 0.f;
-            if (KS == 1) {
-                v = add_warps(m, c);
-            } else {
-                const uint32_t part = smem_u32(tile_sums + m * kInt4Pitch + c);
+            if (mine) {
+                // the CTAs' parts of K may differ by a stage, and so the places of their sums
                 for (int o = 0; o < KS; ++o) {
+                    const int so = (int)(((int64_t)stages * (o + 1)) >> p.k_split_log) - (int)(((int64_t)stages * o) >> p.k_split_log);
+                    const int w = so == s_count ? first_warp[j] : (W * (j * so + 1) - 1) / (count * so);
                     float s;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(s) : "r"(map_to_cta(part, (uint32_t)o)));
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                 : "=f"(s)
+                                 : "r"(map_to_cta(smem_u32(round_sums + ((w + j) * kTokens + m) * kInt4Pitch + c), (uint32_t)o)));
                     v += s;
                 }
             }
-            v *= CodeScale<T>::back;
-            const int n = tile_of(r) * kOut + c % kOut;
-            const bool there = e < m1 * 16 && n < p.n;
-            if constexpr (GATED) {
-                const float u = __shfl_down_sync(0xffffffffu, v, 8);       // the column's other sum
-                if (there && c < 8) static_cast<T*>(p.y)[(int64_t)m * p.ldy + n] = (T)(activate(p.act, v) * u);
-            } else if (there) {
-                static_cast<T*>(p.y)[(int64_t)m * p.ldy + n] = (T)v;
-            }
+            finish(j, m, mine, v);
         }
-        ++r;
-        tile_here = tile_of(r) < tiles;
+        // A round's sums are written over two rounds on, when everyone has passed the barrier after them once more.
     }
-    if (KS > 1) cluster_sync_relaxed();     // peers have read this CTA's sums
+    cluster_sync_relaxed();     // peers have read this CTA's sums
 }
 
 template <typename T, int VEC, int NB, bool GATED>
@@ -446,7 +511,7 @@ static cudaError_t launch_int4_as(const Int4Params& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.grid);
-    cfg.blockDim = dim3(kInt4Threads);
+    cfg.blockDim = dim3(32u << p.warps_log);
     cfg.dynamicSmemBytes = (size_t)p.smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -459,6 +524,27 @@ static cudaError_t launch_int4_as(const Int4Params& p, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = p.k_split_log > 0 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+// How many clusters of 2^k_split_log CTAs the device holds at once, `per_sm` CTAs an SM by their shared memory.
+template <typename T>
+static int resident_int4(int k_split_log, int per_sm) {
+    auto kern = int4_matmul_kernel<T, 4, 1, false>;
+    const size_t smem = (size_t)kInt4Room / per_sm;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kInt4Room) != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1u << k_split_log);
+    cfg.blockDim = dim3((unsigned)kInt4MaxThreads / per_sm);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1u << k_split_log;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess ? n : 0;
 }
 
 template <typename T, int VEC>

@@ -9,7 +9,9 @@ namespace dgb {
 
 constexpr int kInt4TokensMax = 16;
 constexpr int kInt4RowsMax = 1 << 30;     // of Y's columns: tiles past the last are counted too
-constexpr int kInt4Warps = 8;
+constexpr int kInt4RoundTiles = 16;     // tiles of a cluster between two joins, at most; of 9 to 16 tokens half as many, of more
+                                        // rounds than one half as many again
+constexpr int kInt4Room = 224 * 1024;   // shared memory of an SM that its blocks take
 constexpr int kInt4RowBytes = 256;      // a stage: so many bytes of each of a tile's 16 rows
 
 struct Int4Params {
@@ -25,11 +27,13 @@ struct Int4Params {
     uint32_t group_magic;       // floor(2^32 / (group / 32)), at most 2^32 - 1
     int32_t tokens_log;         // tokens, rounded up to a power of two
     int32_t k_split_log;        // CTAs (one cluster) that share K
-    int32_t k_warps_log;        // warps of a CTA that share a tile's part of K
-    int32_t rounds;             // tiles that a warp goes through
+    int32_t warps_log;          // warps of a CTA: 8, two CTAs an SM, or 16
+    int32_t round_tiles;        // tiles of a cluster between two joins; without clusters all of a CTA's
+    int32_t slots;              // places of a warp's sums of a tile, of more rounds than one for two rounds
     int32_t grid, smem;
 };
 
+int int4_resident(int k_split_log, int per_sm);      // clusters of 2^k_split_log CTAs that the device holds at once
 cudaError_t launch_int4_bf16(const Int4Params& p, bool gated, cudaStream_t stream);
 cudaError_t launch_int4_f16(const Int4Params& p, bool gated, cudaStream_t stream);
 

@@ -189,9 +189,13 @@ def _new_rows(like, dtype, to):
     """An empty tensor of like's shape whose rows are a multiple of `to` elements apart."""
     _need(like.dim() == 2, "x: [tokens, columns] expected")
     rows, cols = like.shape
-    wide = -(-cols // to) * to
-    t = like.new_empty(rows, wide, dtype=dtype)
-    return t if wide == cols else t[:, :cols]
+    return _new_matrix(like, rows, cols, -(-cols // to) * to, dtype)
+
+
+def _new_matrix(like, rows, cols, ld, dtype):
+    """An empty [rows, cols] tensor on like's device whose rows are ld elements apart."""
+    t = like.new_empty(rows, ld, dtype=dtype)
+    return t if ld == cols else t[:, :cols]
 
 
 def _checked_norm_backward(here, eps, dy, h, weight, d_sum, dh):
@@ -300,7 +304,6 @@ class GatedPlan(_Plan):
     def backward(self, d_out, x, w, gate_up, dx=None, dw=None, *, d_gate_up=None, need_dx=True, need_dw=True, stream=None):
         """Gradients of run(): (of x, of w), None where it is not needed.  gate_up: what run() kept; d_gate_up: scratch of its
         shape (default: made here), may be gate_up itself, which is then overwritten."""
-        import torch
         if stream is not None and x.is_cuda and stream != current_stream_handle():
             with _as_current(stream, x.device):
                 return self.backward(d_out, x, w, gate_up, dx, dw, d_gate_up=d_gate_up, need_dx=need_dx, need_dw=need_dw)
@@ -308,11 +311,11 @@ class GatedPlan(_Plan):
         _need(d.gradients == 1, "backward: the plan was made without gradients")
         types = _torch_types()
         if d_gate_up is None:
-            d_gate_up = torch.empty(d.tokens, d.ld_gate_up, dtype=types[d.dtype], device=x.device)[:, : 2 * d.features]
+            d_gate_up = _new_matrix(x, d.tokens, 2 * d.features, d.ld_gate_up, types[d.dtype])
         if dx is None and need_dx:
-            dx = torch.empty(d.tokens, d.ld_dx, dtype=types[d.dtype], device=x.device)[:, : d.k]
+            dx = _new_matrix(x, d.tokens, d.k, d.ld_dx, types[d.dtype])
         if dw is None and need_dw:
-            dw = torch.empty(2 * d.features, d.ld_dw, dtype=types[d.dtype_dw], device=x.device)[:, : d.k]
+            dw = _new_matrix(x, 2 * d.features, d.k, d.ld_dw, types[d.dtype_dw])
         if not need_dx:
             dx = None
         if not need_dw:
