@@ -182,6 +182,29 @@ gemm_status_t pipeline_params(gated_plan_s* plan, const void* x, const void* w, 
     return s;
 }
 
+// The pipeline's tiles where 512-wide ones of SM pairs, which the planner takes for a product of this size, would fill two waves at
+// most: an epilogue that ends in half as many columns hides less behind the next tile, and whole waves count for more than tiles.  A
+// wave takes so many microseconds along a K of 4096, and a launch some beside.  Fitted to 65 sizes (130 to 3000 tokens, K 1024 to
+// 4096): 130 x 4096 -> 2 x 4096 19.2 us in pairs, 21.2 in single CTAs; 512 x 4096 -> 2 x 12288 68.7 us 256 wide in three waves, 78.1
+// 512 wide in two; 640 x 1024 -> 2 x 3584 11.3 us in single CTAs, 15.5 in pairs.  Splitting the last wave along K, whose partial sums
+// are of both kinds, cost 3 to 5 us there.
+void choose_tiles(const gated_desc_t& d, int sms, gemm_desc_t* f) {
+    const auto waves = [&](int group, int64_t n) {
+        const int64_t tiles = (d.tokens + 128 * group - 1) / (128 * group) * ((2 * d.features + n - 1) / n), at_once = sms / group;
+        return (double)((tiles + at_once - 1) / at_once);
+    };
+    if (d.tokens <= 128 || d.features < 128 || waves(2, 512) > 2) return;
+    struct Tiles { int32_t n; int group; double wave, beside; };
+    double best = 0;
+    for (const Tiles& o : {Tiles{512, 2, 36.5, 6.4}, Tiles{256, 2, 19.0, 6.4}, Tiles{128, 2, 11.2, 6.4}, Tiles{256, 1, 23.5, 5.0}, Tiles{128, 1, 15.0, 5.0}}) {
+        const double cost = waves(o.group, o.n) * o.wave * (double)d.k / 4096 + o.beside;
+        if (best > 0 && cost >= best) continue;
+        best = cost;
+        f->tile_n = o.n;
+        f->flags = GEMM_FLAG_NO_SINGLE_CTA | (o.group == 2 ? GEMM_FLAG_CTA_GROUP_2 : GEMM_FLAG_CTA_GROUP_1) | (o.n < 512 ? GEMM_FLAG_NO_STREAM_K : 0u);
+    }
+}
+
 // The gradients' products have MN-major operands, for which the planner does not choose 512-wide tiles by itself. They take them where
 // those fill their last wave well enough to make up for its not being split along K as that of 256-wide tiles is: 16384 x 4096 x 4096
 // (7 waves, 96 % full) 298 us, 352 with 256; the whole backward pass of 2048 and 8192 tokens, 4096 -> 2 x 8192, 323 and 1247 us, 349 and
@@ -233,6 +256,7 @@ gemm_status_t gated_plan_create(gated_plan_t* out, const gated_desc_t* desc) {
     f.tile_n = d.tile_n == 0 && d.features < 128 ? 128 : d.tile_n;     // tiles hold whole 64-column chunks of both kinds
     f.stages = d.stages;
     f.max_ctas = d.max_ctas;
+    if (!forced && !p->info.few_tiles) choose_tiles(d, dev.sms, &f);
     s = make_product(&p->forward, &p->info.product, f);
     if (s == GEMM_OK && p->info.few_tiles) {
         // what runs instead

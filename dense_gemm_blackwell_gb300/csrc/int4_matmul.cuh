@@ -21,7 +21,7 @@
 //
 // Bound by memory at first and by latency at the listed sizes: 8 tokens, 4096 -> 77824
 // columns of a pair 36.9 us (4.5 TB/s, 155648 5.2), 24576 17.1 us (3.1 TB/s: 2.2 of a
-// launch, about 3 of bringing X to 304 blocks, and 5 or 6 tiles a block); one token 4096 x
+// launch, about 3 of bringing X to every block, and 10 or 11 tiles an SM); one token 4096 x
 // 4096 4.9 us, of which 1.3 are the bytes.  16 tokens: instructions (195 TFLOP/s).
 //
 // A code is a 16-bit float as it stands: the integers 0..255 in the low bits of an f16 are
