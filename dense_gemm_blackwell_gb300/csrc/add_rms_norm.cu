@@ -9,6 +9,12 @@
 // row's sums take shuffles and one exchange.  A scale block of 128 (32) columns is
 // 16 (4) neighbouring lanes, so its largest magnitude needs shuffles only.  Few
 // rows take one vector a thread (the time is latency), many rows more.
+//
+// Measured: 8192 x 8192 bf16 with a residual to codes with fp32 scales 73 us, 6.4 TB/s of
+// the 471 MB it needs (the copy rate allows 69; 67 % of the issue slots); 1231 x 2893 f16
+// to MXFP8 codes 7.5 us; 8 x 4096 2.4 us, a launch.  Short rows are bound by
+// instructions, which a row's sums and a block's scale cost whatever its length: 32768 x
+// 1024 to MXFP8 31 us where the bytes take 15.
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
@@ -263,6 +269,9 @@ struct NormGradParams {
     float* partials;        // [blocks][hidden rounded up to 8], or NULL
 };
 
+// 8192 x 4096 bf16 48 us with both kernels, 5.6 TB/s (the bytes take 40): instruction issue (58 % of the slots) at 16 warps an SM, whose
+// registers hold the weight gradients; three and four blocks an SM spilled.  The join is 4 of the 48.
+//
 // dh = d_sum + r dy w - h r^3 mean(dy w h): one exchange for both sums of a row.  A thread keeps the same columns in every row
 // that its block takes and sums their weight gradients in registers.
 template <typename T, int VPT, int S>
