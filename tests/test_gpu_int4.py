@@ -76,6 +76,20 @@ def test_gated(t, n, k, group, act, kind):
     check(y, x, codes, scales, z, group, act)
 
 
+@pytest.mark.parametrize("t,n,k,group,act", [
+    (1, 40000, 512, 128, None), (5, 20011, 1536, 64, "silu"), (3, 9000, 700, 32, None), (16, 8200, 28672, 128, None), (12, 4100, 28672, 128, "gelu"),
+    (8, 16411, 4096, 128, "silu"), (11, 30000, 2560, 96, None)])
+def test_many_tiles_a_block(t, n, k, group, act):
+    """Tiles inside a warp's run, tiles that several warps share, and, of a K that a cluster shares, several joins."""
+    x, codes, scales, z = make(t, n if act is None else 2 * n, k, group, torch.bfloat16 if t % 2 else torch.float16, True, seed=9)
+    y = dg.int4_matmul(x, codes, scales, group=group, zeros=z, activation=act)
+    for at in range(0, n, 4096):        # the 64-bit form of some rows at a time
+        pick = torch.arange(at, min(n, at + 4096), device="cuda")
+        rows = pick if act is None else torch.cat((pick, pick + n))
+        check(y[:, pick], x, codes[rows], scales[rows], z[rows], group, act)
+    assert torch.equal(dg.int4_matmul(x, codes, scales, group=group, zeros=z, activation=act), y)
+
+
 @pytest.mark.parametrize("t,n,k,group", [(16, 70, 28672, 128), (16, 33, 45056, 32), (8, 40, 49154, 64), (8, 33, 94208, 32), (1, 17, 94208, 256)])
 def test_long_k(t, n, k, group):
     """X of a block takes a cluster of eight's shared memory, at last that of whole SMs."""
