@@ -14,7 +14,8 @@
 // the 471 MB it needs (the copy rate allows 69; 67 % of the issue slots); 1231 x 2893 f16
 // to MXFP8 codes 7.5 us; 8 x 4096 2.4 us, a launch.  Short rows are bound by
 // instructions, which a row's sums and a block's scale cost whatever its length: 32768 x
-// 1024 to MXFP8 31 us where the bytes take 15.
+// 1024 without a residual to MXFP8 31 us where the bytes take 15 (one warp a row, four
+// vectors a lane: 27, but 9.2 us instead of 7.6 at 4096 rows with a residual).
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
