@@ -219,23 +219,27 @@ struct SingleParams {
 
 // ---------------------------------------------------------------- host helpers
 
-// Raise a kernel's dynamic shared-memory limit only when a launch needs more
-// than any earlier launch on this device did (the attribute call costs a
-// driver round trip; launches reuse the raised limit).
+// Raise a kernel's dynamic shared-memory limit, once per device (the attribute
+// call costs a driver round trip) and to all that a block may opt in to beside
+// the kernel's static shared memory: every caller sets the same value, so
+// neither threads that meet here nor a second record of the same kernel can
+// leave a limit below what another launch has checked.  `done`: what is set.
 constexpr int kMaxDevices = 64;
 template <typename Kernel>
 inline cudaError_t ensure_smem_limit(Kernel kern, size_t smem, std::atomic<int> (&done)[kMaxDevices]) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxDevices)
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (done[dev].load(std::memory_order_acquire) >= (int)smem) return cudaSuccess;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess) {
-        int prev = done[dev].load();
-        while (prev < (int)smem && !done[dev].compare_exchange_weak(prev, (int)smem)) {}
-    }
+    const bool kept = dev >= 0 && dev < kMaxDevices;
+    if (kept && (size_t)done[dev].load(std::memory_order_acquire) >= smem) return cudaSuccess;
+    cudaFuncAttributes facts;
+    int optin = 0;
+    if ((e = cudaFuncGetAttributes(&facts, kern)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
+    const int all = optin - (int)facts.sharedSizeBytes;
+    if (smem > (size_t)all) return cudaErrorInvalidValue;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, all);
+    if (e == cudaSuccess && kept) done[dev].store(all, std::memory_order_release);
     return e;
 }
 

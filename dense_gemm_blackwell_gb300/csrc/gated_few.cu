@@ -227,11 +227,12 @@ __global__ void __launch_bounds__(kGatedFewThreads, 1) gated_few_kernel(const __
     }
 }
 
+static std::atomic<int> smem_set[2][kMaxDevices];      // of the kernel for f16 and for bf16
+
 template <int OUT>
 static cudaError_t launch_typed(const GatedFewParams& p, dim3 grid, size_t smem, cudaStream_t stream) {
     auto kern = gated_few_kernel<OUT>;
-    static std::atomic<int> smem_set[kMaxDevices];
-    cudaError_t e = ensure_smem_limit(kern, smem, smem_set);
+    cudaError_t e = ensure_smem_limit(kern, smem, smem_set[OUT == GEMM_BF16]);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -254,7 +255,7 @@ int gated_few_max_clusters(int dtype, int k_split, const DeviceFacts& dev) {
     if (k_split == 1) return dev.sms;
     auto kern = dtype == GEMM_BF16 ? gated_few_kernel<GEMM_BF16> : gated_few_kernel<GEMM_F16>;
     const size_t smem = (size_t)dev.smem_optin - 2048;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return 0;
+    if (ensure_smem_limit(kern, smem, smem_set[dtype == GEMM_BF16]) != cudaSuccess) return 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)k_split);
     cfg.blockDim = dim3(kGatedFewThreads);

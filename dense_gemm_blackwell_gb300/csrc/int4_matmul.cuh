@@ -531,7 +531,8 @@ template <typename T>
 static int resident_int4(int k_split_log, int per_sm) {
     auto kern = int4_matmul_kernel<T, 4, 1, false>;
     const size_t smem = (size_t)kInt4Room / per_sm;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kInt4Room) != cudaSuccess) return 0;
+    static std::atomic<int> smem_set[kMaxDevices];
+    if (ensure_smem_limit(kern, kInt4Room, smem_set) != cudaSuccess) return 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1u << k_split_log);
     cfg.blockDim = dim3((unsigned)kInt4MaxThreads / per_sm);

@@ -20,8 +20,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapters_kernel(const __grid_cons
     persistent_body<CG, OUT, true>(p, &tail);
 }
 
-// The shared-memory limit set for a kernel on each device: one record per kernel, for a second one would lower the limit
-// that the first believes in.
+// The shared-memory limit set for a kernel on each device.
 template <int CG, int OUT>
 static std::atomic<int> (&persistent_smem())[kMaxDevices] {
     static std::atomic<int> smem_set[kMaxDevices];

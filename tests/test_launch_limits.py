@@ -1,0 +1,133 @@
+"""What the host keeps about kernels and the device from one launch to the next, on a stand-in for the CUDA runtime (no GPU): a kernel's
+shared-memory limit never ends up below what a launch asked for, whichever threads and records raise it."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "dense_gemm_blackwell_gb300", "csrc")
+
+
+def nvcc():
+    for c in (os.environ.get("NVCC"), shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc"):
+        if c and os.path.exists(c):
+            return c
+    return None
+
+
+def compiled(path, name, source):
+    """{first word: the others} of what the host program prints."""
+    cc = nvcc()
+    if cc is None:
+        pytest.skip("nvcc not available")
+    src, exe = path / (name + ".cu"), path / name
+    src.write_text(source)
+    done = subprocess.run([cc, "-std=c++17", "-I" + CSRC, "-I" + os.path.join(ROOT, "include"), str(src), "-o", str(exe)],
+                          capture_output=True, text=True)
+    assert done.returncode == 0, done.stderr
+    out = subprocess.run([str(exe)], check=True, capture_output=True, text=True, timeout=60).stdout
+    return {line.split()[0]: [int(v) for v in line.split()[1:]] for line in out.splitlines()}
+
+
+# The runtime's calls that set and read a kernel's limit.  A device's blocks may have 227 KB, of which the kernels here hold 512 bytes.
+RUNTIME = r'''
+#include <chrono>
+#include <condition_variable>
+#include <cstdio>
+#include <functional>
+#include <map>
+#include <mutex>
+#include <thread>
+#include <cuda_runtime.h>
+
+namespace fake {
+constexpr int kOptin = 232448, kStatic = 512;
+std::mutex mutex;
+std::map<const void*, int> limit;
+std::function<void()> on_set = [] {};
+template <typename K>
+cudaError_t set_attribute(K kern, cudaFuncAttribute, int value) {
+    on_set();
+    std::lock_guard<std::mutex> hold(mutex);
+    if (value > kOptin - kStatic) return cudaErrorInvalidValue;
+    limit[(const void*)kern] = value;
+    return cudaSuccess;
+}
+template <typename K>
+cudaError_t get_attributes(cudaFuncAttributes* a, K) {
+    *a = cudaFuncAttributes{};
+    a->sharedSizeBytes = kStatic;
+    return cudaSuccess;
+}
+inline cudaError_t get_device(int* device) {
+    *device = 0;
+    return cudaSuccess;
+}
+inline cudaError_t device_attribute(int* value, cudaDeviceAttr attr, int) {
+    if (attr != cudaDevAttrMaxSharedMemoryPerBlockOptin) return cudaErrorInvalidValue;
+    *value = kOptin;
+    return cudaSuccess;
+}
+}  // namespace fake
+#define cudaFuncSetAttribute fake::set_attribute
+#define cudaFuncGetAttributes fake::get_attributes
+#define cudaGetDevice fake::get_device
+#define cudaDeviceGetAttribute fake::device_attribute
+'''
+
+
+def test_shared_memory_limits(tmp_path):
+    """Two threads that ask for two sizes of one kernel at once; two records of one kernel; more than a block may have."""
+    got = compiled(tmp_path, "limits", RUNTIME + r'''
+#include "common.cuh"
+__global__ void one(int) {}
+__global__ void two(int) {}
+__global__ void three(int) {}
+
+int main() {
+    using dgb::ensure_smem_limit;
+    static std::atomic<int> set_one[dgb::kMaxDevices], set_two[2][dgb::kMaxDevices], set_three[dgb::kMaxDevices];
+    {
+        // the first thread's call is held up on its way into the driver until the other thread is done (or cannot get on)
+        std::mutex m;
+        std::condition_variable cv;
+        bool held = false, done = false;
+        fake::on_set = [&] {
+            std::unique_lock<std::mutex> l(m);
+            if (held) return;
+            held = true;
+            cv.notify_all();
+            cv.wait_for(l, std::chrono::seconds(1), [&] { return done; });
+        };
+        std::thread small([&] { ensure_smem_limit(one, 60000, set_one); });
+        {
+            std::unique_lock<std::mutex> l(m);
+            cv.wait_for(l, std::chrono::seconds(10), [&] { return held; });
+        }
+        std::thread large([&] {
+            ensure_smem_limit(one, 150000, set_one);
+            std::lock_guard<std::mutex> l(m);
+            done = true;
+            cv.notify_all();
+        });
+        small.join();
+        large.join();
+        fake::on_set = [] {};
+        const int status = ensure_smem_limit(one, 100000, set_one);
+        std::printf("threads %d %d\n", status, fake::limit[(const void*)one]);
+    }
+    ensure_smem_limit(two, 150000, set_two[0]);
+    ensure_smem_limit(two, 60000, set_two[1]);
+    std::printf("records %d %d\n", (int)ensure_smem_limit(two, 150000, set_two[0]), fake::limit[(const void*)two]);
+    int over = ensure_smem_limit(three, fake::kOptin, set_three);
+    std::printf("over %d %d\n", over, (int)ensure_smem_limit(three, fake::kOptin - fake::kStatic, set_three));
+    std::printf("all %d\n", fake::limit[(const void*)three]);
+    return 0;
+}
+''')
+    for name in ("threads", "records"):
+        status, limit = got[name]
+        assert status == 0 and limit >= 150000, (name, got[name])
+    assert got["over"][0] != 0 and got["over"][1] == 0 and got["all"] == [232448 - 512]
