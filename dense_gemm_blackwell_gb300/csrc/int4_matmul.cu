@@ -14,14 +14,18 @@
 
 namespace dgb {
 
-// The device's answer, asked for once.
-static int64_t resident(int k_split_log, int per_sm, int device) {
+// The device's answer, asked for until there is one; a query that fails leaves nothing behind.
+static cudaError_t resident(int k_split_log, int per_sm, int device, int64_t* clusters) {
     static std::atomic<int> known[kMaxDevices][4][3];
-    if (device >= kMaxDevices) return std::max(1, int4_resident(k_split_log, per_sm));
-    std::atomic<int>& at = known[device][k_split_log][per_sm];
-    int n = at.load(std::memory_order_relaxed);
-    if (n == 0) at.store(n = std::max(1, int4_resident(k_split_log, per_sm)), std::memory_order_relaxed);
-    return n;
+    std::atomic<int>* at = device < kMaxDevices ? &known[device][k_split_log][per_sm] : nullptr;
+    int n = at ? at->load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        const cudaError_t e = int4_resident(k_split_log, per_sm, &n);
+        if (e != cudaSuccess) return e;
+        if (at) at->store(n, std::memory_order_relaxed);
+    }
+    *clusters = n;
+    return cudaSuccess;
 }
 
 // A tile is 16 rows of W, a stage 256 bytes of each.  The CTAs of a cluster may share K: X in each CTA's shared memory is what one of
@@ -33,7 +37,7 @@ static int64_t resident(int k_split_log, int per_sm, int device) {
 // tile's sums cost 38 cycles a token, more than twice that in a cluster, a doubling of the cluster 840; 16 warps meet later than 8.
 // Measured, 8 tokens x 4096 -> 4864 and 77824: two CTAs of 8 warps 8.5 and 37.7 us, in clusters of two 7.3 and 45.7, one CTA of 16
 // warps 7.6 and 37.1; 16 tokens -> 77824 in clusters of two 82, one CTA 51.
-bool shape_int4(Int4Params* p, bool gated, const DeviceFacts& dev) {
+gemm_status_t shape_int4(Int4Params* p, bool gated, const DeviceFacts& dev) {
     constexpr int64_t kStageK = 2 * kInt4RowBytes;
     const int64_t tiles = ((int64_t)p->n + (gated ? 7 : 15)) / (gated ? 8 : 16), stages = (p->k + kStageK - 1) / kStageK;
     const int64_t tokens = p->tokens > 8 ? 16 : 8, slot = tokens * 17 * 4;
@@ -47,7 +51,13 @@ bool shape_int4(Int4Params* p, bool gated, const DeviceFacts& dev) {
         for (int ks = 0; ks <= 3 && (1 << ks) <= stages; ++ks) {
             const int64_t mine = (stages + (1 << ks) - 1) >> ks;
             const int64_t base = warps * chunks * 16 * 8 + mine * (kStageK * tokens * 2 + chunks * tokens * 4);
-            const int64_t clusters = std::min<int64_t>(tiles, ks == 0 ? per_sm * dev.sms : resident(ks, per_sm, dev.device));
+            int64_t at_once = per_sm * dev.sms;
+            if (ks > 0) {
+                const cudaError_t e = resident(ks, per_sm, dev.device, &at_once);
+                if (e != cudaSuccess) return status_of(e);
+                if (at_once < 1) continue;
+            }
+            const int64_t clusters = std::min(tiles, at_once);
             const int64_t all = (tiles + clusters - 1) / clusters;      // tiles of a cluster
             int64_t slots = 2 * warps, round_tiles = all;
             if (ks > 0) {
@@ -79,7 +89,7 @@ bool shape_int4(Int4Params* p, bool gated, const DeviceFacts& dev) {
     }
     p->tokens_log = 0;
     while ((1 << p->tokens_log) < p->tokens) ++p->tokens_log;
-    return best > 0;
+    return best > 0 ? GEMM_OK : GEMM_ERR_UNSUPPORTED;       // X does not fit
 }
 
 static bool type16(int32_t t) { return t == GEMM_BF16 || t == GEMM_F16; }
@@ -113,7 +123,7 @@ gemm_status_t int4_matmul_run(const int4_matmul_args_t* args, gemm_stream_t stre
         ((a.n > 1 || gated) && a.ld_codes % 16 != 0))
         return GEMM_ERR_ALIGNMENT;
     DeviceFacts dev;
-    const gemm_status_t s = device_facts(&dev);
+    gemm_status_t s = device_facts(&dev);
     if (s != GEMM_OK) return s;
     Int4Params f{};
     f.x = a.x;
@@ -132,7 +142,7 @@ gemm_status_t int4_matmul_run(const int4_matmul_args_t* args, gemm_stream_t stre
     f.group = a.group;
     f.act = a.activation;
     f.group_magic = (uint32_t)std::min<uint64_t>(UINT32_MAX, (1ull << 32) / (uint32_t)(a.group / 32));
-    if (!shape_int4(&f, gated, dev)) return GEMM_ERR_UNSUPPORTED;       // X does not fit
+    if ((s = shape_int4(&f, gated, dev)) != GEMM_OK) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return status_of(a.dtype == GEMM_BF16 ? launch_int4_bf16(f, gated, st) : launch_int4_f16(f, gated, st));
 }

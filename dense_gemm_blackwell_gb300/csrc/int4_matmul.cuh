@@ -528,11 +528,12 @@ static cudaError_t launch_int4_as(const Int4Params& p, cudaStream_t stream) {
 
 // How many clusters of 2^k_split_log CTAs the device holds at once, `per_sm` CTAs an SM by their shared memory.
 template <typename T>
-static int resident_int4(int k_split_log, int per_sm) {
+static cudaError_t resident_int4(int k_split_log, int per_sm, int* clusters) {
     auto kern = int4_matmul_kernel<T, 4, 1, false>;
     const size_t smem = (size_t)kInt4Room / per_sm;
     static std::atomic<int> smem_set[kMaxDevices];
-    if (ensure_smem_limit(kern, kInt4Room, smem_set) != cudaSuccess) return 0;
+    const cudaError_t e = ensure_smem_limit(kern, kInt4Room, smem_set);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1u << k_split_log);
     cfg.blockDim = dim3((unsigned)kInt4MaxThreads / per_sm);
@@ -544,8 +545,7 @@ static int resident_int4(int k_split_log, int per_sm) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    int n = 0;
-    return cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess ? n : 0;
+    return cudaOccupancyMaxActiveClusters(clusters, kern, &cfg);
 }
 
 template <typename T, int VEC>

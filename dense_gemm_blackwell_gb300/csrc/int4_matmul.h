@@ -33,7 +33,8 @@ struct Int4Params {
     int32_t grid, smem;
 };
 
-int int4_resident(int k_split_log, int per_sm);      // clusters of 2^k_split_log CTAs that the device holds at once
+// Clusters of 2^k_split_log CTAs, `per_sm` CTAs an SM, that the device holds at once.
+cudaError_t int4_resident(int k_split_log, int per_sm, int* clusters);
 cudaError_t launch_int4_bf16(const Int4Params& p, bool gated, cudaStream_t stream);
 cudaError_t launch_int4_f16(const Int4Params& p, bool gated, cudaStream_t stream);
 

@@ -1,10 +1,13 @@
 """What the host keeps about kernels and the device from one launch to the next, on a stand-in for the CUDA runtime (no GPU): a kernel's
-shared-memory limit never ends up below what a launch asked for, whichever threads and records raise it."""
+shared-memory limit never ends up below what a launch asked for, whichever threads and records raise it, and a query that failed is
+not taken for an answer."""
 import os
 import shutil
 import subprocess
 
 import pytest
+
+import dense_gemm_blackwell_gb300 as dg
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "dense_gemm_blackwell_gb300", "csrc")
@@ -131,3 +134,61 @@ int main() {
         status, limit = got[name]
         assert status == 0 and limit >= 150000, (name, got[name])
     assert got["over"][0] != 0 and got["over"][1] == 0 and got["all"] == [232448 - 512]
+
+
+def test_a_failed_query_of_resident_clusters_is_not_kept(tmp_path):
+    """16 tokens of 28672 columns fit a cluster's shared memory only: the call whose query fails says so, and the next one has the
+    device's answer, which is asked for once."""
+    got = compiled(tmp_path, "resident", RUNTIME + r'''
+#include "int4_matmul.cu"
+
+static bool fails = true;
+static int queries = 0, launches = 0, grid = 0, split = 0;
+namespace dgb {
+gemm_status_t status_of(cudaError_t e) { return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA; }
+gemm_status_t device_facts(DeviceFacts* out) {
+    out->device = 0;
+    out->sms = 152;
+    out->smem_optin = fake::kOptin;
+    return GEMM_OK;
+}
+int int4_resident(int k_split_log, int per_sm) {
+    ++queries;
+    return fails ? 0 : (per_sm * 152 * 9 / 10) >> k_split_log;
+}
+cudaError_t int4_resident(int k_split_log, int per_sm, int* clusters) {
+    if ((*clusters = int4_resident(k_split_log, per_sm)) == 0) return cudaErrorInvalidValue;
+    return cudaSuccess;
+}
+cudaError_t launch_int4_bf16(const Int4Params& p, bool, cudaStream_t) {
+    ++launches;
+    grid = p.grid;
+    split = 1 << p.k_split_log;
+    return cudaSuccess;
+}
+cudaError_t launch_int4_f16(const Int4Params& p, bool gated, cudaStream_t stream) { return launch_int4_bf16(p, gated, stream); }
+}  // namespace dgb
+
+int main() {
+    int4_matmul_args_t a = {};
+    a.tokens = 16;
+    a.n = 8192;
+    a.k = 28672;
+    a.group = 128;
+    a.dtype = GEMM_BF16;
+    a.activation = GATED_NONE;
+    a.x = a.codes = a.scales = (void*)4096;
+    a.y = (void*)4096;
+    std::printf("failed %d %d\n", (int)int4_matmul_run(&a, nullptr), launches);
+    fails = false;
+    const int status = (int)int4_matmul_run(&a, nullptr);
+    std::printf("next %d %d %d %d\n", status, launches, grid, split);
+    queries = 0;
+    std::printf("again %d %d %d\n", (int)int4_matmul_run(&a, nullptr), grid, queries);
+    return 0;
+}
+''')
+    assert got["failed"] == [dg.GEMM_ERR_CUDA, 0]
+    status, launches, grid, split = got["next"]
+    assert status == 0 and launches == 1 and split >= 4 and grid > 100, got["next"]
+    assert got["again"] == [0, grid, 0]
