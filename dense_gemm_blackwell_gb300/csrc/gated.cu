@@ -109,14 +109,16 @@ gemm_status_t resolve_gated(gated_desc_t* d) {
 // its sums on their way to the stores cost what its even wave gains (4096 x 2 x 12288: 1 token 31.4 us here, 52 there, 96 37.1 and 37.9,
 // 128 39.6 and 38.0; 4096 x 2 x 4096, 128 tokens: 17.4 and 23.8).  Columns and K are dealt out over one wave of clusters as costs the
 // least: an SM takes in about 50 bytes a cycle and 200 cycles a K block beside; a join costs a start and what its sums cost.  (One
-// wave: a 37th cluster of four CTAs, where the device held 36, doubled the time.)
-bool plan_few_tiles(const gated_desc_t& d, const DeviceFacts& dev, gated_plan_s* p) {
-    if (d.tokens > 128 || (d.tokens > 96 && 2 * d.features >= 128 * (int64_t)dev.sms)) return false;
+// wave: a 37th cluster of four CTAs, where the device held 36, doubled the time.)  Says in info.few_tiles whether it is taken.
+gemm_status_t plan_few_tiles(const gated_desc_t& d, const DeviceFacts& dev, gated_plan_s* p) {
+    if (d.tokens > 128 || (d.tokens > 96 && 2 * d.features >= 128 * (int64_t)dev.sms)) return GEMM_OK;
     const int64_t k_blocks = (d.k + 63) / 64, box_m = (d.tokens + 7) / 8 * 8;
     GatedFewParams& q = p->tiles;
     double best = 0;
     for (int64_t ks = 1; ks <= kGatedFewMaxSplit && ks <= k_blocks; ks *= 2) {
-        const int64_t wave = gated_few_max_clusters(d.dtype, (int)ks, dev);
+        int wave = 0;
+        const cudaError_t e = gated_few_max_clusters(d.dtype, (int)ks, dev, &wave);
+        if (e != cudaSuccess) return status_of(e);
         for (int64_t half = 8; half <= 128; half += 8) {
             if ((d.features + half - 1) / half > wave) continue;
             const double sums = (double)(box_m * 2 * half);
@@ -128,7 +130,8 @@ bool plan_few_tiles(const gated_desc_t& d, const DeviceFacts& dev, gated_plan_s*
             q.k_split = (int32_t)ks;
         }
     }
-    if (best == 0) return false;
+    if (best == 0) return GEMM_OK;
+    p->info.few_tiles = 1;
     q.M = (int32_t)d.tokens;
     q.features = (int32_t)d.features;
     q.k_blocks = (int32_t)k_blocks;
@@ -148,7 +151,7 @@ bool plan_few_tiles(const gated_desc_t& d, const DeviceFacts& dev, gated_plan_s*
     const int64_t bytes = std::max(q.stages * stage, d.tokens * q.sum_pitch * 4);
     p->tiles_grid = dim3((unsigned)((d.features + q.half - 1) / q.half * q.k_split));
     p->tiles_smem = (size_t)(bytes + slack);
-    return true;
+    return GEMM_OK;
 }
 
 // Tensor maps and pointers of a run, kept while the pointers stay the same.
@@ -250,7 +253,10 @@ gemm_status_t gated_plan_create(gated_plan_t* out, const gated_desc_t* desc) {
     f.dtype_d = d.dtype;
     f.lda = d.ldx;
     f.ldb = d.ldw;
-    p->info.few_tiles = d.tokens > 0 && !forced && plan_few_tiles(d, dev, p);
+    if (d.tokens > 0 && !forced && (s = plan_few_tiles(d, dev, p)) != GEMM_OK) {
+        gated_plan_destroy(p);
+        return s;
+    }
     f.flags = d.flags | GEMM_FLAG_NO_SINGLE_CTA;
     if (p->info.few_tiles) f.flags |= GEMM_FLAG_NO_STREAM_K;       // the product's plan holds the error record only
     f.tile_n = d.tile_n == 0 && d.features < 128 ? 128 : d.tile_n;     // tiles hold whole 64-column chunks of both kinds

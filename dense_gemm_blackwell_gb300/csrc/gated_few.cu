@@ -251,11 +251,15 @@ static cudaError_t launch_typed(const GatedFewParams& p, dim3 grid, size_t smem,
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-int gated_few_max_clusters(int dtype, int k_split, const DeviceFacts& dev) {
-    if (k_split == 1) return dev.sms;
+cudaError_t gated_few_max_clusters(int dtype, int k_split, const DeviceFacts& dev, int* clusters) {
+    if (k_split == 1) {
+        *clusters = dev.sms;
+        return cudaSuccess;
+    }
     auto kern = dtype == GEMM_BF16 ? gated_few_kernel<GEMM_BF16> : gated_few_kernel<GEMM_F16>;
     const size_t smem = (size_t)dev.smem_optin - 2048;
-    if (ensure_smem_limit(kern, smem, smem_set[dtype == GEMM_BF16]) != cudaSuccess) return 0;
+    const cudaError_t e = ensure_smem_limit(kern, smem, smem_set[dtype == GEMM_BF16]);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)k_split);
     cfg.blockDim = dim3(kGatedFewThreads);
@@ -267,8 +271,7 @@ int gated_few_max_clusters(int dtype, int k_split, const DeviceFacts& dev) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    int n = 0;
-    return cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess ? n : 0;
+    return cudaOccupancyMaxActiveClusters(clusters, kern, &cfg);
 }
 
 cudaError_t launch_gated_few(const GatedFewParams& p, int dtype, dim3 grid, size_t smem, cudaStream_t stream) {

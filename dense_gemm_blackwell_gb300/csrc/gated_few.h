@@ -38,6 +38,6 @@ struct GatedFewParams {
 cudaError_t launch_gated_few(const GatedFewParams& p, int dtype, dim3 grid, size_t smem, cudaStream_t stream);
 
 // How many clusters of k_split CTAs, an SM's shared memory each, the device holds at once.
-int gated_few_max_clusters(int dtype, int k_split, const DeviceFacts& dev);
+cudaError_t gated_few_max_clusters(int dtype, int k_split, const DeviceFacts& dev, int* clusters);
 
 }  // namespace dgb

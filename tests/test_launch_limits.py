@@ -27,7 +27,7 @@ def compiled(path, name, source):
         pytest.skip("nvcc not available")
     src, exe = path / (name + ".cu"), path / name
     src.write_text(source)
-    done = subprocess.run([cc, "-std=c++17", "-I" + CSRC, "-I" + os.path.join(ROOT, "include"), str(src), "-o", str(exe)],
+    done = subprocess.run([cc, "-std=c++17", "-gencode", "arch=compute_103a,code=sm_103a", "-I" + CSRC, "-I" + os.path.join(ROOT, "include"), str(src), "-o", str(exe)],
                           capture_output=True, text=True)
     assert done.returncode == 0, done.stderr
     out = subprocess.run([str(exe)], check=True, capture_output=True, text=True, timeout=60).stdout
@@ -192,3 +192,85 @@ int main() {
     status, launches, grid, split = got["next"]
     assert status == 0 and launches == 1 and split >= 4 and grid > 100, got["next"]
     assert got["again"] == [0, grid, 0]
+
+
+# gated.cu's plans on stand-ins for the products that they are made of
+GATED = RUNTIME + r'''
+#include "gated.cu"
+#include <vector>
+
+struct gemm_plan_s {};
+static std::vector<gemm_desc_t> made;
+static bool fails = false;
+namespace dgb {
+gemm_status_t status_of(cudaError_t e) { return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA; }
+gemm_status_t device_facts(DeviceFacts* out) {
+    out->device = 0;
+    out->sms = 152;
+    out->smem_optin = fake::kOptin;
+    return GEMM_OK;
+}
+int gated_few_max_clusters(int, int k_split, const DeviceFacts& dev) { return fails && k_split > 1 ? 0 : dev.sms / k_split; }
+cudaError_t gated_few_max_clusters(int dtype, int k_split, const DeviceFacts& dev, int* clusters) {
+    *clusters = gated_few_max_clusters(dtype, k_split, dev);
+    return *clusters > 0 ? cudaSuccess : cudaErrorInvalidValue;
+}
+cudaError_t launch_gated_few(const GatedFewParams&, int, dim3, size_t, cudaStream_t) { return cudaSuccess; }
+cudaError_t launch_gated(const PersistentParams&, const GatedTail&, int, int, int, size_t, cudaStream_t) { return cudaSuccess; }
+gemm_status_t product_params(gemm_plan_t, const void*, const void*, void*, PersistentParams*) { return GEMM_OK; }
+gemm_status_t encode_rows_map(CUtensorMap*, int, const void*, int64_t, int64_t, int64_t, int) { return GEMM_OK; }
+gemm_device_error_t* device_record(gemm_plan_t) { return nullptr; }
+}  // namespace dgb
+extern "C" {
+gemm_status_t gemm_plan_create(gemm_plan_t* plan, const gemm_desc_t* d) {
+    made.push_back(*d);
+    *plan = new gemm_plan_s;
+    return GEMM_OK;
+}
+gemm_status_t gemm_plan_info(gemm_plan_t, gemm_plan_info_t* info) {
+    *info = gemm_plan_info_t{};
+    return GEMM_OK;
+}
+gemm_status_t gemm_plan_destroy(gemm_plan_t plan) {
+    delete plan;
+    return GEMM_OK;
+}
+gemm_status_t gemm_run(gemm_plan_t, const void*, const void*, void*, const float*, const float*, gemm_stream_t) { return GEMM_OK; }
+gemm_status_t gemm_sync_status(gemm_plan_t, gemm_stream_t, gemm_device_error_t*) { return GEMM_OK; }
+}
+
+// One word of the name, then status, whether the kernel for few tokens is taken and its split.
+static void plan(const char* name, int64_t tokens, int64_t features, int64_t k, int gradients = 0) {
+    made.clear();
+    gated_desc_t d = {};
+    d.tokens = tokens;
+    d.features = features;
+    d.k = k;
+    d.dtype = d.dtype_dw = GEMM_BF16;
+    d.gradients = gradients;
+    gated_plan_t p = nullptr;
+    gated_plan_info_t info = {};
+    const int status = (int)gated_plan_create(&p, &d);
+    if (p) gated_plan_info(p, &info);
+    std::printf("%s %d %d %d", name, status, info.few_tiles, info.k_split);
+    for (const gemm_desc_t& g : made) std::printf(" %d", g.tile_n);
+    std::printf("\n");
+    gated_plan_destroy(p);
+}
+'''
+
+
+def test_a_failed_query_is_the_error_of_a_gated_plan(tmp_path):
+    """Where the clusters of a split cannot be asked for, the plan says so instead of quietly going without them."""
+    got = compiled(tmp_path, "plans", GATED + r'''
+int main() {
+    plan("whole", 4, 1024, 8192);
+    fails = true;
+    plan("failed", 4, 1024, 8192);
+    plan("pipeline", 4096, 1024, 8192);
+    return 0;
+}
+''')
+    assert got["whole"][:2] == [0, 1] and got["whole"][2] > 1       # K is shared where it can be
+    assert got["failed"][:2] == [dg.GEMM_ERR_CUDA, 0]
+    assert got["pipeline"][:2] == [0, 0]
