@@ -2,6 +2,7 @@
 // GEMM kernels (host and device).
 #pragma once
 
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 #include <cuda.h>
@@ -236,8 +237,8 @@ inline cudaError_t ensure_smem_limit(Kernel kern, size_t smem, std::atomic<int> 
     int optin = 0;
     if ((e = cudaFuncGetAttributes(&facts, kern)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
-    const int all = optin - (int)facts.sharedSizeBytes;
-    if (smem > (size_t)all) return cudaErrorInvalidValue;
+    // more than that is the runtime's to refuse, which callers that ask for its last error find there
+    const int all = std::max(optin - (int)facts.sharedSizeBytes, (int)smem);
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, all);
     if (e == cudaSuccess && kept) done[dev].store(all, std::memory_order_release);
     return e;

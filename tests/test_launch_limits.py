@@ -49,12 +49,16 @@ namespace fake {
 constexpr int kOptin = 232448, kStatic = 512;
 std::mutex mutex;
 std::map<const void*, int> limit;
+cudaError_t last_error = cudaSuccess;
 std::function<void()> on_set = [] {};
 template <typename K>
 cudaError_t set_attribute(K kern, cudaFuncAttribute, int value) {
     on_set();
     std::lock_guard<std::mutex> hold(mutex);
-    if (value > kOptin - kStatic) return cudaErrorInvalidValue;
+    if (value > kOptin - kStatic) {
+        last_error = cudaErrorInvalidValue;
+        return cudaErrorInvalidValue;
+    }
     limit[(const void*)kern] = value;
     return cudaSuccess;
 }
@@ -125,7 +129,7 @@ int main() {
     ensure_smem_limit(two, 60000, set_two[1]);
     std::printf("records %d %d\n", (int)ensure_smem_limit(two, 150000, set_two[0]), fake::limit[(const void*)two]);
     int over = ensure_smem_limit(three, fake::kOptin, set_three);
-    std::printf("over %d %d\n", over, (int)ensure_smem_limit(three, fake::kOptin - fake::kStatic, set_three));
+    std::printf("over %d %d %d\n", over, (int)fake::last_error, (int)ensure_smem_limit(three, fake::kOptin - fake::kStatic, set_three));
     std::printf("all %d\n", fake::limit[(const void*)three]);
     return 0;
 }
@@ -133,7 +137,7 @@ int main() {
     for name in ("threads", "records"):
         status, limit = got[name]
         assert status == 0 and limit >= 150000, (name, got[name])
-    assert got["over"][0] != 0 and got["over"][1] == 0 and got["all"] == [232448 - 512]
+    assert got["over"][0] == got["over"][1] != 0 and got["over"][2] == 0 and got["all"] == [232448 - 512]
 
 
 def test_a_failed_query_of_resident_clusters_is_not_kept(tmp_path):
