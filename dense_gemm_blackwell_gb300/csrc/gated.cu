@@ -212,8 +212,10 @@ void choose_tiles(const gated_desc_t& d, int sms, gemm_desc_t* f) {
 // those fill their last wave well enough to make up for its not being split along K as that of 256-wide tiles is: 16384 x 4096 x 4096
 // (7 waves, 96 % full) 298 us, 352 with 256; the whole backward pass of 2048 and 8192 tokens, 4096 -> 2 x 8192, 323 and 1247 us, 349 and
 // 1356 with 256. Along a short K the unsplit last wave costs more: at 84 % 4096 x 4096 x 16384 still gains (628 us for the whole pass at
-// 4096 tokens, 642 with 256 in that product), 16384 x 2048 x 2048 loses (205 us, 187 with 256).
+// 4096 tokens, 642 with 256 in that product), 16384 x 2048 x 2048 loses (205 us, 187 with 256).  Up to 128 rows are lone CTAs' tiles,
+// for which waves of pairs say nothing: 64 x 32768 x 16384 153 us in the planner's tiles, 189 with 512, 64 x 36864 x 2048 28 and 43.
 int32_t mn_tile(const gemm_desc_t& g, int sms) {
+    if (g.M <= 128) return 0;
     const int64_t tiles = (g.M + 255) / 256 * ((g.N + 511) / 512), pairs = sms / 2, waves = (tiles + pairs - 1) / pairs;
     return g.K >= 1024 && g.N % 512 == 0 && 10 * tiles >= (g.K >= 4096 ? 8 : 9) * waves * pairs ? 512 : 0;
 }

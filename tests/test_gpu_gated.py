@@ -268,3 +268,8 @@ def test_streams_graphs_and_two_plans():
         for p in plans:
             assert p.sync_status()[0] == dg.GEMM_OK
             p.close()
+
+
+def test_backward_of_few_tokens_takes_no_wide_tiles():
+    with dg.GatedPlan(64, 8192, 32768, gradients=True) as p:
+        assert p.info.dx.tile_n <= 256 and p.info.dw.tile_n <= 256

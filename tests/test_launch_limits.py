@@ -278,3 +278,21 @@ int main() {
     assert got["whole"][:2] == [0, 1] and got["whole"][2] > 1       # K is shared where it can be
     assert got["failed"][:2] == [dg.GEMM_ERR_CUDA, 0]
     assert got["pipeline"][:2] == [0, 0]
+
+
+def test_wide_tiles_of_the_gradients_products(tmp_path):
+    """512 columns a tile where tiles of SM pairs fill their waves; the planner's own where 128 rows or fewer are lone CTAs' tiles."""
+    got = compiled(tmp_path, "plans", GATED + r'''
+int main() {
+    plan("batch", 4096, 8192, 4096, 1);
+    plan("ragged", 4096, 8192, 4104, 1);
+    plan("few", 64, 8192, 32768, 1);
+    plan("narrow", 16384, 64, 32768, 1);
+    return 0;
+}
+''')
+    # of the forward product, of the rows' gradients, of the weights' gradients
+    assert got["batch"][0] == 0 and got["batch"][4:] == [512, 512]
+    assert got["ragged"][4:] == [0, 0]
+    assert got["few"][4:] == [0, 0]
+    assert got["narrow"][4:][1] == 0
