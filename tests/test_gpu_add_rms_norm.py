@@ -317,3 +317,89 @@ def test_streams_and_graphs():
     graph.replay()
     torch.cuda.synchronize()
     assert all(same(a, b) for a, b in zip(want, got)) and all(same(a, b) for a, b in zip(want_g, got_g))
+
+
+# ---------------------------------------------------------------- blocks that take row after row
+
+# With 152 SMs: 3 turns of one row a block and 6 warps a row, 4 of 16 warps, 2 of four rows a block, 5 of four vectors a thread
+MANY = [(2500, 2893), (1500, 8192), (9000, 264), (700, 20000)]
+
+
+def check_scaled(mode, codes, scales, want):
+    t, n = want.shape
+    size = 128 if mode == BLOCK else 32
+    top = torch.nn.functional.pad(want.abs(), (0, -n % size)).unflatten(1, (-1, size)).amax(2)
+    if mode == BLOCK:
+        s = scales.double()
+        assert ((s - top / 448).abs() <= top / 448 * FP32).all()
+    else:
+        e, rest = untile(scales, t, n)
+        assert (rest == 0).all()
+        s = torch.exp2(e.double() - 127)
+        assert (top <= 448 * s * (1 + FP32)).all() and ((top > 224 * s * (1 - FP32)) | (e == 1)).all()
+    check_codes(codes, s.repeat_interleave(size, 1)[:, :n], want)
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("mode", [dg.GEMM_SCALE_NONE, BLOCK, MX])
+@pytest.mark.parametrize("t,n", MANY)
+def test_many_turns(t, n, mode, kind):
+    w = weights(n, kind)
+    for res, weight in ((True, w), (True, None), (False, w)):
+        x, r = rows(t, n, kind, 61, pad=8), rows(t, n, kind, 62, 3.0) if res else None
+        room = torch.full((-(-t // 128) * -(-n // 128) * 512,), 0xAA, dtype=torch.uint8, device="cuda") if mode == MX else None
+        y, scales, h = dg.add_rms_norm(x, weight, residual=r, eps=EPS, scale_mode=mode, scales=room)
+        if res:
+            assert torch.equal(h, (x.float() + r.float()).to(kind))
+        want = exact(h if res else x, weight)
+        if mode == dg.GEMM_SCALE_NONE:
+            near(y, want, kind)
+        else:
+            check_scaled(mode, y, scales, want)
+        # the sum over the residual (or x); a 16-bit output over x: every turn reads its rows before it writes them
+        x2, r2 = x.clone(memory_format=torch.preserve_format), r.clone(memory_format=torch.preserve_format) if res else None
+        over = torch.nn.functional.pad(x2, (0, -n % 8))[:, :n]
+        sum2 = torch.nn.functional.pad(r2, (0, -n % 8))[:, :n] if res else None
+        for _ in range(2):
+            over.copy_(x)
+            if res:
+                sum2.copy_(r)
+            y2, scales2, h2 = dg.add_rms_norm(over, weight, residual=sum2, eps=EPS, scale_mode=mode, out=over if mode == dg.GEMM_SCALE_NONE else None,
+                                              sum_out=sum2)
+            assert torch.equal(y2.view(torch.uint8) if mode else y2, y.view(torch.uint8) if mode else y)
+            assert scales is None or torch.equal(scales2, scales)
+            assert not res or torch.equal(h2, h)
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("t,n", SIZES)
+def test_tiled_scales_of_a_sum(t, n, kind):
+    x, res, w = rows(t, n, kind, 63), rows(t, n, kind, 64, 3.0, pad=8), weights(n, kind)
+    codes, scales, h = dg.add_rms_norm(x, w, residual=res, eps=EPS, scale_mode=MX)
+    assert torch.equal(h, (x.float() + res.float()).to(kind))
+    check_scaled(MX, codes, scales, exact(h, w))
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("t,n", [(3000, 4096), (2500, 2893), (1200, 9000), (800, 20000), (9000, 264)])
+def test_backward_many_turns(t, n, kind):
+    test_backward(t, n, kind)
+    h, dy, dsum, w = rows(t, n, kind, 71, 2.0), rows(t, n, kind, 72), rows(t, n, kind, 73), weights(n, kind)
+    want, want_w = dg.add_rms_norm_backward(dy, h, w, d_sum=dsum)
+    for over in ("dy", "dsum", "h"):
+        c = {k: torch.nn.functional.pad(v, (0, -n % 8))[:, :n] for k, v in dict(dy=dy.clone(), dsum=dsum.clone(), h=h.clone()).items()}
+        dh, dw = dg.add_rms_norm_backward(c["dy"], c["h"], w, d_sum=c["dsum"], out=c[over])
+        assert torch.equal(dh, want) and torch.equal(dw, want_w)
+
+
+@pytest.mark.parametrize("mode", [BLOCK, MX])
+def test_a_weight_that_is_not_a_number_stays_in_its_column(mode):
+    """Its code is NaN in every row; the block's scale and other codes are those without it."""
+    x, w = rows(40, 1000, torch.bfloat16, 81), weights(1000, torch.bfloat16)
+    w[333] = 0
+    want, want_scales, _ = dg.add_rms_norm(x, w, eps=EPS, scale_mode=mode)
+    w[333] = float("nan")
+    got, scales, _ = dg.add_rms_norm(x, w, eps=EPS, scale_mode=mode)
+    others = torch.arange(1000, device="cuda") != 333
+    assert got.float()[:, 333].isnan().all() and torch.equal(scales, want_scales)
+    assert torch.equal(got.view(torch.uint8)[:, others], want.view(torch.uint8)[:, others])

@@ -270,6 +270,29 @@ def test_streams_graphs_and_two_plans():
             p.close()
 
 
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("t,f,k", [(100, 9736, 128), (128, 9728, 72), (96, 19472, 64), (3, 19464, 72)])
+def test_few_tokens_of_wide_layers(t, f, k, kind):
+    """97 to 128 tokens of layers wide enough for the pipeline, and columns that one wave of CTAs does not hold."""
+    assert run(t, f, k, kind, "silu", keep=t % 2 == 0).few_tiles == 0
+
+
+def test_backward_many_turns():
+    """The pass over memory takes its grid two and a half times over H."""
+    test_backward(3000, 2048, 64, "gelu", True, torch.bfloat16)
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dw_f32", [True, False])
+@pytest.mark.parametrize("t,f,act", [(2304, 1152, "silu"), (2300, 1144, "gelu_tanh")])
+def test_backward_wide_tiles(t, f, act, dw_f32, kind):
+    """Both products in 512-wide tiles, with tokens and features of whole groups of 64 and not."""
+    k = 4096
+    with dg.GatedPlan(t, f, k, dtype=CODE[kind], gradients=True, dtype_dw=dg.GEMM_F32 if dw_f32 else None) as p:
+        assert p.info.dx.tile_n == 512 and p.info.dw.tile_n == 512
+    test_backward(t, f, k, act, dw_f32, kind)
+
+
 def test_backward_of_few_tokens_takes_no_wide_tiles():
     with dg.GatedPlan(64, 8192, 32768, gradients=True) as p:
         assert p.info.dx.tile_n <= 256 and p.info.dw.tile_n <= 256

@@ -49,3 +49,24 @@ def test_groups_and_boxes_give_the_same_bits(m, n, k):
         out.append(d[:m, :n])
     assert torch.equal(out[0], out[1])
     assert (out[0].double() - a[:, :m].double().T @ b[:, :n].double()).abs().max() < 1e-2
+
+
+def test_groups_and_boxes_of_a_short_k():
+    test_groups_and_boxes_give_the_same_bits(192, 128, 96)
+
+
+@pytest.mark.parametrize("flags", [dg.GEMM_FLAG_CTA_GROUP_1, dg.GEMM_FLAG_CTA_GROUP_2])
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("m,n,k,ctas", [(512, 1024, 2048, 0), (600, 1096, 200, 0), (1024, 1536, 1600, 6)])
+def test_16_bit_outputs(m, n, k, ctas, kind, flags):
+    """Integers' products are exact in fp32 and rounded once."""
+    gen = torch.Generator(device="cuda").manual_seed(m + n + k + 1)
+    a, b = (torch.randint(-4, 5, (k, c), generator=gen, device="cuda").to(kind) for c in (m, n))
+    want = (a.double().T @ b.double()).to(kind)
+    code = dg.GEMM_BF16 if kind == torch.bfloat16 else dg.GEMM_F16
+    d = torch.full((m, n), float("nan"), dtype=kind, device="cuda")
+    desc = dg.make_desc(m, n, k, dtype_a=code, dtype_d=code, major_a=1, major_b=1, flags=flags, tile_n=512, max_ctas=ctas)
+    with dg.Plan(desc) as plan:
+        plan.run(a, b, d)
+        assert plan.sync_status()[0] == dg.GEMM_OK
+        assert plan.info.tile_n == 512 and torch.equal(d, want)
