@@ -1,5 +1,8 @@
 """GPU: kernels whose shared memory differs from call to call and from plan to plan, launched by several threads and after smaller plans
 were made: no launch is refused, and results are those of one thread."""
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -8,6 +11,7 @@ import torch
 import dense_gemm_blackwell_gb300 as dg
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -93,3 +97,34 @@ def test_threads_with_calls_of_many_sizes():
         for i in indices:
             pairs = zip(got[i], want[i]) if i >= len(work) else [(got[i], want[i])]
             assert all(torch.equal(a, b) for a, b in pairs), i
+
+
+COLD = """
+import torch
+import dense_gemm_blackwell_gb300 as dg
+dg.build()
+torch.manual_seed(0)
+bf16 = lambda *s: torch.randn(*s, device="cuda").to(torch.bfloat16)
+x, r, w = bf16(8, 8192), bf16(8, 8192), bf16(8192)
+codes = torch.randint(0, 256, (512, 4096), device="cuda").to(torch.uint8)
+scales, w2, out = bf16(512, 64) * 0.01, bf16(512, 8192) * 0.01, bf16(8, 256)
+plan = dg.GatedPlan(8, 256, 8192)
+torch.cuda.synchronize()
+def step():
+    n, s, h = dg.add_rms_norm(x, w, residual=r, scale_mode=dg.GEMM_SCALE_BLOCK_1x128_128x128)
+    return s, h, *dg.add_rms_norm_backward(x, r, w), dg.int4_matmul(x, codes, scales), plan.run(x, w2, out)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    captured = step()
+graph.replay()
+torch.cuda.synchronize()
+captured = [t.clone() for t in captured]
+assert all(torch.equal(a, b) for a, b in zip(captured, step()))
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """What a kernel's first launch asks of the runtime may be asked while a graph is recorded."""
+    done = subprocess.run([sys.executable, "-c", COLD], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and done.stdout.strip().endswith("same"), done.stderr[-2000:]
