@@ -190,11 +190,14 @@ gemm_status_t pipeline_params(gated_plan_s* plan, const void* x, const void* w, 
 // wave takes so many microseconds along a K of 4096, and a launch some beside.  Fitted to 65 sizes (130 to 3000 tokens, K 1024 to
 // 4096): 130 x 4096 -> 2 x 4096 19.2 us in pairs, 21.2 in single CTAs; 512 x 4096 -> 2 x 12288 68.7 us 256 wide in three waves, 78.1
 // 512 wide in two; 640 x 1024 -> 2 x 3584 11.3 us in single CTAs, 15.5 in pairs.  Splitting the last wave along K, whose partial sums
-// are of both kinds, cost 3 to 5 us there.
+// are of both kinds, cost 3 to 5 us there.  Tiles for half of the device or less share K where that saves more than the 14 us that
+// the parts' join takes of a long one: 130 x 16384 -> 2 x 1024 27.6 us, 43.0 unsplit, 130 x 28672 -> 2 x 512 33.6 and 72.0; 130 x
+// 6144 -> 2 x 1024, which would save 13 of its tiles' time, 19.9 and 19.0.
 void choose_tiles(const gated_desc_t& d, int sms, gemm_desc_t* f) {
+    const auto tiles = [&](int group, int64_t n) { return (d.tokens + 128 * group - 1) / (128 * group) * ((2 * d.features + n - 1) / n); };
     const auto waves = [&](int group, int64_t n) {
-        const int64_t tiles = (d.tokens + 128 * group - 1) / (128 * group) * ((2 * d.features + n - 1) / n), at_once = sms / group;
-        return (double)((tiles + at_once - 1) / at_once);
+        const int64_t at_once = sms / group;
+        return (double)((tiles(group, n) + at_once - 1) / at_once);
     };
     if (d.tokens <= 128 || d.features < 128 || waves(2, 512) > 2) return;
     struct Tiles { int32_t n; int group; double wave, beside; };
@@ -203,8 +206,10 @@ void choose_tiles(const gated_desc_t& d, int sms, gemm_desc_t* f) {
         const double cost = waves(o.group, o.n) * o.wave * (double)d.k / 4096 + o.beside;
         if (best > 0 && cost >= best) continue;
         best = cost;
+        const int64_t parts = sms / o.group / tiles(o.group, o.n);
+        const bool split = o.n == 512 || (parts > 1 && o.wave * (double)d.k / 4096 * (1.0 - 1.0 / (double)parts) > 14);
         f->tile_n = o.n;
-        f->flags = GEMM_FLAG_NO_SINGLE_CTA | (o.group == 2 ? GEMM_FLAG_CTA_GROUP_2 : GEMM_FLAG_CTA_GROUP_1) | (o.n < 512 ? GEMM_FLAG_NO_STREAM_K : 0u);
+        f->flags = GEMM_FLAG_NO_SINGLE_CTA | (o.group == 2 ? GEMM_FLAG_CTA_GROUP_2 : GEMM_FLAG_CTA_GROUP_1) | (split ? 0u : GEMM_FLAG_NO_STREAM_K);
     }
 }
 

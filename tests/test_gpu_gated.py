@@ -296,3 +296,10 @@ def test_backward_wide_tiles(t, f, act, dw_f32, kind):
 def test_backward_of_few_tokens_takes_no_wide_tiles():
     with dg.GatedPlan(64, 8192, 32768, gradients=True) as p:
         assert p.info.dx.tile_n <= 256 and p.info.dw.tile_n <= 256
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("t,f,k,split", [(130, 512, 28672, True), (200, 1000, 16392, True), (260, 136, 12288, True), (130, 1024, 6144, False)])
+def test_few_tiles_of_a_long_k_share_it(t, f, k, split, kind):
+    info = run(t, f, k, kind, "silu", keep=t != 200)
+    assert info.few_tiles == 0 and (info.product.stream_k_tiles > 0) == split

@@ -296,3 +296,23 @@ int main() {
     assert got["ragged"][4:] == [0, 0]
     assert got["few"][4:] == [0, 0]
     assert got["narrow"][4:][1] == 0
+
+
+def test_few_tiles_of_a_long_k_share_it(tmp_path):
+    """The pipeline's tiles may be split along K where most of the device would have none and K is long."""
+    got = compiled(tmp_path, "plans", GATED + r'''
+static void flags(const char* name, int64_t tokens, int64_t features, int64_t k) {
+    plan("-", tokens, features, k);
+    std::printf("%s %d\n", name, (made[0].flags & GEMM_FLAG_NO_STREAM_K) != 0);
+}
+int main() {
+    flags("long", 130, 512, 28672);
+    flags("longer", 256, 1024, 28672);
+    flags("short", 130, 1024, 4096);
+    flags("medium", 130, 1024, 6144);
+    flags("many", 256, 4096, 14336);
+    return 0;
+}
+''')
+    whole = {name: flag[0] for name, flag in got.items() if name != "-"}
+    assert whole == {"long": 0, "longer": 0, "short": 1, "medium": 1, "many": 1}
