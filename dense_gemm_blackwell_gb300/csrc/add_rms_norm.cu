@@ -10,9 +10,13 @@
 // 16 (4) neighbouring lanes, so its largest magnitude needs shuffles only.  Few
 // rows take one vector a thread (the time is latency), many rows more.
 //
-// Measured: 8192 x 8192 bf16 with a residual to codes with fp32 scales 73 us, 6.4 TB/s of
-// the 471 MB it needs (the copy rate allows 69; 67 % of the issue slots); 1231 x 2893 f16
-// to MXFP8 codes 7.5 us; 8 x 4096 2.4 us, a launch.  Short rows are bound by
+// Measured, in a graph: 8192 x 8192 bf16 with a residual to codes with fp32 scales 73 us,
+// 6.4 TB/s of the 471 MB it needs (the copy rate allows 69; 67 % of the issue slots), to
+// 16 bits 91 us, 5.9 TB/s; 8192 x 4096 to 16 bits 47; 1231 x 2893 f16 to MXFP8 codes 7.5
+// us; 8 x 4096 2.4 us, a launch (a call from Python takes 13.4 and 4.7 of the last two).
+// Rows past 16384 elements take four vectors a thread, which 64 registers do not hold (192
+// to 268 bytes spilled): 4096 x 32768 194 us to codes (139 allowed), 193 to 16 bits (158).
+// Short rows are bound by
 // instructions, which a row's sums and a block's scale cost whatever its length: 32768 x
 // 1024 without a residual to MXFP8 31 us where the bytes take 15 (one warp a row, four
 // vectors a lane: 27, but 9.2 us instead of 7.6 at 4096 rows with a residual).
@@ -108,7 +112,8 @@ struct NormParams {
 constexpr int kOutSame = 0, kOutBlock128 = 1, kOutMx = 2;
 
 // Rows of a thread on the way or in use: two, but for rows past 16384 elements one, as two of theirs may not fit.  (Three and four
-// are no faster: 8192 x 8192 with a residual to codes 79 and 93 us where two take 79.)
+// were no faster when they were tried: 8192 x 8192 with a residual to codes 79 and 93 us where two took 79, before other steps
+// brought them to 73.)
 template <int VPT>
 __host__ __device__ constexpr int norm_stages() { return VPT == 4 ? 1 : 2; }
 
@@ -272,6 +277,8 @@ struct NormGradParams {
 
 // 8192 x 4096 bf16 48 us with both kernels, 5.6 TB/s (the bytes take 40): instruction issue (58 % of the slots) at 16 warps an SM, whose
 // registers hold the weight gradients; three and four blocks an SM spilled.  The join is 4 of the 48.
+// Rows past 16384 elements take eight vectors a thread and spill (192 to 508 bytes): 4096 x 32768 348 us, where the bytes take 158;
+// 4096 x 16384, four vectors, 88 of 79.
 //
 // dh = d_sum + r dy w - h r^3 mean(dy w h): one exchange for both sums of a row.  A thread keeps the same columns in every row
 // that its block takes and sums their weight gradients in registers.

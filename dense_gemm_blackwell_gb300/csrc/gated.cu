@@ -34,6 +34,10 @@ struct SlopeParams {
     int32_t features, act;
 };
 
+// Both gradients are rounded to 16 bits once, because the products after it take 16-bit operands: at 4096 x 4096 -> 2 x 8192 bf16
+// the errors of dX and dW against 64 bits are 0.0023 of their size, 0.0017 with gradients in 32 bits, which is the outputs' own
+// rounding.  A second 16-bit term would double both products, 590 of the pass's 640 us.
+//
 // Bound by memory: 10 bytes an element of H, 4096 x 8192 in 48 us, 7.0 TB/s (the gradients are partly still in L2 when it ends).
 template <typename T>
 __global__ void __launch_bounds__(kSlopeThreads) gated_slope_kernel(const __grid_constant__ SlopeParams p) {
@@ -216,7 +220,7 @@ void choose_tiles(const gated_desc_t& d, int sms, gemm_desc_t* f) {
 // The gradients' products have MN-major operands, for which the planner does not choose 512-wide tiles by itself. They take them where
 // those fill their last wave well enough to make up for its not being split along K as that of 256-wide tiles is: 16384 x 4096 x 4096
 // (7 waves, 96 % full) 298 us, 352 with 256; the whole backward pass of 2048 and 8192 tokens, 4096 -> 2 x 8192, 323 and 1247 us, 349 and
-// 1356 with 256. Along a short K the unsplit last wave costs more: at 84 % 4096 x 4096 x 16384 still gains (628 us for the whole pass at
+// 1356 with 256 (in a graph; a loop of calls under the power cap takes a tenth more). Along a short K the unsplit last wave costs more: at 84 % 4096 x 4096 x 16384 still gains (628 us for the whole pass at
 // 4096 tokens, 642 with 256 in that product), 16384 x 2048 x 2048 loses (205 us, 187 with 256).  Up to 128 rows are lone CTAs' tiles,
 // for which waves of pairs say nothing: 64 x 32768 x 16384 153 us in the planner's tiles, 189 with 512, 64 x 36864 x 2048 28 and 43.
 int32_t mn_tile(const gemm_desc_t& g, int sms) {

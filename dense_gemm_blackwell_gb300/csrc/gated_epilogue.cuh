@@ -13,8 +13,10 @@ namespace dgb {
 // (a whole tile up to 256 wide, or 256 columns of a 512-wide one) holds gates in its first half and ups in its second: a warp
 // takes chunks of 64 output columns (128 bytes), 32 gates and 32 ups at a time, so that both sums of an element meet in one
 // thread's registers and are never rounded before their product.  Bound by the tensor cores where the tiles are many: 8192 x 4096 -> 2 x
-// 16384 bf16 1104 us, 2.0 PFLOP/s (1215 when the power cap has set in), which is the plain product's rate; writing both sums out and reading them back would move 1.1 GB
-// more, 158 us.  One wave of tiles shows the epilogue: 777 x 1001 -> 2 x 1544 13.7 us, of which the product is 8.8.
+// 16384 bf16 1104 us in a graph, 2.0 PFLOP/s (1215 to 1226 in a loop of calls, when the power cap has set in), which is the plain
+// product's rate; writing both sums out and reading them back would move 1.1 GB more, 158 us.  Keeping both sums for the backward
+// pass: 1190 us where 1120 were measured beside it, 283 and 276 at 4096 x 4096 -> 2 x 8192.  One wave of tiles shows the
+// epilogue: 777 x 1001 -> 2 x 1544 13.7 us, of which the product is 8.8.
 template <int CG, int OUT>
 __device__ __forceinline__ void gated_epilogue(const PersistentParams& p, const GatedTail& q, uint8_t* staging, uint32_t tmem_base,
                                                uint32_t tfull0, uint32_t tempty0, volatile uint32_t* abort_flag, uint32_t rank,

@@ -19,10 +19,11 @@
 // few tiles or X does not fit, and join once in a few tiles.  All sums are fp32 in an
 // order that the sizes alone decide.
 //
-// Bound by memory at first and by latency at the listed sizes: 8 tokens, 4096 -> 77824
-// columns of a pair 36.9 us (4.5 TB/s, 155648 5.2), 24576 17.1 us (3.1 TB/s: 2.2 of a
-// launch, about 3 of bringing X to every block, and 10 or 11 tiles an SM); one token 4096 x
-// 4096 4.9 us, of which 1.3 are the bytes.  16 tokens: instructions (195 TFLOP/s).
+// Bound by memory at first and by latency at smaller sizes: a gated pair of 8 tokens, 4096
+// -> 2 x 38912 36.9 us (4.5 TB/s; 2 x 77824 64.7 us, 5.2), 2 x 12288 17.1 us (3.1 TB/s:
+// 2.2 of a launch, about 3 of bringing X to every block, and 10 or 11 tiles an SM); one
+// token 4096 x 4096 4.9 us, of which 1.3 are the bytes.  16 tokens: instructions (195
+// TFLOP/s); in groups of 128 these spill 8 to 18 bytes a thread.
 //
 // A code is a 16-bit float as it stands: the integers 0..255 in the low bits of an f16 are
 // the multiples of its least step 2^-24, of a bf16 those of 2^-133 (subnormal numbers and

@@ -38,9 +38,10 @@ extern "C" {
  *   GEMM_SCALE_MX_E8M0_32          E4M3 codes and E8M0 scales of every 32 columns in gemm.h's tiles: gemm_run_mx's A and sf_a.
  *                                  s is the least power of two, at least 2^-126, with max|n| <= 448 s.  All bytes of the
  *                                  ceil(tokens/128) x ceil(hidden/128) tiles are written, those past the matrix as 0.
- * Codes are rounded to nearest even and saturate at +-448; a NaN gives the code of NaN (the block's scale is that of its other
- * values).  Infinite h gives NaN at its place and zeros in the rest of the row.  Squares are summed in fp32: rows with |h| past
- * about 1e18 give zeros. */
+ * Codes are rounded to nearest even and saturate at +-448.  A NaN weight gives the code of NaN in its column, and the block's
+ * scale is that of its other values; a NaN in h makes all of its row NaN, whose scales then say nothing.  Infinite h gives NaN at
+ * its place and zeros in the rest of the row.  Squares are summed in fp32: rows with |h| past about 1e18 give zeros, and without
+ * eps rows whose |h| are all under about 1e-19 lose bits and under 1e-23 are infinite or NaN. */
 typedef struct {
     int32_t tokens, hidden;     /* hidden 1..32768; tokens 0 (no-op) .. 2^30 */
     int32_t dtype;              /* GEMM_BF16 or GEMM_F16: x, residual, weight, sum and an unscaled y */
@@ -145,7 +146,8 @@ gemm_status_t gated_plan_destroy(gated_plan_t plan);
  * low half of byte k/2 when k is even.  Products of codes are exact; their sums, the zero points'
  * part, which is taken off a group's sum, and the scaling are fp32; y is rounded once.
  * Infinities and NaN of x and of the scales stay with their token or weight row (an infinite x gives NaN or infinities).  A bf16 x
- * past 2^63 counts as infinite, and one under 2^-57 may lose bits. */
+ * past 2^63 counts as infinite, and one under 2^-57 may lose bits; so does a result for bf16 x under about 2^-70, as its sum is
+ * held in steps of 2^-69. */
 typedef struct {
     int32_t tokens;             /* 0 (no-op) .. 16; more go through the product, with the weights in another form */
     int32_t n, k;               /* n 1..2^30; k even, and such that X fits the shared memory of a cluster: 94208 and less does for up

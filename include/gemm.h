@@ -133,8 +133,8 @@ typedef struct {
     int64_t stride_sa, stride_sb;  /* between batch entries of the scales: floats (fp32 block scales) or bytes
                                       (MX/NV tiles); 0 = packed */
     uint32_t flags;             /* GEMM_FLAG_* */
-    int32_t tile_n;             /* N extent of one output tile: a multiple of 16 in 16..256, or 512 (16-bit/tf32
-                                   operands: two N = 256 MMAs per K step, one 512-column accumulator);
+    int32_t tile_n;             /* N extent of one output tile: a multiple of 16 in 16..256, or 512 (16-bit operands
+                                   and K-major tf32: two N = 256 MMAs per K step, one 512-column accumulator);
                                    block-scaled fp8: 128 or 256; MX/NV: 256; 0 = planner */
     int32_t stages;             /* shared-memory ring depth (2..16); 0 = planner */
     int32_t max_ctas;           /* cap on persistent CTAs; 0 = all SMs */
